@@ -469,6 +469,105 @@ rbkv_status rbkv_frame_attention(rbkv_frame* f, const void* q, const void* k_cac
  * passes loaded since it was last read). */
 rbkv_status rbkv_frame_device_status(rbkv_frame* f, rbkv_stream stream);
 
+/* ---- a step whose metadata lives on the device -------------------------------
+ *
+ * A pass is composed on the host.  In steady decoding the host has nothing to
+ * decide: every request takes its next token (or the tokens a device-side
+ * sampler accepted), and only lengths change.  These calls make such a step
+ * from lengths that are already on the device - block tables, slots, row
+ * offsets and the attention's work plan - with no copy to or from the host
+ * and no synchronisation, so that a whole decoding loop can be captured once
+ * as a CUDA graph and replayed.  The batch may share one prefix (a system
+ * prompt, a document): its keys are attended by all rows of the batch in one
+ * product, each sequence's own keys by its own rows, and the two parts are
+ * joined by their log-sum-exps.
+ *
+ * FastGen guide, "Paged KV Memory Management" (block tables, a pool of free
+ * blocks); "Two-Phase Softmax Reduction" (the join).
+ *
+ * A sequence's table, lengths and positions count its own tokens; the prefix
+ * has a block list of its own, which no sequence's table holds.  Rotary or
+ * learned positions of a token are prefix_len + position. */
+
+/* The arrays of a step, all in device memory, owned by the caller.  They stay
+ * valid for any number of layers until the next build.  Two steps in flight
+ * at once (two streams, two graphs) need tables of their own. */
+typedef struct {
+  int32_t num_seqs;        /* S: request slots (an idle slot takes no tokens) */
+  int32_t max_blocks;      /* entries of one row of block_table */
+  int32_t max_tokens;      /* rows of Q, O, K_new, V_new, slot and position */
+  int32_t* block_table;    /* [S][max_blocks] in/out: entries past a sequence's
+                              blocks are never read */
+  int32_t* free_words;     /* [ceil(num_blocks / 32)] in/out: bit i of word w set =
+                              block 32 w + i is free */
+  int32_t* q_start;        /* [S + 1] out: first row of each sequence; q_start[S] = rows */
+  int32_t* ctx;            /* [S] out: tokens cached after the step */
+  int32_t* position;       /* [max_tokens] out: position in the sequence; -1 past the rows */
+  int32_t* slot;           /* [max_tokens] out: block * B + offset; -1 past the rows */
+  int32_t* plan;           /* [rbkv_step_plan_ints] opaque */
+  int32_t* status;         /* [4] zero at first; see rbkv_step_device_status */
+} rbkv_step_tables;
+
+/* int32 entries of `plan` (0 for sizes below 1). */
+int64_t rbkv_step_plan_ints(int32_t num_seqs, int32_t max_tokens);
+
+/* Build a step: sequence s holds seen[s] tokens and takes n_new[s] >= 0 more.
+ * Each sequence receives the blocks its new tokens begin, lowest free id
+ * first, in sequence order (the composer's rule), and they leave the free
+ * bits.  table_in / free_in: where the block table and the free bits before
+ * the step are read (NULL: t->block_table / t->free_words, in place).  seen
+ * may be t->ctx when the block table is built in place.
+ * All or nothing: a negative length (RBKV_ERR_INVALID), more rows than
+ * max_tokens or a sequence beyond max_blocks (RBKV_ERR_WORKSPACE) or too few
+ * free blocks (RBKV_ERR_NO_BLOCKS) is recorded in the status words, and the
+ * step is empty: no rows, ctx = seen, table and free bits as they were.  A
+ * block id outside the pool in a table is recorded as
+ * RBKV_ERR_DEVICE_BOUNDS and its rows get slot -1.
+ * Errors of the call: RBKV_ERR_INVALID, RBKV_ERR_UNSUPPORTED, RBKV_ERR_CUDA. */
+rbkv_status rbkv_step_build(const rbkv_config* cfg, const rbkv_step_tables* t,
+                            const int32_t* seen, const int32_t* n_new,
+                            const int32_t* table_in, const int32_t* free_in,
+                            rbkv_stream stream);
+
+/* Return the blocks of the sequences with done[s] != 0 (those of ctx[s]
+ * tokens) to the free bits and set their ctx to 0.  The tables must be the
+ * last step's. */
+rbkv_status rbkv_step_release(const rbkv_config* cfg, const rbkv_step_tables* t,
+                              const int32_t* done, rbkv_stream stream);
+
+/* rbkv_kv_append for the step built last: k_new and v_new are
+ * [max_tokens][H_kv][D]; rows past the step's rows are not read. */
+rbkv_status rbkv_step_append(const rbkv_config* cfg, const rbkv_step_tables* t,
+                             const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                             rbkv_stream stream);
+
+/* Bytes of workspace rbkv_step_attention needs (0: none, also for arguments
+ * that it would refuse). */
+size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                 int32_t prefix_len);
+
+/* Attention of the step built last, after its append:
+ *   O[r][h][:] = sum_i softmax_i(Q[r][h] . K[i] / sqrt(D)) V[i]
+ * over the prefix's keys 0 .. prefix_len - 1 (block prefix_table[i / B], slot
+ * i % B) and the keys 0 .. position[r] of the row's sequence.  q, o:
+ * [max_tokens][H_q][D]; rows past the step's rows are not written.
+ * prefix_len >= 0 (prefix_table may be NULL at 0: paged attention of the
+ * step).  workspace: rbkv_step_workspace_bytes, 256-byte aligned, not used by
+ * other work until this call's kernels end (calls that overlap, and graphs
+ * that run at the same time, need one each).
+ * A block id outside the pool is skipped and recorded in the status words.
+ * Errors: RBKV_ERR_INVALID, RBKV_ERR_UNSUPPORTED, RBKV_ERR_WORKSPACE,
+ * RBKV_ERR_CUDA. */
+rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* t, const void* q,
+                                const void* k_cache, const void* v_cache,
+                                const int32_t* prefix_table, int32_t prefix_len, void* o,
+                                void* workspace, size_t workspace_bytes, rbkv_stream stream);
+
+/* Wait for `stream`, then read and clear the status words: RBKV_OK or the
+ * first error since they were last read (see rbkv_step_build; also
+ * RBKV_ERR_TIMEOUT, as rbkv_pass_device_status). */
+rbkv_status rbkv_step_device_status(const rbkv_step_tables* t, rbkv_stream stream);
+
 /* ---- the rest of a decoder layer: tensor-core GEMM and RMSNorm --------------
  *
  * DeepSpeed-FastGen paper summary page, idea I1: a forward pass's latency

@@ -28,6 +28,9 @@ What it computes, plainly and slowly:
   note: replicas behind a load balancer; the policy is this repository's
   reading), loads recomputed from the held requests at every decision.
 
+* ``step``       - a step built from device-side lengths (tables, slots) and
+  attention over a shared prefix and a sequence's own keys, in plain loops.
+
 Pins (tests marked ``not gpu``): the tiny configuration's worked pass, budget
 and conservation invariants, brute force on tiny inputs, closed forms,
 PyTorch's scaled-dot-product attention as an independent library special case,
@@ -37,7 +40,7 @@ block ids, parity unpinned (only that rule and the pool invariants - distinct
 ids, ceil(ctx / B) held per sequence, all-or-nothing - hold them).
 """
 from .composer import Composer, PassMeta, InvalidRequest, NoBlocks, budget_for_latency, latency_at  # noqa: F401
-from . import router  # noqa: F401
+from . import router, step  # noqa: F401
 from .cache import BlockedCache, kv_append  # noqa: F401
 from .attention import (  # noqa: F401
     widen,

@@ -71,6 +71,12 @@ class _FrameCaps(C.Structure):
         "max_combine_rows", "max_parts", "packed_units", "chunk_items")]
 
 
+class _StepTables(C.Structure):
+    _fields_ = [("num_seqs", C.c_int32), ("max_blocks", C.c_int32), ("max_tokens", C.c_int32)] + \
+        [(n, C.c_void_p) for n in ("block_table", "free_words", "q_start", "ctx", "position",
+                                   "slot", "plan", "status")]
+
+
 # Every symbol include/rbkv.h declares, with (restype, argtypes).
 _P = C.c_void_p
 SIGNATURES = {
@@ -120,6 +126,17 @@ SIGNATURES = {
     "rbkv_rmsnorm_bf16": (C.c_int, [_P, _P, _P, C.c_int64, C.c_int64, C.c_float, _P]),
     "rbkv_gemm_bf16_qkv": (C.c_int, [_P, _P, _P, _P, _P, C.c_int64, C.c_int64, C.c_int64,
                                      C.c_int64, _P, C.c_size_t, _P, _P]),
+    "rbkv_step_plan_ints": (C.c_int64, [C.c_int32, C.c_int32]),
+    "rbkv_step_build": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables), _P, _P, _P, _P,
+                                  _P]),
+    "rbkv_step_release": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables), _P, _P]),
+    "rbkv_step_append": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables), _P, _P, _P, _P,
+                                   _P]),
+    "rbkv_step_workspace_bytes": (C.c_size_t, [C.POINTER(_Config), C.POINTER(_StepTables),
+                                               C.c_int32]),
+    "rbkv_step_attention": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables), _P, _P, _P, _P,
+                                      C.c_int32, _P, _P, C.c_size_t, _P]),
+    "rbkv_step_device_status": (C.c_int, [C.POINTER(_StepTables), _P]),
     "rbkv_router_create": (C.c_int, [C.c_int32, C.POINTER(_P)]),
     "rbkv_router_destroy": (None, [_P]),
     "rbkv_router_assign": (C.c_int, [_P, C.c_int64, C.c_int32, C.c_int32,
@@ -357,6 +374,11 @@ def _stream(stream):
     return _P(stream.cuda_stream)
 
 
+def _device(device):
+    import torch
+    return torch.cuda.device(device)
+
+
 def _dev_ptr(t, name, dtype, shape):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -485,6 +507,142 @@ class Frame:
             self.close()
         except Exception:
             pass
+
+
+class StepTables:
+    """Block tables, slots and the attention plan of a step, on the GPU.
+
+    ``build`` makes them from device-side lengths, with no host work and no
+    synchronisation, so that a decoding loop can be captured once as a CUDA
+    graph and replayed; ``append`` and ``attention`` then run any number of
+    layers on them.  The batch may share one prefix with a block list of its
+    own (``prefix_table``), whose keys all rows attend together::
+
+        t = StepTables(cfg, num_seqs, max_blocks, max_tokens)
+        t.build(t.ctx, n_new)                        # n_new: int32 [num_seqs] on the GPU
+        t.append(k_new, v_new, k_cache, v_cache)     # rows in sequence order
+        t.attention(q, k_cache, v_cache, prefix_table=ids, prefix_len=n, o=o, workspace=ws)
+        t.release(done)                              # finished requests' blocks
+
+    Arrays (int32, device memory): ``block_table`` [num_seqs][max_blocks],
+    ``free`` (one bit per block, set = free; all free at first), ``q_start``
+    [num_seqs + 1], ``ctx`` [num_seqs] (0 at first), ``position`` and ``slot``
+    [max_tokens] (-1 past the step's rows).  Lengths, tables and positions
+    count a sequence's own tokens, not the prefix.  A step that does not fit
+    is empty and ``device_status`` says why.
+    """
+
+    def __init__(self, config: Config, num_seqs: int, max_blocks: int, max_tokens: int,
+                 device="cuda"):
+        import torch
+        self.config = config
+        self.num_seqs, self.max_blocks = int(num_seqs), int(max_blocks)
+        self.max_tokens = int(max_tokens)
+        ints = int(lib().rbkv_step_plan_ints(self.num_seqs, self.max_tokens))
+        if ints == 0 or self.max_blocks < 1 or config.num_blocks < 1:
+            raise ValueError("num_seqs, max_blocks, max_tokens and num_blocks must be >= 1")
+        words = -(-config.num_blocks // 32)
+
+        def full(value, *shape):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+
+        self.block_table = full(-1, self.num_seqs, self.max_blocks)
+        self.free = full(-1, words)
+        if config.num_blocks % 32:
+            self.free[-1] = (1 << (config.num_blocks % 32)) - 1
+        self.q_start, self.ctx = full(0, self.num_seqs + 1), full(0, self.num_seqs)
+        self.position, self.slot = full(-1, self.max_tokens), full(-1, self.max_tokens)
+        self.plan, self.status = full(0, ints), full(0, 4)
+        self.device = self.block_table.device
+        self._cfg = config._c()
+        self._t = _StepTables(self.num_seqs, self.max_blocks, self.max_tokens,
+                              *(x.data_ptr() for x in (
+                                  self.block_table, self.free, self.q_start, self.ctx,
+                                  self.position, self.slot, self.plan, self.status)))
+
+    def _ptr(self, t, name, dtype, shape):
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the tables on {self.device}")
+        return _dev_ptr(t, name, dtype, shape)
+
+    def _ints(self, t, name, shape):
+        import torch
+        return self._ptr(t, name, torch.int32, shape)
+
+    def _args(self):
+        return C.byref(self._cfg), C.byref(self._t)
+
+    def build(self, seen, n_new, block_table=None, free=None, stream=None) -> "StepTables":
+        """Sequence s holds ``seen[s]`` tokens and takes ``n_new[s]`` more.
+        ``block_table`` / ``free``: read from these instead of the tables' own
+        (which are written either way)."""
+        S = (self.num_seqs,)
+        table = _P(None) if block_table is None else \
+            self._ints(block_table, "block_table", self.block_table.shape)
+        bits = _P(None) if free is None else self._ints(free, "free", self.free.shape)
+        with _device(self.device):
+            _check(lib().rbkv_step_build(*self._args(), self._ints(seen, "seen", S),
+                                         self._ints(n_new, "n_new", S), table, bits,
+                                         _stream(stream)))
+        return self
+
+    def release(self, done, stream=None) -> None:
+        """Free the blocks of the sequences with ``done[s] != 0`` (int32)."""
+        with _device(self.device):
+            _check(lib().rbkv_step_release(*self._args(),
+                                           self._ints(done, "done", (self.num_seqs,)),
+                                           _stream(stream)))
+
+    def append(self, k_new, v_new, k_cache, v_cache, stream=None) -> None:
+        """Scatter the step's K/V rows ([max_tokens][H_kv][D]) into the caches."""
+        c = self.config
+        dt, row = c.torch_dtype, (self.max_tokens, c.num_heads_kv, c.head_dim)
+        with _device(self.device):
+            _check(lib().rbkv_step_append(
+                *self._args(), self._ptr(k_new, "k_new", dt, row),
+                self._ptr(v_new, "v_new", dt, row),
+                self._ptr(k_cache, "k_cache", dt, c.cache_shape()),
+                self._ptr(v_cache, "v_cache", dt, c.cache_shape()), _stream(stream)))
+
+    def workspace_bytes(self, prefix_len: int = 0) -> int:
+        return int(lib().rbkv_step_workspace_bytes(*self._args(), int(prefix_len)))
+
+    def attention(self, q, k_cache, v_cache, prefix_table=None, prefix_len: int = 0, o=None,
+                  workspace=None, stream=None):
+        """Every row attends the prefix and its sequence's keys up to its own;
+        returns O ([max_tokens][H_q][D]; rows past the step's are left as they
+        were)."""
+        import torch
+        c = self.config
+        dt, shape = c.torch_dtype, (self.max_tokens, c.num_heads_q, c.head_dim)
+        prefix_len = int(prefix_len)
+        table = _P(None)
+        if prefix_table is not None:
+            if prefix_table.dim() != 1 or prefix_table.numel() * c.block_size < prefix_len:
+                raise ValueError("prefix_table must list the blocks of prefix_len tokens")
+            table = self._ints(prefix_table, "prefix_table", prefix_table.shape)
+        with _device(self.device):
+            st = _stream(stream)
+            need = self.workspace_bytes(prefix_len)
+            if o is None or (need and workspace is None):
+                with torch.cuda.stream(torch.cuda.ExternalStream(st.value or 0, self.device)):
+                    if o is None:
+                        o = torch.empty(shape, dtype=dt, device=self.device)
+                    if need and workspace is None:
+                        workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if workspace is not None and workspace.device != self.device:
+                raise ValueError("workspace is on another device than the tables")
+            ws, ws_bytes = _ws(workspace)
+            _check(lib().rbkv_step_attention(
+                *self._args(), self._ptr(q, "q", dt, shape),
+                self._ptr(k_cache, "k_cache", dt, c.cache_shape()),
+                self._ptr(v_cache, "v_cache", dt, c.cache_shape()), table, prefix_len,
+                self._ptr(o, "o", dt, shape), ws, ws_bytes, st))
+        return o
+
+    def device_status(self, stream=None) -> None:
+        with _device(self.device):
+            _check(lib().rbkv_step_device_status(C.byref(self._t), _stream(stream)))
 
 
 def budget_for_latency(tokens, latency, bound: float) -> int:
@@ -641,5 +799,5 @@ class Router:
             pass
 
 
-__all__ = ["gemm", "gemm_qkv", "gemm_workspace_bytes", "rmsnorm", "Router", "Frame", "budget_for_latency", "seq_states", "SeqStates", "ragged_attention_noalloc", "kernel_launches", "profile_enable", "profile_reset", "profile_read", "Config", "Composer", "Pass", "PassMeta", "kv_append", "ragged_attention",
+__all__ = ["gemm", "gemm_qkv", "gemm_workspace_bytes", "rmsnorm", "Router", "Frame", "StepTables", "budget_for_latency", "seq_states", "SeqStates", "ragged_attention_noalloc", "kernel_launches", "profile_enable", "profile_reset", "profile_read", "Config", "Composer", "Pass", "PassMeta", "kv_append", "ragged_attention",
            "RbkvError", "NoBlocksError", "lib", "library_path", "SIGNATURES"]

@@ -755,7 +755,9 @@ rbkv_status ensure_device(rbkv_pass* p, cudaStream_t st) {
   return RBKV_OK;
 }
 
-rbkv_status check_config(const rbkv_config* c) {
+}  // namespace
+
+rbkv_status rbkv::check_config(const rbkv_config* c) {
   if (!c) return fail(RBKV_ERR_INVALID, "config is NULL");
   if (c->num_heads_q < 1 || c->num_heads_kv < 1 || c->num_heads_q % c->num_heads_kv)
     return fail(RBKV_ERR_INVALID, "num_heads_q must be a positive multiple of num_heads_kv");
@@ -771,8 +773,6 @@ rbkv_status check_config(const rbkv_config* c) {
     return fail(RBKV_ERR_UNSUPPORTED, "at most 64 query heads per KV head");
   return RBKV_OK;
 }
-
-}  // namespace
 
 // ---- attention on a pass already on the device, with a given scratch ---------
 // Used by the entry point that allocates nothing (rbkv_noalloc.cu): unlike
@@ -1202,6 +1202,11 @@ rbkv_status read_device_status(void* dev, cudaStream_t st) {
   if (e != cudaSuccess) return cuda_fail(e, "device status read");
   const int32_t word = words[0];
   if (word == kDevBounds) return fail(RBKV_ERR_DEVICE_BOUNDS, "a kernel met an out-of-range block id");
+  // a step built from device lengths (rbkv_step_build) that was not scheduled
+  if (word == RBKV_ERR_NO_BLOCKS) return fail(RBKV_ERR_NO_BLOCKS, "the step needs more blocks than are free");
+  if (word == RBKV_ERR_WORKSPACE)
+    return fail(RBKV_ERR_WORKSPACE, "the step exceeds max_tokens or max_blocks of its tables");
+  if (word == RBKV_ERR_INVALID) return fail(RBKV_ERR_INVALID, "the step has a negative length");
   if (word == kDevTimeout)
     return fail(RBKV_ERR_TIMEOUT, "a bounded device wait gave up (site " + std::to_string(words[1]) +
                                       ", index " + std::to_string(words[2]) + ", block " +
@@ -1212,6 +1217,10 @@ rbkv_status read_device_status(void* dev, cudaStream_t st) {
 }
 
 }  // namespace
+
+rbkv_status rbkv::read_status_words(int32_t* words, cudaStream_t st) {
+  return read_device_status(words, st);
+}
 
 extern "C" {
 

@@ -224,6 +224,10 @@ rbkv_status attention_on_device(rbkv_pass* p, const void* q, const void* k_cache
                                 const void* v_cache, void* o, void* scratch,
                                 size_t scratch_bytes, cudaStream_t st);
 rbkv_status set_error(rbkv_status st, const char* msg);
+// Whether the kernels can run this shape (records the message when not).
+rbkv_status check_config(const rbkv_config* c);
+// Wait for the stream, then read and clear four status words on the device.
+rbkv_status read_status_words(int32_t* words, cudaStream_t st);
 // Count n kernel launches made outside rbkv_host.cpp (rbkv_kernel_launches).
 void note_launches(int64_t n);
 }  // namespace rbkv
