@@ -26,7 +26,7 @@ LIB = LIBDIR / "librbkv.so"
 SOURCES = ["rbkv_host.cpp", "rbkv_kernels.cu", "rbkv_decode.cu", "rbkv_chunk.cu",
            "rbkv_chunk_single.cu", "rbkv_noalloc.cu", "rbkv_router.cpp",
            "rbkv_gemm.cu", "rbkv_layer.cpp", "rbkv_step.cpp", "rbkv_tables.cu",
-           "rbkv_step_generic.cu"]
+           "rbkv_step_generic.cu", "rbkv_step_stream.cu", "rbkv_step_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -162,6 +162,9 @@ int decode_ctas_per_sm(const ShapeInfo& s);
 // rows of head_dim elements, boxes of 64 columns x box_rows rows, 128 B swizzle.
 cudaError_t make_cache_tmap(::CUtensorMap_st* m, const void* cache, int64_t rows,
                             int head_dim, int box_rows);
+// Q [tokens][H_q][D] bf16 as a 3-D tensor: boxes of 64 columns x the g heads of
+// a group x 128 / g tokens, 128 B swizzle.
+cudaError_t make_q_tmap(::CUtensorMap_st* m, const void* q, int64_t tokens, const ShapeInfo& s);
 // Any row-major bf16 [rows][cols] matrix, same box width and swizzle.
 cudaError_t make_tmap_2d(::CUtensorMap_st* m, const void* ptr, int64_t rows, int64_t cols,
                          int box_rows);

@@ -6,6 +6,8 @@
 
 #include "rbkv_step.h"
 
+#include <cuda_runtime.h>
+
 using namespace rbkv;
 
 namespace {
@@ -54,6 +56,14 @@ BuildArgs build_args(const rbkv_config* c, const rbkv_step_tables* t) {
   a.plan = t->plan;
   a.status = t->status;
   return a;
+}
+
+cudaError_t num_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && *sms < 1) e = cudaErrorInvalidDevice;
+  return e;
 }
 
 ShapeInfo shape(const rbkv_config* c) {
@@ -144,10 +154,11 @@ rbkv_status rbkv_step_append(const rbkv_config* cfg, const rbkv_step_tables* t,
 
 size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables* t,
                                  int32_t prefix_len) {
-  (void)cfg;
-  (void)t;
-  (void)prefix_len;
-  return 0;
+  if (check_tables(cfg, t) != RBKV_OK || prefix_len < 0) return 0;
+  const ShapeInfo s = shape(cfg);
+  int sms = 0;
+  if (!step_fast_supported(s) || num_sms(&sms) != cudaSuccess) return 0;
+  return step_workspace(s, t->max_tokens, sms, nullptr, nullptr);
 }
 
 rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* t, const void* q,
@@ -164,9 +175,6 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
   if (prefix_len < 0) return invalid("prefix_len must be >= 0");
   if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4)))
     return invalid("a prefix needs a 4-byte aligned block list");
-  const size_t need = rbkv_step_workspace_bytes(cfg, t, prefix_len);
-  if (need > 0 && (!workspace || workspace_bytes < need))
-    return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
   if (!aligned(workspace, 256)) return invalid("workspace must be 256-byte aligned");
   DevStep ds = {};
   ds.num_seqs = t->num_seqs;
@@ -181,9 +189,28 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
   ds.prefix_table = prefix_table;
   ds.prefix_len = prefix_len;
   const ShapeInfo s = shape(cfg);
-  cudaError_t e = launch_step_generic(ds, s, q, k_cache, v_cache, o, (cudaStream_t)stream);
+  const cudaStream_t cs = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (!step_fast_supported(s)) {
+    e = launch_step_generic(ds, s, q, k_cache, v_cache, o, cs);
+    if (e == cudaSuccess) note_launches(1);
+  } else {
+    int sms = 0;
+    e = num_sms(&sms);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    StepWorkspace w;
+    const size_t need = step_workspace(s, t->max_tokens, sms, workspace, &w);
+    if (!workspace || workspace_bytes < need)
+      return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
+    // a step of at most 16 packed rows has no work for the tile kernel
+    const bool tiles = !step_prefix_streamed(t->max_tokens, s.g);
+    if (tiles) e = launch_step_tile(ds, s, w, q, k_cache, v_cache, o, true, cs);
+    if (e == cudaSuccess)
+      e = launch_step_stream(ds, s, w, q, k_cache, v_cache, o, !tiles, cs);
+    if (e == cudaSuccess) e = launch_step_combine(ds, s, w, o, cs);
+    if (e == cudaSuccess) note_launches(tiles ? 3 : 2);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "step attention launch");
-  note_launches(1);
   return RBKV_OK;
 }
 

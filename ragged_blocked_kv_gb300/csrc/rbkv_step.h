@@ -113,6 +113,67 @@ struct DevStep {
   int32_t prefix_len;
 };
 
+// Work is cut evenly over the CTAs of a persistent grid.  All key tiles of a
+// kernel's work units lie on one line, units one after the other; with
+// G' = min(grid, total), CTA c walks the tiles [start(c), start(c + 1)),
+// start(c) = floor(c total / G').  A unit is so cut into one segment per CTA
+// that meets it.  The segment at a unit's first tile writes its result to the
+// unit's own rows of the workspace; a segment that begins inside a unit can
+// only be the first of its CTA, and goes to that CTA's spill rows.
+__host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, int64_t ctas) {
+  return c * total / ctas;
+}
+
+// The units of the streaming kernel: (streamed sequence, KV head), the KV
+// heads of a sequence in order; then, when the whole step has at most
+// kStepPackedRows packed rows, the prefix as one more sequence.
+// The units of the tile kernel: (KV head, pair of query tiles) over the
+// prefix unless it is streamed; then (tiled sequence, KV head, pair).
+struct StepWork {
+  int64_t stream_own, stream_total;   // 64-key tiles
+  int64_t tile_prefix, tile_total;    // key-tile steps
+  int32_t prefix_stream_tiles;        // 64-key tiles of the prefix, when streamed
+  int32_t prefix_tile_steps;          // 128-key tiles of the prefix, when tiled
+  int32_t prefix_pairs;               // pairs of query tiles over the prefix
+};
+
+__host__ __device__ __forceinline__ bool step_prefix_streamed(int32_t max_tokens, int32_t g) {
+  return (int64_t)max_tokens * g <= kStepPackedRows;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo& s,
+                                              const StepPlan& plan) {
+  StepWork w;
+  const int32_t T = plan.header[kPlanRows];
+  const bool streamed = step_prefix_streamed(ds.max_tokens, s.g);
+  const int32_t P = T > 0 ? ds.prefix_len : 0;
+  w.prefix_stream_tiles = streamed ? (P + kStepStreamKeys - 1) / kStepStreamKeys : 0;
+  w.prefix_tile_steps = streamed ? 0 : (int32_t)(((int64_t)P + kStepTileKeys - 1) / kStepTileKeys);
+  const int32_t pair = 2 * step_tile_tokens(s.g);
+  w.prefix_pairs = (T + pair - 1) / pair;
+  w.stream_own = (int64_t)plan.header[kPlanStreamTiles] * s.H_kv;
+  w.stream_total = w.stream_own + (int64_t)w.prefix_stream_tiles * s.H_kv;
+  w.tile_prefix = (int64_t)s.H_kv * w.prefix_pairs * w.prefix_tile_steps;
+  w.tile_total = w.tile_prefix + (int64_t)plan.header[kPlanTileSteps] * s.H_kv;
+  return w;
+}
+#endif
+
+// The workspace: fp32 partial outputs (head dim 128) and base-2 log-sum-exps.
+struct StepWorkspace {
+  float *own_o, *pre_o;         // [max_tokens][H_q][128]
+  float *own_lse, *pre_lse;     // [max_tokens][H_q]
+  float *stream_o, *stream_lse; // spill rows [stream grid][kStepPackedRows]
+  float *tile_o, *tile_lse;     // spill rows [tile grid][2 kStepTileRows]
+  int32_t stream_grid, tile_grid;
+};
+
+bool step_fast_supported(const ShapeInfo& s);
+// Carve a workspace at `base` (may be null); returns its bytes.
+size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* base,
+                      StepWorkspace* w);
+
 struct BuildArgs {
   int32_t num_seqs, max_blocks, max_tokens, num_blocks;
   int32_t block_size, group;
@@ -126,4 +187,15 @@ cudaError_t launch_step_release(const BuildArgs& a, const int32_t* done, cudaStr
 cudaError_t launch_step_generic(const DevStep& ds, const ShapeInfo& s, const void* q,
                                 const void* k_cache, const void* v_cache, void* o,
                                 cudaStream_t st);
+// The fast path's three kernels.  The first one launched of the first two
+// waits for the stream's previous kernel (`first`); the other starts beside
+// it and waits for it before ending; the combine waits for both.
+cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                             const void* q, const void* k_cache, const void* v_cache, void* o,
+                             bool first, cudaStream_t st);
+cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                               const void* q, const void* k_cache, const void* v_cache, void* o,
+                               bool first, cudaStream_t st);
+cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                                void* o, cudaStream_t st);
 }  // namespace rbkv

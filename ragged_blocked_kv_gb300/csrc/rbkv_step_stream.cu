@@ -1,0 +1,687 @@
+// Streaming attention of a step: units of at most 16 packed query rows (a
+// sequence's new tokens x the heads of one KV group) over the sequence's own
+// keys; every cached K/V byte is read once, so HBM bounds it.
+//
+// The units' 64-key tiles lie on one line that is cut evenly over the CTAs
+// (rbkv_step.h): two CTAs per SM, each with
+//  - a producer warp that streams K and V tiles through the block table with
+//    TMA (128-byte swizzle) into a 3-stage ring of 32 KB stages;
+//  - four consumer warps that share every tile, 16 keys each: S = Q K^T with
+//    m16n8k16 MMAs (the rows padded to 16; the contraction is tiny, so they
+//    only lift the bound that CUDA cores would set), an online softmax in
+//    registers, O += P V; at the end of a segment their (max, sum, O) are
+//    merged through shared memory, half of the head dim at a time (16 KB of
+//    scratch beside the ring leaves room for two CTAs per SM).
+// Every wait is bounded; on timeout the kernel records RBKV_ERR_TIMEOUT and
+// returns.
+#include <algorithm>
+#include <atomic>
+
+#include "rbkv_step.h"
+#include "rbkv_ptx.cuh"
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace rbkv {
+
+namespace {
+
+constexpr int kStages = 3;
+constexpr int kConsumers = 4;
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kKeys = kStepStreamKeys;
+constexpr int kHalf = kKeys * 128;            // 64 rows x 128 B (64 bf16 of head_dim)
+constexpr int kTile = 2 * kHalf;              // K or V tile, head_dim 128
+constexpr int kStage = 2 * kTile;             // K + V
+constexpr int kRows = kStepPackedRows;
+constexpr int kScratch = kConsumers * kRows * 64 * 4;   // [warp][row][64] fp32
+constexpr int kMl = kConsumers * kRows * 2 * 4;         // (max, sum) per warp and row
+constexpr int kSmemBytes = kStages * kStage + kScratch + kMl + 2 * kStages * 8 + 16;
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr long long kWaitLimit = 4000000000LL;   // ~2 s of SM clock
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Shared {
+  uint8_t* stages;
+  float* scratch;
+  float* ml;
+  uint64_t* full;
+  uint64_t* empty;
+  volatile int* abort_flag;
+};
+
+__device__ __forceinline__ Shared carve(uint8_t* raw) {
+  Shared s;
+  s.stages = raw;
+  s.scratch = reinterpret_cast<float*>(raw + kStages * kStage);
+  s.ml = s.scratch + kScratch / 4;
+  s.full = reinterpret_cast<uint64_t*>(s.ml + kMl / 4);
+  s.empty = s.full + kStages;
+  s.abort_flag = reinterpret_cast<volatile int*>(s.empty + kStages);
+  return s;
+}
+
+// Byte offset, inside one K or V tile, of the 16-byte chunk holding elements
+// d..d+7 (d % 8 == 0) of key row `key` (128-byte swizzle, each 64-column half
+// a separate 8 KB box).
+__device__ __forceinline__ uint32_t tile_off(int key, int d) {
+  const int half = d >> 6;
+  const int chunk = (d & 63) >> 3;
+  return half * kHalf + key * 128 + ((chunk ^ (key & 7)) << 4);
+}
+
+// One segment: the key tiles [tile, tile_end) of a unit.
+struct Segment {
+  const int32_t* table;
+  int row, n_tok;        // first row and tokens of the unit
+  int kv_head;
+  int tile, tile_end;
+  int keys;              // keys of the unit's last row
+  int diag;              // keys of its first row (the prefix: every row sees all)
+  bool prefix, head, whole;
+};
+
+// Walks a CTA's part [x, end) of the line.
+struct Walk {
+  int64_t x, end;
+  int unit;              // streamed sequence
+  int seq, cum, n_tiles; // of that sequence
+};
+
+// The last i with cum[i] <= v among i in [0, n), cum[0] = 0: every lane tests
+// one of 32 places of the range that is left.
+__device__ __forceinline__ int search(const int32_t* cum, int n, int64_t v, int lane) {
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) >> 5;
+    const int at = lo + lane * step;
+    const bool le = lane * step < len && cum[at] <= v;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int k = 31 - __clz(m);          // lane 0 always holds
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void load_unit(Walk& w, const StepPlan& plan) {
+  w.seq = plan.stream_seq[w.unit];
+  w.cum = plan.stream_cum[w.unit];
+  w.n_tiles = plan.stream_cum[w.unit + 1] - w.cum;
+}
+
+__device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const ShapeInfo& s,
+                                             const StepPlan& plan, const StepWork& work,
+                                             Segment& g) {
+  if (w.x >= w.end) return false;
+  int64_t unit0;
+  int n_tiles;
+  if (w.x < work.stream_own) {
+    if (w.x >= (int64_t)s.H_kv * (w.cum + w.n_tiles)) {
+      ++w.unit;
+      load_unit(w, plan);
+    }
+    const int64_t base = (int64_t)s.H_kv * w.cum;
+    n_tiles = w.n_tiles;
+    g.kv_head = (int)((w.x - base) / n_tiles);
+    unit0 = base + (int64_t)g.kv_head * n_tiles;
+    g.prefix = false;
+    g.row = ds.q_start[w.seq];
+    g.n_tok = ds.q_start[w.seq + 1] - g.row;
+    g.keys = ds.ctx[w.seq];
+    g.diag = g.keys - g.n_tok + 1;
+    g.table = ds.block_table + (int64_t)w.seq * ds.max_blocks;
+  } else {
+    n_tiles = work.prefix_stream_tiles;
+    g.kv_head = (int)((w.x - work.stream_own) / n_tiles);
+    unit0 = work.stream_own + (int64_t)g.kv_head * n_tiles;
+    g.prefix = true;
+    g.row = 0;
+    g.n_tok = plan.header[kPlanRows];
+    g.keys = g.diag = ds.prefix_len;
+    g.table = ds.prefix_table;
+  }
+  g.tile = (int)(w.x - unit0);
+  g.tile_end = (int)min((int64_t)n_tiles, w.end - unit0);
+  g.head = g.tile == 0;
+  g.whole = g.head && g.tile_end == n_tiles;
+  w.x += g.tile_end - g.tile;
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+    step_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
+                       StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
+                       __nv_bfloat16* __restrict__ o, int first) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (first) ptx::pdl_wait_previous();
+  ptx::pdl_launch_dependents();
+  Shared sm = carve(smem_raw);
+  volatile int& abort_flag = *sm.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = shp.g, B = shp.B, H_kv = shp.H_kv;
+  const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+  const StepWork work = step_work(ds, shp, plan);
+  const int64_t ctas = min((int64_t)gridDim.x, work.stream_total);
+  if ((ptx::smem_u32(smem_raw) & 1023) || blockIdx.x >= ctas) {
+    // (the swizzled tile layout needs a 1024-byte aligned base)
+    if (threadIdx.x == 0 && blockIdx.x < ctas) atomicCAS(ds.status, 0, kDevBounds);
+    ptx::pdl_wait_previous();   // the grid's completion still covers its predecessor
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.empty[s], kConsumers);
+    }
+    abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  Walk walk;
+  walk.x = step_cut(blockIdx.x, work.stream_total, ctas);
+  walk.end = step_cut(blockIdx.x + 1, work.stream_total, ctas);
+  walk.unit = walk.seq = walk.cum = walk.n_tiles = 0;
+  if (walk.x < work.stream_own) {
+    walk.unit = search(plan.stream_cum, plan.header[kPlanStreamed], walk.x / H_kv, lane);
+    load_unit(walk, plan);
+  }
+  __syncthreads();
+
+  Segment it;
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&tmap_k);
+      ptx::tma_prefetch_desc(&tmap_v);
+      uint32_t idx = 0;
+      const int box_rows = B < kKeys ? B : kKeys;
+      while (!abort_flag && next_segment(walk, ds, shp, plan, work, it)) {
+        for (int j = it.tile; j < it.tile_end; ++j, ++idx) {
+          const int s = idx % kStages;
+          if (idx >= (uint32_t)kStages &&
+              !ptx::mbar_wait(&sm.empty[s], ((idx / kStages) - 1) & 1, kWaitLimit)) {
+            ptx::report_wait(ds.status, kDevTimeout, 61, (int)idx);
+            abort_flag = 1;
+            break;
+          }
+          const int k0 = j * kKeys;
+          uint8_t* kdst = sm.stages + s * kStage;
+          uint8_t* vdst = kdst + kTile;
+          // boxes of box_rows keys; none past the unit's last key
+          int nsub = 0, loads = 0;
+          int32_t rows[kKeys / 8];
+          for (int r = 0; r < kKeys && k0 + r < it.keys; r += box_rows) {
+            const int32_t blk = it.table[(k0 + r) / B];
+            if (blk < 0 || blk >= ds.num_blocks) {
+              atomicCAS(ds.status, 0, kDevBounds);
+              rows[nsub++] = -1;
+              continue;
+            }
+            rows[nsub++] = (blk * H_kv + it.kv_head) * B + ((k0 + r) % B);
+            ++loads;
+          }
+          ptx::mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(loads * box_rows * 128 * 4));
+          for (int i = 0; i < nsub; ++i) {
+            if (rows[i] < 0) continue;
+            const int off = i * box_rows * 128;
+            ptx::tma_load_2d(kdst + off, &tmap_k, 0, rows[i], &sm.full[s]);
+            ptx::tma_load_2d(kdst + kHalf + off, &tmap_k, 64, rows[i], &sm.full[s]);
+            ptx::tma_load_2d(vdst + off, &tmap_v, 0, rows[i], &sm.full[s]);
+            ptx::tma_load_2d(vdst + kHalf + off, &tmap_v, 64, rows[i], &sm.full[s]);
+          }
+        }
+        if (abort_flag) break;
+      }
+      // let every load this CTA issued land before the CTA can exit
+      for (uint32_t t = idx > (uint32_t)kStages ? idx - kStages : 0; t < idx; ++t)
+        ptx::mbar_wait(&sm.full[t % kStages], (t / kStages) & 1, kWaitLimit);
+    }
+    ptx::pdl_wait_previous();
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const float qk_scale = shp.scale * kLog2e;
+  const int r0 = lane >> 2, r1 = r0 + 8;      // fragment rows: token r / g, head r % g
+  const int t0 = r0 / g, t1 = r1 / g;
+  const int cq = (lane & 3) * 2;              // fragment column pair
+  const uint32_t stages_u32 = ptx::smem_u32(sm.stages);
+  uint32_t tile_base = 0;
+
+  // the unit's query rows as m16n8k16 A fragments; rows past its end are zero
+  auto load_q = [&](const Segment& u, uint32_t(&dst)[8][4]) {
+    const bool live0 = t0 < u.n_tok, live1 = t1 < u.n_tok;
+    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(
+        q + ((int64_t)(u.row + t0) * shp.H_q + u.kv_head * g + r0 % g) * 128);
+    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(
+        q + ((int64_t)(u.row + t1) * shp.H_q + u.kv_head * g + r1 % g) * 128);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const int c = (kk * 16 + cq) >> 1;
+      dst[kk][0] = live0 ? __ldg(q0 + c) : 0u;
+      dst[kk][1] = live1 ? __ldg(q1 + c) : 0u;
+      dst[kk][2] = live0 ? __ldg(q0 + c + 4) : 0u;
+      dst[kk][3] = live1 ? __ldg(q1 + c + 4) : 0u;
+    }
+  };
+  uint32_t qa[8][4];
+  bool more = next_segment(walk, ds, shp, plan, work, it);
+  if (more) load_q(it, qa);
+
+  while (more) {
+    const int nt = it.tile_end - it.tile;
+    const int nrg = it.n_tok * g;
+    const int lim0 = min(it.keys, it.diag + t0), lim1 = min(it.keys, it.diag + t1);
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float acc_o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc_o[i][0] = acc_o[i][1] = acc_o[i][2] = acc_o[i][3] = 0.f;
+
+    // every warp takes 16 keys (rows 16*warp .. 16*warp+15) of every tile, so
+    // each warp consumes the stages strictly in order
+    const int wk = warp * 16;
+    for (int j = 0; j < nt && !abort_flag; ++j) {
+      const uint32_t idx = tile_base + j;
+      const int s = idx % kStages;
+      if (!ptx::mbar_wait(&sm.full[s], (idx / kStages) & 1, kWaitLimit)) {
+        // give up on this unit; the merge barriers below are still met by
+        // every consumer warp, then all of them leave together
+        if (lane == 0) {
+          ptx::report_wait(ds.status, kDevTimeout, 62, (int)idx);
+          abort_flag = 1;
+        }
+        __syncwarp();
+        break;
+      }
+      const int k0 = (it.tile + j) * kKeys;
+      const int valid = min(kKeys, it.keys - k0) - wk;   // valid keys of this warp's 16
+      const uint32_t kt = stages_u32 + s * kStage;
+      const uint32_t vt = kt + kTile;
+      if (valid < 16) {
+        // rows past the unit's last key may hold anything (unwritten cache
+        // slots, stale tiles): zero this warp's such V rows so 0 * V stays 0
+        uint8_t* vrow = sm.stages + s * kStage + kTile;
+        const int from = valid < 0 ? 0 : valid;
+        for (int e = lane; e < (16 - from) * 16; e += 32) {
+          const int key = wk + from + e / 16, c = e % 16;
+          *reinterpret_cast<uint4*>(vrow + (c >> 3) * kHalf + key * 128 + ((c & 7) << 4)) =
+              make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      if (valid > 0) {
+        // S = Q K^T over this warp's 16 keys: 2 n-tiles of 8 keys
+        float sc[2][4];
+        sc[0][0] = sc[0][1] = sc[0][2] = sc[0][3] = 0.f;
+        sc[1][0] = sc[1][1] = sc[1][2] = sc[1][3] = 0.f;
+        const int mi = lane >> 3;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int key = wk + (mi >> 1) * 8 + (lane & 7);
+          const int d = kk * 16 + (mi & 1) * 8;
+          uint32_t b0, b1, b2, b3;
+          ptx::ldsm_x4(kt + tile_off(key, d), b0, b1, b2, b3);
+          ptx::mma_bf16_16816(sc[0], qa[kk], b0, b1);
+          ptx::mma_bf16_16816(sc[1], qa[kk], b2, b3);
+        }
+        // scale, mask keys past each row's limit, online softmax (rows r0 and r1)
+        const int valid0 = min(kKeys, lim0 - k0) - wk, valid1 = min(kKeys, lim1 - k0) - wk;
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = n * 8 + cq;
+          sc[n][0] = key < valid0 ? sc[n][0] * qk_scale : -INFINITY;
+          sc[n][1] = key + 1 < valid0 ? sc[n][1] * qk_scale : -INFINITY;
+          sc[n][2] = key < valid1 ? sc[n][2] * qk_scale : -INFINITY;
+          sc[n][3] = key + 1 < valid1 ? sc[n][3] * qk_scale : -INFINITY;
+          mx0 = fmaxf(mx0, fmaxf(sc[n][0], sc[n][1]));
+          mx1 = fmaxf(mx1, fmaxf(sc[n][2], sc[n][3]));
+        }
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+        // a row with no visible key so far keeps max -inf: its terms are 0
+        const float b0 = mn0 == -INFINITY ? 0.f : mn0, b1 = mn1 == -INFINITY ? 0.f : mn1;
+        const float c0 = ptx::ex2(m0 - b0), c1 = ptx::ex2(m1 - b1);
+        m0 = mn0;
+        m1 = mn1;
+        const float p00 = ptx::ex2(sc[0][0] - b0), p01 = ptx::ex2(sc[0][1] - b0);
+        const float p02 = ptx::ex2(sc[0][2] - b1), p03 = ptx::ex2(sc[0][3] - b1);
+        const float p10 = ptx::ex2(sc[1][0] - b0), p11 = ptx::ex2(sc[1][1] - b0);
+        const float p12 = ptx::ex2(sc[1][2] - b1), p13 = ptx::ex2(sc[1][3] - b1);
+        l0 = l0 * c0 + (p00 + p01 + p10 + p11);
+        l1 = l1 * c1 + (p02 + p03 + p12 + p13);
+        // the weights enter the value product as bf16 (its operand type): each
+        // off by at most 2^-8 of itself; their sum above stays fp32
+        uint32_t pa[4];
+        pa[0] = ptx::pack_bf16x2(p00, p01);
+        pa[1] = ptx::pack_bf16x2(p02, p03);
+        pa[2] = ptx::pack_bf16x2(p10, p11);
+        pa[3] = ptx::pack_bf16x2(p12, p13);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          acc_o[i][0] *= c0;
+          acc_o[i][1] *= c0;
+          acc_o[i][2] *= c1;
+          acc_o[i][3] *= c1;
+        }
+        // O += P V over the 16 keys: 16 n-tiles of 8 head-dim columns
+#pragma unroll
+        for (int dp2 = 0; dp2 < 8; ++dp2) {
+          const int key = wk + (mi & 1) * 8 + (lane & 7);
+          const int d = dp2 * 16 + (mi >> 1) * 8;
+          uint32_t v0, v1, v2, v3;
+          ptx::ldsm_x4_t(vt + tile_off(key, d), v0, v1, v2, v3);
+          ptx::mma_bf16_16816(acc_o[2 * dp2], pa, v0, v1);
+          ptx::mma_bf16_16816(acc_o[2 * dp2 + 1], pa, v2, v3);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&sm.empty[s]);
+      }
+    }
+    tile_base += nt;
+
+    // the next segment and its queries, loaded while this one is merged
+    const Segment cur = it;
+    more = next_segment(walk, ds, shp, plan, work, it);
+    uint32_t qn[8][4];
+    if (more) load_q(it, qn);
+
+    // ---- merge the four warps' states and write the segment's result -------
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if ((lane & 3) == 0) {
+      sm.ml[(warp * kRows + r0) * 2 + 0] = m0;
+      sm.ml[(warp * kRows + r0) * 2 + 1] = l0;
+      sm.ml[(warp * kRows + r1) * 2 + 0] = m1;
+      sm.ml[(warp * kRows + r1) * 2 + 1] = l1;
+    }
+    ptx::named_bar_sync(1, kConsumers * 32);
+    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kConsumers; ++w) {
+      M0 = fmaxf(M0, sm.ml[(w * kRows + r0) * 2]);
+      M1 = fmaxf(M1, sm.ml[(w * kRows + r1) * 2]);
+    }
+#pragma unroll
+    for (int w = 0; w < kConsumers; ++w) {
+      const float mw0 = sm.ml[(w * kRows + r0) * 2], mw1 = sm.ml[(w * kRows + r1) * 2];
+      if (mw0 != -INFINITY) L0 += ptx::ex2(mw0 - M0) * sm.ml[(w * kRows + r0) * 2 + 1];
+      if (mw1 != -INFINITY) L1 += ptx::ex2(mw1 - M1) * sm.ml[(w * kRows + r1) * 2 + 1];
+    }
+    const float f0 = (m0 == -INFINITY || L0 == 0.f) ? 0.f : ptx::ex2(m0 - M0) / L0;
+    const float f1 = (m1 == -INFINITY || L1 == 0.f) ? 0.f : ptx::ex2(m1 - M1) / L1;
+    // where row r of the segment goes: O itself when nothing is to be joined,
+    // the unit's rows of the workspace, or this CTA's spill rows
+    const bool direct = cur.whole && ds.prefix_len == 0;
+    float* part = cur.head ? (cur.prefix ? ws.pre_o : ws.own_o) : ws.stream_o;
+    float* lse = cur.head ? (cur.prefix ? ws.pre_lse : ws.own_lse) : ws.stream_lse;
+    auto place = [&](int r) -> int64_t {
+      return cur.head || direct ? (int64_t)(cur.row + r / g) * shp.H_q + cur.kv_head * g + r % g
+                                : (int64_t)blockIdx.x * kRows + r;
+    };
+    const int t = threadIdx.x;   // 0..127
+    float* scr = sm.scratch + warp * kRows * 64;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      // each warp stores its rescaled O, 64 columns (8-column groups permuted
+      // by the row, for the banks); then all four are summed per element
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int a = hf * 8 + i;
+        if (r0 < nrg)
+          *reinterpret_cast<float2*>(scr + r0 * 64 + ((i ^ (r0 & 7)) << 3) + cq) =
+              make_float2(acc_o[a][0] * f0, acc_o[a][1] * f0);
+        if (r1 < nrg)
+          *reinterpret_cast<float2*>(scr + r1 * 64 + ((i ^ (r1 & 7)) << 3) + cq) =
+              make_float2(acc_o[a][2] * f1, acc_o[a][3] * f1);
+      }
+      ptx::named_bar_sync(1, kConsumers * 32);
+      for (int e = t; e < nrg * 16; e += kConsumers * 32) {
+        const int r = e >> 4, c4 = (e & 15) * 4;
+        const int at = r * 64 + (((c4 >> 3) ^ (r & 7)) << 3) + (c4 & 7);
+        float4 a = *reinterpret_cast<const float4*>(sm.scratch + at);
+#pragma unroll
+        for (int w = 1; w < kConsumers; ++w) {
+          const float4 b = *reinterpret_cast<const float4*>(sm.scratch + w * kRows * 64 + at);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        const int64_t to = place(r) * 128 + hf * 64 + c4;
+        if (direct) {
+          uint2 packed;
+          packed.x = ptx::pack_bf16x2(a.x, a.y);
+          packed.y = ptx::pack_bf16x2(a.z, a.w);
+          *reinterpret_cast<uint2*>(o + to) = packed;
+        } else {
+          *reinterpret_cast<float4*>(part + to) = a;
+        }
+      }
+      if (hf == 0) ptx::named_bar_sync(1, kConsumers * 32);
+    }
+    if (!direct && warp == 0 && (lane & 3) == 0) {
+      if (r0 < nrg) lse[place(r0)] = L0 > 0.f ? M0 + log2f(L0) : -INFINITY;
+      if (r1 < nrg) lse[place(r1)] = L1 > 0.f ? M1 + log2f(L1) : -INFINITY;
+    }
+    // all consumer warps leave together if anyone gave up
+    if (ptx::named_bar_or(1, kConsumers * 32, abort_flag != 0)) break;
+    if (more) {
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) qa[kk][x] = qn[kk][x];
+    }
+  }
+  ptx::pdl_wait_previous();
+}
+
+// ---------------------------------------------------------------------------
+// The join: one warp per (row, query head), four columns per lane.
+// ---------------------------------------------------------------------------
+// O = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M) over the row's partial
+// outputs: its own part and the prefix's, each with the spills of the CTAs
+// whose cuts fall inside its unit.  The cuts are a formula, so nothing is
+// searched or stored.  Bound by the partials' traffic (from L2, they were
+// just written) and a launch.
+struct Join {
+  float M, L;
+  float4 acc;
+  __device__ __forceinline__ void add(float lse, float4 v) {
+    if (lse == -INFINITY) return;
+    const float m = fmaxf(M, lse);
+    const float a = M == -INFINITY ? 0.f : exp2f(M - m), b = exp2f(lse - m);
+    M = m;
+    L = L * a + b;
+    acc.x = acc.x * a + v.x * b;
+    acc.y = acc.y * a + v.y * b;
+    acc.z = acc.z * a + v.z * b;
+    acc.w = acc.w * a + v.w * b;
+  }
+};
+
+// Adds the spills of the cuts strictly inside (begin, end) of a line; rows
+// [ctas][stride], this row's at `row`.  Returns the number of cuts strictly
+// inside the row's unit (begin, unit_end): a unit's two query tiles may see
+// different numbers of its key tiles.
+__device__ __forceinline__ int add_spills(Join& j, const float* o, const float* lse, int stride,
+                                          int row, int64_t begin, int64_t end,
+                                          int64_t unit_end, int64_t total, int64_t ctas,
+                                          int lane) {
+  int n = 0;
+  int64_t c = begin * ctas / total;
+  while (step_cut(c, total, ctas) <= begin) ++c;
+  for (; c < ctas && step_cut(c, total, ctas) < unit_end; ++c, ++n) {
+    if (step_cut(c, total, ctas) >= end) continue;
+    const int64_t at = c * stride + row;
+    j.add(lse[at], reinterpret_cast<const float4*>(o + at * 128)[lane]);
+  }
+  return n;
+}
+
+constexpr int kJoinWarps = 4;
+
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    step_combine_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
+                        __nv_bfloat16* __restrict__ o) {
+  ptx::pdl_wait_previous();
+  ptx::pdl_launch_dependents();
+  const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+  const StepWork work = step_work(ds, shp, plan);
+  const int lane = threadIdx.x & 31;
+  const int g = shp.g, H_kv = shp.H_kv, tpt = step_tile_tokens(g);
+  const int64_t items = (int64_t)plan.header[kPlanRows] * shp.H_q;
+  const int64_t s_ctas = min((int64_t)ws.stream_grid, work.stream_total);
+  const int64_t t_ctas = min((int64_t)ws.tile_grid, work.tile_total);
+  for (int64_t w = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); w < items;
+       w += (int64_t)gridDim.x * kJoinWarps) {
+    const int t = (int)(w / shp.H_q), h = (int)(w % shp.H_q), kvh = h / g, hh = h - kvh * g;
+    const int seq = plan.row_seq[t];
+    const int unit = plan.seq_unit[seq];
+    const int i = t - ds.q_start[seq];          // the row's token among its sequence's
+    Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    j.add(ws.own_lse[w], reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane]);
+    const bool pre = ds.prefix_len > 0;
+    if (pre) j.add(ws.pre_lse[w], reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane]);
+    int joined = pre;
+    if (unit >= 0) {
+      const int64_t cum = plan.stream_cum[unit];
+      const int n = (int)(plan.stream_cum[unit + 1] - cum);
+      const int64_t a = H_kv * cum + (int64_t)kvh * n;
+      joined += add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, i * g + hh, a, a + n,
+                           a + n, work.stream_total, s_ctas, lane);
+    } else {
+      const int n_new = ds.q_start[seq + 1] - ds.q_start[seq];
+      const int seen = ds.ctx[seq] - n_new;
+      const int u = -1 - unit, k = i / (2 * tpt), x = (i / tpt) & 1;
+      const int64_t cum = plan.tile_cum[u];
+      const int64_t steps = plan.tile_cum[u + 1] - cum;
+      const int64_t a = work.tile_prefix + H_kv * cum + (int64_t)kvh * steps +
+                        step_steps_before(seen, 2 * tpt, k);
+      // key tiles of the row's own query tile
+      const int end = min(n_new, (2 * k + x + 1) * tpt);
+      const int n = (seen + end + kStepTileKeys - 1) / kStepTileKeys;
+      joined += add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
+                           x * kStepTileRows + (i % tpt) * g + hh, a, a + n,
+                           a + step_pair_steps(seen, n_new, 2 * tpt, k), work.tile_total, t_ctas,
+                           lane);
+    }
+    if (pre && work.prefix_stream_tiles) {
+      const int n = work.prefix_stream_tiles;
+      const int64_t a = work.stream_own + (int64_t)kvh * n;
+      add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, t * g + hh, a, a + n, a + n,
+                 work.stream_total, s_ctas, lane);
+    } else if (pre) {
+      const int n = work.prefix_tile_steps;
+      const int64_t a = ((int64_t)kvh * work.prefix_pairs + t / (2 * tpt)) * n;
+      add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
+                 ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g + hh, a, a + n, a + n,
+                 work.tile_total, t_ctas, lane);
+    }
+    if (!joined) continue;      // the unit was whole: its kernel wrote O
+    const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
+    uint2 out;
+    out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
+    out.y = ptx::pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
+    reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
+  }
+}
+
+}  // namespace
+
+bool step_fast_supported(const ShapeInfo& s) {
+  const bool block_ok = (s.B % kStepTileKeys == 0) || (kStepTileKeys % s.B == 0 && s.B % 8 == 0);
+  return s.dtype == 0 && s.D == 128 && s.g <= 64 && block_ok;
+}
+
+size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* base,
+                      StepWorkspace* w) {
+  size_t at = 0;
+  auto take = [&](int64_t floats) -> float* {
+    float* p = base ? reinterpret_cast<float*>((char*)base + at) : nullptr;
+    at += ((size_t)floats * 4 + 255) / 256 * 256;
+    return p;
+  };
+  const int64_t rows = (int64_t)max_tokens * s.H_q;
+  StepWorkspace v;
+  v.stream_grid = 2 * sms;
+  v.tile_grid = sms;
+  v.own_o = take(rows * 128);
+  v.pre_o = take(rows * 128);
+  v.own_lse = take(rows);
+  v.pre_lse = take(rows);
+  v.stream_o = take((int64_t)v.stream_grid * kStepPackedRows * 128);
+  v.stream_lse = take((int64_t)v.stream_grid * kStepPackedRows);
+  v.tile_o = take((int64_t)v.tile_grid * 2 * kStepTileRows * 128);
+  v.tile_lse = take((int64_t)v.tile_grid * 2 * kStepTileRows);
+  if (w) *w = v;
+  return at;
+}
+
+cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                               const void* q, const void* k_cache, const void* v_cache, void* o,
+                               bool first, cudaStream_t st) {
+  const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
+  const int box_rows = s.B < kKeys ? s.B : kKeys;
+  CUtensorMap tk, tv;
+  cudaError_t e = make_cache_tmap(&tk, k_cache, rows, s.D, box_rows);
+  if (e == cudaSuccess) e = make_cache_tmap(&tv, v_cache, rows, s.D, box_rows);
+  if (e != cudaSuccess) return e;
+  // the shared-memory limit is raised once per device
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load() & bit)) {
+    e = cudaFuncSetAttribute(step_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(step_stream_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)w.stream_grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, step_stream_kernel, tk, tv, ds, s, w, (const __nv_bfloat16*)q,
+                            (__nv_bfloat16*)o, first ? 1 : 0);
+}
+
+cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                                void* o, cudaStream_t st) {
+  const int64_t warps = (int64_t)ds.max_tokens * s.H_q;
+  const int64_t blocks = std::min<int64_t>((warps + kJoinWarps - 1) / kJoinWarps,
+                                           (int64_t)w.tile_grid * 16);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, step_combine_kernel, ds, s, w, (__nv_bfloat16*)o);
+}
+
+}  // namespace rbkv
