@@ -34,8 +34,9 @@ rbkv_status check_tables(const rbkv_config* c, const rbkv_step_tables* t) {
     return invalid("NULL table array");
   if (!aligned(t->block_table, 4) || !aligned(t->free_words, 4) || !aligned(t->q_start, 4) ||
       !aligned(t->ctx, 4) || !aligned(t->position, 4) || !aligned(t->slot, 4) ||
-      !aligned(t->plan, 4) || !aligned(t->status, 4))
+      !aligned(t->status, 4))
     return invalid("table arrays must be 4-byte aligned");
+  if (!aligned(t->plan, 16)) return invalid("plan must be 16-byte aligned");
   return RBKV_OK;
 }
 

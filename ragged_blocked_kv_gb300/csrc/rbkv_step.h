@@ -16,46 +16,60 @@ constexpr int kStepTileRows = 128;      // packed query rows per tensor-core til
 // Tokens whose packed rows fill one tensor-core query tile.
 __host__ __device__ __forceinline__ int step_tile_tokens(int g) { return kStepTileRows / g; }
 
+// What a unit of work costs beside its key tiles (queries in, results out), in
+// key tiles of its kernel, for the even cut of the work over the CTAs.
+constexpr int kStepStreamUnit = 1;
+constexpr int kStepTileUnit = 2;
+
 // Header words of the plan.
 enum {
   kPlanRows = 0,        // query rows of the step (q_start[num_seqs])
   kPlanStreamed = 1,    // sequences on the streaming kernel
   kPlanTiled = 2,       // sequences on the tile kernel
-  kPlanStreamTiles = 3, // 64-key tiles of the streamed sequences, for one KV head
-  kPlanTileSteps = 4,   // key-tile steps of the tiled sequences, for one KV head
+  kPlanStreamLen = 3,   // line length of the streamed sequences, for one KV head
+  kPlanTileLen = 4,     // line length of the tiled sequences, for one KV head
   kPlanHeader = 16
 };
 
-// The plan: int32 arrays in one buffer.
+// A sequence of a kernel's work list.  cum: line length before it, for one KV
+// head; tiles: 64-key tiles (streamed) or line length (tiled).
+struct StepSeq {
+  int32_t seq, row, n_new, ctx, cum, tiles;
+  int32_t pad[2];
+};
+static_assert(sizeof(StepSeq) == 32, "StepSeq is 8 int32");
+
+// A query row: unit >= 0: entry of the streamed list; else -1 - unit: entry of
+// the tiled list.  token: its index among its sequence's new tokens.
+struct StepRow {
+  int32_t unit, token, cum, tiles;
+};
+static_assert(sizeof(StepRow) == 16, "StepRow is 4 int32");
+
+// The plan: one int32 buffer (16-byte aligned).
 struct StepPlan {
   int32_t* header;      // [kPlanHeader]
-  int32_t* row_seq;     // [max_tokens] sequence of each row
-  int32_t* seq_unit;    // [S] index into stream_seq, or -1 - index into tile_seq
-  int32_t* stream_seq;  // [S] streamed sequences, in order
-  int32_t* stream_cum;  // [S + 1] 64-key tiles before each of them
-  int32_t* tile_seq;    // [S] tiled sequences, in order
-  int32_t* tile_cum;    // [S + 1] key-tile steps before each of them
-  int32_t* first_new;   // [S] scratch: rank of a sequence's first new block
+  StepRow* rows;        // [max_tokens]
+  StepSeq* streamed;    // [S], in sequence order
+  StepSeq* tiled;       // [S], in sequence order
+  StepRow* of_seq;      // [S] scratch: unit, cum and tiles of a sequence; token is
+                        // the rank of its first new block
   int32_t* new_ids;     // [max_tokens] scratch: the new block ids, by rank
 };
 
 __host__ __device__ __forceinline__ int64_t step_plan_ints(int64_t num_seqs, int64_t max_tokens) {
-  return kPlanHeader + 2 * max_tokens + 6 * num_seqs + 2;
+  return kPlanHeader + 5 * max_tokens + 20 * num_seqs;
 }
 
 __host__ __device__ __forceinline__ StepPlan step_plan(int32_t* p, int32_t num_seqs,
                                                        int32_t max_tokens) {
   StepPlan v;
-  const int64_t S = num_seqs;
   v.header = p;
-  v.row_seq = p + kPlanHeader;
-  v.seq_unit = v.row_seq + max_tokens;
-  v.stream_seq = v.seq_unit + S;
-  v.stream_cum = v.stream_seq + S;
-  v.tile_seq = v.stream_cum + S + 1;
-  v.tile_cum = v.tile_seq + S;
-  v.first_new = v.tile_cum + S + 1;
-  v.new_ids = v.first_new + S;
+  v.rows = reinterpret_cast<StepRow*>(p + kPlanHeader);
+  v.streamed = reinterpret_cast<StepSeq*>(v.rows + max_tokens);
+  v.tiled = v.streamed + num_seqs;
+  v.of_seq = reinterpret_cast<StepRow*>(v.tiled + num_seqs);
+  v.new_ids = reinterpret_cast<int32_t*>(v.of_seq + num_seqs);
   return v;
 }
 
@@ -82,23 +96,25 @@ __host__ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int6
 
 // A tiled sequence's new tokens are taken in pairs of tensor-core tiles of
 // `pair` tokens together.  Pair k sees the keys below
-// seen + min(n_new, (k + 1) pair): its key-tile steps, and those before it.
-__host__ __device__ __forceinline__ int32_t step_pair_steps(int32_t seen, int32_t n_new,
+// seen + min(n_new, (k + 1) pair): its key tiles; the line length of the pairs
+// before it; and the line length of all of them.
+__host__ __device__ __forceinline__ int32_t step_pair_tiles(int32_t seen, int32_t n_new,
                                                             int32_t pair, int32_t k) {
   const int64_t end = (int64_t)(k + 1) * pair;
   const int64_t keys = seen + (end < n_new ? end : (int64_t)n_new);
   return (int32_t)((keys + kStepTileKeys - 1) / kStepTileKeys);
 }
-__host__ __device__ __forceinline__ int64_t step_steps_before(int32_t seen, int32_t pair,
-                                                              int32_t k) {
+__host__ __device__ __forceinline__ int64_t step_len_before(int32_t seen, int32_t pair,
+                                                            int32_t k) {
   // every pair before another one is whole
-  return floor_sum(k, kStepTileKeys, pair, (int64_t)seen + pair + kStepTileKeys - 1);
+  return floor_sum(k, kStepTileKeys, pair, (int64_t)seen + pair + kStepTileKeys - 1) +
+         (int64_t)k * kStepTileUnit;
 }
-__host__ __device__ __forceinline__ int64_t step_seq_steps(int32_t seen, int32_t n_new,
-                                                           int32_t pair) {
+__host__ __device__ __forceinline__ int64_t step_seq_len(int32_t seen, int32_t n_new,
+                                                         int32_t pair) {
   const int32_t pairs = (int32_t)(((int64_t)n_new + pair - 1) / pair);
-  return step_steps_before(seen, pair, pairs - 1) +
-         step_pair_steps(seen, n_new, pair, pairs - 1);
+  return step_len_before(seen, pair, pairs - 1) +
+         step_pair_tiles(seen, n_new, pair, pairs - 1) + kStepTileUnit;
 }
 
 // What the kernels of a step see.
@@ -113,15 +129,19 @@ struct DevStep {
   int32_t prefix_len;
 };
 
-// Work is cut evenly over the CTAs of a persistent grid.  All key tiles of a
-// kernel's work units lie on one line, units one after the other; with
-// G' = min(grid, total), CTA c walks the tiles [start(c), start(c + 1)),
-// start(c) = floor(c total / G').  A unit is so cut into one segment per CTA
-// that meets it.  The segment at a unit's first tile writes its result to the
-// unit's own rows of the workspace; a segment that begins inside a unit can
-// only be the first of its CTA, and goes to that CTA's spill rows.
+// Work is cut evenly over the CTAs of a persistent grid.  A kernel's units lie
+// on one line, one after the other, each as long as its key tiles and a fixed
+// length for what it costs beside them (first the fixed length, then the
+// tiles); with G' = min(grid, total), CTA c takes [start(c), start(c + 1)),
+// start(c) = floor(c total / G').  A unit is so cut into segments of key tiles.
+// The segment at a unit's first tile writes its result to the unit's own rows
+// of the workspace; a segment that begins inside a unit can only be the first
+// of its CTA, and goes to that CTA's spill rows.
 __host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, int64_t ctas) {
-  return c * total / ctas;
+  const uint64_t p = (uint64_t)(c * total);
+  // (a 64-bit division takes several times as long)
+  if (p >> 32) return (int64_t)(p / (uint64_t)ctas);
+  return (int64_t)((uint32_t)p / (uint32_t)ctas);
 }
 
 // The units of the streaming kernel: (streamed sequence, KV head), the KV
@@ -130,8 +150,8 @@ __host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, i
 // The units of the tile kernel: (KV head, pair of query tiles) over the
 // prefix unless it is streamed; then (tiled sequence, KV head, pair).
 struct StepWork {
-  int64_t stream_own, stream_total;   // 64-key tiles
-  int64_t tile_prefix, tile_total;    // key-tile steps
+  int64_t stream_own, stream_total;
+  int64_t tile_prefix, tile_total;
   int32_t prefix_stream_tiles;        // 64-key tiles of the prefix, when streamed
   int32_t prefix_tile_steps;          // 128-key tiles of the prefix, when tiled
   int32_t prefix_pairs;               // pairs of query tiles over the prefix
@@ -152,10 +172,14 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
   w.prefix_tile_steps = streamed ? 0 : (int32_t)(((int64_t)P + kStepTileKeys - 1) / kStepTileKeys);
   const int32_t pair = 2 * step_tile_tokens(s.g);
   w.prefix_pairs = (T + pair - 1) / pair;
-  w.stream_own = (int64_t)plan.header[kPlanStreamTiles] * s.H_kv;
-  w.stream_total = w.stream_own + (int64_t)w.prefix_stream_tiles * s.H_kv;
-  w.tile_prefix = (int64_t)s.H_kv * w.prefix_pairs * w.prefix_tile_steps;
-  w.tile_total = w.tile_prefix + (int64_t)plan.header[kPlanTileSteps] * s.H_kv;
+  w.stream_own = (int64_t)plan.header[kPlanStreamLen] * s.H_kv;
+  w.stream_total = w.stream_own;
+  if (w.prefix_stream_tiles)
+    w.stream_total += (int64_t)(w.prefix_stream_tiles + kStepStreamUnit) * s.H_kv;
+  w.tile_prefix = 0;
+  if (w.prefix_tile_steps)
+    w.tile_prefix = (int64_t)s.H_kv * w.prefix_pairs * (w.prefix_tile_steps + kStepTileUnit);
+  w.tile_total = w.tile_prefix + (int64_t)plan.header[kPlanTileLen] * s.H_kv;
   return w;
 }
 #endif

@@ -44,8 +44,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int64_t w = (int64_t)blockIdx.x * kWarps + warp; w < items;
        w += (int64_t)gridDim.x * kWarps) {
     const int t = (int)(w / s.H_q), h = (int)(w % s.H_q), kvh = h / s.g;
-    const int seq = plan.row_seq[t];
-    const int own = ds.ctx[seq] - (ds.q_start[seq + 1] - 1 - t);   // keys the row sees
+    const StepRow r = plan.rows[t];
+    const StepSeq e = r.unit >= 0 ? plan.streamed[r.unit] : plan.tiled[-1 - r.unit];
+    const int seq = e.seq, own = e.ctx - e.n_new + r.token + 1;   // keys the row sees
     const int32_t* table = ds.block_table + (int64_t)seq * ds.max_blocks;
     const T* qrow = q + ((int64_t)t * s.H_q + h) * D;
     for (int d = lane; d < D; d += 32) q_s[warp][d] = to_f(qrow[d]) * (s.scale * kLog2e);

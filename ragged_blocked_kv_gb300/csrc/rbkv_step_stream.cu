@@ -38,30 +38,13 @@ constexpr int kStage = 2 * kTile;             // K + V
 constexpr int kRows = kStepPackedRows;
 constexpr int kScratch = kConsumers * kRows * 64 * 4;   // [warp][row][64] fp32
 constexpr int kMl = kConsumers * kRows * 2 * 4;         // (max, sum) per warp and row
-constexpr int kSmemBytes = kStages * kStage + kScratch + kMl + 2 * kStages * 8 + 16;
+constexpr int kSegments = 4;            // published segments; more than kStages
+static_assert(kSegments > kStages && (2 * kStages + kSegments) % 2 == 0, "segment ring");
+constexpr int kSmemBytes =
+    kStages * kStage + kScratch + kMl + (2 * kStages + kSegments) * 8 + kSegments * 32 + 16;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr long long kWaitLimit = 4000000000LL;   // ~2 s of SM clock
 constexpr float kLog2e = 1.4426950408889634f;
-
-struct Shared {
-  uint8_t* stages;
-  float* scratch;
-  float* ml;
-  uint64_t* full;
-  uint64_t* empty;
-  volatile int* abort_flag;
-};
-
-__device__ __forceinline__ Shared carve(uint8_t* raw) {
-  Shared s;
-  s.stages = raw;
-  s.scratch = reinterpret_cast<float*>(raw + kStages * kStage);
-  s.ml = s.scratch + kScratch / 4;
-  s.full = reinterpret_cast<uint64_t*>(s.ml + kMl / 4);
-  s.empty = s.full + kStages;
-  s.abort_flag = reinterpret_cast<volatile int*>(s.empty + kStages);
-  return s;
-}
 
 // Byte offset, inside one K or V tile, of the 16-byte chunk holding elements
 // d..d+7 (d % 8 == 0) of key row `key` (128-byte swizzle, each 64-column half
@@ -72,84 +55,122 @@ __device__ __forceinline__ uint32_t tile_off(int key, int d) {
   return half * kHalf + key * 128 + ((chunk ^ (key & 7)) << 4);
 }
 
-// One segment: the key tiles [tile, tile_end) of a unit.
-struct Segment {
-  const int32_t* table;
+// One segment of a unit, as the producer publishes it to the consumers.
+struct __align__(16) Segment {
   int row, n_tok;        // first row and tokens of the unit
   int kv_head;
-  int tile, tile_end;
+  int tile, tiles;       // first key tile, and number of them (0: no more segments)
   int keys;              // keys of the unit's last row
   int diag;              // keys of its first row (the prefix: every row sees all)
-  bool prefix, head, whole;
+  int flags;
+};
+static_assert(sizeof(Segment) == 32, "Segment is 8 int32");
+enum { kPrefix = 1, kHead = 2, kWhole = 4 };
+
+struct Shared {
+  uint8_t* stages;
+  float* scratch;
+  float* ml;
+  uint64_t* full;
+  uint64_t* empty;
+  uint64_t* published;
+  Segment* segments;
+  volatile int* abort_flag;
 };
 
-// Walks a CTA's part [x, end) of the line.
+__device__ __forceinline__ Shared carve(uint8_t* raw) {
+  Shared s;
+  s.stages = raw;
+  s.scratch = reinterpret_cast<float*>(raw + kStages * kStage);
+  s.ml = s.scratch + kScratch / 4;
+  s.full = reinterpret_cast<uint64_t*>(s.ml + kMl / 4);
+  s.empty = s.full + kStages;
+  s.published = s.empty + kStages;
+  s.segments = reinterpret_cast<Segment*>(s.published + kSegments);
+  s.abort_flag = reinterpret_cast<volatile int*>(s.segments + kSegments);
+  return s;
+}
+
+// The producer's walk over its CTA's part [x, end) of the line.  Units follow
+// one another without a division: the next KV head, then the next sequence,
+// whose entry is loaded one sequence ahead.
 struct Walk {
-  int64_t x, end;
-  int unit;              // streamed sequence
-  int seq, cum, n_tiles; // of that sequence
-};
+  int64_t end, unit0;    // end of the part; the unit's place on the line
+  int unit, kv_head;
+  StepSeq cur, next;
+  const int32_t* table;
 
-// The last i with cum[i] <= v among i in [0, n), cum[0] = 0: every lane tests
-// one of 32 places of the range that is left.
-__device__ __forceinline__ int search(const int32_t* cum, int n, int64_t v, int lane) {
-  int lo = 0, len = n;
-  while (len > 1) {
-    const int step = (len + 31) >> 5;
-    const int at = lo + lane * step;
-    const bool le = lane * step < len && cum[at] <= v;
-    const unsigned m = __ballot_sync(0xffffffffu, le);
-    const int k = 31 - __clz(m);          // lane 0 always holds
-    lo += k * step;
-    len = min(step, len - k * step);
-  }
-  return lo;
-}
-
-__device__ __forceinline__ void load_unit(Walk& w, const StepPlan& plan) {
-  w.seq = plan.stream_seq[w.unit];
-  w.cum = plan.stream_cum[w.unit];
-  w.n_tiles = plan.stream_cum[w.unit + 1] - w.cum;
-}
-
-__device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const ShapeInfo& s,
-                                             const StepPlan& plan, const StepWork& work,
-                                             Segment& g) {
-  if (w.x >= w.end) return false;
-  int64_t unit0;
-  int n_tiles;
-  if (w.x < work.stream_own) {
-    if (w.x >= (int64_t)s.H_kv * (w.cum + w.n_tiles)) {
-      ++w.unit;
-      load_unit(w, plan);
+  __device__ __forceinline__ void enter(const DevStep& ds, const ShapeInfo& s,
+                                        const StepPlan& plan, const StepWork& work) {
+    if (unit < plan.header[kPlanStreamed]) {
+      next = plan.streamed[min(unit + 1, ds.num_seqs - 1)];
+      unit0 = (int64_t)s.H_kv * cur.cum + (int64_t)kv_head * (cur.tiles + kStepStreamUnit);
+      table = ds.block_table + (int64_t)cur.seq * ds.max_blocks;
+    } else {
+      cur.row = 0;
+      cur.n_new = plan.header[kPlanRows];
+      cur.ctx = ds.prefix_len;
+      cur.tiles = work.prefix_stream_tiles;
+      unit0 = work.stream_own + (int64_t)kv_head * (cur.tiles + kStepStreamUnit);
+      table = ds.prefix_table;
     }
-    const int64_t base = (int64_t)s.H_kv * w.cum;
-    n_tiles = w.n_tiles;
-    g.kv_head = (int)((w.x - base) / n_tiles);
-    unit0 = base + (int64_t)g.kv_head * n_tiles;
-    g.prefix = false;
-    g.row = ds.q_start[w.seq];
-    g.n_tok = ds.q_start[w.seq + 1] - g.row;
-    g.keys = ds.ctx[w.seq];
-    g.diag = g.keys - g.n_tok + 1;
-    g.table = ds.block_table + (int64_t)w.seq * ds.max_blocks;
-  } else {
-    n_tiles = work.prefix_stream_tiles;
-    g.kv_head = (int)((w.x - work.stream_own) / n_tiles);
-    unit0 = work.stream_own + (int64_t)g.kv_head * n_tiles;
-    g.prefix = true;
-    g.row = 0;
-    g.n_tok = plan.header[kPlanRows];
-    g.keys = g.diag = ds.prefix_len;
-    g.table = ds.prefix_table;
   }
-  g.tile = (int)(w.x - unit0);
-  g.tile_end = (int)min((int64_t)n_tiles, w.end - unit0);
-  g.head = g.tile == 0;
-  g.whole = g.head && g.tile_end == n_tiles;
-  w.x += g.tile_end - g.tile;
-  return true;
-}
+
+  __device__ __forceinline__ void start(int64_t x, const DevStep& ds, const ShapeInfo& s,
+                                        const StepPlan& plan, const StepWork& work) {
+    int64_t base = work.stream_own;
+    unit = plan.header[kPlanStreamed];
+    int len = work.prefix_stream_tiles + kStepStreamUnit;
+    if (x < work.stream_own) {
+      // the last sequence at or before x
+      const int32_t v = (int32_t)(x / s.H_kv);
+      int lo = 0, hi = unit - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (plan.streamed[mid].cum <= v) lo = mid;
+        else hi = mid - 1;
+      }
+      unit = lo;
+      cur = plan.streamed[unit];
+      base = (int64_t)s.H_kv * cur.cum;
+      len = cur.tiles + kStepStreamUnit;
+    }
+    kv_head = (int)(x - base) / len;    // (a sequence's line fits 32 bits with its heads)
+    enter(ds, s, plan, work);
+  }
+
+  // The segment of the unit in [x, end), and on to the next unit; false when
+  // the part has no tile of it.
+  __device__ __forceinline__ bool segment(int64_t x, Segment& g, const int32_t*& ids,
+                                          const DevStep& ds, const ShapeInfo& s,
+                                          const StepPlan& plan, const StepWork& work,
+                                          int64_t& x_next) {
+    const bool prefix = unit >= plan.header[kPlanStreamed];
+    const int n = cur.tiles;
+    g.row = cur.row;
+    g.n_tok = cur.n_new;
+    g.kv_head = kv_head;
+    g.keys = cur.ctx;
+    g.diag = prefix ? cur.ctx : cur.ctx - cur.n_new + 1;
+    ids = table;
+    const int64_t from = x - unit0 - kStepStreamUnit, to = end - unit0 - kStepStreamUnit;
+    const int last = (int)(to < 0 ? 0 : to < n ? to : n);
+    g.tile = (int)(from < 0 ? 0 : from);
+    g.tiles = last - g.tile;
+    g.flags = (prefix ? kPrefix : 0) | (g.tile == 0 ? kHead : 0) |
+              (g.tile == 0 && last == n ? kWhole : 0);
+    x_next = unit0 + n + kStepStreamUnit;
+    if (x_next < end) {
+      if (++kv_head == s.H_kv) {
+        kv_head = 0;
+        ++unit;
+        cur = next;
+      }
+      enter(ds, s, plan, work);
+    }
+    return g.tiles > 0;
+  }
+};
 
 __global__ void __launch_bounds__(kThreads, 2)
     step_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -177,63 +198,96 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(&sm.full[s], 1);
       ptx::mbar_init(&sm.empty[s], kConsumers);
     }
+    for (int s = 0; s < kSegments; ++s) ptx::mbar_init(&sm.published[s], 1);
     abort_flag = 0;
     ptx::fence_barrier_init();
   }
-  Walk walk;
-  walk.x = step_cut(blockIdx.x, work.stream_total, ctas);
-  walk.end = step_cut(blockIdx.x + 1, work.stream_total, ctas);
-  walk.unit = walk.seq = walk.cum = walk.n_tiles = 0;
-  if (walk.x < work.stream_own) {
-    walk.unit = search(plan.stream_cum, plan.header[kPlanStreamed], walk.x / H_kv, lane);
-    load_unit(walk, plan);
-  }
   __syncthreads();
 
-  Segment it;
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       ptx::tma_prefetch_desc(&tmap_k);
       ptx::tma_prefetch_desc(&tmap_v);
-      uint32_t idx = 0;
       const int box_rows = B < kKeys ? B : kKeys;
-      while (!abort_flag && next_segment(walk, ds, shp, plan, work, it)) {
-        for (int j = it.tile; j < it.tile_end; ++j, ++idx) {
+      Walk walk;
+      walk.end = step_cut(blockIdx.x + 1, work.stream_total, ctas);
+      int64_t x = step_cut(blockIdx.x, work.stream_total, ctas);
+      walk.start(x, ds, shp, plan, work);
+      Segment it, nx;
+      const int32_t *ids, *nx_ids;
+      auto next = [&](Segment& g, const int32_t*& p) {
+        while (x < walk.end) {
+          int64_t to;
+          const bool some = walk.segment(x, g, p, ds, shp, plan, work, to);
+          x = to;
+          if (some) return;
+        }
+        g.tiles = 0;
+      };
+      // block ids of a tile's boxes (none past the unit's last key), loaded
+      // one tile ahead so that their latency hides behind the ring's waits
+      int32_t blk[kKeys / 8];
+      auto look = [&](const Segment& g, const int32_t* p, int j) {
+        const int k0 = (g.tile + j) * kKeys;
+#pragma unroll
+        for (int i = 0; i < kKeys / 8; ++i)
+          if (i * box_rows < kKeys && k0 + i * box_rows < g.keys)
+            blk[i] = p[(k0 + i * box_rows) / B];
+      };
+      uint32_t idx = 0, seg = 0;
+      bool stop = false;
+      next(it, ids);
+      if (it.tiles) look(it, ids, 0);
+      for (;; ++seg) {
+        // (a slot of the segment ring is free again once a tile three before
+        // the next one was released: kSegments > kStages)
+        sm.segments[seg % kSegments] = it;
+        ptx::mbar_arrive(&sm.published[seg % kSegments]);
+        if (it.tiles == 0 || stop) break;
+        next(nx, nx_ids);
+        for (int j = 0; j < it.tiles; ++j, ++idx) {
           const int s = idx % kStages;
-          if (idx >= (uint32_t)kStages &&
-              !ptx::mbar_wait(&sm.empty[s], ((idx / kStages) - 1) & 1, kWaitLimit)) {
+          if (abort_flag ||
+              (idx >= (uint32_t)kStages &&
+               !ptx::mbar_wait(&sm.empty[s], ((idx / kStages) - 1) & 1, kWaitLimit))) {
             ptx::report_wait(ds.status, kDevTimeout, 61, (int)idx);
             abort_flag = 1;
+            stop = true;
             break;
           }
-          const int k0 = j * kKeys;
+          const int k0 = (it.tile + j) * kKeys;
           uint8_t* kdst = sm.stages + s * kStage;
           uint8_t* vdst = kdst + kTile;
-          // boxes of box_rows keys; none past the unit's last key
-          int nsub = 0, loads = 0;
-          int32_t rows[kKeys / 8];
-          for (int r = 0; r < kKeys && k0 + r < it.keys; r += box_rows) {
-            const int32_t blk = it.table[(k0 + r) / B];
-            if (blk < 0 || blk >= ds.num_blocks) {
-              atomicCAS(ds.status, 0, kDevBounds);
-              rows[nsub++] = -1;
-              continue;
+          int loads = 0;
+#pragma unroll
+          for (int i = 0; i < kKeys / 8; ++i) {
+            if (i * box_rows < kKeys && k0 + i * box_rows < it.keys) {
+              if (blk[i] < 0 || blk[i] >= ds.num_blocks)
+                atomicCAS(ds.status, 0, kDevBounds);
+              else
+                ++loads;
             }
-            rows[nsub++] = (blk * H_kv + it.kv_head) * B + ((k0 + r) % B);
-            ++loads;
           }
           ptx::mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(loads * box_rows * 128 * 4));
-          for (int i = 0; i < nsub; ++i) {
-            if (rows[i] < 0) continue;
-            const int off = i * box_rows * 128;
-            ptx::tma_load_2d(kdst + off, &tmap_k, 0, rows[i], &sm.full[s]);
-            ptx::tma_load_2d(kdst + kHalf + off, &tmap_k, 64, rows[i], &sm.full[s]);
-            ptx::tma_load_2d(vdst + off, &tmap_v, 0, rows[i], &sm.full[s]);
-            ptx::tma_load_2d(vdst + kHalf + off, &tmap_v, 64, rows[i], &sm.full[s]);
+#pragma unroll
+          for (int i = 0; i < kKeys / 8; ++i) {
+            if (i * box_rows < kKeys && k0 + i * box_rows < it.keys && blk[i] >= 0 &&
+                blk[i] < ds.num_blocks) {
+              const int row = (blk[i] * H_kv + it.kv_head) * B + ((k0 + i * box_rows) % B);
+              const int off = i * box_rows * 128;
+              ptx::tma_load_2d(kdst + off, &tmap_k, 0, row, &sm.full[s]);
+              ptx::tma_load_2d(kdst + kHalf + off, &tmap_k, 64, row, &sm.full[s]);
+              ptx::tma_load_2d(vdst + off, &tmap_v, 0, row, &sm.full[s]);
+              ptx::tma_load_2d(vdst + kHalf + off, &tmap_v, 64, row, &sm.full[s]);
+            }
           }
+          if (j + 1 < it.tiles) look(it, ids, j + 1);
+          else if (nx.tiles) look(nx, nx_ids, 0);
         }
-        if (abort_flag) break;
+        if (stop) break;
+        it = nx;
+        ids = nx_ids;
       }
       // let every load this CTA issued land before the CTA can exit
       for (uint32_t t = idx > (uint32_t)kStages ? idx - kStages : 0; t < idx; ++t)
@@ -268,11 +322,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   uint32_t qa[8][4];
-  bool more = next_segment(walk, ds, shp, plan, work, it);
+  // the next published segment; one without tiles ends the walk
+  uint32_t seg = 0;
+  auto take = [&](Segment& u) -> bool {
+    if (!ptx::mbar_wait(&sm.published[seg % kSegments], (seg / kSegments) & 1, kWaitLimit)) {
+      if (lane == 0) {
+        ptx::report_wait(ds.status, kDevTimeout, 63, (int)seg);
+        abort_flag = 1;
+      }
+      u.tiles = 0;
+    } else {
+      u = sm.segments[seg % kSegments];
+    }
+    ++seg;
+    return __all_sync(0xffffffffu, u.tiles > 0);
+  };
+  Segment it;
+  bool more = take(it);
+  if (ptx::named_bar_or(1, kConsumers * 32, abort_flag != 0)) more = false;
   if (more) load_q(it, qa);
 
   while (more) {
-    const int nt = it.tile_end - it.tile;
+    const int nt = it.tiles;
     const int nrg = it.n_tok * g;
     const int lim0 = min(it.keys, it.diag + t0), lim1 = min(it.keys, it.diag + t1);
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -391,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // the next segment and its queries, loaded while this one is merged
     const Segment cur = it;
-    more = next_segment(walk, ds, shp, plan, work, it);
+    more = !abort_flag && take(it);
     uint32_t qn[8][4];
     if (more) load_q(it, qn);
 
@@ -423,12 +494,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float f1 = (m1 == -INFINITY || L1 == 0.f) ? 0.f : ptx::ex2(m1 - M1) / L1;
     // where row r of the segment goes: O itself when nothing is to be joined,
     // the unit's rows of the workspace, or this CTA's spill rows
-    const bool direct = cur.whole && ds.prefix_len == 0;
-    float* part = cur.head ? (cur.prefix ? ws.pre_o : ws.own_o) : ws.stream_o;
-    float* lse = cur.head ? (cur.prefix ? ws.pre_lse : ws.own_lse) : ws.stream_lse;
+    const bool head = cur.flags & kHead, pre = cur.flags & kPrefix;
+    const bool direct = (cur.flags & kWhole) && ds.prefix_len == 0;
+    float* part = head ? (pre ? ws.pre_o : ws.own_o) : ws.stream_o;
+    float* lse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.stream_lse;
     auto place = [&](int r) -> int64_t {
-      return cur.head || direct ? (int64_t)(cur.row + r / g) * shp.H_q + cur.kv_head * g + r % g
-                                : (int64_t)blockIdx.x * kRows + r;
+      return head ? (int64_t)(cur.row + r / g) * shp.H_q + cur.kv_head * g + r % g
+                  : (int64_t)blockIdx.x * kRows + r;
     };
     const int t = threadIdx.x;   // 0..127
     float* scr = sm.scratch + warp * kRows * 64;
@@ -511,23 +583,27 @@ struct Join {
   }
 };
 
-// Adds the spills of the cuts strictly inside (begin, end) of a line; rows
-// [ctas][stride], this row's at `row`.  Returns the number of cuts strictly
-// inside the row's unit (begin, unit_end): a unit's two query tiles may see
-// different numbers of its key tiles.
-__device__ __forceinline__ int add_spills(Join& j, const float* o, const float* lse, int stride,
-                                          int row, int64_t begin, int64_t end,
-                                          int64_t unit_end, int64_t total, int64_t ctas,
-                                          int lane) {
-  int n = 0;
-  int64_t c = begin * ctas / total;
-  while (step_cut(c, total, ctas) <= begin) ++c;
-  for (; c < ctas && step_cut(c, total, ctas) < unit_end; ++c, ++n) {
-    if (step_cut(c, total, ctas) >= end) continue;
+// The spills of the cuts inside a unit at `begin` of a line, of a fixed length
+// `unit` and `tiles` key tiles (`row_tiles` of them seen by the row: a unit's
+// two query tiles may see different numbers).  Spill rows are [ctas][stride],
+// this row's at `row`.  Returns whether the unit was cut between its tiles.
+__device__ __forceinline__ bool add_spills(Join& j, const float* o, const float* lse, int stride,
+                                           int row, int64_t begin, int unit, int tiles,
+                                           int row_tiles, int64_t total, int ctas, int lane) {
+  bool cut = false;
+  // the first cut after `begin`, from an estimate that is off by one at most
+  int64_t c = (int64_t)((float)begin * (float)ctas / (float)total) - 1;
+  c = c < 0 ? 0 : c;
+  while (c < ctas && step_cut(c, total, ctas) <= begin + unit) ++c;
+  for (; c < ctas; ++c) {
+    const int64_t tile = step_cut(c, total, ctas) - begin - unit;   // first tile behind it
+    if (tile >= tiles) break;
+    cut = true;
+    if (tile >= row_tiles) continue;
     const int64_t at = c * stride + row;
     j.add(lse[at], reinterpret_cast<const float4*>(o + at * 128)[lane]);
   }
-  return n;
+  return cut;
 }
 
 constexpr int kJoinWarps = 4;
@@ -541,53 +617,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const StepWork work = step_work(ds, shp, plan);
   const int lane = threadIdx.x & 31;
   const int g = shp.g, H_kv = shp.H_kv, tpt = step_tile_tokens(g);
-  const int64_t items = (int64_t)plan.header[kPlanRows] * shp.H_q;
-  const int64_t s_ctas = min((int64_t)ws.stream_grid, work.stream_total);
-  const int64_t t_ctas = min((int64_t)ws.tile_grid, work.tile_total);
+  const int T = plan.header[kPlanRows];
+  const int s_ctas = (int)min((int64_t)ws.stream_grid, work.stream_total);
+  const int t_ctas = (int)min((int64_t)ws.tile_grid, work.tile_total);
+  const bool pre = ds.prefix_len > 0;
+  const int64_t items = (int64_t)T * shp.H_q;
   for (int64_t w = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); w < items;
        w += (int64_t)gridDim.x * kJoinWarps) {
-    const int t = (int)(w / shp.H_q), h = (int)(w % shp.H_q), kvh = h / g, hh = h - kvh * g;
-    const int seq = plan.row_seq[t];
-    const int unit = plan.seq_unit[seq];
-    const int i = t - ds.q_start[seq];          // the row's token among its sequence's
+    const int t = (int)(w / shp.H_q), h = (int)(w - (int64_t)t * shp.H_q);
+    const int kvh = h / g, hh = h - kvh * g;
+    const StepRow r = plan.rows[t];
+    const float own_l = ws.own_lse[w];
+    const float4 own_v = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane];
     Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    j.add(ws.own_lse[w], reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane]);
-    const bool pre = ds.prefix_len > 0;
+    bool joined = pre;
     if (pre) j.add(ws.pre_lse[w], reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane]);
-    int joined = pre;
-    if (unit >= 0) {
-      const int64_t cum = plan.stream_cum[unit];
-      const int n = (int)(plan.stream_cum[unit + 1] - cum);
-      const int64_t a = H_kv * cum + (int64_t)kvh * n;
-      joined += add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, i * g + hh, a, a + n,
-                           a + n, work.stream_total, s_ctas, lane);
+    j.add(own_l, own_v);
+    if (r.unit >= 0) {
+      const int64_t a = (int64_t)H_kv * r.cum + (int64_t)kvh * (r.tiles + kStepStreamUnit);
+      joined |= add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, r.token * g + hh, a,
+                           kStepStreamUnit, r.tiles, r.tiles, work.stream_total, s_ctas, lane);
     } else {
-      const int n_new = ds.q_start[seq + 1] - ds.q_start[seq];
-      const int seen = ds.ctx[seq] - n_new;
-      const int u = -1 - unit, k = i / (2 * tpt), x = (i / tpt) & 1;
-      const int64_t cum = plan.tile_cum[u];
-      const int64_t steps = plan.tile_cum[u + 1] - cum;
-      const int64_t a = work.tile_prefix + H_kv * cum + (int64_t)kvh * steps +
-                        step_steps_before(seen, 2 * tpt, k);
+      const StepSeq e = plan.tiled[-1 - r.unit];
+      const int seen = e.ctx - e.n_new, k = r.token / (2 * tpt), x = (r.token / tpt) & 1;
+      const int64_t a = work.tile_prefix + (int64_t)H_kv * r.cum + (int64_t)kvh * r.tiles +
+                        step_len_before(seen, 2 * tpt, k);
       // key tiles of the row's own query tile
-      const int end = min(n_new, (2 * k + x + 1) * tpt);
-      const int n = (seen + end + kStepTileKeys - 1) / kStepTileKeys;
-      joined += add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
-                           x * kStepTileRows + (i % tpt) * g + hh, a, a + n,
-                           a + step_pair_steps(seen, n_new, 2 * tpt, k), work.tile_total, t_ctas,
-                           lane);
+      const int end = min(e.n_new, (2 * k + x + 1) * tpt);
+      joined |= add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
+                           x * kStepTileRows + (r.token % tpt) * g + hh, a, kStepTileUnit,
+                           step_pair_tiles(seen, e.n_new, 2 * tpt, k),
+                           (seen + end + kStepTileKeys - 1) / kStepTileKeys, work.tile_total,
+                           t_ctas, lane);
     }
     if (pre && work.prefix_stream_tiles) {
       const int n = work.prefix_stream_tiles;
-      const int64_t a = work.stream_own + (int64_t)kvh * n;
-      add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, t * g + hh, a, a + n, a + n,
+      add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, t * g + hh,
+                 work.stream_own + (int64_t)kvh * (n + kStepStreamUnit), kStepStreamUnit, n, n,
                  work.stream_total, s_ctas, lane);
     } else if (pre) {
       const int n = work.prefix_tile_steps;
-      const int64_t a = ((int64_t)kvh * work.prefix_pairs + t / (2 * tpt)) * n;
       add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
-                 ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g + hh, a, a + n, a + n,
-                 work.tile_total, t_ctas, lane);
+                 ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g + hh,
+                 ((int64_t)kvh * work.prefix_pairs + t / (2 * tpt)) * (n + kStepTileUnit),
+                 kStepTileUnit, n, n, work.tile_total, t_ctas, lane);
     }
     if (!joined) continue;      // the unit was whole: its kernel wrote O
     const float inv = j.L > 0.f ? 1.f / j.L : 0.f;

@@ -117,63 +117,65 @@ struct Walk {
 __device__ __forceinline__ bool next_item(Walk& w, const DevStep& ds, const ShapeInfo& s,
                                           const StepPlan& plan, const StepWork& work, int tpt,
                                           Item& it) {
-  if (w.x >= w.end) return false;
-  int first, last;       // the unit's tiles [first, last) of this segment
-  if (w.x < work.tile_prefix) {
-    const int n = work.prefix_tile_steps;
-    const int64_t unit = w.x / n;
-    const int rp = (int)(unit % work.prefix_pairs);
-    const int T = plan.header[kPlanRows];
-    it.kv_head = (int)(unit / work.prefix_pairs);
-    first = (int)(w.x - unit * n);
-    last = (int)min((int64_t)n, w.end - unit * n);
-    it.prefix = true;
-    it.whole = first == 0 && last == n;
-    it.table = ds.prefix_table;
-    it.row[0] = rp * 2 * tpt;
-    it.n_tok[0] = min(tpt, T - it.row[0]);
-    it.n_tok[1] = max(0, min(tpt, T - it.row[0] - tpt));
-    it.pos = ds.prefix_len - 1;
-    it.ke = min(ds.prefix_len, last * kKeys);
-    it.n[0] = last - first;
-    it.n[1] = it.n_tok[1] > 0 ? last - first : 0;
-  } else {
-    const int64_t y = w.x - work.tile_prefix;
-    while (y >= (int64_t)s.H_kv * plan.tile_cum[w.unit + 1]) ++w.unit;
-    const int cum = plan.tile_cum[w.unit];
-    const int steps = plan.tile_cum[w.unit + 1] - cum;
-    const int seq = plan.tile_seq[w.unit];
-    const int q0 = ds.q_start[seq], n_new = ds.q_start[seq + 1] - q0;
-    const int seen = ds.ctx[seq] - n_new;
-    int64_t r = y - (int64_t)s.H_kv * cum;
-    it.kv_head = (int)(r / steps);
-    r -= (int64_t)it.kv_head * steps;
-    int k = 0, n = step_pair_steps(seen, n_new, 2 * tpt, 0);
-    while (r >= n) {
-      r -= n;
-      n = step_pair_steps(seen, n_new, 2 * tpt, ++k);
+  while (w.x < w.end) {
+    int n, k = 0;          // the unit's key tiles
+    int64_t unit0;         // its place on the line
+    StepSeq e;
+    if (w.x < work.tile_prefix) {
+      n = work.prefix_tile_steps;
+      const int64_t unit = w.x / (n + kStepTileUnit);
+      unit0 = unit * (n + kStepTileUnit);
+      it.kv_head = (int)(unit / work.prefix_pairs);
+      const int T = plan.header[kPlanRows];
+      const int rp = (int)(unit - (int64_t)it.kv_head * work.prefix_pairs);
+      it.prefix = true;
+      it.table = ds.prefix_table;
+      it.row[0] = rp * 2 * tpt;
+      it.n_tok[0] = min(tpt, T - it.row[0]);
+      it.n_tok[1] = max(0, min(tpt, T - it.row[0] - tpt));
+      it.pos = ds.prefix_len - 1;
+    } else {
+      e = plan.tiled[w.unit];
+      while (w.x - work.tile_prefix >= (int64_t)s.H_kv * ((int64_t)e.cum + e.tiles))
+        e = plan.tiled[++w.unit];
+      const int seen = e.ctx - e.n_new;
+      const int64_t base = work.tile_prefix + (int64_t)s.H_kv * e.cum;
+      it.kv_head = (int)((w.x - base) / e.tiles);
+      unit0 = base + (int64_t)it.kv_head * e.tiles;
+      n = step_pair_tiles(seen, e.n_new, 2 * tpt, 0);
+      while (w.x - unit0 >= n + kStepTileUnit) {
+        unit0 += n + kStepTileUnit;
+        n = step_pair_tiles(seen, e.n_new, 2 * tpt, ++k);
+      }
+      const int off = k * 2 * tpt;
+      it.prefix = false;
+      it.table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
+      it.row[0] = e.row + off;
+      it.n_tok[0] = min(tpt, e.n_new - off);
+      it.n_tok[1] = max(0, min(tpt, e.n_new - off - tpt));
+      it.pos = seen + off;
     }
-    first = (int)r;
-    last = (int)min((int64_t)n, first + (w.end - w.x));
-    const int off = k * 2 * tpt;
-    it.prefix = false;
-    it.whole = first == 0 && last == n;
-    it.table = ds.block_table + (int64_t)seq * ds.max_blocks;
-    it.row[0] = q0 + off;
-    it.n_tok[0] = min(tpt, n_new - off);
-    it.n_tok[1] = max(0, min(tpt, n_new - off - tpt));
-    it.pos = seen + off;
-    const int keys_a = seen + off + it.n_tok[0];
-    it.ke = min(keys_a + it.n_tok[1], last * kKeys);
-    it.n[0] = max(0, min(last, (keys_a + kKeys - 1) / kKeys) - first);
-    it.n[1] = it.n_tok[1] > 0 ? last - first : 0;
+    // the unit's tiles [first, last) of this segment
+    const int64_t from = w.x - unit0 - kStepTileUnit, to = w.end - unit0 - kStepTileUnit;
+    const int first = (int)(from < 0 ? 0 : from);
+    const int last = (int)(to < 0 ? 0 : to < n ? to : n);
+    w.x = unit0 + n + kStepTileUnit;
+    if (first >= last) continue;
+    // (the prefix: pos is its last key for every row; else A's rows see the
+    // keys up to pos + their index, B's from there on)
+    const int keys_a = it.prefix ? it.pos + 1 : it.pos + it.n_tok[0];
+    const int keys = it.prefix ? it.pos + 1 : keys_a + it.n_tok[1];
+    it.head = first == 0;
+    it.whole = it.head && last == n;
+    it.row[1] = it.row[0] + tpt;
+    it.kb = first * kKeys;
+    it.ke = (int)min((int64_t)keys, (int64_t)last * kKeys);
+    it.nmax = last - first;
+    it.n[0] = max(0, min(last, (int)(((int64_t)keys_a + kKeys - 1) / kKeys)) - first);
+    it.n[1] = it.n_tok[1] > 0 ? it.nmax : 0;
+    return true;
   }
-  it.row[1] = it.row[0] + tpt;
-  it.head = first == 0;
-  it.kb = first * kKeys;
-  it.nmax = last - first;
-  w.x += last - first;
-  return true;
+  return false;
 }
 
 // The box of a query tile's half: 64 head dims x g heads x 128/g tokens, its
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int hi = plan.header[kPlanTiled] - 1;
     while (walk.unit < hi) {
       const int mid = (walk.unit + hi + 1) >> 1;
-      if (plan.tile_cum[mid] <= v) walk.unit = mid;
+      if (plan.tiled[mid].cum <= v) walk.unit = mid;
       else hi = mid - 1;
     }
   }

@@ -25,7 +25,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 
 constexpr int32_t kErrInvalid = -1, kErrNoBlocks = -2, kErrCapacity = -6;
-constexpr int64_t kMaxSteps = (int64_t)1 << 30;   // tiles or steps of one KV head
+constexpr int64_t kMaxLen = (int64_t)1 << 30;   // line length of one KV head
 
 // Block counts of a sequence, clamped to its table row (a sequence out of
 // range is reported and nothing is scheduled; the clamps keep the copy of its
@@ -39,7 +39,7 @@ __device__ __forceinline__ void blocks_of(int64_t seen, int64_t n_new, int32_t B
   need = (int32_t)(e < max_blocks ? e : max_blocks);
 }
 
-enum { kTokens = 0, kGrow, kStreamed, kTiled, kStreamTiles, kTileSteps, kSums };
+enum { kTokens = 0, kGrow, kStreamed, kTiled, kStreamLen, kTileLen, kSums };
 
 struct Sums {
   int64_t v[kSums];
@@ -60,10 +60,10 @@ __device__ __forceinline__ int32_t measure(const BuildArgs& a, int32_t seen, int
   if (n_new == 0) return 0;
   if ((int64_t)n_new * a.group <= kStepPackedRows) {
     s.v[kStreamed] = 1;
-    s.v[kStreamTiles] = (ctx + kStepStreamKeys - 1) / kStepStreamKeys;
+    s.v[kStreamLen] = (ctx + kStepStreamKeys - 1) / kStepStreamKeys + kStepStreamUnit;
   } else {
     s.v[kTiled] = 1;
-    s.v[kTileSteps] = step_seq_steps(seen, n_new, 2 * step_tile_tokens(a.group));
+    s.v[kTileLen] = step_seq_len(seen, n_new, 2 * step_tile_tokens(a.group));
   }
   return 0;
 }
@@ -228,8 +228,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     free_before += r < rank ? f : 0;
     err = min(err, remote_i32(&sh.err, r));
   }
-  if (err == 0 && (total[kTokens] > a.max_tokens || total[kStreamTiles] > kMaxSteps ||
-                   total[kTileSteps] > kMaxSteps))
+  if (err == 0 && (total[kTokens] > a.max_tokens || total[kStreamLen] > kMaxLen ||
+                   total[kTileLen] > kMaxLen))
     err = kErrCapacity;
   if (err == 0 && total[kGrow] > free_total) err = kErrNoBlocks;
   const bool ok = err == 0;
@@ -267,16 +267,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       for (int i = 0; i < kSums; ++i) v[i] += carry[i];
       a.ctx[s] = seen + n_new;
       a.q_start[s] = v[kTokens];
-      plan.first_new[s] = v[kGrow];
+      StepRow of = {0, v[kGrow], 0, 0};
+      StepSeq e = {s, v[kTokens], n_new, seen + n_new, 0, 0, {0, 0}};
       if (x.v[kStreamed]) {
-        plan.seq_unit[s] = v[kStreamed];
-        plan.stream_seq[v[kStreamed]] = s;
-        plan.stream_cum[v[kStreamed]] = v[kStreamTiles];
+        of.unit = v[kStreamed];
+        of.cum = e.cum = v[kStreamLen];
+        of.tiles = e.tiles = (int32_t)x.v[kStreamLen] - kStepStreamUnit;
+        plan.streamed[of.unit] = e;
       } else if (x.v[kTiled]) {
-        plan.seq_unit[s] = -1 - v[kTiled];
-        plan.tile_seq[v[kTiled]] = s;
-        plan.tile_cum[v[kTiled]] = v[kTileSteps];
+        of.unit = -1 - v[kTiled];
+        of.cum = e.cum = v[kTileLen];
+        of.tiles = e.tiles = (int32_t)x.v[kTileLen];
+        plan.tiled[v[kTiled]] = e;
       }
+      plan.of_seq[s] = of;
     }
 #pragma unroll
     for (int i = 0; i < kSums; ++i) carry[i] += sum[i];
@@ -286,10 +290,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     plan.header[kPlanRows] = T;
     plan.header[kPlanStreamed] = ok ? (int32_t)total[kStreamed] : 0;
     plan.header[kPlanTiled] = ok ? (int32_t)total[kTiled] : 0;
-    plan.header[kPlanStreamTiles] = ok ? (int32_t)total[kStreamTiles] : 0;
-    plan.header[kPlanTileSteps] = ok ? (int32_t)total[kTileSteps] : 0;
-    plan.stream_cum[plan.header[kPlanStreamed]] = plan.header[kPlanStreamTiles];
-    plan.tile_cum[plan.header[kPlanTiled]] = plan.header[kPlanTileSteps];
+    plan.header[kPlanStreamLen] = ok ? (int32_t)total[kStreamLen] : 0;
+    plan.header[kPlanTileLen] = ok ? (int32_t)total[kTileLen] : 0;
     if (!ok) atomicCAS(a.status, 0, err);
   }
 
@@ -336,14 +338,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const int seen = a.ctx[s] - n, pos = seen + r - q0;
     const int held = (int)(((int64_t)seen + B - 1) / B);
     const int c = pos / B, off = pos - c * B;
+    StepRow of = plan.of_seq[s];
     int32_t id;
     if (c < held) {
       id = a.table_in[(int64_t)s * a.max_blocks + c];
     } else {
-      id = plan.new_ids[plan.first_new[s] + c - held];
+      id = plan.new_ids[of.token + c - held];
       if (off == 0) a.table[(int64_t)s * a.max_blocks + c] = id;
     }
-    plan.row_seq[r] = s;
+    of.token = r - q0;
+    plan.rows[r] = of;
     a.position[r] = pos;
     if (id < 0 || id >= a.num_blocks) {
       atomicCAS(a.status, 0, kDevBounds);
