@@ -555,94 +555,103 @@ class StepTables:
         self.plan, self.status = full(0, ints), full(0, 4)
         self.device = self.block_table.device
         self._cfg = config._c()
-        self._t = _StepTables(self.num_seqs, self.max_blocks, self.max_tokens,
-                              *(x.data_ptr() for x in (
-                                  self.block_table, self.free, self.q_start, self.ctx,
-                                  self.position, self.slot, self.plan, self.status)))
+        self._tables = _StepTables(self.num_seqs, self.max_blocks, self.max_tokens,
+                                   *(x.data_ptr() for x in (
+                                       self.block_table, self.free, self.q_start, self.ctx,
+                                       self.position, self.slot, self.plan, self.status)))
+        self._c, self._t = C.byref(self._cfg), C.byref(self._tables)
+        self._i32, self._dt = torch.int32, config.torch_dtype
+        self._q_shape = torch.Size((self.max_tokens, config.num_heads_q, config.head_dim))
+        self._kv_shape = torch.Size((self.max_tokens, config.num_heads_kv, config.head_dim))
+        self._cache_shape = torch.Size(config.cache_shape())
 
-    def _ptr(self, t, name, dtype, shape):
+    def _ptr(self, t, name, dtype, shape) -> int:
+        if t.device == self.device and t.dtype is dtype and t.shape == shape and \
+                t.is_contiguous() and t.is_cuda:
+            return t.data_ptr()
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the tables on {self.device}")
-        return _dev_ptr(t, name, dtype, shape)
+        return _dev_ptr(t, name, dtype, shape).value
 
-    def _ints(self, t, name, shape):
+    def _call(self, fn, *args, stream=None) -> None:
+        """A library call on the tables' device (the current one or not)."""
         import torch
-        return self._ptr(t, name, torch.int32, shape)
-
-    def _args(self):
-        return C.byref(self._cfg), C.byref(self._t)
+        if torch.cuda.current_device() == self.device.index:
+            _check(fn(self._c, self._t, *args, _stream(stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(self._c, self._t, *args, _stream(stream)))
 
     def build(self, seen, n_new, block_table=None, free=None, stream=None) -> "StepTables":
         """Sequence s holds ``seen[s]`` tokens and takes ``n_new[s]`` more.
         ``block_table`` / ``free``: read from these instead of the tables' own
         (which are written either way)."""
-        S = (self.num_seqs,)
-        table = _P(None) if block_table is None else \
-            self._ints(block_table, "block_table", self.block_table.shape)
-        bits = _P(None) if free is None else self._ints(free, "free", self.free.shape)
-        with _device(self.device):
-            _check(lib().rbkv_step_build(*self._args(), self._ints(seen, "seen", S),
-                                         self._ints(n_new, "n_new", S), table, bits,
-                                         _stream(stream)))
+        i32, S = self._i32, self.ctx.shape
+        self._call(lib().rbkv_step_build, self._ptr(seen, "seen", i32, S),
+                   self._ptr(n_new, "n_new", i32, S),
+                   None if block_table is None else
+                   self._ptr(block_table, "block_table", i32, self.block_table.shape),
+                   None if free is None else self._ptr(free, "free", i32, self.free.shape),
+                   stream=stream)
         return self
 
     def release(self, done, stream=None) -> None:
         """Free the blocks of the sequences with ``done[s] != 0`` (int32)."""
-        with _device(self.device):
-            _check(lib().rbkv_step_release(*self._args(),
-                                           self._ints(done, "done", (self.num_seqs,)),
-                                           _stream(stream)))
+        self._call(lib().rbkv_step_release, self._ptr(done, "done", self._i32, self.ctx.shape),
+                   stream=stream)
 
     def append(self, k_new, v_new, k_cache, v_cache, stream=None) -> None:
         """Scatter the step's K/V rows ([max_tokens][H_kv][D]) into the caches."""
-        c = self.config
-        dt, row = c.torch_dtype, (self.max_tokens, c.num_heads_kv, c.head_dim)
-        with _device(self.device):
-            _check(lib().rbkv_step_append(
-                *self._args(), self._ptr(k_new, "k_new", dt, row),
-                self._ptr(v_new, "v_new", dt, row),
-                self._ptr(k_cache, "k_cache", dt, c.cache_shape()),
-                self._ptr(v_cache, "v_cache", dt, c.cache_shape()), _stream(stream)))
+        dt, row, cache = self._dt, self._kv_shape, self._cache_shape
+        self._call(lib().rbkv_step_append, self._ptr(k_new, "k_new", dt, row),
+                   self._ptr(v_new, "v_new", dt, row), self._ptr(k_cache, "k_cache", dt, cache),
+                   self._ptr(v_cache, "v_cache", dt, cache), stream=stream)
 
     def workspace_bytes(self, prefix_len: int = 0) -> int:
-        return int(lib().rbkv_step_workspace_bytes(*self._args(), int(prefix_len)))
+        with _device(self.device):
+            return int(lib().rbkv_step_workspace_bytes(self._c, self._t, int(prefix_len)))
 
     def attention(self, q, k_cache, v_cache, prefix_table=None, prefix_len: int = 0, o=None,
                   workspace=None, stream=None):
         """Every row attends the prefix and its sequence's keys up to its own;
         returns O ([max_tokens][H_q][D]; rows past the step's are left as they
         were)."""
-        import torch
-        c = self.config
-        dt, shape = c.torch_dtype, (self.max_tokens, c.num_heads_q, c.head_dim)
         prefix_len = int(prefix_len)
-        table = _P(None)
+        table = None
         if prefix_table is not None:
-            if prefix_table.dim() != 1 or prefix_table.numel() * c.block_size < prefix_len:
+            if prefix_table.dim() != 1 or \
+                    prefix_table.shape[0] * self.config.block_size < prefix_len:
                 raise ValueError("prefix_table must list the blocks of prefix_len tokens")
-            table = self._ints(prefix_table, "prefix_table", prefix_table.shape)
-        with _device(self.device):
-            st = _stream(stream)
-            need = self.workspace_bytes(prefix_len)
-            if o is None or (need and workspace is None):
-                with torch.cuda.stream(torch.cuda.ExternalStream(st.value or 0, self.device)):
-                    if o is None:
-                        o = torch.empty(shape, dtype=dt, device=self.device)
-                    if need and workspace is None:
-                        workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            if workspace is not None and workspace.device != self.device:
-                raise ValueError("workspace is on another device than the tables")
-            ws, ws_bytes = _ws(workspace)
-            _check(lib().rbkv_step_attention(
-                *self._args(), self._ptr(q, "q", dt, shape),
-                self._ptr(k_cache, "k_cache", dt, c.cache_shape()),
-                self._ptr(v_cache, "v_cache", dt, c.cache_shape()), table, prefix_len,
-                self._ptr(o, "o", dt, shape), ws, ws_bytes, st))
+            table = self._ptr(prefix_table, "prefix_table", self._i32, prefix_table.shape)
+        if o is None or workspace is None:
+            o, workspace = self._outputs(o, workspace, prefix_len, stream)
+        if workspace.device != self.device:
+            raise ValueError("workspace is on another device than the tables")
+        dt, cache = self._dt, self._cache_shape
+        self._call(lib().rbkv_step_attention, self._ptr(q, "q", dt, self._q_shape),
+                   self._ptr(k_cache, "k_cache", dt, cache),
+                   self._ptr(v_cache, "v_cache", dt, cache), table, prefix_len,
+                   self._ptr(o, "o", dt, self._q_shape), workspace.data_ptr(),
+                   workspace.numel() * workspace.element_size(), stream=stream)
         return o
+
+    def _outputs(self, o, workspace, prefix_len, stream):
+        """O and a workspace where none was given, allocated on the stream that
+        uses them."""
+        import torch
+        with _device(self.device):
+            st = torch.cuda.ExternalStream(_stream(stream).value or 0, self.device)
+            with torch.cuda.stream(st):
+                if o is None:
+                    o = torch.empty(self._q_shape, dtype=self._dt, device=self.device)
+                if workspace is None:
+                    need = int(lib().rbkv_step_workspace_bytes(self._c, self._t, prefix_len))
+                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return o, workspace
 
     def device_status(self, stream=None) -> None:
         with _device(self.device):
-            _check(lib().rbkv_step_device_status(C.byref(self._t), _stream(stream)))
+            _check(lib().rbkv_step_device_status(self._t, _stream(stream)))
 
 
 def budget_for_latency(tokens, latency, bound: float) -> int:

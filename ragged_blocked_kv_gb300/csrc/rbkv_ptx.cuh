@@ -97,6 +97,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int
       : "memory");
 }
 
+// The same from a 4-D tensor, at (0, 0, 0, w).
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int32_t w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Order this thread's earlier generic-proxy shared-memory accesses before
 // later async-proxy accesses (TMA writes, tensor-core reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {

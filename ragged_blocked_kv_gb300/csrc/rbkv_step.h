@@ -73,6 +73,12 @@ __host__ __device__ __forceinline__ StepPlan step_plan(int32_t* p, int32_t num_s
   return v;
 }
 
+// a / b for a >= 0, b > 0 (a 64-bit division takes several times as long).
+__host__ __device__ __forceinline__ int64_t step_div(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Sum of floor((a i + b) / m) over i = 0 .. n - 1, for n, a, b >= 0 and m > 0.
 // The whole multiples of m in a and b are summed in closed form; what is left
 // counts lattice points under a line, which is the same sum with the axes
@@ -80,13 +86,14 @@ __host__ __device__ __forceinline__ StepPlan step_plan(int32_t* p, int32_t num_s
 __host__ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t total = 0;
   while (n > 0) {
-    total += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
+    const int64_t qa = step_div(a, m), qb = step_div(b, m);
+    total += n * (n - 1) / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
     const int64_t top = a * n + b;
     if (top < m) break;
-    n = top / m;
-    b = top % m;
+    n = step_div(top, m);
+    b = top - n * m;
     const int64_t t = a;
     a = m;
     m = t;
@@ -138,10 +145,7 @@ struct DevStep {
 // of the workspace; a segment that begins inside a unit can only be the first
 // of its CTA, and goes to that CTA's spill rows.
 __host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, int64_t ctas) {
-  const uint64_t p = (uint64_t)(c * total);
-  // (a 64-bit division takes several times as long)
-  if (p >> 32) return (int64_t)(p / (uint64_t)ctas);
-  return (int64_t)((uint32_t)p / (uint32_t)ctas);
+  return step_div(c * total, ctas);
 }
 
 // The units of the streaming kernel: (streamed sequence, KV head), the KV

@@ -32,8 +32,8 @@ constexpr int kStages = 3;
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kKeys = kStepStreamKeys;
-constexpr int kHalf = kKeys * 128;            // 64 rows x 128 B (64 bf16 of head_dim)
-constexpr int kTile = 2 * kHalf;              // K or V tile, head_dim 128
+constexpr int kGroup = 16 * 256;              // 16 keys of K or V, head_dim 128
+constexpr int kTile = kKeys * 256;            // K or V tile
 constexpr int kStage = 2 * kTile;             // K + V
 constexpr int kRows = kStepPackedRows;
 constexpr int kScratch = kConsumers * kRows * 64 * 4;   // [warp][row][64] fp32
@@ -47,12 +47,12 @@ constexpr long long kWaitLimit = 4000000000LL;   // ~2 s of SM clock
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Byte offset, inside one K or V tile, of the 16-byte chunk holding elements
-// d..d+7 (d % 8 == 0) of key row `key` (128-byte swizzle, each 64-column half
-// a separate 8 KB box).
+// d..d+7 (d % 8 == 0) of key row `key`: groups of 16 keys, each as two halves
+// of the head dim, 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_off(int key, int d) {
-  const int half = d >> 6;
   const int chunk = (d & 63) >> 3;
-  return half * kHalf + key * 128 + ((chunk ^ (key & 7)) << 4);
+  return (key >> 4) * kGroup + (d >> 6) * (kGroup / 2) + (key & 15) * 128 +
+         ((chunk ^ (key & 7)) << 4);
 }
 
 // One segment of a unit, as the producer publishes it to the consumers.
@@ -116,19 +116,22 @@ struct Walk {
     }
   }
 
+  // (every lane of the warp calls it: the search tests 32 places at a time)
   __device__ __forceinline__ void start(int64_t x, const DevStep& ds, const ShapeInfo& s,
-                                        const StepPlan& plan, const StepWork& work) {
+                                        const StepPlan& plan, const StepWork& work, int lane) {
     int64_t base = work.stream_own;
     unit = plan.header[kPlanStreamed];
     int len = work.prefix_stream_tiles + kStepStreamUnit;
     if (x < work.stream_own) {
       // the last sequence at or before x
       const int32_t v = (int32_t)(x / s.H_kv);
-      int lo = 0, hi = unit - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (plan.streamed[mid].cum <= v) lo = mid;
-        else hi = mid - 1;
+      int lo = 0, left = unit;
+      while (left > 1) {
+        const int step = (left + 31) >> 5;
+        const bool le = lane * step < left && plan.streamed[lo + lane * step].cum <= v;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lane 0 always holds
+        lo += k * step;
+        left = min(step, left - k * step);
       }
       unit = lo;
       cur = plan.streamed[unit];
@@ -172,9 +175,13 @@ struct Walk {
   }
 };
 
+// The caches as tensor maps: boxes of 64 keys or a block, and of 16 keys.
+struct Maps {
+  CUtensorMap k, v, k_one, v_one;
+};
+
 __global__ void __launch_bounds__(kThreads, 2)
-    step_stream_kernel(const __grid_constant__ CUtensorMap tmap_k,
-                       const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
+    step_stream_kernel(const __grid_constant__ Maps maps, DevStep ds, ShapeInfo shp,
                        StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
                        __nv_bfloat16* __restrict__ o, int first) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -206,14 +213,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
+    Walk walk;
+    walk.end = step_cut(blockIdx.x + 1, work.stream_total, ctas);
+    int64_t x = step_cut(blockIdx.x, work.stream_total, ctas);
+    walk.start(x, ds, shp, plan, work, lane);
     if (lane == 0) {
-      ptx::tma_prefetch_desc(&tmap_k);
-      ptx::tma_prefetch_desc(&tmap_v);
       const int box_rows = B < kKeys ? B : kKeys;
-      Walk walk;
-      walk.end = step_cut(blockIdx.x + 1, work.stream_total, ctas);
-      int64_t x = step_cut(blockIdx.x, work.stream_total, ctas);
-      walk.start(x, ds, shp, plan, work);
       Segment it, nx;
       const int32_t *ids, *nx_ids;
       auto next = [&](Segment& g, const int32_t*& p) {
@@ -259,27 +264,43 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int k0 = (it.tile + j) * kKeys;
           uint8_t* kdst = sm.stages + s * kStage;
           uint8_t* vdst = kdst + kTile;
-          int loads = 0;
+          // boxes of box_rows keys; of a box that the unit's keys end in, only
+          // the 16-key groups that hold some (whole boxes would read 32 keys
+          // too many per unit on average: a tenth of the traffic at 256 keys)
+          uint32_t keys = 0;
 #pragma unroll
           for (int i = 0; i < kKeys / 8; ++i) {
-            if (i * box_rows < kKeys && k0 + i * box_rows < it.keys) {
+            const int left = it.keys - k0 - i * box_rows;
+            if (i * box_rows < kKeys && left > 0) {
               if (blk[i] < 0 || blk[i] >= ds.num_blocks)
                 atomicCAS(ds.status, 0, kDevBounds);
               else
-                ++loads;
+                keys += left >= box_rows ? box_rows : min(box_rows, (left + 15) & ~15);
             }
           }
-          ptx::mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(loads * box_rows * 128 * 4));
+          ptx::mbar_arrive_expect_tx(&sm.full[s], keys * 512);
 #pragma unroll
           for (int i = 0; i < kKeys / 8; ++i) {
-            if (i * box_rows < kKeys && k0 + i * box_rows < it.keys && blk[i] >= 0 &&
-                blk[i] < ds.num_blocks) {
+            const int left = it.keys - k0 - i * box_rows;
+            if (i * box_rows < kKeys && left > 0 && blk[i] >= 0 && blk[i] < ds.num_blocks) {
               const int row = (blk[i] * H_kv + it.kv_head) * B + ((k0 + i * box_rows) % B);
-              const int off = i * box_rows * 128;
-              ptx::tma_load_2d(kdst + off, &tmap_k, 0, row, &sm.full[s]);
-              ptx::tma_load_2d(kdst + kHalf + off, &tmap_k, 64, row, &sm.full[s]);
-              ptx::tma_load_2d(vdst + off, &tmap_v, 0, row, &sm.full[s]);
-              ptx::tma_load_2d(vdst + kHalf + off, &tmap_v, 64, row, &sm.full[s]);
+              if (box_rows < 16) {
+                // 8-key blocks: half a group per copy
+                const int off = (i >> 1) * kGroup + (i & 1) * 8 * 128;
+                ptx::tma_load_2d(kdst + off, &maps.k, 0, row, &sm.full[s]);
+                ptx::tma_load_2d(kdst + off + kGroup / 2, &maps.k, 64, row, &sm.full[s]);
+                ptx::tma_load_2d(vdst + off, &maps.v, 0, row, &sm.full[s]);
+                ptx::tma_load_2d(vdst + off + kGroup / 2, &maps.v, 64, row, &sm.full[s]);
+              } else if (left > box_rows - 16) {
+                ptx::tma_load_4d(kdst + i * box_rows * 256, &maps.k, row >> 4, &sm.full[s]);
+                ptx::tma_load_4d(vdst + i * box_rows * 256, &maps.v, row >> 4, &sm.full[s]);
+              } else {
+                for (int f = 0; f < left; f += 16) {
+                  const int at = (i * box_rows + f) * 256;
+                  ptx::tma_load_4d(kdst + at, &maps.k_one, (row + f) >> 4, &sm.full[s]);
+                  ptx::tma_load_4d(vdst + at, &maps.v_one, (row + f) >> 4, &sm.full[s]);
+                }
+              }
             }
           }
           if (j + 1 < it.tiles) look(it, ids, j + 1);
@@ -374,12 +395,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (valid < 16) {
         // rows past the unit's last key may hold anything (unwritten cache
         // slots, stale tiles): zero this warp's such V rows so 0 * V stays 0
-        uint8_t* vrow = sm.stages + s * kStage + kTile;
+        uint8_t* vrow = sm.stages + s * kStage + kTile + warp * kGroup;
         const int from = valid < 0 ? 0 : valid;
         for (int e = lane; e < (16 - from) * 16; e += 32) {
-          const int key = wk + from + e / 16, c = e % 16;
-          *reinterpret_cast<uint4*>(vrow + (c >> 3) * kHalf + key * 128 + ((c & 7) << 4)) =
-              make_uint4(0, 0, 0, 0);
+          const int key = from + e / 16, c = e % 16;
+          *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kGroup / 2) + key * 128 +
+                                    ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
       }
@@ -564,110 +585,169 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------------------
 // O = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M) over the row's partial
 // outputs: its own part and the prefix's, each with the spills of the CTAs
-// whose cuts fall inside its unit.  The cuts are a formula, so nothing is
-// searched or stored.  Bound by the partials' traffic (from L2, they were
-// just written) and a launch.
-struct Join {
-  float M, L;
-  float4 acc;
-  __device__ __forceinline__ void add(float lse, float4 v) {
-    if (lse == -INFINITY) return;
-    const float m = fmaxf(M, lse);
-    const float a = M == -INFINITY ? 0.f : exp2f(M - m), b = exp2f(lse - m);
-    M = m;
-    L = L * a + b;
-    acc.x = acc.x * a + v.x * b;
-    acc.y = acc.y * a + v.y * b;
-    acc.z = acc.z * a + v.z * b;
-    acc.w = acc.w * a + v.w * b;
-  }
+// whose cuts fall inside its unit.  The cuts are a formula; a block works out
+// those of its row and KV heads once, one thread each, and its warps then
+// join the heads: lane i weighs source i, all lanes add four columns of each.
+// Bound by the partials' traffic (from L2, they were just written).
+constexpr int kJoinWarps = 4;
+constexpr int kJoinHeads = 8;     // query heads of a block
+
+// Spills of a unit that a row joins: CTAs [first, first + n).
+struct Spills {
+  int first, n;
+  bool cut;       // the unit was cut between its tiles
 };
 
-// The spills of the cuts inside a unit at `begin` of a line, of a fixed length
-// `unit` and `tiles` key tiles (`row_tiles` of them seen by the row: a unit's
-// two query tiles may see different numbers).  Spill rows are [ctas][stride],
-// this row's at `row`.  Returns whether the unit was cut between its tiles.
-__device__ __forceinline__ bool add_spills(Join& j, const float* o, const float* lse, int stride,
-                                           int row, int64_t begin, int unit, int tiles,
-                                           int row_tiles, int64_t total, int ctas, int lane) {
-  bool cut = false;
-  // the first cut after `begin`, from an estimate that is off by one at most
-  int64_t c = (int64_t)((float)begin * (float)ctas / (float)total) - 1;
+// For a unit at `begin` of a line, of a fixed length `unit` and `tiles` key
+// tiles, `row_tiles` of them seen by the row (a unit's two query tiles may see
+// different numbers).
+__device__ __forceinline__ Spills spills_of(int64_t begin, int unit, int tiles, int row_tiles,
+                                            int64_t total, int ctas) {
+  Spills s = {0, 0, false};
+  // the first cut behind the unit's first tile, from an estimate that is off
+  // by one at most
+  int c = (int)((float)begin * (float)ctas / (float)total) - 1;
   c = c < 0 ? 0 : c;
   while (c < ctas && step_cut(c, total, ctas) <= begin + unit) ++c;
+  s.first = c;
+  // (a CTA's part is at least one long: tiles bounds the cuts)
   for (; c < ctas; ++c) {
     const int64_t tile = step_cut(c, total, ctas) - begin - unit;   // first tile behind it
     if (tile >= tiles) break;
-    cut = true;
-    if (tile >= row_tiles) continue;
-    const int64_t at = c * stride + row;
-    j.add(lse[at], reinterpret_cast<const float4*>(o + at * 128)[lane]);
+    s.cut = true;
+    if (tile < row_tiles) ++s.n;
   }
-  return cut;
+  return s;
 }
-
-constexpr int kJoinWarps = 4;
 
 __global__ void __launch_bounds__(kJoinWarps * 32)
     step_combine_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
                         __nv_bfloat16* __restrict__ o) {
+  __shared__ Spills spills[2 * kJoinHeads];     // [KV head of the block][own, prefix]
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = shp.g, H_kv = shp.H_kv, tpt = step_tile_tokens(g);
   const int T = plan.header[kPlanRows];
   const int s_ctas = (int)min((int64_t)ws.stream_grid, work.stream_total);
   const int t_ctas = (int)min((int64_t)ws.tile_grid, work.tile_total);
   const bool pre = ds.prefix_len > 0;
-  const int64_t items = (int64_t)T * shp.H_q;
-  for (int64_t w = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); w < items;
-       w += (int64_t)gridDim.x * kJoinWarps) {
-    const int t = (int)(w / shp.H_q), h = (int)(w - (int64_t)t * shp.H_q);
-    const int kvh = h / g, hh = h - kvh * g;
+  const bool pre_streamed = work.prefix_stream_tiles > 0;
+  const int h0 = blockIdx.x * kJoinHeads, h1 = min(h0 + kJoinHeads, shp.H_q);
+  const int kv0 = h0 / g, n_kv = (h1 - 1) / g - kv0 + 1;
+  for (int t = blockIdx.y; t < T; t += gridDim.y) {
     const StepRow r = plan.rows[t];
-    const float own_l = ws.own_lse[w];
-    const float4 own_v = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane];
-    Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    bool joined = pre;
-    if (pre) j.add(ws.pre_lse[w], reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane]);
-    j.add(own_l, own_v);
-    if (r.unit >= 0) {
-      const int64_t a = (int64_t)H_kv * r.cum + (int64_t)kvh * (r.tiles + kStepStreamUnit);
-      joined |= add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, r.token * g + hh, a,
-                           kStepStreamUnit, r.tiles, r.tiles, work.stream_total, s_ctas, lane);
-    } else {
-      const StepSeq e = plan.tiled[-1 - r.unit];
-      const int seen = e.ctx - e.n_new, k = r.token / (2 * tpt), x = (r.token / tpt) & 1;
-      const int64_t a = work.tile_prefix + (int64_t)H_kv * r.cum + (int64_t)kvh * r.tiles +
-                        step_len_before(seen, 2 * tpt, k);
-      // key tiles of the row's own query tile
-      const int end = min(e.n_new, (2 * k + x + 1) * tpt);
-      joined |= add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
-                           x * kStepTileRows + (r.token % tpt) * g + hh, a, kStepTileUnit,
-                           step_pair_tiles(seen, e.n_new, 2 * tpt, k),
-                           (seen + end + kStepTileKeys - 1) / kStepTileKeys, work.tile_total,
-                           t_ctas, lane);
+    int own_row = r.token * g;          // row of the sequence's first head in a spill
+    const int pair = r.token / (2 * tpt), in_pair = r.token - pair * 2 * tpt;
+    if (r.unit < 0)
+      own_row = in_pair < tpt ? in_pair * g : kStepTileRows + (in_pair - tpt) * g;
+    if (threadIdx.x < 2 * n_kv) {
+      const int kvh = kv0 + (threadIdx.x >> 1);
+      int64_t begin, total = work.stream_total;
+      int unit = kStepStreamUnit, tiles, seen_tiles, ctas = s_ctas;
+      if (threadIdx.x & 1) {
+        if (pre_streamed) {
+          tiles = work.prefix_stream_tiles;
+          begin = work.stream_own + (int64_t)kvh * (tiles + unit);
+        } else {
+          tiles = work.prefix_tile_steps;
+          unit = kStepTileUnit;
+          begin = ((int64_t)kvh * work.prefix_pairs + t / (2 * tpt)) * (tiles + unit);
+          total = work.tile_total;
+          ctas = t_ctas;
+        }
+        seen_tiles = tiles;
+      } else if (r.unit >= 0) {
+        seen_tiles = tiles = r.tiles;
+        begin = (int64_t)H_kv * r.cum + (int64_t)kvh * (tiles + unit);
+      } else {
+        const StepSeq e = plan.tiled[-1 - r.unit];
+        const int seen = e.ctx - e.n_new;
+        tiles = step_pair_tiles(seen, e.n_new, 2 * tpt, pair);
+        // key tiles of the row's own query tile
+        const int end = min(e.n_new, (2 * pair + (in_pair < tpt ? 1 : 2)) * tpt);
+        seen_tiles = (seen + end + kStepTileKeys - 1) / kStepTileKeys;
+        unit = kStepTileUnit;
+        begin = work.tile_prefix + (int64_t)H_kv * r.cum + (int64_t)kvh * r.tiles +
+                step_len_before(seen, 2 * tpt, pair);
+        total = work.tile_total;
+        ctas = t_ctas;
+      }
+      Spills s = {0, 0, false};
+      if (pre || !(threadIdx.x & 1)) s = spills_of(begin, unit, tiles, seen_tiles, total, ctas);
+      spills[threadIdx.x] = s;
     }
-    if (pre && work.prefix_stream_tiles) {
-      const int n = work.prefix_stream_tiles;
-      add_spills(j, ws.stream_o, ws.stream_lse, kStepPackedRows, t * g + hh,
-                 work.stream_own + (int64_t)kvh * (n + kStepStreamUnit), kStepStreamUnit, n, n,
-                 work.stream_total, s_ctas, lane);
-    } else if (pre) {
-      const int n = work.prefix_tile_steps;
-      add_spills(j, ws.tile_o, ws.tile_lse, 2 * kStepTileRows,
-                 ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g + hh,
-                 ((int64_t)kvh * work.prefix_pairs + t / (2 * tpt)) * (n + kStepTileUnit),
-                 kStepTileUnit, n, n, work.tile_total, t_ctas, lane);
+    __syncthreads();
+    for (int h = h0 + warp; h < h1; h += kJoinWarps) {
+      const int64_t w = (int64_t)t * shp.H_q + h;
+      const int kvh = h / g, hh = h - kvh * g;
+      const Spills a = spills[2 * (kvh - kv0)], p = spills[2 * (kvh - kv0) + 1];
+      if (!pre && !a.cut) continue;      // the unit was whole: its kernel wrote O
+      // sources: the unit's own rows, the prefix's, and the spills of both
+      const int base = pre ? 2 : 1, n = base + a.n + p.n;
+      float M = -INFINITY, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s0 = 0; s0 < n; s0 += 32) {
+        const int i = s0 + lane;
+        const float* src = ws.own_o + w * 128;
+        const float* lse = ws.own_lse + w;
+        if (i == 1 && pre) {
+          src = ws.pre_o + w * 128;
+          lse = ws.pre_lse + w;
+        } else if (i >= base) {
+          const bool mine = i < base + a.n;
+          const bool streamed = mine ? r.unit >= 0 : pre_streamed;
+          const int c = mine ? a.first + i - base : p.first + i - base - a.n;
+          int at = hh;
+          if (mine) at += own_row;
+          else if (streamed) at += t * g;
+          else at += ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g;
+          const int64_t row = streamed ? (int64_t)c * kStepPackedRows + at
+                                       : (int64_t)c * 2 * kStepTileRows + at;
+          src = (streamed ? ws.stream_o : ws.tile_o) + row * 128;
+          lse = (streamed ? ws.stream_lse : ws.tile_lse) + row;
+        }
+        const float l = i < n ? *lse : -INFINITY;
+        float m = l;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        m = fmaxf(m, M);
+        // (a source without a visible key has log-sum-exp -inf and weight 0)
+        const float wt = l == -INFINITY ? 0.f : exp2f(l - m);
+        const float keep = M == -INFINITY ? 0.f : exp2f(M - m);
+        float sum = wt;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        M = m;
+        L = L * keep + sum;
+        acc.x *= keep;
+        acc.y *= keep;
+        acc.z *= keep;
+        acc.w *= keep;
+        const int count = min(32, n - s0);
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+          const float* from = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, (unsigned long long)src, k));
+          const float f = __shfl_sync(0xffffffffu, wt, k);
+          const float4 v = reinterpret_cast<const float4*>(from)[lane];
+          if (f != 0.f) {   // (an empty source's rows hold no sum: 0 x NaN is NaN)
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+        }
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      uint2 out;
+      out.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
+      out.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
+      reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
     }
-    if (!joined) continue;      // the unit was whole: its kernel wrote O
-    const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
-    uint2 out;
-    out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
-    out.y = ptx::pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
-    reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
+    __syncthreads();   // the next row's spills replace these
   }
 }
 
@@ -707,9 +787,19 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
                                bool first, cudaStream_t st) {
   const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
   const int box_rows = s.B < kKeys ? s.B : kKeys;
-  CUtensorMap tk, tv;
-  cudaError_t e = make_cache_tmap(&tk, k_cache, rows, s.D, box_rows);
-  if (e == cudaSuccess) e = make_cache_tmap(&tv, v_cache, rows, s.D, box_rows);
+  Maps maps;
+  cudaError_t e;
+  if (box_rows < 16) {
+    e = make_cache_tmap(&maps.k, k_cache, rows, s.D, box_rows);
+    if (e == cudaSuccess) e = make_cache_tmap(&maps.v, v_cache, rows, s.D, box_rows);
+    maps.k_one = maps.k;
+    maps.v_one = maps.v;
+  } else {
+    e = make_group_tmap(&maps.k, k_cache, rows, box_rows / 16);
+    if (e == cudaSuccess) e = make_group_tmap(&maps.v, v_cache, rows, box_rows / 16);
+    if (e == cudaSuccess) e = make_group_tmap(&maps.k_one, k_cache, rows, 1);
+    if (e == cudaSuccess) e = make_group_tmap(&maps.v_one, v_cache, rows, 1);
+  }
   if (e != cudaSuccess) return e;
   // the shared-memory limit is raised once per device
   static std::atomic<uint64_t> attr_done{0};
@@ -736,17 +826,16 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_stream_kernel, tk, tv, ds, s, w, (const __nv_bfloat16*)q,
+  return cudaLaunchKernelEx(&cfg, step_stream_kernel, maps, ds, s, w, (const __nv_bfloat16*)q,
                             (__nv_bfloat16*)o, first ? 1 : 0);
 }
 
 cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                                 void* o, cudaStream_t st) {
-  const int64_t warps = (int64_t)ds.max_tokens * s.H_q;
-  const int64_t blocks = std::min<int64_t>((warps + kJoinWarps - 1) / kJoinWarps,
-                                           (int64_t)w.tile_grid * 16);
+  const int chunks = (s.H_q + kJoinHeads - 1) / kJoinHeads;
+  const int rows = std::min(ds.max_tokens, std::max(1, w.tile_grid * 16 / chunks));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)chunks, (unsigned)std::min(rows, 65535));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

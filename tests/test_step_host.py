@@ -113,10 +113,10 @@ def test_binding_checks(rbkv):
     t = rbkv.StepTables(cfg, 4, 8, 16, device="cpu")
     assert t.free.tolist() == [-1, 1]            # 33 blocks: the second word holds one
     with pytest.raises(ValueError):              # not on a GPU
-        t._ints(torch.zeros(4, dtype=torch.int32), "seen", (4,))
+        t._ptr(torch.zeros(4, dtype=torch.int32), "seen", torch.int32, (4,))
     other = torch.zeros(4, dtype=torch.int32, device="meta")
     with pytest.raises(ValueError, match="is on meta"):
-        t._ints(other, "seen", (4,))
+        t._ptr(other, "seen", torch.int32, (4,))
     with pytest.raises(ValueError, match="prefix_table"):
         t.attention(None, None, None, prefix_table=torch.zeros(2, dtype=torch.int32),
                     prefix_len=33)
