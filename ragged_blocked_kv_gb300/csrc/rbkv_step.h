@@ -9,7 +9,8 @@ namespace rbkv {
 // Sequences whose packed query rows (new tokens x heads of a KV group) number
 // at most this go to the streaming kernel, longer ones to the tile kernel.
 constexpr int kStepPackedRows = 16;
-constexpr int kStepStreamKeys = 64;     // keys per tile of the streaming kernel
+constexpr int kStepStreamKeys = 16;     // keys per tile of the streaming kernel
+constexpr int kStepPipes = 8;           // its pipelines (warps) per SM
 constexpr int kStepTileKeys = 128;      // keys per tile of the tensor-core kernel
 constexpr int kStepTileRows = 128;      // packed query rows per tensor-core tile
 
@@ -18,7 +19,7 @@ __host__ __device__ __forceinline__ int step_tile_tokens(int g) { return kStepTi
 
 // What a unit of work costs beside its key tiles (queries in, results out), in
 // key tiles of its kernel, for the even cut of the work over the CTAs.
-constexpr int kStepStreamUnit = 1;
+constexpr int kStepStreamUnit = 2;
 constexpr int kStepTileUnit = 2;
 
 // Header words of the plan.
@@ -32,7 +33,7 @@ enum {
 };
 
 // A sequence of a kernel's work list.  cum: line length before it, for one KV
-// head; tiles: 64-key tiles (streamed) or line length (tiled).
+// head; tiles: 16-key tiles (streamed) or line length (tiled).
 struct StepSeq {
   int32_t seq, row, n_new, ctx, cum, tiles;
   int32_t pad[2];
@@ -156,7 +157,8 @@ __host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, i
 struct StepWork {
   int64_t stream_own, stream_total;
   int64_t tile_prefix, tile_total;
-  int32_t prefix_stream_tiles;        // 64-key tiles of the prefix, when streamed
+  int32_t rows, streamed;             // query rows; streamed sequences
+  int32_t prefix_stream_tiles;        // 16-key tiles of the prefix, when streamed
   int32_t prefix_tile_steps;          // 128-key tiles of the prefix, when tiled
   int32_t prefix_pairs;               // pairs of query tiles over the prefix
 };
@@ -169,14 +171,17 @@ __host__ __device__ __forceinline__ bool step_prefix_streamed(int32_t max_tokens
 __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo& s,
                                               const StepPlan& plan) {
   StepWork w;
-  const int32_t T = plan.header[kPlanRows];
+  const int4 h = *reinterpret_cast<const int4*>(plan.header);
+  const int32_t T = h.x;
+  w.rows = T;
+  w.streamed = h.y;
   const bool streamed = step_prefix_streamed(ds.max_tokens, s.g);
   const int32_t P = T > 0 ? ds.prefix_len : 0;
   w.prefix_stream_tiles = streamed ? (P + kStepStreamKeys - 1) / kStepStreamKeys : 0;
   w.prefix_tile_steps = streamed ? 0 : (int32_t)(((int64_t)P + kStepTileKeys - 1) / kStepTileKeys);
   const int32_t pair = 2 * step_tile_tokens(s.g);
   w.prefix_pairs = (T + pair - 1) / pair;
-  w.stream_own = (int64_t)plan.header[kPlanStreamLen] * s.H_kv;
+  w.stream_own = (int64_t)h.w * s.H_kv;
   w.stream_total = w.stream_own;
   if (w.prefix_stream_tiles)
     w.stream_total += (int64_t)(w.prefix_stream_tiles + kStepStreamUnit) * s.H_kv;
@@ -196,6 +201,13 @@ struct StepWorkspace {
   float *tile_o, *tile_lse;     // spill rows [tile grid][2 kStepTileRows]
   int32_t stream_grid, tile_grid;
 };
+
+#ifdef __CUDACC__
+// Pipelines of the streaming kernel that take part.
+__device__ __forceinline__ int64_t step_pipes(const StepWorkspace& ws, const StepWork& work) {
+  return min((int64_t)ws.stream_grid, work.stream_total);
+}
+#endif
 
 bool step_fast_supported(const ShapeInfo& s);
 // Carve a workspace at `base` (may be null); returns its bytes.

@@ -2,18 +2,21 @@
 // sequence's new tokens x the heads of one KV group) over the sequence's own
 // keys; every cached K/V byte is read once, so HBM bounds it.
 //
-// The units' 64-key tiles lie on one line that is cut evenly over the CTAs
-// (rbkv_step.h): two CTAs per SM, each with
-//  - a producer warp that streams K and V tiles through the block table with
-//    TMA (128-byte swizzle) into a 3-stage ring of 32 KB stages;
-//  - four consumer warps that share every tile, 16 keys each: S = Q K^T with
-//    m16n8k16 MMAs (the rows padded to 16; the contraction is tiny, so they
-//    only lift the bound that CUDA cores would set), an online softmax in
-//    registers, O += P V; at the end of a segment their (max, sum, O) are
-//    merged through shared memory, half of the head dim at a time (16 KB of
-//    scratch beside the ring leaves room for two CTAs per SM).
+// The units lie on one line in groups of 16 keys, cut evenly (rbkv_step.h) over
+// eight warps per SM.  Each warp is a pipeline of its own: lane 0 keeps a ring
+// of three 8 KB groups (16 keys of K and V, one TMA copy each) in flight,
+// and the warp multiplies, exponentiates and accumulates a group at a time:
+//   S^T = K Q^T   (m16n8k16: 16 keys x 8 query rows, one or two such tiles)
+//   P^T = exp2(S^T - running maximum of the row), rounded to bf16
+//   O^T += V^T P^T (16 head dims x 8 rows per MMA)
+// with the keys and head dims on the MMAs' 16-row side, so a group of 4 or 8
+// heads wastes at most half of the narrow side, where Q on the 16-row side
+// would waste three quarters.  No warp waits for another: no merge, no block
+// barrier; 128 KB in flight per SM cover the latency.  (Four warps sharing
+// 64-key tiles of a common ring, merged per unit, held 5.2 TB/s on 512
+// sequences of 256 keys: the merge idled the ring.)
 // Every wait is bounded; on timeout the kernel records RBKV_ERR_TIMEOUT and
-// returns.
+// the warp drains its copies and returns.
 #include <algorithm>
 #include <atomic>
 
@@ -28,38 +31,40 @@ namespace rbkv {
 
 namespace {
 
+constexpr int kWarps = kStepPipes;
+constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
-constexpr int kConsumers = 4;
-constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kKeys = kStepStreamKeys;
-constexpr int kGroup = 16 * 256;              // 16 keys of K or V, head_dim 128
-constexpr int kTile = kKeys * 256;            // K or V tile
-constexpr int kStage = 2 * kTile;             // K + V
+constexpr int kKeys = kStepStreamKeys;        // keys of a group
+constexpr int kHalf = kKeys * 128;            // 16 rows x 128 B (64 bf16 of head_dim)
+constexpr int kGroup = 2 * kHalf;             // a group of K or V, head_dim 128
+constexpr int kStage = 2 * kGroup;            // K + V
 constexpr int kRows = kStepPackedRows;
-constexpr int kScratch = kConsumers * kRows * 64 * 4;   // [warp][row][64] fp32
-constexpr int kMl = kConsumers * kRows * 2 * 4;         // (max, sum) per warp and row
-constexpr int kSegments = 4;            // published segments; more than kStages
-static_assert(kSegments > kStages && (2 * kStages + kSegments) % 2 == 0, "segment ring");
+constexpr int kSegments = kStages + 2;        // segments that a warp's window can meet
 constexpr int kSmemBytes =
-    kStages * kStage + kScratch + kMl + (2 * kStages + kSegments) * 8 + kSegments * 32 + 16;
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+    kWarps * (kStages * kStage + kSegments * 32 + kStages * 8);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 constexpr long long kWaitLimit = 4000000000LL;   // ~2 s of SM clock
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Byte offset, inside one K or V tile, of the 16-byte chunk holding elements
-// d..d+7 (d % 8 == 0) of key row `key`: groups of 16 keys, each as two halves
-// of the head dim, 128-byte swizzle.
-__device__ __forceinline__ uint32_t tile_off(int key, int d) {
-  const int chunk = (d & 63) >> 3;
-  return (key >> 4) * kGroup + (d >> 6) * (kGroup / 2) + (key & 15) * 128 +
-         ((chunk ^ (key & 7)) << 4);
+// Byte offset, inside a group, of the 16-byte chunk holding elements d..d+7
+// (d % 8 == 0) of key row `key`: two halves of the head dim, 128-byte swizzle.
+__device__ __forceinline__ uint32_t group_off(int key, int d) {
+  return (d >> 6) * kHalf + key * 128 + ((((d & 63) >> 3) ^ (key & 7)) << 4);
 }
 
-// One segment of a unit, as the producer publishes it to the consumers.
+// The 8 x 8 transpose of a matrix of 16-bit elements held two per lane (row
+// lane / 4, columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// One segment of a unit.
 struct __align__(16) Segment {
   int row, n_tok;        // first row and tokens of the unit
   int kv_head;
-  int tile, tiles;       // first key tile, and number of them (0: no more segments)
+  int group, groups;     // first group of keys, and number of them (0: no more)
   int keys;              // keys of the unit's last row
   int diag;              // keys of its first row (the prefix: every row sees all)
   int flags;
@@ -67,48 +72,43 @@ struct __align__(16) Segment {
 static_assert(sizeof(Segment) == 32, "Segment is 8 int32");
 enum { kPrefix = 1, kHead = 2, kWhole = 4 };
 
-struct Shared {
-  uint8_t* stages;
-  float* scratch;
-  float* ml;
-  uint64_t* full;
-  uint64_t* empty;
-  uint64_t* published;
-  Segment* segments;
-  volatile int* abort_flag;
+// The caches as tensor maps: boxes of 16 keys, both halves (8-key blocks: 8
+// keys and one half).
+struct Maps {
+  CUtensorMap k, v;
 };
 
-__device__ __forceinline__ Shared carve(uint8_t* raw) {
-  Shared s;
-  s.stages = raw;
-  s.scratch = reinterpret_cast<float*>(raw + kStages * kStage);
-  s.ml = s.scratch + kScratch / 4;
-  s.full = reinterpret_cast<uint64_t*>(s.ml + kMl / 4);
-  s.empty = s.full + kStages;
-  s.published = s.empty + kStages;
-  s.segments = reinterpret_cast<Segment*>(s.published + kSegments);
-  s.abort_flag = reinterpret_cast<volatile int*>(s.segments + kSegments);
-  return s;
-}
-
-// The producer's walk over its CTA's part [x, end) of the line.  Units follow
-// one another without a division: the next KV head, then the next sequence,
-// whose entry is loaded one sequence ahead.
+// A warp's walk over its part [x, end) of the line, one group per issue().
+// Every lane holds the same state; block ids are held 32 to a warp.  Units
+// follow one another without a division: the next KV head, then the next
+// sequence, whose entry is loaded one sequence ahead and whose first ids when
+// the current sequence's last head begins.
 struct Walk {
   int64_t end, unit0;    // end of the part; the unit's place on the line
+  int64_t next_x;        // where the unit after this one begins
   int unit, kv_head;
+  int left;              // groups of the segment not issued yet
+  int entry, sub;        // of the next group: block list entry, group in the block
+  int window;            // first entry of the ids held
+  int ids, ids_next;     // this lane's
   StepSeq cur, next;
   const int32_t* table;
+  uint32_t seg;          // segments published
+
+  __device__ __forceinline__ int load_ids(const int32_t* t, int from, int n, int lane) const {
+    return from + lane < n ? t[from + lane] : 0;
+  }
+  // entries of the block list that the unit's keys take
+  __device__ __forceinline__ int entries(int keys, int B) const { return (keys + B - 1) / B; }
 
   __device__ __forceinline__ void enter(const DevStep& ds, const ShapeInfo& s,
                                         const StepPlan& plan, const StepWork& work) {
-    if (unit < plan.header[kPlanStreamed]) {
-      next = plan.streamed[min(unit + 1, ds.num_seqs - 1)];
+    if (unit < work.streamed) {
       unit0 = (int64_t)s.H_kv * cur.cum + (int64_t)kv_head * (cur.tiles + kStepStreamUnit);
       table = ds.block_table + (int64_t)cur.seq * ds.max_blocks;
     } else {
       cur.row = 0;
-      cur.n_new = plan.header[kPlanRows];
+      cur.n_new = work.rows;
       cur.ctx = ds.prefix_len;
       cur.tiles = work.prefix_stream_tiles;
       unit0 = work.stream_own + (int64_t)kv_head * (cur.tiles + kStepStreamUnit);
@@ -116,468 +116,418 @@ struct Walk {
     }
   }
 
-  // (every lane of the warp calls it: the search tests 32 places at a time)
   __device__ __forceinline__ void start(int64_t x, const DevStep& ds, const ShapeInfo& s,
                                         const StepPlan& plan, const StepWork& work, int lane) {
     int64_t base = work.stream_own;
-    unit = plan.header[kPlanStreamed];
+    unit = work.streamed;
     int len = work.prefix_stream_tiles + kStepStreamUnit;
     if (x < work.stream_own) {
-      // the last sequence at or before x
-      const int32_t v = (int32_t)(x / s.H_kv);
-      int lo = 0, left = unit;
-      while (left > 1) {
-        const int step = (left + 31) >> 5;
-        const bool le = lane * step < left && plan.streamed[lo + lane * step].cum <= v;
+      // the last sequence at or before x: 32 places tested at a time
+      const int32_t v = (int32_t)step_div(x, s.H_kv);
+      int lo = 0, n = unit;
+      while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const bool le = lane * step < n && plan.streamed[lo + lane * step].cum <= v;
         const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));   // lane 0 always holds
         lo += k * step;
-        left = min(step, left - k * step);
+        n = min(step, n - k * step);
       }
       unit = lo;
       cur = plan.streamed[unit];
+      next = plan.streamed[min(unit + 1, ds.num_seqs - 1)];
       base = (int64_t)s.H_kv * cur.cum;
       len = cur.tiles + kStepStreamUnit;
     }
-    kv_head = (int)(x - base) / len;    // (a sequence's line fits 32 bits with its heads)
+    kv_head = (int)step_div(x - base, len);
     enter(ds, s, plan, work);
+    next_x = x;
+    left = 0;
+    seg = 0;
+    window = -1;
+    ids_next = 0;
+    if (unit < work.streamed && kv_head == s.H_kv - 1) prefetch(ds, s, work, lane);
   }
 
-  // The segment of the unit in [x, end), and on to the next unit; false when
-  // the part has no tile of it.
-  __device__ __forceinline__ bool segment(int64_t x, Segment& g, const int32_t*& ids,
-                                          const DevStep& ds, const ShapeInfo& s,
-                                          const StepPlan& plan, const StepWork& work,
-                                          int64_t& x_next) {
-    const bool prefix = unit >= plan.header[kPlanStreamed];
-    const int n = cur.tiles;
-    g.row = cur.row;
-    g.n_tok = cur.n_new;
-    g.kv_head = kv_head;
-    g.keys = cur.ctx;
-    g.diag = prefix ? cur.ctx : cur.ctx - cur.n_new + 1;
-    ids = table;
-    const int64_t from = x - unit0 - kStepStreamUnit, to = end - unit0 - kStepStreamUnit;
-    const int last = (int)(to < 0 ? 0 : to < n ? to : n);
-    g.tile = (int)(from < 0 ? 0 : from);
-    g.tiles = last - g.tile;
-    g.flags = (prefix ? kPrefix : 0) | (g.tile == 0 ? kHead : 0) |
-              (g.tile == 0 && last == n ? kWhole : 0);
-    x_next = unit0 + n + kStepStreamUnit;
-    if (x_next < end) {
-      if (++kv_head == s.H_kv) {
-        kv_head = 0;
-        ++unit;
-        cur = next;
+  __device__ __forceinline__ void prefetch(const DevStep& ds, const ShapeInfo& s,
+                                           const StepWork& work, int lane) {
+    if (unit + 1 < work.streamed)
+      ids_next = load_ids(ds.block_table + (int64_t)next.seq * ds.max_blocks, 0,
+                          entries(next.ctx, s.B), lane);
+  }
+
+  // Publishes the next segment of the part; false when there is none.
+  __device__ __forceinline__ bool advance(Segment* segments, const DevStep& ds,
+                                          const ShapeInfo& s, const StepPlan& plan,
+                                          const StepWork& work, int lane) {
+    while (next_x < end) {
+      if (next_x > unit0 + cur.tiles + kStepStreamUnit - 1) {   // on to the next unit
+        bool moved = false;
+        if (++kv_head == s.H_kv) {
+          kv_head = 0;
+          ++unit;
+          cur = next;
+          moved = true;
+        }
+        enter(ds, s, plan, work);
+        if (moved) {
+          window = -1;
+          if (unit < work.streamed) {
+            next = plan.streamed[min(unit + 1, ds.num_seqs - 1)];
+            ids = ids_next;
+            window = 0;
+          }
+        }
+        if (unit < work.streamed && kv_head == s.H_kv - 1) prefetch(ds, s, work, lane);
       }
-      enter(ds, s, plan, work);
+      const int n = cur.tiles;
+      const int64_t from = next_x - unit0 - kStepStreamUnit, to = end - unit0 - kStepStreamUnit;
+      const int first = (int)(from < 0 ? 0 : from);
+      const int last = (int)(to < 0 ? 0 : to < n ? to : n);
+      next_x = unit0 + n + kStepStreamUnit;
+      if (first >= last) continue;
+      left = last - first;
+      const bool prefix = unit >= work.streamed;
+      if (s.B >= kKeys) {
+        const int per = s.B / kKeys;
+        entry = first / per;
+        sub = first - entry * per;
+      } else {
+        entry = 2 * first;
+        sub = 0;
+      }
+      const int n_entries = entries(cur.ctx, s.B);
+      if (window < 0 || entry < window || entry >= window + 32) {
+        window = entry;
+        ids = load_ids(table, window, n_entries, lane);
+      }
+      Segment g;
+      g.row = cur.row;
+      g.n_tok = cur.n_new;
+      g.kv_head = kv_head;
+      g.group = first;
+      g.groups = left;
+      g.keys = cur.ctx;
+      g.diag = prefix ? cur.ctx : cur.ctx - cur.n_new + 1;
+      g.flags = (prefix ? kPrefix : 0) | (first == 0 ? kHead : 0) |
+                (first == 0 && last == n ? kWhole : 0);
+      segments[seg % kSegments] = g;      // (every lane the same values)
+      ++seg;
+      return true;
     }
-    return g.tiles > 0;
+    return false;
+  }
+
+  // The next block id of the list.
+  __device__ __forceinline__ int id_at(int e, const ShapeInfo& s, int lane) {
+    if (e >= window + 32 || e < window) {
+      window = e;
+      ids = load_ids(table, window, entries(cur.ctx, s.B), lane);
+    }
+    return __shfl_sync(0xffffffffu, ids, e - window);
+  }
+
+  // Loads the next group into `stage`; false when the part has ended.
+  __device__ __forceinline__ bool issue(uint8_t* stage, uint64_t* full, Segment* segments,
+                                        const Maps& maps, const DevStep& ds, const ShapeInfo& s,
+                                        const StepPlan& plan, const StepWork& work, int lane) {
+    if (left == 0 && !advance(segments, ds, s, plan, work, lane)) return false;
+    --left;
+    const int blk = id_at(entry, s, lane);
+    bool ok = (uint32_t)blk < (uint32_t)ds.num_blocks;
+    const int row = (blk * s.H_kv + kv_head) * s.B + sub * kKeys;
+    if (s.B >= kKeys) {
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(full, ok ? kStage : 0);
+        if (ok) {
+          ptx::tma_load_4d(stage, &maps.k, row >> 4, full);
+          ptx::tma_load_4d(stage + kGroup, &maps.v, row >> 4, full);
+        }
+      }
+      if (++sub * kKeys == s.B) {
+        sub = 0;
+        ++entry;
+      }
+    } else {
+      // 8-key blocks: a group is two of them, or one at the unit's end
+      const bool two = entry + 1 < entries(cur.ctx, s.B);
+      const int blk1 = two ? id_at(entry + 1, s, lane) : 0;
+      const bool ok1 = (uint32_t)blk1 < (uint32_t)ds.num_blocks;
+      const int row1 = (blk1 * s.H_kv + kv_head) * s.B;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(full, (ok ? kStage / 2 : 0) + (two && ok1 ? kStage / 2 : 0));
+        if (ok) {
+          ptx::tma_load_2d(stage, &maps.k, 0, row, full);
+          ptx::tma_load_2d(stage + kHalf, &maps.k, 64, row, full);
+          ptx::tma_load_2d(stage + kGroup, &maps.v, 0, row, full);
+          ptx::tma_load_2d(stage + kGroup + kHalf, &maps.v, 64, row, full);
+        }
+        if (two && ok1) {
+          ptx::tma_load_2d(stage + 1024, &maps.k, 0, row1, full);
+          ptx::tma_load_2d(stage + kHalf + 1024, &maps.k, 64, row1, full);
+          ptx::tma_load_2d(stage + kGroup + 1024, &maps.v, 0, row1, full);
+          ptx::tma_load_2d(stage + kGroup + kHalf + 1024, &maps.v, 64, row1, full);
+        }
+      }
+      ok = ok && ok1;
+      entry += 2;
+    }
+    if (!ok && lane == 0) atomicCAS(ds.status, 0, kDevBounds);
+    return true;
   }
 };
 
-// The caches as tensor maps: boxes of 64 keys or a block, and of 16 keys.
-struct Maps {
-  CUtensorMap k, v, k_one, v_one;
+// The queries of a unit as the B operand of S^T = K Q^T: row n of tile i is
+// packed row 8 i + n (token / g, head % g); rows past the unit's are zero.
+template <int NT>
+__device__ __forceinline__ void load_q(uint32_t (&qb)[NT][8][2], const Segment& u,
+                                       const ShapeInfo& s, const __nv_bfloat16* q, int lane) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = 8 * i + (lane >> 2), tok = r / s.g;
+    const bool live = tok < u.n_tok;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(
+                            q + ((int64_t)(u.row + tok) * s.H_q + u.kv_head * s.g +
+                                 (r - tok * s.g)) * 128) + (lane & 3);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      qb[i][kk][0] = live ? __ldg(p + kk * 8) : 0u;
+      qb[i][kk][1] = live ? __ldg(p + kk * 8 + 4) : 0u;
+    }
+  }
+}
+
+// A warp's ring.
+struct Ring {
+  uint8_t* stages;
+  uint64_t* full;
+  Segment* segments;
+  uint32_t issued, taken;
+  bool failed;
 };
 
-__global__ void __launch_bounds__(kThreads, 2)
+// Works through one segment: NT tiles of 8 packed rows.
+template <int NT>
+__device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk& walk,
+                                            const Maps& maps, const DevStep& ds,
+                                            const ShapeInfo& s, const StepPlan& plan,
+                                            const StepWork& work, const StepWorkspace& ws,
+                                            const __nv_bfloat16* q, __nv_bfloat16* o,
+                                            int64_t pipe, int lane) {
+  uint32_t qb[NT][8][2];
+  load_q<NT>(qb, it, s, q, lane);
+  const float qk_scale = s.scale * kLog2e;
+  const int c2 = (lane & 3) * 2;               // this lane's query rows: 8 i + c2, + 1
+  const int kr = lane >> 2;                    // ... and keys (or head dims): kr, kr + 8
+  int lim[NT][2];                              // keys that they see
+  float m[NT][2], l[NT][2], acc[NT][8][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      lim[i][e] = min(it.keys, it.diag + (8 * i + c2 + e) / s.g);
+      m[i][e] = -INFINITY;
+      l[i][e] = 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
+  }
+  // ldmatrix rows of this lane: K as [key][dim] tiles, V transposed
+  const int k_key = (lane & 7) + ((lane >> 3) & 1) * 8, k_d = (lane >> 4) * 8;
+  const int v_key = (lane & 7) + (lane >> 4) * 8, v_d = ((lane >> 3) & 1) * 8;
+
+  for (int j = 0; j < it.groups; ++j) {
+    const int st = ring.taken % kStages;
+    if (!ptx::mbar_wait(&ring.full[st], (ring.taken / kStages) & 1, kWaitLimit)) {
+      if (lane == 0) ptx::report_wait(ds.status, kDevTimeout, 62, (int)ring.taken);
+      ring.failed = true;
+    }
+    ring.failed = __any_sync(0xffffffffu, ring.failed);
+    if (ring.failed) return;
+    const int key0 = (it.group + j) * kKeys;
+    uint8_t* stage = ring.stages + st * kStage;
+    const uint32_t kt = ptx::smem_u32(stage), vt = kt + kGroup;
+    if (key0 + kKeys > it.keys) {
+      // rows past the unit's last key may hold anything (unwritten cache
+      // slots): zero those of V so 0 * V stays 0
+      const int from = it.keys - key0;
+      for (int e = lane; e < (kKeys - from) * 16; e += 32) {
+        const int key = from + e / 16, c = e % 16;
+        *reinterpret_cast<uint4*>(stage + kGroup + (c >> 3) * kHalf + key * 128 +
+                                  ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+    // S^T = K Q^T, the head dim in two chains of MMAs
+    float sc[NT][4], sd[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sc[i][x] = sd[i][x] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 8; kk += 2) {
+      uint32_t a[4], b[4];
+      ptx::ldsm_x4(kt + group_off(k_key, kk * 16 + k_d), a[0], a[1], a[2], a[3]);
+      ptx::ldsm_x4(kt + group_off(k_key, kk * 16 + 16 + k_d), b[0], b[1], b[2], b[3]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        ptx::mma_bf16_16816(sc[i], a, qb[i][kk][0], qb[i][kk][1]);
+        ptx::mma_bf16_16816(sd[i], b, qb[i][kk + 1][0], qb[i][kk + 1][1]);
+      }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // rows' scores of keys kr and kr + 8, masked; the row's maximum over
+        // the eight lanes that share it
+        float x = (sc[i][e] + sd[i][e]) * qk_scale, y = (sc[i][2 + e] + sd[i][2 + e]) * qk_scale;
+        x = key0 + kr < lim[i][e] ? x : -INFINITY;
+        y = key0 + kr + 8 < lim[i][e] ? y : -INFINITY;
+        float top = fmaxf(x, y);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float mn = fmaxf(m[i][e], top);
+        // a row with no visible key so far keeps max -inf: its terms are 0
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float corr = ptx::ex2(m[i][e] - base);
+        m[i][e] = mn;
+        x = ptx::ex2(x - base);
+        y = ptx::ex2(y - base);
+        l[i][e] = fmaf(l[i][e], corr, x + y);
+        sc[i][e] = x;
+        sc[i][2 + e] = y;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          acc[i][t][e] *= corr;
+          acc[i][t][2 + e] *= corr;
+        }
+      }
+      // the weights enter the value product as bf16 (its operand type): each
+      // off by at most 2^-8 of itself; their sum above stays fp32.  [key][row]
+      // pairs become the [row][key] pairs of the B operand.
+      pb[i][0] = transpose8(ptx::pack_bf16x2(sc[i][0], sc[i][1]));
+      pb[i][1] = transpose8(ptx::pack_bf16x2(sc[i][2], sc[i][3]));
+    }
+    // O^T += V^T P^T: 8 tiles of 16 head dims
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      uint32_t a[4];
+      ptx::ldsm_x4_t(vt + group_off(v_key, t * 16 + v_d), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) ptx::mma_bf16_16816(acc[i][t], a, pb[i][0], pb[i][1]);
+    }
+    ++ring.taken;
+    __syncwarp();
+    // the stage is free: the next group of the part
+    if (lane == 0) ptx::fence_proxy_async_smem();
+    if (walk.issue(stage, &ring.full[st], ring.segments, maps, ds, s, plan, work, lane))
+      ++ring.issued;
+  }
+
+  // ---- the segment's result: O itself when nothing is to be joined, the
+  // unit's rows of the workspace, or this warp's spill rows ----
+  const bool head = it.flags & kHead, pre = it.flags & kPrefix;
+  const bool direct = (it.flags & kWhole) && ds.prefix_len == 0;
+  float* part = head ? (pre ? ws.pre_o : ws.own_o) : ws.stream_o;
+  float* lse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.stream_lse;
+  const int nrg = it.n_tok * s.g;
+  auto place = [&](int r) -> int64_t {
+    const int tok = r / s.g;
+    return head ? (int64_t)(it.row + tok) * s.H_q + it.kv_head * s.g + (r - tok * s.g)
+                : pipe * kRows + r;
+  };
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    float inv[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[i][e];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      inv[e] = sum > 0.f ? 1.f / sum : 0.f;
+      const int r = 8 * i + c2 + e;
+      if (!direct && r < nrg) {
+        const int64_t to = place(r);
+        if (kr == 0) lse[to] = sum > 0.f ? m[i][e] + log2f(sum) : -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          part[to * 128 + t * 16 + kr] = acc[i][t][e] * inv[e];
+          part[to * 128 + t * 16 + kr + 8] = acc[i][t][2 + e] * inv[e];
+        }
+      }
+    }
+    if (direct) {
+      const int r = 8 * i + kr;               // after the transpose: one row, two dims
+      const int64_t to = r < nrg ? place(r) : 0;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t v = transpose8(ptx::pack_bf16x2(acc[i][t][2 * x] * inv[0],
+                                                         acc[i][t][2 * x + 1] * inv[1]));
+          if (r < nrg)
+            *reinterpret_cast<uint32_t*>(o + to * 128 + t * 16 + 8 * x + c2) = v;
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
     step_stream_kernel(const __grid_constant__ Maps maps, DevStep ds, ShapeInfo shp,
                        StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
                        __nv_bfloat16* __restrict__ o, int first) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (first) ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
-  Shared sm = carve(smem_raw);
-  volatile int& abort_flag = *sm.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = shp.g, B = shp.B, H_kv = shp.H_kv;
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int64_t ctas = min((int64_t)gridDim.x, work.stream_total);
-  if ((ptx::smem_u32(smem_raw) & 1023) || blockIdx.x >= ctas) {
-    // (the swizzled tile layout needs a 1024-byte aligned base)
-    if (threadIdx.x == 0 && blockIdx.x < ctas) atomicCAS(ds.status, 0, kDevBounds);
-    ptx::pdl_wait_previous();   // the grid's completion still covers its predecessor
-    return;
-  }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&sm.full[s], 1);
-      ptx::mbar_init(&sm.empty[s], kConsumers);
-    }
-    for (int s = 0; s < kSegments; ++s) ptx::mbar_init(&sm.published[s], 1);
-    abort_flag = 0;
-    ptx::fence_barrier_init();
-  }
-  __syncthreads();
-
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
-    Walk walk;
-    walk.end = step_cut(blockIdx.x + 1, work.stream_total, ctas);
-    int64_t x = step_cut(blockIdx.x, work.stream_total, ctas);
-    walk.start(x, ds, shp, plan, work, lane);
+  const int64_t pipes = step_pipes(ws, work);
+  // neighbouring parts on different SMs
+  const int64_t pipe = (int64_t)warp * gridDim.x + blockIdx.x;
+  if (ptx::smem_u32(smem_raw) & 1023) {
+    // the swizzled layout needs a 1024-byte aligned base
+    if (threadIdx.x == 0) atomicCAS(ds.status, 0, kDevBounds);
+  } else if (pipe < pipes) {
+    Ring ring;
+    ring.stages = smem_raw + warp * kStages * kStage;
+    ring.segments =
+        reinterpret_cast<Segment*>(smem_raw + kWarps * kStages * kStage) + warp * kSegments;
+    ring.full = reinterpret_cast<uint64_t*>(smem_raw + kWarps * (kStages * kStage +
+                                                                 kSegments * 32)) +
+                warp * kStages;
+    ring.issued = ring.taken = 0;
+    ring.failed = false;
     if (lane == 0) {
-      const int box_rows = B < kKeys ? B : kKeys;
-      Segment it, nx;
-      const int32_t *ids, *nx_ids;
-      auto next = [&](Segment& g, const int32_t*& p) {
-        while (x < walk.end) {
-          int64_t to;
-          const bool some = walk.segment(x, g, p, ds, shp, plan, work, to);
-          x = to;
-          if (some) return;
-        }
-        g.tiles = 0;
-      };
-      // block ids of a tile's boxes (none past the unit's last key), loaded
-      // one tile ahead so that their latency hides behind the ring's waits
-      int32_t blk[kKeys / 8];
-      auto look = [&](const Segment& g, const int32_t* p, int j) {
-        const int k0 = (g.tile + j) * kKeys;
-#pragma unroll
-        for (int i = 0; i < kKeys / 8; ++i)
-          if (i * box_rows < kKeys && k0 + i * box_rows < g.keys)
-            blk[i] = p[(k0 + i * box_rows) / B];
-      };
-      uint32_t idx = 0, seg = 0;
-      bool stop = false;
-      next(it, ids);
-      if (it.tiles) look(it, ids, 0);
-      for (;; ++seg) {
-        // (a slot of the segment ring is free again once a tile three before
-        // the next one was released: kSegments > kStages)
-        sm.segments[seg % kSegments] = it;
-        ptx::mbar_arrive(&sm.published[seg % kSegments]);
-        if (it.tiles == 0 || stop) break;
-        next(nx, nx_ids);
-        for (int j = 0; j < it.tiles; ++j, ++idx) {
-          const int s = idx % kStages;
-          if (abort_flag ||
-              (idx >= (uint32_t)kStages &&
-               !ptx::mbar_wait(&sm.empty[s], ((idx / kStages) - 1) & 1, kWaitLimit))) {
-            ptx::report_wait(ds.status, kDevTimeout, 61, (int)idx);
-            abort_flag = 1;
-            stop = true;
-            break;
-          }
-          const int k0 = (it.tile + j) * kKeys;
-          uint8_t* kdst = sm.stages + s * kStage;
-          uint8_t* vdst = kdst + kTile;
-          // boxes of box_rows keys; of a box that the unit's keys end in, only
-          // the 16-key groups that hold some (whole boxes would read 32 keys
-          // too many per unit on average: a tenth of the traffic at 256 keys)
-          uint32_t keys = 0;
-#pragma unroll
-          for (int i = 0; i < kKeys / 8; ++i) {
-            const int left = it.keys - k0 - i * box_rows;
-            if (i * box_rows < kKeys && left > 0) {
-              if (blk[i] < 0 || blk[i] >= ds.num_blocks)
-                atomicCAS(ds.status, 0, kDevBounds);
-              else
-                keys += left >= box_rows ? box_rows : min(box_rows, (left + 15) & ~15);
-            }
-          }
-          ptx::mbar_arrive_expect_tx(&sm.full[s], keys * 512);
-#pragma unroll
-          for (int i = 0; i < kKeys / 8; ++i) {
-            const int left = it.keys - k0 - i * box_rows;
-            if (i * box_rows < kKeys && left > 0 && blk[i] >= 0 && blk[i] < ds.num_blocks) {
-              const int row = (blk[i] * H_kv + it.kv_head) * B + ((k0 + i * box_rows) % B);
-              if (box_rows < 16) {
-                // 8-key blocks: half a group per copy
-                const int off = (i >> 1) * kGroup + (i & 1) * 8 * 128;
-                ptx::tma_load_2d(kdst + off, &maps.k, 0, row, &sm.full[s]);
-                ptx::tma_load_2d(kdst + off + kGroup / 2, &maps.k, 64, row, &sm.full[s]);
-                ptx::tma_load_2d(vdst + off, &maps.v, 0, row, &sm.full[s]);
-                ptx::tma_load_2d(vdst + off + kGroup / 2, &maps.v, 64, row, &sm.full[s]);
-              } else if (left > box_rows - 16) {
-                ptx::tma_load_4d(kdst + i * box_rows * 256, &maps.k, row >> 4, &sm.full[s]);
-                ptx::tma_load_4d(vdst + i * box_rows * 256, &maps.v, row >> 4, &sm.full[s]);
-              } else {
-                for (int f = 0; f < left; f += 16) {
-                  const int at = (i * box_rows + f) * 256;
-                  ptx::tma_load_4d(kdst + at, &maps.k_one, (row + f) >> 4, &sm.full[s]);
-                  ptx::tma_load_4d(vdst + at, &maps.v_one, (row + f) >> 4, &sm.full[s]);
-                }
-              }
-            }
-          }
-          if (j + 1 < it.tiles) look(it, ids, j + 1);
-          else if (nx.tiles) look(nx, nx_ids, 0);
-        }
-        if (stop) break;
-        it = nx;
-        ids = nx_ids;
-      }
-      // let every load this CTA issued land before the CTA can exit
-      for (uint32_t t = idx > (uint32_t)kStages ? idx - kStages : 0; t < idx; ++t)
-        ptx::mbar_wait(&sm.full[t % kStages], (t / kStages) & 1, kWaitLimit);
+      for (int i = 0; i < kStages; ++i) ptx::mbar_init(&ring.full[i], 1);
+      ptx::fence_barrier_init();
     }
-    ptx::pdl_wait_previous();
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
-  const float qk_scale = shp.scale * kLog2e;
-  const int r0 = lane >> 2, r1 = r0 + 8;      // fragment rows: token r / g, head r % g
-  const int t0 = r0 / g, t1 = r1 / g;
-  const int cq = (lane & 3) * 2;              // fragment column pair
-  const uint32_t stages_u32 = ptx::smem_u32(sm.stages);
-  uint32_t tile_base = 0;
-
-  // the unit's query rows as m16n8k16 A fragments; rows past its end are zero
-  auto load_q = [&](const Segment& u, uint32_t(&dst)[8][4]) {
-    const bool live0 = t0 < u.n_tok, live1 = t1 < u.n_tok;
-    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(
-        q + ((int64_t)(u.row + t0) * shp.H_q + u.kv_head * g + r0 % g) * 128);
-    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(
-        q + ((int64_t)(u.row + t1) * shp.H_q + u.kv_head * g + r1 % g) * 128);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const int c = (kk * 16 + cq) >> 1;
-      dst[kk][0] = live0 ? __ldg(q0 + c) : 0u;
-      dst[kk][1] = live1 ? __ldg(q1 + c) : 0u;
-      dst[kk][2] = live0 ? __ldg(q0 + c + 4) : 0u;
-      dst[kk][3] = live1 ? __ldg(q1 + c + 4) : 0u;
-    }
-  };
-  uint32_t qa[8][4];
-  // the next published segment; one without tiles ends the walk
-  uint32_t seg = 0;
-  auto take = [&](Segment& u) -> bool {
-    if (!ptx::mbar_wait(&sm.published[seg % kSegments], (seg / kSegments) & 1, kWaitLimit)) {
-      if (lane == 0) {
-        ptx::report_wait(ds.status, kDevTimeout, 63, (int)seg);
-        abort_flag = 1;
-      }
-      u.tiles = 0;
-    } else {
-      u = sm.segments[seg % kSegments];
-    }
-    ++seg;
-    return __all_sync(0xffffffffu, u.tiles > 0);
-  };
-  Segment it;
-  bool more = take(it);
-  if (ptx::named_bar_or(1, kConsumers * 32, abort_flag != 0)) more = false;
-  if (more) load_q(it, qa);
-
-  while (more) {
-    const int nt = it.tiles;
-    const int nrg = it.n_tok * g;
-    const int lim0 = min(it.keys, it.diag + t0), lim1 = min(it.keys, it.diag + t1);
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float acc_o[16][4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc_o[i][0] = acc_o[i][1] = acc_o[i][2] = acc_o[i][3] = 0.f;
-
-    // every warp takes 16 keys (rows 16*warp .. 16*warp+15) of every tile, so
-    // each warp consumes the stages strictly in order
-    const int wk = warp * 16;
-    for (int j = 0; j < nt && !abort_flag; ++j) {
-      const uint32_t idx = tile_base + j;
-      const int s = idx % kStages;
-      if (!ptx::mbar_wait(&sm.full[s], (idx / kStages) & 1, kWaitLimit)) {
-        // give up on this unit; the merge barriers below are still met by
-        // every consumer warp, then all of them leave together
-        if (lane == 0) {
-          ptx::report_wait(ds.status, kDevTimeout, 62, (int)idx);
-          abort_flag = 1;
-        }
-        __syncwarp();
-        break;
-      }
-      const int k0 = (it.tile + j) * kKeys;
-      const int valid = min(kKeys, it.keys - k0) - wk;   // valid keys of this warp's 16
-      const uint32_t kt = stages_u32 + s * kStage;
-      const uint32_t vt = kt + kTile;
-      if (valid < 16) {
-        // rows past the unit's last key may hold anything (unwritten cache
-        // slots, stale tiles): zero this warp's such V rows so 0 * V stays 0
-        uint8_t* vrow = sm.stages + s * kStage + kTile + warp * kGroup;
-        const int from = valid < 0 ? 0 : valid;
-        for (int e = lane; e < (16 - from) * 16; e += 32) {
-          const int key = from + e / 16, c = e % 16;
-          *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kGroup / 2) + key * 128 +
-                                    ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-      }
-      if (valid > 0) {
-        // S = Q K^T over this warp's 16 keys: 2 n-tiles of 8 keys
-        float sc[2][4];
-        sc[0][0] = sc[0][1] = sc[0][2] = sc[0][3] = 0.f;
-        sc[1][0] = sc[1][1] = sc[1][2] = sc[1][3] = 0.f;
-        const int mi = lane >> 3;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const int key = wk + (mi >> 1) * 8 + (lane & 7);
-          const int d = kk * 16 + (mi & 1) * 8;
-          uint32_t b0, b1, b2, b3;
-          ptx::ldsm_x4(kt + tile_off(key, d), b0, b1, b2, b3);
-          ptx::mma_bf16_16816(sc[0], qa[kk], b0, b1);
-          ptx::mma_bf16_16816(sc[1], qa[kk], b2, b3);
-        }
-        // scale, mask keys past each row's limit, online softmax (rows r0 and r1)
-        const int valid0 = min(kKeys, lim0 - k0) - wk, valid1 = min(kKeys, lim1 - k0) - wk;
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = n * 8 + cq;
-          sc[n][0] = key < valid0 ? sc[n][0] * qk_scale : -INFINITY;
-          sc[n][1] = key + 1 < valid0 ? sc[n][1] * qk_scale : -INFINITY;
-          sc[n][2] = key < valid1 ? sc[n][2] * qk_scale : -INFINITY;
-          sc[n][3] = key + 1 < valid1 ? sc[n][3] * qk_scale : -INFINITY;
-          mx0 = fmaxf(mx0, fmaxf(sc[n][0], sc[n][1]));
-          mx1 = fmaxf(mx1, fmaxf(sc[n][2], sc[n][3]));
-        }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-        // a row with no visible key so far keeps max -inf: its terms are 0
-        const float b0 = mn0 == -INFINITY ? 0.f : mn0, b1 = mn1 == -INFINITY ? 0.f : mn1;
-        const float c0 = ptx::ex2(m0 - b0), c1 = ptx::ex2(m1 - b1);
-        m0 = mn0;
-        m1 = mn1;
-        const float p00 = ptx::ex2(sc[0][0] - b0), p01 = ptx::ex2(sc[0][1] - b0);
-        const float p02 = ptx::ex2(sc[0][2] - b1), p03 = ptx::ex2(sc[0][3] - b1);
-        const float p10 = ptx::ex2(sc[1][0] - b0), p11 = ptx::ex2(sc[1][1] - b0);
-        const float p12 = ptx::ex2(sc[1][2] - b1), p13 = ptx::ex2(sc[1][3] - b1);
-        l0 = l0 * c0 + (p00 + p01 + p10 + p11);
-        l1 = l1 * c1 + (p02 + p03 + p12 + p13);
-        // the weights enter the value product as bf16 (its operand type): each
-        // off by at most 2^-8 of itself; their sum above stays fp32
-        uint32_t pa[4];
-        pa[0] = ptx::pack_bf16x2(p00, p01);
-        pa[1] = ptx::pack_bf16x2(p02, p03);
-        pa[2] = ptx::pack_bf16x2(p10, p11);
-        pa[3] = ptx::pack_bf16x2(p12, p13);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          acc_o[i][0] *= c0;
-          acc_o[i][1] *= c0;
-          acc_o[i][2] *= c1;
-          acc_o[i][3] *= c1;
-        }
-        // O += P V over the 16 keys: 16 n-tiles of 8 head-dim columns
-#pragma unroll
-        for (int dp2 = 0; dp2 < 8; ++dp2) {
-          const int key = wk + (mi & 1) * 8 + (lane & 7);
-          const int d = dp2 * 16 + (mi >> 1) * 8;
-          uint32_t v0, v1, v2, v3;
-          ptx::ldsm_x4_t(vt + tile_off(key, d), v0, v1, v2, v3);
-          ptx::mma_bf16_16816(acc_o[2 * dp2], pa, v0, v1);
-          ptx::mma_bf16_16816(acc_o[2 * dp2 + 1], pa, v2, v3);
-        }
-      }
+    __syncwarp();
+    Walk walk;
+    walk.end = step_cut(pipe + 1, work.stream_total, pipes);
+    walk.start(step_cut(pipe, work.stream_total, pipes), ds, shp, plan, work, lane);
+    for (int i = 0; i < kStages; ++i)
+      if (walk.issue(ring.stages + i * kStage, &ring.full[i], ring.segments, maps, ds, shp, plan,
+                     work, lane))
+        ++ring.issued;
+    __syncwarp();
+    for (uint32_t n = 0; n < walk.seg && !ring.failed; ++n) {
+      const Segment it = ring.segments[n % kSegments];
+      if (it.n_tok * shp.g <= 8)
+        run_segment<1>(it, ring, walk, maps, ds, shp, plan, work, ws, q, o, pipe, lane);
+      else
+        run_segment<2>(it, ring, walk, maps, ds, shp, plan, work, ws, q, o, pipe, lane);
       __syncwarp();
-      if (lane == 0) {
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&sm.empty[s]);
-      }
     }
-    tile_base += nt;
-
-    // the next segment and its queries, loaded while this one is merged
-    const Segment cur = it;
-    more = !abort_flag && take(it);
-    uint32_t qn[8][4];
-    if (more) load_q(it, qn);
-
-    // ---- merge the four warps' states and write the segment's result -------
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if ((lane & 3) == 0) {
-      sm.ml[(warp * kRows + r0) * 2 + 0] = m0;
-      sm.ml[(warp * kRows + r0) * 2 + 1] = l0;
-      sm.ml[(warp * kRows + r1) * 2 + 0] = m1;
-      sm.ml[(warp * kRows + r1) * 2 + 1] = l1;
-    }
-    ptx::named_bar_sync(1, kConsumers * 32);
-    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) {
-      M0 = fmaxf(M0, sm.ml[(w * kRows + r0) * 2]);
-      M1 = fmaxf(M1, sm.ml[(w * kRows + r1) * 2]);
-    }
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) {
-      const float mw0 = sm.ml[(w * kRows + r0) * 2], mw1 = sm.ml[(w * kRows + r1) * 2];
-      if (mw0 != -INFINITY) L0 += ptx::ex2(mw0 - M0) * sm.ml[(w * kRows + r0) * 2 + 1];
-      if (mw1 != -INFINITY) L1 += ptx::ex2(mw1 - M1) * sm.ml[(w * kRows + r1) * 2 + 1];
-    }
-    const float f0 = (m0 == -INFINITY || L0 == 0.f) ? 0.f : ptx::ex2(m0 - M0) / L0;
-    const float f1 = (m1 == -INFINITY || L1 == 0.f) ? 0.f : ptx::ex2(m1 - M1) / L1;
-    // where row r of the segment goes: O itself when nothing is to be joined,
-    // the unit's rows of the workspace, or this CTA's spill rows
-    const bool head = cur.flags & kHead, pre = cur.flags & kPrefix;
-    const bool direct = (cur.flags & kWhole) && ds.prefix_len == 0;
-    float* part = head ? (pre ? ws.pre_o : ws.own_o) : ws.stream_o;
-    float* lse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.stream_lse;
-    auto place = [&](int r) -> int64_t {
-      return head ? (int64_t)(cur.row + r / g) * shp.H_q + cur.kv_head * g + r % g
-                  : (int64_t)blockIdx.x * kRows + r;
-    };
-    const int t = threadIdx.x;   // 0..127
-    float* scr = sm.scratch + warp * kRows * 64;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      // each warp stores its rescaled O, 64 columns (8-column groups permuted
-      // by the row, for the banks); then all four are summed per element
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int a = hf * 8 + i;
-        if (r0 < nrg)
-          *reinterpret_cast<float2*>(scr + r0 * 64 + ((i ^ (r0 & 7)) << 3) + cq) =
-              make_float2(acc_o[a][0] * f0, acc_o[a][1] * f0);
-        if (r1 < nrg)
-          *reinterpret_cast<float2*>(scr + r1 * 64 + ((i ^ (r1 & 7)) << 3) + cq) =
-              make_float2(acc_o[a][2] * f1, acc_o[a][3] * f1);
-      }
-      ptx::named_bar_sync(1, kConsumers * 32);
-      for (int e = t; e < nrg * 16; e += kConsumers * 32) {
-        const int r = e >> 4, c4 = (e & 15) * 4;
-        const int at = r * 64 + (((c4 >> 3) ^ (r & 7)) << 3) + (c4 & 7);
-        float4 a = *reinterpret_cast<const float4*>(sm.scratch + at);
-#pragma unroll
-        for (int w = 1; w < kConsumers; ++w) {
-          const float4 b = *reinterpret_cast<const float4*>(sm.scratch + w * kRows * 64 + at);
-          a.x += b.x;
-          a.y += b.y;
-          a.z += b.z;
-          a.w += b.w;
-        }
-        const int64_t to = place(r) * 128 + hf * 64 + c4;
-        if (direct) {
-          uint2 packed;
-          packed.x = ptx::pack_bf16x2(a.x, a.y);
-          packed.y = ptx::pack_bf16x2(a.z, a.w);
-          *reinterpret_cast<uint2*>(o + to) = packed;
-        } else {
-          *reinterpret_cast<float4*>(part + to) = a;
-        }
-      }
-      if (hf == 0) ptx::named_bar_sync(1, kConsumers * 32);
-    }
-    if (!direct && warp == 0 && (lane & 3) == 0) {
-      if (r0 < nrg) lse[place(r0)] = L0 > 0.f ? M0 + log2f(L0) : -INFINITY;
-      if (r1 < nrg) lse[place(r1)] = L1 > 0.f ? M1 + log2f(L1) : -INFINITY;
-    }
-    // all consumer warps leave together if anyone gave up
-    if (ptx::named_bar_or(1, kConsumers * 32, abort_flag != 0)) break;
-    if (more) {
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) qa[kk][x] = qn[kk][x];
-    }
+    // after a timeout: copies in flight must land before the CTA exits
+    for (; ring.failed && ring.taken < ring.issued; ++ring.taken)
+      ptx::mbar_wait(&ring.full[ring.taken % kStages], (ring.taken / kStages) & 1, kWaitLimit);
   }
-  ptx::pdl_wait_previous();
+  ptx::pdl_wait_previous();   // the grid's completion covers its predecessor
 }
 
 // ---------------------------------------------------------------------------
@@ -586,9 +536,25 @@ __global__ void __launch_bounds__(kThreads, 2)
 // O = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M) over the row's partial
 // outputs: its own part and the prefix's, each with the spills of the CTAs
 // whose cuts fall inside its unit.  The cuts are a formula; a block works out
-// those of its row and KV heads once, one thread each, and its warps then
-// join the heads: lane i weighs source i, all lanes add four columns of each.
-// Bound by the partials' traffic (from L2, they were just written).
+// those of its row and KV heads once, one thread each, while the main sources
+// of its heads are on their way.  Bound by latency, and by the partials'
+// traffic (from L2, they were just written).
+struct Join {
+  float M, L;
+  float4 acc;
+  // (a source without a visible key has log-sum-exp -inf and weight 0)
+  __device__ __forceinline__ void add(float lse, float4 v) {
+    if (lse == -INFINITY) return;
+    const float m = fmaxf(M, lse);
+    const float a = M == -INFINITY ? 0.f : exp2f(M - m), b = exp2f(lse - m);
+    M = m;
+    L = L * a + b;
+    acc.x = acc.x * a + v.x * b;
+    acc.y = acc.y * a + v.y * b;
+    acc.z = acc.z * a + v.z * b;
+    acc.w = acc.w * a + v.w * b;
+  }
+};
 constexpr int kJoinWarps = 4;
 constexpr int kJoinHeads = 8;     // query heads of a block
 
@@ -631,13 +597,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = shp.g, H_kv = shp.H_kv, tpt = step_tile_tokens(g);
   const int T = plan.header[kPlanRows];
-  const int s_ctas = (int)min((int64_t)ws.stream_grid, work.stream_total);
+  const int s_ctas = (int)step_pipes(ws, work);
   const int t_ctas = (int)min((int64_t)ws.tile_grid, work.tile_total);
   const bool pre = ds.prefix_len > 0;
   const bool pre_streamed = work.prefix_stream_tiles > 0;
   const int h0 = blockIdx.x * kJoinHeads, h1 = min(h0 + kJoinHeads, shp.H_q);
   const int kv0 = h0 / g, n_kv = (h1 - 1) / g - kv0 + 1;
   for (int t = blockIdx.y; t < T; t += gridDim.y) {
+    // the two main sources of the warp's heads, requested before anything
+    // that depends on the row's place
+    constexpr int kPer = kJoinHeads / kJoinWarps;
+    float own_l[kPer], pre_l[kPer];
+    float4 own_v[kPer], pre_v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int h = h0 + warp + i * kJoinWarps;
+      if (h < h1) {
+        const int64_t w = (int64_t)t * shp.H_q + h;
+        own_l[i] = ws.own_lse[w];
+        own_v[i] = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane];
+        if (pre) {
+          pre_l[i] = ws.pre_lse[w];
+          pre_v[i] = reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane];
+        }
+      }
+    }
     const StepRow r = plan.rows[t];
     int own_row = r.token * g;          // row of the sequence's first head in a spill
     const int pair = r.token / (2 * tpt), in_pair = r.token - pair * 2 * tpt;
@@ -680,71 +664,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       spills[threadIdx.x] = s;
     }
     __syncthreads();
-    for (int h = h0 + warp; h < h1; h += kJoinWarps) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int h = h0 + warp + i * kJoinWarps;
+      if (h >= h1) continue;
       const int64_t w = (int64_t)t * shp.H_q + h;
       const int kvh = h / g, hh = h - kvh * g;
       const Spills a = spills[2 * (kvh - kv0)], p = spills[2 * (kvh - kv0) + 1];
       if (!pre && !a.cut) continue;      // the unit was whole: its kernel wrote O
-      // sources: the unit's own rows, the prefix's, and the spills of both
-      const int base = pre ? 2 : 1, n = base + a.n + p.n;
-      float M = -INFINITY, L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s0 = 0; s0 < n; s0 += 32) {
-        const int i = s0 + lane;
-        const float* src = ws.own_o + w * 128;
-        const float* lse = ws.own_lse + w;
-        if (i == 1 && pre) {
-          src = ws.pre_o + w * 128;
-          lse = ws.pre_lse + w;
-        } else if (i >= base) {
-          const bool mine = i < base + a.n;
+      Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      j.add(own_l[i], own_v[i]);
+      if (pre) j.add(pre_l[i], pre_v[i]);
+      // then the spills, four in flight at a time
+      const int n = a.n + p.n;
+      const int pre_row = pre_streamed ? t * g
+                          : ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g;
+      for (int s0 = 0; s0 < n; s0 += 4) {
+        float l[4];
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = min(s0 + u, n - 1);
+          const bool mine = k < a.n;
           const bool streamed = mine ? r.unit >= 0 : pre_streamed;
-          const int c = mine ? a.first + i - base : p.first + i - base - a.n;
-          int at = hh;
-          if (mine) at += own_row;
-          else if (streamed) at += t * g;
-          else at += ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g;
-          const int64_t row = streamed ? (int64_t)c * kStepPackedRows + at
-                                       : (int64_t)c * 2 * kStepTileRows + at;
-          src = (streamed ? ws.stream_o : ws.tile_o) + row * 128;
-          lse = (streamed ? ws.stream_lse : ws.tile_lse) + row;
+          const int c = mine ? a.first + k : p.first + k - a.n;
+          const int64_t row = (int64_t)c * (streamed ? kStepPackedRows : 2 * kStepTileRows) +
+                              (mine ? own_row : pre_row) + hh;
+          l[u] = (streamed ? ws.stream_lse : ws.tile_lse)[row];
+          v[u] = reinterpret_cast<const float4*>((streamed ? ws.stream_o : ws.tile_o) +
+                                                 row * 128)[lane];
         }
-        const float l = i < n ? *lse : -INFINITY;
-        float m = l;
 #pragma unroll
-        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        m = fmaxf(m, M);
-        // (a source without a visible key has log-sum-exp -inf and weight 0)
-        const float wt = l == -INFINITY ? 0.f : exp2f(l - m);
-        const float keep = M == -INFINITY ? 0.f : exp2f(M - m);
-        float sum = wt;
-#pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        M = m;
-        L = L * keep + sum;
-        acc.x *= keep;
-        acc.y *= keep;
-        acc.z *= keep;
-        acc.w *= keep;
-        const int count = min(32, n - s0);
-#pragma unroll 8
-        for (int k = 0; k < count; ++k) {
-          const float* from = reinterpret_cast<const float*>(
-              __shfl_sync(0xffffffffu, (unsigned long long)src, k));
-          const float f = __shfl_sync(0xffffffffu, wt, k);
-          const float4 v = reinterpret_cast<const float4*>(from)[lane];
-          if (f != 0.f) {   // (an empty source's rows hold no sum: 0 x NaN is NaN)
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
-          }
-        }
+        for (int u = 0; u < 4; ++u)
+          if (s0 + u < n) j.add(l[u], v[u]);
       }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
       uint2 out;
-      out.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
-      out.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
+      out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
+      out.y = ptx::pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
       reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
     }
     __syncthreads();   // the next row's spills replace these
@@ -768,7 +725,7 @@ size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* bas
   };
   const int64_t rows = (int64_t)max_tokens * s.H_q;
   StepWorkspace v;
-  v.stream_grid = 2 * sms;
+  v.stream_grid = kStepPipes * sms;
   v.tile_grid = sms;
   v.own_o = take(rows * 128);
   v.pre_o = take(rows * 128);
@@ -786,19 +743,14 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
                                const void* q, const void* k_cache, const void* v_cache, void* o,
                                bool first, cudaStream_t st) {
   const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
-  const int box_rows = s.B < kKeys ? s.B : kKeys;
   Maps maps;
   cudaError_t e;
-  if (box_rows < 16) {
-    e = make_cache_tmap(&maps.k, k_cache, rows, s.D, box_rows);
-    if (e == cudaSuccess) e = make_cache_tmap(&maps.v, v_cache, rows, s.D, box_rows);
-    maps.k_one = maps.k;
-    maps.v_one = maps.v;
+  if (s.B < kKeys) {
+    e = make_cache_tmap(&maps.k, k_cache, rows, s.D, s.B);
+    if (e == cudaSuccess) e = make_cache_tmap(&maps.v, v_cache, rows, s.D, s.B);
   } else {
-    e = make_group_tmap(&maps.k, k_cache, rows, box_rows / 16);
-    if (e == cudaSuccess) e = make_group_tmap(&maps.v, v_cache, rows, box_rows / 16);
-    if (e == cudaSuccess) e = make_group_tmap(&maps.k_one, k_cache, rows, 1);
-    if (e == cudaSuccess) e = make_group_tmap(&maps.v_one, v_cache, rows, 1);
+    e = make_group_tmap(&maps.k, k_cache, rows, 1);
+    if (e == cudaSuccess) e = make_group_tmap(&maps.v, v_cache, rows, 1);
   }
   if (e != cudaSuccess) return e;
   // the shared-memory limit is raised once per device
@@ -817,7 +769,7 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
     attr_done.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)w.stream_grid);
+  cfg.gridDim = dim3((unsigned)(w.stream_grid / kStepPipes));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
