@@ -531,121 +531,123 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The join: one warp per (row, query head), four columns per lane.
+// The join: W warps per (row, query head), four columns per lane.
 // ---------------------------------------------------------------------------
 // O = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M) over the row's partial
 // outputs: its own part and the prefix's, each with the spills of the CTAs
-// whose cuts fall inside its unit.  The cuts are a formula; a block works out
-// those of its row and KV heads once, one thread each, while the main sources
-// of its heads are on their way.  Bound by latency, and by the partials'
-// traffic (from L2, they were just written).
+// (or pipelines) whose cuts fall inside its unit.  Which those are is a
+// formula: cut c is at floor(c total / G), so the first cut at or behind p is
+// ceil(p G / total).  One thread per KV head and part works them out while the
+// main sources are on their way.  A row has a handful of sources and one warp
+// joins them; a step of few rows over a long prefix has a hundred (every
+// pipeline streamed a piece), and eight warps share them.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinWideRows = 32;   // steps of at most this many rows: W = 8
+
+// Spills of a unit that a row joins: of CTAs [first, first + n).
+struct Spills {
+  int first, n;
+  int cut;        // the unit was cut between its tiles
+};
+
+__device__ __forceinline__ int first_cut(int64_t p, int64_t total, int ctas) {
+  return (int)step_div(p * ctas + total - 1, total);
+}
+
+// Partial outputs of one part (own or prefix): source k's row.
+struct Part {
+  const float *o, *lse;
+  int row, stride;
+};
+
 struct Join {
   float M, L;
   float4 acc;
-  // (a source without a visible key has log-sum-exp -inf and weight 0)
-  __device__ __forceinline__ void add(float lse, float4 v) {
-    if (lse == -INFINITY) return;
-    const float m = fmaxf(M, lse);
-    const float a = M == -INFINITY ? 0.f : exp2f(M - m), b = exp2f(lse - m);
+  // N more sources (missing ones and those without a visible key have
+  // log-sum-exp -inf)
+  template <int N>
+  __device__ __forceinline__ void add(const float (&l)[N], const float4 (&v)[N]) {
+    float m = M;
+#pragma unroll
+    for (int u = 0; u < N; ++u) m = fmaxf(m, l[u]);
+    const float base = m == -INFINITY ? 0.f : m;
+    const float keep = ptx::ex2(M - base);
     M = m;
-    L = L * a + b;
-    acc.x = acc.x * a + v.x * b;
-    acc.y = acc.y * a + v.y * b;
-    acc.z = acc.z * a + v.z * b;
-    acc.w = acc.w * a + v.w * b;
+    L *= keep;
+    acc.x *= keep;
+    acc.y *= keep;
+    acc.z *= keep;
+    acc.w *= keep;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const float w = ptx::ex2(l[u] - base);
+      L += w;
+      acc.x = fmaf(w, v[u].x, acc.x);
+      acc.y = fmaf(w, v[u].y, acc.y);
+      acc.z = fmaf(w, v[u].z, acc.z);
+      acc.w = fmaf(w, v[u].w, acc.w);
+    }
   }
 };
-constexpr int kJoinWarps = 4;
-constexpr int kJoinHeads = 8;     // query heads of a block
 
-// Spills of a unit that a row joins: CTAs [first, first + n).
-struct Spills {
-  int first, n;
-  bool cut;       // the unit was cut between its tiles
-};
-
-// For a unit at `begin` of a line, of a fixed length `unit` and `tiles` key
-// tiles, `row_tiles` of them seen by the row (a unit's two query tiles may see
-// different numbers).
-__device__ __forceinline__ Spills spills_of(int64_t begin, int unit, int tiles, int row_tiles,
-                                            int64_t total, int ctas) {
-  Spills s = {0, 0, false};
-  // the first cut behind the unit's first tile, from an estimate that is off
-  // by one at most
-  int c = (int)((float)begin * (float)ctas / (float)total) - 1;
-  c = c < 0 ? 0 : c;
-  while (c < ctas && step_cut(c, total, ctas) <= begin + unit) ++c;
-  s.first = c;
-  // (a CTA's part is at least one long: tiles bounds the cuts)
-  for (; c < ctas; ++c) {
-    const int64_t tile = step_cut(c, total, ctas) - begin - unit;   // first tile behind it
-    if (tile >= tiles) break;
-    s.cut = true;
-    if (tile < row_tiles) ++s.n;
-  }
-  return s;
-}
-
+template <int W>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     step_combine_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
                         __nv_bfloat16* __restrict__ o) {
-  __shared__ Spills spills[2 * kJoinHeads];     // [KV head of the block][own, prefix]
+  constexpr int kHeads = kJoinWarps / W;      // query heads of a block
+  __shared__ Spills spills[2 * kHeads];       // [KV head of the block][own, prefix]
+  __shared__ float4 wide_acc[W > 1 ? kJoinWarps * 32 : 1];
+  __shared__ float wide_ml[W > 1 ? kJoinWarps * 2 : 1];
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = shp.g, tpt = step_tile_tokens(g);
+  const bool pre = ds.prefix_len > 0;
+  const int h0 = blockIdx.x * kHeads, h = h0 + warp / W, wi = warp % W;
+  const bool live = h < shp.H_q;
+  const int kv0 = h0 / g, kvh = h / g;
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = shp.g, H_kv = shp.H_kv, tpt = step_tile_tokens(g);
-  const int T = plan.header[kPlanRows];
   const int s_ctas = (int)step_pipes(ws, work);
   const int t_ctas = (int)min((int64_t)ws.tile_grid, work.tile_total);
-  const bool pre = ds.prefix_len > 0;
   const bool pre_streamed = work.prefix_stream_tiles > 0;
-  const int h0 = blockIdx.x * kJoinHeads, h1 = min(h0 + kJoinHeads, shp.H_q);
-  const int kv0 = h0 / g, n_kv = (h1 - 1) / g - kv0 + 1;
-  for (int t = blockIdx.y; t < T; t += gridDim.y) {
-    // the two main sources of the warp's heads, requested before anything
-    // that depends on the row's place
-    constexpr int kPer = kJoinHeads / kJoinWarps;
-    float own_l[kPer], pre_l[kPer];
-    float4 own_v[kPer], pre_v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int h = h0 + warp + i * kJoinWarps;
-      if (h < h1) {
-        const int64_t w = (int64_t)t * shp.H_q + h;
-        own_l[i] = ws.own_lse[w];
-        own_v[i] = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane];
-        if (pre) {
-          pre_l[i] = ws.pre_lse[w];
-          pre_v[i] = reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane];
-        }
+  for (int t = blockIdx.y; t < work.rows; t += gridDim.y) {
+    const int64_t w = (int64_t)t * shp.H_q + h;
+    // the two main sources, requested before anything that depends on the
+    // row's place
+    float l2[2] = {-INFINITY, -INFINITY};
+    float4 v2[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (live && wi == 0) {
+      l2[0] = ws.own_lse[w];
+      v2[0] = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane];
+      if (pre) {
+        l2[1] = ws.pre_lse[w];
+        v2[1] = reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane];
       }
     }
     const StepRow r = plan.rows[t];
-    int own_row = r.token * g;          // row of the sequence's first head in a spill
     const int pair = r.token / (2 * tpt), in_pair = r.token - pair * 2 * tpt;
-    if (r.unit < 0)
-      own_row = in_pair < tpt ? in_pair * g : kStepTileRows + (in_pair - tpt) * g;
-    if (threadIdx.x < 2 * n_kv) {
-      const int kvh = kv0 + (threadIdx.x >> 1);
-      int64_t begin, total = work.stream_total;
-      int unit = kStepStreamUnit, tiles, seen_tiles, ctas = s_ctas;
-      if (threadIdx.x & 1) {
+    if (threadIdx.x < 2 * kHeads) {
+      const int kv = kv0 + (threadIdx.x >> 1);
+      int64_t begin = 0, total = work.stream_total;
+      int unit = kStepStreamUnit, tiles = 0, seen_tiles = 0, ctas = s_ctas;
+      if (kv >= shp.H_kv) {
+        // (past the last head)
+      } else if (threadIdx.x & 1) {
         if (pre_streamed) {
           tiles = work.prefix_stream_tiles;
-          begin = work.stream_own + (int64_t)kvh * (tiles + unit);
-        } else {
+          begin = work.stream_own + (int64_t)kv * (tiles + unit);
+        } else if (pre) {
           tiles = work.prefix_tile_steps;
           unit = kStepTileUnit;
-          begin = ((int64_t)kvh * work.prefix_pairs + t / (2 * tpt)) * (tiles + unit);
+          begin = ((int64_t)kv * work.prefix_pairs + t / (2 * tpt)) * (tiles + unit);
           total = work.tile_total;
           ctas = t_ctas;
         }
         seen_tiles = tiles;
       } else if (r.unit >= 0) {
         seen_tiles = tiles = r.tiles;
-        begin = (int64_t)H_kv * r.cum + (int64_t)kvh * (tiles + unit);
+        begin = (int64_t)shp.H_kv * r.cum + (int64_t)kv * (tiles + unit);
       } else {
         const StepSeq e = plan.tiled[-1 - r.unit];
         const int seen = e.ctx - e.n_new;
@@ -654,55 +656,92 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const int end = min(e.n_new, (2 * pair + (in_pair < tpt ? 1 : 2)) * tpt);
         seen_tiles = (seen + end + kStepTileKeys - 1) / kStepTileKeys;
         unit = kStepTileUnit;
-        begin = work.tile_prefix + (int64_t)H_kv * r.cum + (int64_t)kvh * r.tiles +
+        begin = work.tile_prefix + (int64_t)shp.H_kv * r.cum + (int64_t)kv * r.tiles +
                 step_len_before(seen, 2 * tpt, pair);
         total = work.tile_total;
         ctas = t_ctas;
       }
-      Spills s = {0, 0, false};
-      if (pre || !(threadIdx.x & 1)) s = spills_of(begin, unit, tiles, seen_tiles, total, ctas);
+      Spills s = {0, 0, 0};
+      if (tiles > 0) {
+        s.first = first_cut(begin + unit + 1, total, ctas);
+        s.n = max(0, first_cut(begin + unit + seen_tiles, total, ctas) - s.first);
+        s.cut = first_cut(begin + unit + tiles, total, ctas) > s.first;
+      }
       spills[threadIdx.x] = s;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int h = h0 + warp + i * kJoinWarps;
-      if (h >= h1) continue;
-      const int64_t w = (int64_t)t * shp.H_q + h;
-      const int kvh = h / g, hh = h - kvh * g;
+    if (live) {
       const Spills a = spills[2 * (kvh - kv0)], p = spills[2 * (kvh - kv0) + 1];
-      if (!pre && !a.cut) continue;      // the unit was whole: its kernel wrote O
+      const int hh = h - kvh * g;
       Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      j.add(own_l[i], own_v[i]);
-      if (pre) j.add(pre_l[i], pre_v[i]);
-      // then the spills, four in flight at a time
+      j.add<2>(l2, v2);
       const int n = a.n + p.n;
-      const int pre_row = pre_streamed ? t * g
-                          : ((t / tpt) & 1) * kStepTileRows + (t % tpt) * g;
-      for (int s0 = 0; s0 < n; s0 += 4) {
-        float l[4];
-        float4 v[4];
+      if (n > wi) {
+        const int tile_row = in_pair < tpt ? in_pair * g : kStepTileRows + (in_pair - tpt) * g;
+        const int pre_in = t % (2 * tpt);
+        const int pre_row = pre_in < tpt ? pre_in * g : kStepTileRows + (pre_in - tpt) * g;
+        const Part mine = r.unit >= 0
+            ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + r.token * g + hh,
+                   kStepPackedRows}
+            : Part{ws.tile_o, ws.tile_lse, a.first * 2 * kStepTileRows + tile_row + hh,
+                   2 * kStepTileRows};
+        const Part theirs = pre_streamed
+            ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + t * g + hh,
+                   kStepPackedRows}
+            : Part{ws.tile_o, ws.tile_lse, p.first * 2 * kStepTileRows + pre_row + hh,
+                   2 * kStepTileRows};
+        constexpr int kAtOnce = W > 1 ? 8 : 4;
+        for (int k0 = wi; k0 < n; k0 += kAtOnce * W) {
+          float l[kAtOnce];
+          float4 v[kAtOnce];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int k = min(s0 + u, n - 1);
-          const bool mine = k < a.n;
-          const bool streamed = mine ? r.unit >= 0 : pre_streamed;
-          const int c = mine ? a.first + k : p.first + k - a.n;
-          const int64_t row = (int64_t)c * (streamed ? kStepPackedRows : 2 * kStepTileRows) +
-                              (mine ? own_row : pre_row) + hh;
-          l[u] = (streamed ? ws.stream_lse : ws.tile_lse)[row];
-          v[u] = reinterpret_cast<const float4*>((streamed ? ws.stream_o : ws.tile_o) +
-                                                 row * 128)[lane];
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int k = k0 + u * W;
+            l[u] = -INFINITY;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < n) {
+              const bool m = k < a.n;
+              const int row = m ? mine.row + k * mine.stride
+                                : theirs.row + (k - a.n) * theirs.stride;
+              l[u] = (m ? mine.lse : theirs.lse)[row];
+              v[u] = reinterpret_cast<const float4*>((m ? mine.o : theirs.o) +
+                                                     (int64_t)row * 128)[lane];
+            }
+          }
+          j.add<kAtOnce>(l, v);
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (s0 + u < n) j.add(l[u], v[u]);
       }
-      const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
-      uint2 out;
-      out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
-      out.y = ptx::pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
-      reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
+      if (W > 1) {
+        wide_acc[threadIdx.x] = j.acc;
+        if (lane == 0) {
+          wide_ml[warp * 2] = j.M;
+          wide_ml[warp * 2 + 1] = j.L;
+        }
+        __syncthreads();       // (W = 8: the block is one head, live as a whole)
+        if (wi == 0) {
+#pragma unroll
+          for (int x = 1; x < W; ++x) {
+            float m = wide_ml[x * 2], base = fmaxf(j.M, m);
+            base = base == -INFINITY ? 0.f : base;
+            const float keep = ptx::ex2(j.M - base), f = ptx::ex2(m - base);
+            const float4 v = wide_acc[x * 32 + lane];
+            j.M = fmaxf(j.M, m);
+            j.L = j.L * keep + wide_ml[x * 2 + 1] * f;
+            j.acc.x = j.acc.x * keep + v.x * f;
+            j.acc.y = j.acc.y * keep + v.y * f;
+            j.acc.z = j.acc.z * keep + v.z * f;
+            j.acc.w = j.acc.w * keep + v.w * f;
+          }
+        }
+      }
+      // (a unit that was whole and alone: its kernel wrote O)
+      if (wi == 0 && (pre || a.cut)) {
+        const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
+        uint2 out;
+        out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
+        out.y = ptx::pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
+        reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
+      }
     }
     __syncthreads();   // the next row's spills replace these
   }
@@ -784,7 +823,9 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
 
 cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                                 void* o, cudaStream_t st) {
-  const int chunks = (s.H_q + kJoinHeads - 1) / kJoinHeads;
+  const bool wide = ds.max_tokens <= kJoinWideRows;
+  const int heads = wide ? 1 : kJoinWarps;
+  const int chunks = (s.H_q + heads - 1) / heads;
   const int rows = std::min(ds.max_tokens, std::max(1, w.tile_grid * 16 / chunks));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)chunks, (unsigned)std::min(rows, 65535));
@@ -795,7 +836,8 @@ cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const Ste
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_combine_kernel, ds, s, w, (__nv_bfloat16*)o);
+  return cudaLaunchKernelEx(&cfg, wide ? step_combine_kernel<kJoinWarps> : step_combine_kernel<1>,
+                            ds, s, w, (__nv_bfloat16*)o);
 }
 
 }  // namespace rbkv
