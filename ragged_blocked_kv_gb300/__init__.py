@@ -374,6 +374,16 @@ def _stream(stream):
     return _P(stream.cuda_stream)
 
 
+def _raw_stream(index: int) -> int:
+    """Handle of the current stream of a device (the current one): the short
+    way where torch has it, as a Stream object costs a small step's time."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if get is not None:
+        return get(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 def _device(device):
     import torch
     return torch.cuda.device(device)
@@ -561,13 +571,14 @@ class StepTables:
                                        self.position, self.slot, self.plan, self.status)))
         self._c, self._t = C.byref(self._cfg), C.byref(self._tables)
         self._i32, self._dt = torch.int32, config.torch_dtype
+        self._on_gpu = self.device.type == "cuda"
         self._q_shape = torch.Size((self.max_tokens, config.num_heads_q, config.head_dim))
         self._kv_shape = torch.Size((self.max_tokens, config.num_heads_kv, config.head_dim))
         self._cache_shape = torch.Size(config.cache_shape())
 
     def _ptr(self, t, name, dtype, shape) -> int:
         if t.device == self.device and t.dtype is dtype and t.shape == shape and \
-                t.is_contiguous() and t.is_cuda:
+                t.is_contiguous() and self._on_gpu:
             return t.data_ptr()
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the tables on {self.device}")
@@ -576,11 +587,13 @@ class StepTables:
     def _call(self, fn, *args, stream=None) -> None:
         """A library call on the tables' device (the current one or not)."""
         import torch
-        if torch.cuda.current_device() == self.device.index:
-            _check(fn(self._c, self._t, *args, _stream(stream)))
-        else:
+        if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
-                _check(fn(self._c, self._t, *args, _stream(stream)))
+                return _check(fn(self._c, self._t, *args, _stream(stream)))
+        st = _raw_stream(self.device.index) if stream is None else _stream(stream)
+        status = fn(self._c, self._t, *args, st)
+        if status != OK:
+            _check(status)
 
     def build(self, seen, n_new, block_table=None, free=None, stream=None) -> "StepTables":
         """Sequence s holds ``seen[s]`` tokens and takes ``n_new[s]`` more.

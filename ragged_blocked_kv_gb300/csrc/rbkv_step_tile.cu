@@ -178,6 +178,16 @@ __device__ __forceinline__ bool next_item(Walk& w, const DevStep& ds, const Shap
   return false;
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // The box of a query tile's half: 64 head dims x g heads x 128/g tokens, its
 // packed rows in order (tokens past max_tokens read as zero).
 __device__ __forceinline__ void load_q_box(void* dst, const CUtensorMap* m, int d, int head,
@@ -343,7 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // The whole warp walks the loop and waits, so that every operand of an MMA is
+    // a warp-uniform value; one elected lane issues.
+    {
+      const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc_s = instr_desc(kRows, kKeys, 0);
       constexpr uint32_t idesc_o = instr_desc(kRows, 128, 1);
       // descriptor words: the high word is common to every operand; the low
@@ -357,21 +371,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // read P_X over the same columns: MMAs of one thread run in order)
       auto issue_qk = [&](int x, uint32_t gk, bool last) {
         const uint32_t qt = q_lo + ((x * kTileBytes) >> 4);
-        const uint32_t kt = k_lo + (((gk % kStages) * kTileBytes) >> 4);
-        const uint32_t d = tmem + x * kTileCols;
+        const uint32_t kt =
+            __shfl_sync(0xffffffffu, k_lo + (((gk % kStages) * kTileBytes) >> 4), 0);
+        const uint32_t d = tm + x * kTileCols;
         // head dims 16kk .. 16kk+15 in step kk: the half kk/4 of Q and K, 32-byte step kk%4
-        tc_mma_ss_k128(d, qt, kt, hi, idesc_s, false);
-        tc_commit(&bars->s_full[x]);
-        if (last) tc_commit(&bars->q_empty[x]);
+        if (leader) {
+          tc_mma_ss_k128(d, qt, kt, hi, idesc_s, false);
+          tc_commit(&bars->s_full[x]);
+          if (last) tc_commit(&bars->q_empty[x]);
+        }
+        __syncwarp();
       };
       // O_X += P_X V
       auto issue_pv = [&](int x, uint32_t gv, bool acc) {
-        const uint32_t vt = v_lo + (((gv % kStages) * kTileBytes) >> 4);
-        const uint32_t pt = tmem + x * kTileCols;
+        const uint32_t vt =
+            __shfl_sync(0xffffffffu, v_lo + (((gv % kStages) * kTileBytes) >> 4), 0);
+        const uint32_t pt = tm + x * kTileCols;
         // keys 16kk .. 16kk+15 in step kk: P columns 8kk.., V rows 16kk.. (MN-major)
         static_assert(kKeys == 128 && kHalf == 16384, "the K = 128 issue blocks assume these");
-        tc_mma_ts_k128(pt + kOCol, pt, vt, hi, idesc_o, acc);
-        tc_commit(&bars->o_done[x]);
+        if (leader) {
+          tc_mma_ts_k128(pt + kOCol, pt, vt, hi, idesc_o, acc);
+          tc_commit(&bars->o_done[x]);
+        }
+        __syncwarp();
       };
       bool ok = true;
       int site = 0, at = 0;
@@ -382,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // none: the barrier's transaction count already covers the copy.
       auto wait_bar = [&](uint64_t* bar, uint32_t parity, int where, int index,
                           bool tmem_sync) {
-        if (!ptx::mbar_wait(bar, parity, kWaitLimit) || *abort_flag) {
+        const bool got = ptx::mbar_wait(bar, parity, kWaitLimit) && !*abort_flag;
+        if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           site = where;
           at = index;
@@ -405,12 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (it.n[x] > 0) issue_qk(x, base, it.n[x] == 1);
-        tc_commit(&bars->kv_empty[base % kStages]);
+        if (leader) tc_commit(&bars->kv_empty[base % kStages]);
         // then per key tile j: PV_A(j) QK_A(j+1) PV_B(j) QK_B(j+1), each tile's
-        // products as soon as its softmax has written P
+        // products as soon as its softmax has written P.  The softmax threads
+        // have also seen V_j and K_j+1 land before they report P: a wait of the
+        // issuing thread costs 200 to 450 cycles while its products are queued
         for (int j = 0; ok && j < it.nmax; ++j) {
           const uint32_t gv = base + 2 * j + 1, gk = gv + 1;
-          bool v_in = false, k_in = false;
           #pragma unroll
           for (int x = 0; ok && x < 2; ++x) {
             if (j >= it.n[x]) continue;
@@ -418,38 +442,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j == 0 && oi[x] > 0 &&   // the previous item's epilogue must have read O_X
                 !wait_bar(&bars->o_free[x], (oi[x] - 1) & 1, 47, (int)oi[x], true))
               break;
-            if (!v_in && !wait_bar(&bars->kv_full[gv % kStages], (gv / kStages) & 1, 45, (int)gv, false))
-              break;
-            v_in = true;
             issue_pv(x, gv, j > 0);
             ++c[x];
-            if (j + 1 < it.n[x]) {
-              if (!k_in && !wait_bar(&bars->kv_full[gk % kStages], (gk / kStages) & 1, 48, (int)gk, false))
-                break;
-              k_in = true;
-              issue_qk(x, gk, j + 2 == it.n[x]);
-            }
+            if (j + 1 < it.n[x]) issue_qk(x, gk, j + 2 == it.n[x]);
           }
           if (!ok) break;
           // a stage is released once every product that reads it was issued
-          // (and its copy has landed)
-          tc_commit(&bars->kv_empty[gv % kStages]);
-          if (j + 1 < it.nmax) {
-            if (!k_in && !wait_bar(&bars->kv_full[gk % kStages], (gk / kStages) & 1, 49, (int)gk, false))
-              break;
-            tc_commit(&bars->kv_empty[gk % kStages]);
-          }
+          if (leader) tc_commit(&bars->kv_empty[gv % kStages]);
+          if (j + 1 < it.nmax && leader) tc_commit(&bars->kv_empty[gk % kStages]);
         }
         #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (it.n[x] > 0) ++oi[x];
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         ptx::report_wait(ds.status, kDevTimeout, site, at);
         *abort_flag = 1;
       }
       // every MMA issued must finish before tensor memory is released
-      tc_commit(&bars->drain);
+      if (leader) tc_commit(&bars->drain);
+      __syncwarp();
       ptx::mbar_wait(&bars->drain, 0, kWaitLimit);
     }
   }
@@ -583,16 +595,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ps =
             ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         l = l * corr + ps;
+        // V_j and K_j+1 have landed (the issuing thread relies on it)
+        const uint32_t gv = g_item + 2 * j + 1;     // ring index of V_j
+        bool landed = ptx::mbar_wait(&bars->kv_full[gv % kStages], (gv / kStages) & 1, kWaitLimit);
+        if (landed && j + 1 < it.nmax)
+          landed = ptx::mbar_wait(&bars->kv_full[(gv + 1) % kStages], ((gv + 1) / kStages) & 1,
+                                  kWaitLimit);
+        if (!__all_sync(0xffffffffu, landed)) {
+          ok = false;
+          site = 52;
+          at = (int)gv;
+          break;
+        }
         if (zeroer && j == it.nmax - 1 && (it.ke % kKeys) != 0) {
-          const uint32_t gv = g_item + 2 * j + 1;     // ring index of V_j
           const int s = gv % kStages;
-          const bool landed = ptx::mbar_wait(&bars->kv_full[s], (gv / kStages) & 1, kWaitLimit);
-          if (!__all_sync(0xffffffffu, landed)) {
-            ok = false;
-            site = 52;
-            at = (int)gv;
-            break;
-          }
           uint8_t* vt = kv_s + s * kTileBytes;
           const int valid = it.ke - key0;
           for (int e = row; e < (kKeys - valid) * 16; e += kRows) {
