@@ -11,6 +11,7 @@
 // Three prefix sums (tokens, blocks, free bits) and two scatters: a few
 // hundred KB at most, so the time is latency - launches and dependent loads.
 #include <algorithm>
+#include <atomic>
 
 #include "rbkv_step.h"
 
@@ -21,58 +22,65 @@ namespace rbkv {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+// What one CTA builds; larger steps take a cluster.
+constexpr int kOneSeqs = 2048, kOneBlocks = 131072, kOneRows = 8192;
+constexpr int kSmemSeqs = 2048;       // sequences of a CTA whose offsets stay on chip
 
 constexpr int32_t kErrInvalid = -1, kErrNoBlocks = -2, kErrCapacity = -6;
-constexpr int64_t kMaxLen = (int64_t)1 << 30;   // line length of one KV head
+// Lengths of the work lines of one KV head, and rows, stay below this.
+constexpr float kMaxLen = 1073741824.f;
 
 // Block counts of a sequence, clamped to its table row (a sequence out of
 // range is reported and nothing is scheduled; the clamps keep the copy of its
 // row in bounds).
-__device__ __forceinline__ void blocks_of(int64_t seen, int64_t n_new, int32_t B,
+__device__ __forceinline__ void blocks_of(int32_t seen, int32_t n_new, int32_t B,
                                           int32_t max_blocks, int32_t& held, int32_t& need) {
-  const int64_t h = seen > 0 ? (seen + B - 1) / B : 0;
-  const int64_t c = seen + n_new;
-  const int64_t e = c > 0 ? (c + B - 1) / B : 0;
+  const int64_t c = (int64_t)seen + n_new;
+  const int64_t h = seen > 0 ? step_div((int64_t)seen + B - 1, B) : 0;
+  const int64_t e = c > 0 ? step_div(c + B - 1, B) : 0;
   held = (int32_t)(h < max_blocks ? h : max_blocks);
   need = (int32_t)(e < max_blocks ? e : max_blocks);
 }
 
-enum { kTokens = 0, kGrow, kStreamed, kTiled, kStreamLen, kTileLen, kSums };
+enum { kTokens = 0, kGrow, kStreamed, kTiled, kStreamLen, kTileLen, kFreeBits, kSums };
 
-struct Sums {
-  int64_t v[kSums];
-};
-
-// One sequence's contribution to the sums; false when its lengths are wrong.
+// One sequence's contribution to the sums (0 where its lengths are wrong).
 __device__ __forceinline__ int32_t measure(const BuildArgs& a, int32_t seen, int32_t n_new,
-                                           Sums& s) {
+                                           int32_t (&v)[kSums]) {
 #pragma unroll
-  for (int i = 0; i < kSums; ++i) s.v[i] = 0;
+  for (int i = 0; i < kSums; ++i) v[i] = 0;
   if (seen < 0 || n_new < 0) return kErrInvalid;
-  const int64_t ctx = (int64_t)seen + n_new;
-  const int64_t need = (ctx + a.block_size - 1) / a.block_size;
-  if (need > a.max_blocks || ctx > 0x7fffffff) return kErrCapacity;
-  if (n_new > a.max_tokens) return kErrCapacity;
-  s.v[kTokens] = n_new;
-  s.v[kGrow] = need - ((int64_t)seen + a.block_size - 1) / a.block_size;
+  const uint32_t ctx = (uint32_t)seen + (uint32_t)n_new, B = (uint32_t)a.block_size;
+  if (ctx > 0x7fffffffu || n_new > a.max_tokens) return kErrCapacity;
+  const uint32_t need = (ctx + B - 1) / B;
+  if (need > (uint32_t)a.max_blocks) return kErrCapacity;
+  v[kTokens] = n_new;
+  v[kGrow] = (int32_t)(need - ((uint32_t)seen + B - 1) / B);
   if (n_new == 0) return 0;
   if ((int64_t)n_new * a.group <= kStepPackedRows) {
-    s.v[kStreamed] = 1;
-    s.v[kStreamLen] = (ctx + kStepStreamKeys - 1) / kStepStreamKeys + kStepStreamUnit;
+    v[kStreamed] = 1;
+    v[kStreamLen] = (int32_t)((ctx + kStepStreamKeys - 1) / kStepStreamKeys) + kStepStreamUnit;
   } else {
-    s.v[kTiled] = 1;
-    s.v[kTileLen] = step_seq_len(seen, n_new, 2 * step_tile_tokens(a.group));
+    v[kTiled] = 1;
+    const int64_t len = step_seq_len(seen, n_new, 2 * step_tile_tokens(a.group));
+    if (len >= (int64_t)kMaxLen) return kErrCapacity;
+    v[kTileLen] = (int32_t)len;
   }
   return 0;
 }
 
 struct Shared {
-  int64_t sums[kSums];     // this CTA's, read by the other CTAs of the cluster
-  int64_t free_bits;
+  int32_t sums[kSums];     // this CTA's, read by the other CTAs of the cluster
+  float big;               // an upper bound of the sums that could overflow
   int32_t err;
-  int32_t warp_sum[kSums + 1][kWarps];
+  int32_t warp_sum[kSums][kWarps];
+  float warp_big[kWarps];
+  int32_t warp_err[kWarps];
+  int32_t q_start[kSmemSeqs + 1];
+  int32_t seen[kSmemSeqs];
+  StepRow of[kSmemSeqs];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -80,83 +88,43 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// (also orders the CTAs' global writes before the reads that follow it)
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+__device__ __forceinline__ uint32_t remote_b32(const void* p, uint32_t rank) {
   const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ int64_t remote_i64(const int64_t* p, uint32_t rank) {
-  int64_t v;
-  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ int32_t remote_i32(const int32_t* p, uint32_t rank) {
-  int32_t v;
-  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
 
-// Exclusive block-wide prefix sums of N counters at once; `total` gets the
-// block's sums.  Every thread of the block calls it.
-template <int N>
-__device__ __forceinline__ void block_scan(int32_t (&v)[N], int32_t (&total)[N], Shared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t inc[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) inc[i] = v[i];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int32_t up = __shfl_up_sync(0xffffffffu, inc[i], off);
-      if (lane >= off) inc[i] += up;
-    }
-  }
-  __syncthreads();   // the previous use of warp_sum is over
-  if (lane == 31) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) sh.warp_sum[i][warp] = inc[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int32_t w = lane < kWarps ? sh.warp_sum[i][lane] : 0;
-    int32_t sum = w, before = lane < warp ? w : 0;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      before += __shfl_xor_sync(0xffffffffu, before, off);
-    }
-    total[i] = sum;
-    v[i] = inc[i] - v[i] + before;
-  }
-}
-
-// The first cluster of the grid builds the step; every further CTA copies the
-// part of the table that no sequence grows into (when the table is not built
-// in place).  The eight CTAs of the building cluster each own a slice of the
-// sequences and of the bitmap, exchange their sums through distributed shared
-// memory, and meet again once the new ids are written.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    build_kernel(BuildArgs a) {
-  __shared__ Shared sh;
+// C CTAs (one, or a cluster of eight) build the step, each a slice of the
+// sequences and of the bitmap; every further CTA copies the part of the table
+// that no sequence grows into (when the table is not built in place).  A
+// thread owns consecutive sequences and bitmap words, so one block-wide scan
+// of all sums gives every offset; the CTAs exchange their totals through
+// distributed shared memory and meet again once the new ids are written.
+// One CTA has no cluster barrier and no exchange: it is the faster one up to
+// the sizes that its caller allows it.
+template <int C>
+__global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = a.num_seqs, B = a.block_size;
 
-  if (blockIdx.x >= kCluster) {
-    const int64_t warps = (int64_t)(gridDim.x - kCluster) * kWarps;
-    for (int64_t s = (int64_t)(blockIdx.x - kCluster) * kWarps + (tid >> 5); s < S; s += warps) {
+  if (blockIdx.x >= C) {
+    const int warps = (gridDim.x - C) * kWarps;
+    for (int s = (blockIdx.x - C) * kWarps + warp; s < S; s += warps) {
       int32_t held, need;
       blocks_of(a.seen[s], a.n_new[s], B, a.max_blocks, held, need);
-      const int32_t* src = a.table_in + s * a.max_blocks;
-      int32_t* dst = a.table + s * a.max_blocks;
+      const int32_t* src = a.table_in + (int64_t)s * a.max_blocks;
+      int32_t* dst = a.table + (int64_t)s * a.max_blocks;
 #pragma unroll 4
       for (int c = lane; c < a.max_blocks; c += 32)
         if (c < held || c >= need) dst[c] = src[c];
@@ -165,12 +133,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   }
 
   const StepPlan plan = step_plan(a.plan, S, a.max_tokens);
-  const uint32_t rank = cluster_rank();
-  const int per = (S + kCluster - 1) / kCluster;
-  const int s0 = min((int)rank * per, S), s1 = min(s0 + per, S);
+  const uint32_t rank = C > 1 ? cluster_rank() : 0;
+  const int per = (S + C - 1) / C;
+  const int s0 = min((int)rank * per, S), n_seqs = min(per, S - s0);
   const int W = (a.num_blocks + 31) / 32;
-  const int wper = (W + kCluster - 1) / kCluster;
-  const int w0 = min((int)rank * wper, W), w1 = min(w0 + wper, W);
+  const int wper = (W + C - 1) / C;
+  const int w0 = min((int)rank * wper, W), n_words = min(wper, W - w0);
+  // this thread's: sequences [sa, sb) and words [wa, wb) of the CTA's
+  const int ks = (n_seqs + kThreads - 1) / kThreads, kw = (n_words + kThreads - 1) / kThreads;
+  const int sa = min(tid * ks, n_seqs), sb = min(sa + ks, n_seqs);
+  const int wa = min(tid * kw, n_words), wb = min(wa + kw, n_words);
+  const bool on_chip = n_seqs <= kSmemSeqs;
   // bits past the pool's last block count for nothing
   auto pool_word = [&](int w) -> uint32_t {
     const uint32_t x = (uint32_t)a.free_in[w];
@@ -178,167 +151,207 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     return left >= 32 ? x : x & ((1u << left) - 1u);
   };
 
-  // ---- this CTA's sums ----
-  Sums mine = {};
-  int64_t bits = 0;
-  int32_t err = 0;
-  for (int s = s0 + tid; s < s1; s += kThreads) {
-    Sums x;
-    err = min(err, measure(a, a.seen[s], a.n_new[s], x));
+  // ---- the thread's sums, and their scan over the block ----
+  int32_t mine[kSums], err = 0;
+  float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) mine.v[i] += x.v[i];
+  for (int i = 0; i < kSums; ++i) mine[i] = 0;
+  for (int i = sa; i < sb; ++i) {
+    int32_t v[kSums];
+    err = min(err, measure(a, a.seen[s0 + i], a.n_new[s0 + i], v));
+    big += (float)v[kTokens] + (float)v[kStreamLen] + (float)v[kTileLen];
+#pragma unroll
+    for (int x = 0; x < kSums; ++x) mine[x] += v[x];
   }
-  for (int w = w0 + tid; w < w1; w += kThreads) bits += __popc(pool_word(w));
-  if (tid < kSums) sh.sums[tid] = 0;
-  if (tid == 0) {
-    sh.free_bits = 0;
-    sh.err = 0;
+  for (int w = wa; w < wb; ++w) mine[kFreeBits] += __popc(pool_word(w0 + w));
+  int32_t at[kSums];       // sums before this thread
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) at[i] = mine[i];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+      const int32_t up = __shfl_up_sync(0xffffffffu, at[i], off);
+      if (lane >= off) at[i] += up;
+    }
+    big += __shfl_xor_sync(0xffffffffu, big, off);
+    err = min(err, __shfl_xor_sync(0xffffffffu, err, off));
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) sh.warp_sum[i][warp] = at[i];
+    sh.warp_big[warp] = big;
+    sh.warp_err[warp] = err;
+  }
+  __syncthreads();
+  if (warp < kSums) {
+    // warp i scans sum i over the warps
+    const int32_t w = sh.warp_sum[warp][lane];
+    int32_t inc = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t up = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += up;
+    }
+    sh.warp_sum[warp][lane] = inc - w;
+    if (lane == 31) sh.sums[warp] = inc;
+  } else if (warp == kSums) {
+    float b = sh.warp_big[lane];
+    int32_t e = sh.warp_err[lane];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      b += __shfl_xor_sync(0xffffffffu, b, off);
+      e = min(e, __shfl_xor_sync(0xffffffffu, e, off));
+    }
+    if (lane == 0) {
+      sh.big = b;
+      sh.err = e;
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int off = 16; off; off >>= 1) {
-#pragma unroll
-    for (int i = 0; i < kSums; ++i) mine.v[i] += __shfl_xor_sync(0xffffffffu, mine.v[i], off);
-    bits += __shfl_xor_sync(0xffffffffu, bits, off);
-    err = min(err, __shfl_xor_sync(0xffffffffu, err, off));
-  }
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kSums; ++i)
-      atomicAdd((unsigned long long*)&sh.sums[i], (unsigned long long)mine.v[i]);
-    atomicAdd((unsigned long long*)&sh.free_bits, (unsigned long long)bits);
-    atomicMin(&sh.err, err);
-  }
-  cluster_sync();
+  for (int i = 0; i < kSums; ++i) at[i] += sh.warp_sum[i][warp] - mine[i];
 
-  // ---- the cluster's sums, and those before this CTA ----
-  int64_t total[kSums], before[kSums], free_total = 0, free_before = 0;
-  err = 0;
+  // ---- the step's totals, and what the CTAs before this one hold ----
+  int32_t total[kSums];
+  if constexpr (C == 1) {
 #pragma unroll
-  for (int i = 0; i < kSums; ++i) total[i] = before[i] = 0;
-  for (uint32_t r = 0; r < kCluster; ++r) {
+    for (int i = 0; i < kSums; ++i) total[i] = sh.sums[i];
+    big = sh.big;
+    err = sh.err;
+  } else {
+    cluster_sync();
+    // lane r reads CTA r's; the warp adds them up
+    const uint32_t r = lane & (C - 1);
 #pragma unroll
     for (int i = 0; i < kSums; ++i) {
-      const int64_t x = remote_i64(&sh.sums[i], r);
-      total[i] += x;
-      before[i] += r < rank ? x : 0;
+      const int32_t x = (int32_t)remote_b32(&sh.sums[i], r);
+      int32_t sum = x, before = r < rank ? x : 0;
+#pragma unroll
+      for (int off = C / 2; off; off >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+      }
+      total[i] = sum;
+      at[i] += before;
     }
-    const int64_t f = remote_i64(&sh.free_bits, r);
-    free_total += f;
-    free_before += r < rank ? f : 0;
-    err = min(err, remote_i32(&sh.err, r));
+    big = __uint_as_float(remote_b32(&sh.big, r));
+    err = (int32_t)remote_b32(&sh.err, r);
+#pragma unroll
+    for (int off = C / 2; off; off >>= 1) {
+      big += __shfl_xor_sync(0xffffffffu, big, off);
+      err = min(err, __shfl_xor_sync(0xffffffffu, err, off));
+    }
   }
-  if (err == 0 && (total[kTokens] > a.max_tokens || total[kStreamLen] > kMaxLen ||
-                   total[kTileLen] > kMaxLen))
-    err = kErrCapacity;
-  if (err == 0 && total[kGrow] > free_total) err = kErrNoBlocks;
+  // (below kMaxLen the 32-bit sums are exact)
+  if (err == 0 && (big >= kMaxLen || total[kTokens] > a.max_tokens)) err = kErrCapacity;
+  if (err == 0 && total[kGrow] > total[kFreeBits]) err = kErrNoBlocks;
   const bool ok = err == 0;
-  const int32_t T = ok ? (int32_t)total[kTokens] : 0;
-  const int32_t grow_total = ok ? (int32_t)total[kGrow] : 0;
+  const int32_t T = ok ? total[kTokens] : 0, grow = ok ? total[kGrow] : 0;
 
   // ---- per sequence: offsets and work lists ----
-  int32_t carry[kSums];
-#pragma unroll
-  for (int i = 0; i < kSums; ++i) carry[i] = ok ? (int32_t)before[i] : 0;
-  for (int base = s0; base < s1; base += kThreads) {
-    const int s = base + tid;
-    const bool live = s < s1;
-    const int32_t seen = live ? a.seen[s] : 0, n_new = live ? a.n_new[s] : 0;
+  for (int i = sa; i < sb; ++i) {
+    const int s = s0 + i;
+    const int32_t seen = a.seen[s], n_new = a.n_new[s];
     if (!ok) {
-      if (live) {
+      if (a.table != a.table_in) {
         int32_t held, need;
         blocks_of(seen, n_new, B, a.max_blocks, held, need);
-        if (a.table != a.table_in)
-          for (int c = held; c < need; ++c)
-            a.table[(int64_t)s * a.max_blocks + c] = a.table_in[(int64_t)s * a.max_blocks + c];
-        a.ctx[s] = seen;
-        a.q_start[s] = 0;
+        for (int c = held; c < need; ++c)
+          a.table[(int64_t)s * a.max_blocks + c] = a.table_in[(int64_t)s * a.max_blocks + c];
       }
+      a.ctx[s] = seen;
+      a.q_start[s] = 0;
       continue;
     }
-    Sums x;
-    measure(a, seen, n_new, x);
-    int32_t v[kSums], sum[kSums];
-#pragma unroll
-    for (int i = 0; i < kSums; ++i) v[i] = (int32_t)x.v[i];
-    block_scan<kSums>(v, sum, sh);
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < kSums; ++i) v[i] += carry[i];
-      a.ctx[s] = seen + n_new;
-      a.q_start[s] = v[kTokens];
-      StepRow of = {0, v[kGrow], 0, 0};
-      StepSeq e = {s, v[kTokens], n_new, seen + n_new, 0, 0, {0, 0}};
-      if (x.v[kStreamed]) {
-        of.unit = v[kStreamed];
-        of.cum = e.cum = v[kStreamLen];
-        of.tiles = e.tiles = (int32_t)x.v[kStreamLen] - kStepStreamUnit;
-        plan.streamed[of.unit] = e;
-      } else if (x.v[kTiled]) {
-        of.unit = -1 - v[kTiled];
-        of.cum = e.cum = v[kTileLen];
-        of.tiles = e.tiles = (int32_t)x.v[kTileLen];
-        plan.tiled[v[kTiled]] = e;
-      }
+    int32_t v[kSums];
+    measure(a, seen, n_new, v);
+    a.ctx[s] = seen + n_new;
+    a.q_start[s] = at[kTokens];
+    StepRow of = {0, at[kGrow], 0, 0};
+    StepSeq e = {s, at[kTokens], n_new, seen + n_new, 0, 0, {0, 0}};
+    if (v[kStreamed]) {
+      of.unit = at[kStreamed];
+      of.cum = e.cum = at[kStreamLen];
+      of.tiles = e.tiles = v[kStreamLen] - kStepStreamUnit;
+      plan.streamed[of.unit] = e;
+    } else if (v[kTiled]) {
+      of.unit = -1 - at[kTiled];
+      of.cum = e.cum = at[kTileLen];
+      of.tiles = e.tiles = v[kTileLen];
+      plan.tiled[at[kTiled]] = e;
+    }
+    if (on_chip) {
+      sh.q_start[i] = at[kTokens];
+      sh.seen[i] = seen;
+      sh.of[i] = of;
+    } else {
       plan.of_seq[s] = of;
     }
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) carry[i] += sum[i];
+    for (int x = 0; x < kFreeBits; ++x) at[x] += v[x];
+    if (i == n_seqs - 1 && on_chip) sh.q_start[n_seqs] = at[kTokens];
   }
   if (rank == 0 && tid == 0) {
     a.q_start[S] = T;
     plan.header[kPlanRows] = T;
-    plan.header[kPlanStreamed] = ok ? (int32_t)total[kStreamed] : 0;
-    plan.header[kPlanTiled] = ok ? (int32_t)total[kTiled] : 0;
-    plan.header[kPlanStreamLen] = ok ? (int32_t)total[kStreamLen] : 0;
-    plan.header[kPlanTileLen] = ok ? (int32_t)total[kTileLen] : 0;
+    plan.header[kPlanStreamed] = ok ? total[kStreamed] : 0;
+    plan.header[kPlanTiled] = ok ? total[kTiled] : 0;
+    plan.header[kPlanStreamLen] = ok ? total[kStreamLen] : 0;
+    plan.header[kPlanTileLen] = ok ? total[kTileLen] : 0;
     if (!ok) atomicCAS(a.status, 0, err);
   }
 
   // ---- the lowest free ids, taken out of the bitmap ----
-  int32_t rank0 = (int32_t)min(free_before, (int64_t)0x7fffffff);
-  for (int base = w0; base < w1; base += kThreads) {
-    const int w = base + tid;
-    const bool live = w < w1;
-    const uint32_t pool = live ? pool_word(w) : 0u;
-    int32_t v[1] = {__popc(pool)}, sum[1];
-    block_scan<1>(v, sum, sh);
-    if (live) {
-      uint32_t taken = 0, left = pool;
-      int32_t k = rank0 + v[0];
-      while (left && k < grow_total) {
-        const int b = __ffs(left) - 1;
-        left &= left - 1;
-        taken |= 1u << b;
-        plan.new_ids[k++] = w * 32 + b;
+  int32_t k = at[kFreeBits];
+  for (int i = wa; i < wb; ++i) {
+    const int w = w0 + i;
+    uint32_t left = pool_word(w), taken = 0;
+    if (k + __popc(left) <= grow) {
+      taken = left;        // the whole word
+    } else {
+      uint32_t rest = left;
+      for (int n = k; n < grow; ++n) {
+        taken |= rest & (0u - rest);
+        rest &= rest - 1;
       }
+    }
+    const int next = k + __popc(left);
+    for (uint32_t rest = taken; rest; rest &= rest - 1)
+      plan.new_ids[k++] = w * 32 + __ffs(rest) - 1;
+    if (a.free_words != a.free_in || taken)
       a.free_words[w] = (int32_t)((uint32_t)a.free_in[w] & ~taken);
-    }
-    rank0 += sum[0];
+    k = next;
   }
-  cluster_sync();
 
-  // ---- rows: positions, slots, and the entry of each block that begins ----
-  for (int r = (int)rank * kThreads + tid; r < a.max_tokens; r += kCluster * kThreads) {
-    if (r >= T) {
-      a.position[r] = -1;
-      a.slot[r] = -1;
-      continue;
-    }
-    // the last sequence that starts at or before row r and is not empty: the
-    // first one that ends behind it
-    int lo = 0, hi = S - 1;
+  // ---- rows past the step's ----
+  for (int64_t r = T + (int64_t)rank * kThreads + tid; r < a.max_tokens;
+       r += (int64_t)C * kThreads) {
+    a.position[r] = -1;
+    a.slot[r] = -1;
+  }
+  if constexpr (C == 1) __syncthreads();
+  else cluster_sync();
+  if (!ok || n_seqs <= 0) return;
+
+  // ---- the rows of this CTA's sequences: positions, slots, and the entry of
+  // each block that begins ----
+  const int32_t* q_start = on_chip ? sh.q_start : a.q_start + s0;
+  const int r1 = q_start[n_seqs];
+  for (int r = q_start[0] + tid; r < r1; r += kThreads) {
+    // the first sequence that ends behind row r
+    int lo = 0, hi = n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (a.q_start[mid + 1] > r) hi = mid;
+      if (q_start[mid + 1] > r) hi = mid;
       else lo = mid + 1;
     }
-    const int s = lo;
-    const int q0 = a.q_start[s], n = a.q_start[s + 1] - q0;
-    const int seen = a.ctx[s] - n, pos = seen + r - q0;
-    const int held = (int)(((int64_t)seen + B - 1) / B);
-    const int c = pos / B, off = pos - c * B;
-    StepRow of = plan.of_seq[s];
+    const int s = s0 + lo, q0 = q_start[lo];
+    const int seen = on_chip ? sh.seen[lo] : a.ctx[s] - (q_start[lo + 1] - q0);
+    StepRow of = on_chip ? sh.of[lo] : plan.of_seq[s];
+    const int pos = seen + r - q0;
+    const int held = (int)(((uint32_t)seen + B - 1) / (uint32_t)B);
+    const int c = (int)((uint32_t)pos / (uint32_t)B), off = pos - c * B;
     int32_t id;
     if (c < held) {
       id = a.table_in[(int64_t)s * a.max_blocks + c];
@@ -385,22 +398,42 @@ cudaError_t launch_step_build(const BuildArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  const bool one = a.num_seqs <= kOneSeqs && a.num_blocks <= kOneBlocks &&
+                   a.max_tokens <= kOneRows;
+  const int ctas = one ? 1 : kCluster;
   int copies = 0;
   if (a.table != a.table_in) {
-    const int64_t warps = a.num_seqs;
-    copies = (int)std::min<int64_t>((warps + kWarps - 1) / kWarps, std::max(1, 2 * sms));
-    copies = (copies + kCluster - 1) / kCluster * kCluster;
+    copies = std::min((a.num_seqs + kWarps - 1) / kWarps, std::max(1, sms));
+    copies = (copies + ctas - 1) / ctas * ctas;
+  }
+  auto fn = one ? build_kernel<1> : build_kernel<kCluster>;
+  // the shared-memory limit is raised once per device
+  static std::atomic<uint64_t> attr_done{0};
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load() & bit)) {
+    e = cudaFuncSetAttribute(build_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Shared));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(build_kernel<kCluster>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster + copies);
+  cfg.gridDim = dim3((unsigned)(ctas + copies));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, build_kernel, a);
+  cfg.numAttrs = one ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
 cudaError_t launch_step_release(const BuildArgs& a, const int32_t* done, cudaStream_t st) {
