@@ -79,6 +79,12 @@ ShapeInfo shape(const rbkv_config* c) {
   return s;
 }
 
+size_t workspace_of(const ShapeInfo& s, const rbkv_step_tables* t, int32_t prefix_len, int sms) {
+  if (step_fast_supported(s)) return step_workspace(s, t->max_tokens, sms, nullptr, nullptr);
+  const int splits = step_generic_splits(s, t->max_tokens, t->max_blocks, prefix_len, sms);
+  return step_generic_workspace(s, t->max_tokens, splits);
+}
+
 }  // namespace
 
 extern "C" {
@@ -158,8 +164,8 @@ size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables*
   if (check_tables(cfg, t) != RBKV_OK || prefix_len < 0) return 0;
   const ShapeInfo s = shape(cfg);
   int sms = 0;
-  if (!step_fast_supported(s) || num_sms(&sms) != cudaSuccess) return 0;
-  return step_workspace(s, t->max_tokens, sms, nullptr, nullptr);
+  if (num_sms(&sms) != cudaSuccess) return 0;
+  return workspace_of(s, t, prefix_len, sms);
 }
 
 rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* t, const void* q,
@@ -191,18 +197,19 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
   ds.prefix_len = prefix_len;
   const ShapeInfo s = shape(cfg);
   const cudaStream_t cs = (cudaStream_t)stream;
-  cudaError_t e = cudaSuccess;
+  int sms = 0;
+  cudaError_t e = num_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  const size_t need = workspace_of(s, t, prefix_len, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
   if (!step_fast_supported(s)) {
-    e = launch_step_generic(ds, s, q, k_cache, v_cache, o, cs);
-    if (e == cudaSuccess) note_launches(1);
+    const int splits = step_generic_splits(s, t->max_tokens, t->max_blocks, prefix_len, sms);
+    e = launch_step_generic(ds, s, q, k_cache, v_cache, o, workspace, splits, sms, cs);
+    if (e == cudaSuccess) note_launches(splits > 1 ? 2 : 1);
   } else {
-    int sms = 0;
-    e = num_sms(&sms);
-    if (e != cudaSuccess) return cuda_fail(e, "device query");
     StepWorkspace w;
-    const size_t need = step_workspace(s, t->max_tokens, sms, workspace, &w);
-    if (!workspace || workspace_bytes < need)
-      return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
+    step_workspace(s, t->max_tokens, sms, workspace, &w);
     // a step of at most 16 packed rows has no work for the tile kernel
     const bool tiles = !step_prefix_streamed(t->max_tokens, s.g);
     if (tiles) e = launch_step_tile(ds, s, w, q, k_cache, v_cache, o, true, cs);

@@ -223,10 +223,17 @@ struct BuildArgs {
 
 cudaError_t launch_step_build(const BuildArgs& a, cudaStream_t st);
 cudaError_t launch_step_release(const BuildArgs& a, const int32_t* done, cudaStream_t st);
-// CUDA-core attention of a step: every type and shape.
+// CUDA-core attention of a step: every type and shape, its packed rows eight to
+// a block and the keys of each shared by `splits` blocks (more than one: with
+// a workspace and a second kernel).
+constexpr int kStepGenericRows = 8;
+constexpr int kStepGenericSplits = 32;
+int step_generic_splits(const ShapeInfo& s, int32_t max_tokens, int32_t max_blocks,
+                        int32_t prefix_len, int sms);
+size_t step_generic_workspace(const ShapeInfo& s, int32_t max_tokens, int splits);
 cudaError_t launch_step_generic(const DevStep& ds, const ShapeInfo& s, const void* q,
                                 const void* k_cache, const void* v_cache, void* o,
-                                cudaStream_t st);
+                                void* workspace, int splits, int sms, cudaStream_t st);
 // The fast path's three kernels.  The first one launched of the first two
 // waits for the stream's previous kernel (`first`); the other starts beside
 // it and waits for it before ending; the combine waits for both.

@@ -1,11 +1,22 @@
-// Attention of a step on the CUDA cores: every type, head dim and block size.
+// Attention of a step on the CUDA cores: every type, head dim and block size
+// (fp32 steps, and bf16 shapes off the tensor-core kernels).
 //
-// Row t of sequence s, query head h: softmax over the prefix's keys
-// 0 .. prefix_len - 1 and the sequence's own keys 0 .. position[t].  One warp
-// per (row, head) walks the keys 32 at a time, one per lane, with a running
-// maximum and sum; the value rows are then added with the lanes spread over
-// the head dim.
+// A block takes eight packed rows (row = token * g + head) of one KV head.
+// Over the prefix all eight see the same keys; behind it each token sees its
+// own sequence's.  Keys go 32 at a time, one per lane, so that one read of a
+// key row serves all rows (its dot products take q from shared memory as
+// broadcasts); the weights pass through shared memory to the value product,
+// where the lanes hold the head dim and one read of a value row serves all
+// rows.  The 32-key chunks of both parts are dealt to the block's eight warps
+// (and, where there are few rows, to `splits` blocks); each warp keeps an
+// online softmax per row, and the warps are joined by their maxima and sums
+// in shared memory.  All arithmetic is fp32 FMAs.  Bound by the shared-memory
+// reads of q and the weights, and by latency at the sizes it is used for.
+#include <algorithm>
+#include <atomic>
+
 #include "rbkv_step.h"
+#include "rbkv_ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -14,8 +25,10 @@ namespace rbkv {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMaxDPerLane = 8;   // head_dim <= 256
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = kStepGenericRows;     // packed rows of a block
+static_assert(kRows == 8, "the weights of a key are read as two float4");
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <class T> __device__ __forceinline__ float to_f(T x);
@@ -29,113 +42,312 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
   return __float2bfloat16_rn(x);
 }
 
-template <class T>
-__global__ void __launch_bounds__(kWarps * 32)
+// Four consecutive elements.
+__device__ __forceinline__ float4 load4(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                     __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+}
+
+// Shared memory: q [kRows][D], each warp's weights [32 keys][kRows], and for
+// the join O [warp][row][D] and (max, sum) [warp][row].
+__host__ __device__ constexpr int smem_floats(int D) {
+  return kRows * D + kWarps * 32 * kRows + kWarps * kRows * D + kWarps * kRows * 2;
+}
+
+// kPer: head-dim elements per lane, D = 32 dpl with dpl <= kPer.
+template <class T, int kPer>
+__global__ void __launch_bounds__(kThreads)
     step_generic_kernel(DevStep ds, ShapeInfo s, const T* __restrict__ q,
                         const T* __restrict__ k_cache, const T* __restrict__ v_cache,
-                        T* __restrict__ o) {
-  __shared__ float q_s[kWarps][256];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                        T* __restrict__ o, float* __restrict__ part_o,
+                        float* __restrict__ part_lse, int splits) {
+  extern __shared__ __align__(16) float smem[];
+  ptx::pdl_wait_previous();
+  ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int D = s.D, B = s.B, H_kv = s.H_kv, dpl = D / 32;
-  const int64_t items = (int64_t)plan.header[kPlanRows] * s.H_q;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + warp; w < items;
-       w += (int64_t)gridDim.x * kWarps) {
-    const int t = (int)(w / s.H_q), h = (int)(w % s.H_q), kvh = h / s.g;
-    const StepRow r = plan.rows[t];
-    const StepSeq e = r.unit >= 0 ? plan.streamed[r.unit] : plan.tiled[-1 - r.unit];
-    const int seq = e.seq, own = e.ctx - e.n_new + r.token + 1;   // keys the row sees
-    const int32_t* table = ds.block_table + (int64_t)seq * ds.max_blocks;
-    const T* qrow = q + ((int64_t)t * s.H_q + h) * D;
-    for (int d = lane; d < D; d += 32) q_s[warp][d] = to_f(qrow[d]) * (s.scale * kLog2e);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f;
-    float acc[kMaxDPerLane];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = s.D, B = s.B, H_kv = s.H_kv, g = s.g, dpl = D / 32;
+  float* q_s = smem;
+  float* p_s = smem + kRows * D + warp * 32 * kRows;
+  float* join_o = smem + kRows * D + kWarps * 32 * kRows;
+  float* join_ml = join_o + kWarps * kRows * D;
+  const int T_rows = plan.header[kPlanRows];
+  const int n_rows = T_rows * g;               // packed rows of a KV head
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int stride = kWarps * splits, mine = split * kWarps + warp;
+
+  for (int row0 = blockIdx.x * kRows; row0 < n_rows; row0 += gridDim.x * kRows) {
+    const int rows = min(kRows, n_rows - row0);
+    for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+      const int r = e / D, d = e - r * D, t = (row0 + r) / g, h = kvh * g + (row0 + r) % g;
+      q_s[e] = r < rows ? to_f(q[((int64_t)t * s.H_q + h) * D + d]) * (s.scale * kLog2e) : 0.f;
+    }
+    __syncthreads();
+    float m[kRows], l[kRows], acc[kRows][kPer];
 #pragma unroll
-    for (int i = 0; i < kMaxDPerLane; ++i) acc[i] = 0.f;
-    for (int part = 0; part < 2; ++part) {
-      const int n = part ? own : ds.prefix_len;
-      const int32_t* ids = part ? table : ds.prefix_table;
-      for (int k0 = 0; k0 < n; k0 += 32) {
-        const int key = k0 + lane;
-        float sc = -INFINITY;
-        int64_t row_off = -1;
-        if (key < n) {
-          const int32_t blk = ids[key / B];
-          if (blk >= 0 && blk < ds.num_blocks) {
-            row_off = (((int64_t)blk * H_kv + kvh) * B + key % B) * D;
-            const T* krow = k_cache + row_off;
-            float dot = 0.f;
-            for (int d = 0; d < D; ++d) dot = fmaf(q_s[warp][d], to_f(krow[d]), dot);
-            sc = dot;
-          } else {
-            atomicCAS(ds.status, 0, kDevBounds);
+    for (int r = 0; r < kRows; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[r][i] = 0.f;
+    }
+
+    // One 32-key chunk for the rows [ra, rb) of the block; row r sees the keys
+    // below lim0 + (token of r - first token).
+    auto chunk = [&](const int32_t* ids, int k0, int n, int ra, int rb, int lim0, int tok0,
+                     bool causal) {
+      const int key = k0 + lane;
+      int64_t off = -1;
+      if (key < n) {
+        const int blk = ids[key / B];
+        if ((uint32_t)blk < (uint32_t)ds.num_blocks)
+          off = (((int64_t)blk * H_kv + kvh) * B + key % B) * D;
+        else
+          atomicCAS(ds.status, 0, kDevBounds);
+      }
+      float x[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) x[r] = 0.f;
+      if (off >= 0) {
+        const T* kr = k_cache + off;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+          const float4 k = load4(kr + d);
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            if (r >= ra && r < rb) {
+              const float4 a = *reinterpret_cast<const float4*>(q_s + r * D + d);
+              x[r] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, x[r]))));
+            }
           }
         }
-        float top = sc;
+      }
 #pragma unroll
-        for (int off = 16; off; off >>= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float m_new = fmaxf(m, top);
-        if (m_new == -INFINITY) continue;   // every key so far skipped
-        const float corr = exp2f(m - m_new);
-        const float p = exp2f(sc - m_new);
-        float sum = p;
+      for (int r = 0; r < kRows; ++r) {
+        float p = 0.f;
+        if (r >= ra && r < rb) {
+          const int lim = causal ? lim0 + (row0 + r) / g - tok0 : lim0;
+          const float sc = off >= 0 && key < lim ? x[r] : -INFINITY;
+          float top = sc;
 #pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        l = l * corr + sum;
+          for (int f = 16; f; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
+          const float mn = fmaxf(m[r], top);
+          // a row with no visible key so far keeps max -inf: its terms are 0
+          const float base = mn == -INFINITY ? 0.f : mn;
+          const float corr = exp2f(m[r] - base);
+          p = exp2f(sc - base);
+          float sum = p;
 #pragma unroll
-        for (int i = 0; i < kMaxDPerLane; ++i) acc[i] *= corr;
-        for (int j = 0; j < 32; ++j) {
-          const float pj = __shfl_sync(0xffffffffu, p, j);
-          const int64_t roff = __shfl_sync(0xffffffffu, row_off, j);
-          if (roff < 0) continue;
-          const T* vrow = v_cache + roff;
+          for (int f = 16; f; f >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, f);
+          m[r] = mn;
+          l[r] = fmaf(l[r], corr, sum);
 #pragma unroll
-          for (int i = 0; i < kMaxDPerLane; ++i)
-            if (i < dpl) acc[i] = fmaf(pj, to_f(vrow[lane + 32 * i]), acc[i]);
+          for (int i = 0; i < kPer; ++i) acc[r][i] *= corr;
         }
-        m = m_new;
+        p_s[lane * kRows + r] = p;
+      }
+      __syncwarp();
+      // the keys that some row sees (the others' values may be anything)
+      const int last = causal ? min(n, lim0 + (row0 + rb - 1) / g - tok0) : n;
+      const int count = min(32, last - k0);
+#pragma unroll 2
+      for (int j = 0; j < count; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, off, j);
+        if (at < 0) continue;
+        const float4 pa = *reinterpret_cast<const float4*>(p_s + j * kRows);
+        const float4 pb = *reinterpret_cast<const float4*>(p_s + j * kRows + 4);
+        const float w[kRows] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (i < dpl) {
+            const float v = to_f(v_cache[at + lane + 32 * i]);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+              // (a key past a causal row's limit has weight 0 and a written,
+              // finite or not, value of a later token: skip it, as 0 x inf is NaN)
+              if (w[r] != 0.f) acc[r][i] = fmaf(w[r], v, acc[r][i]);
+          }
+        }
+      }
+      __syncwarp();
+    };
+
+    int c = 0;      // chunks dealt so far
+    for (int k0 = 0; k0 < ds.prefix_len; k0 += 32, ++c)
+      if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, ds.prefix_len,
+                                    0, false);
+    for (int ra = 0; ra < rows;) {
+      // the rows of one sequence: row0 + ra .. row0 + rb - 1
+      const int t = (row0 + ra) / g;
+      const StepRow info = plan.rows[t];
+      const StepSeq e = info.unit >= 0 ? plan.streamed[info.unit] : plan.tiled[-1 - info.unit];
+      const int rb = min(rows, (e.row + e.n_new) * g - row0);
+      const int lim0 = e.ctx - e.n_new + info.token + 1;      // keys that token t sees
+      const int n = lim0 + (row0 + rb - 1) / g - t;           // and the last one
+      const int32_t* table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
+      for (int k0 = 0; k0 < n; k0 += 32, ++c)
+        if (c % stride == mine) chunk(table, k0, n, ra, rb, lim0, t, true);
+      ra = rb;
+    }
+
+    // ---- join the warps ----
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (lane == 0) {
+        join_ml[(warp * kRows + r) * 2] = m[r];
+        join_ml[(warp * kRows + r) * 2 + 1] = l[r];
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < dpl) join_o[(warp * kRows + r) * D + lane + 32 * i] = acc[r][i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * D; e += kThreads) {
+      const int r = e / D, d = e - r * D;
+      float M = -INFINITY, L = 0.f, a = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, join_ml[(w * kRows + r) * 2]);
+      const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(join_ml[(w * kRows + r) * 2] - base);
+        L = fmaf(f, join_ml[(w * kRows + r) * 2 + 1], L);
+        a = fmaf(f, join_o[(w * kRows + r) * D + d], a);
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const int64_t at = (int64_t)((row0 + r) / g) * s.H_q + kvh * g + (row0 + r) % g;
+      if (splits == 1) {
+        o[at * D + d] = from_f<T>(a * inv);
+      } else {
+        const int64_t to = (int64_t)split * ds.max_tokens * s.H_q + at;
+        part_o[to * D + d] = a * inv;
+        if (d == 0) part_lse[to] = L > 0.f ? M + log2f(L) : -INFINITY;
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    T* orow = o + ((int64_t)t * s.H_q + h) * D;
+    __syncthreads();
+  }
+}
+
+// O of the splits of a step: one warp per (row, query head).
+template <class T>
+__global__ void __launch_bounds__(128)
+    step_generic_join_kernel(DevStep ds, ShapeInfo s, const float* __restrict__ part_o,
+                             const float* __restrict__ part_lse, T* __restrict__ o, int splits) {
+  ptx::pdl_wait_previous();
+  ptx::pdl_launch_dependents();
+  const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+  const int lane = threadIdx.x & 31, D = s.D;
+  const int64_t rows = (int64_t)plan.header[kPlanRows] * s.H_q;
+  const int64_t all = (int64_t)ds.max_tokens * s.H_q;
+  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); w < rows;
+       w += (int64_t)gridDim.x * 4) {
+    const float mine = lane < splits ? part_lse[lane * all + w] : -INFINITY;
+    float M = mine;
 #pragma unroll
-    for (int i = 0; i < kMaxDPerLane; ++i)
-      if (i < dpl) orow[lane + 32 * i] = from_f<T>(acc[i] * inv);
-    __syncwarp();
+    for (int f = 16; f; f >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, f));
+    float f = mine == -INFINITY ? 0.f : exp2f(mine - M);
+    float sum = f;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    f = sum > 0.f ? f / sum : 0.f;
+    for (int d = lane; d < D; d += 32) {
+      float a = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < splits; ++i) {
+        const float wt = __shfl_sync(0xffffffffu, f, i);
+        a = fmaf(wt, part_o[(i * all + w) * D + d], a);
+      }
+      o[w * D + d] = from_f<T>(a);
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_step_generic(const DevStep& ds, const ShapeInfo& s, const void* q,
-                                const void* k_cache, const void* v_cache, void* o,
-                                cudaStream_t st) {
-  int dev = 0, sms = 0;
+// Blocks that share a block of rows: as many as bring the grid near two blocks
+// per SM, at most one per 256 keys of the prefix or of the longest sequence
+// the tables hold (a split costs a second launch).
+int step_generic_splits(const ShapeInfo& s, int32_t max_tokens, int32_t max_blocks,
+                        int32_t prefix_len, int sms) {
+  const int64_t units = ((int64_t)max_tokens * s.g + kRows - 1) / kRows * s.H_kv;
+  const int64_t keys = (int64_t)prefix_len + (int64_t)max_blocks * s.B;
+  const int64_t n = std::min<int64_t>(2 * (int64_t)sms / units, keys / 256);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(n, kStepGenericSplits));
+}
+
+size_t step_generic_workspace(const ShapeInfo& s, int32_t max_tokens, int splits) {
+  if (splits == 1) return 0;
+  return (size_t)splits * max_tokens * s.H_q * (s.D + 1) * 4;
+}
+
+namespace {
+
+template <class T, int kPer>
+cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, const void* k_cache,
+                        const void* v_cache, void* o, float* part_o, float* part_lse, int splits,
+                        int sms, cudaStream_t st) {
+  const int bytes = smem_floats(s.D) * 4;
+  // the shared-memory limit is raised once per device
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t warps = (int64_t)ds.max_tokens * s.H_q;
-  int64_t blocks = (warps + kWarps - 1) / kWarps;
-  if (blocks > (int64_t)sms * 16) blocks = (int64_t)sms * 16;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load() & bit)) {
+    e = cudaFuncSetAttribute(step_generic_kernel<T, kPer>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_floats(kPer * 32) * 4);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit);
+  }
+  const int64_t tiles = ((int64_t)ds.max_tokens * s.g + kRows - 1) / kRows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, (int64_t)sms * 16), (unsigned)s.H_kv,
+                     (unsigned)splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, step_generic_kernel<T, kPer>, ds, s, (const T*)q,
+                         (const T*)k_cache, (const T*)v_cache, (T*)o, part_o, part_lse, splits);
+  if (e != cudaSuccess || splits == 1) return e;
+  const int64_t warps = (int64_t)ds.max_tokens * s.H_q;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((warps + 3) / 4, (int64_t)sms * 16));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, step_generic_join_kernel<T>, ds, s, (const float*)part_o,
+                            (const float*)part_lse, (T*)o, splits);
+}
+
+template <class T>
+cudaError_t launch_type(const DevStep& ds, const ShapeInfo& s, const void* q, const void* k_cache,
+                        const void* v_cache, void* o, float* po, float* pl, int splits, int sms,
+                        cudaStream_t st) {
+  if (s.D <= 64)
+    return launch_rows<T, 2>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
+  if (s.D <= 128)
+    return launch_rows<T, 4>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
+  return launch_rows<T, 8>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_step_generic(const DevStep& ds, const ShapeInfo& s, const void* q,
+                                const void* k_cache, const void* v_cache, void* o,
+                                void* workspace, int splits, int sms, cudaStream_t st) {
+  float* po = (float*)workspace;
+  float* pl = po ? po + (size_t)splits * ds.max_tokens * s.H_q * s.D : nullptr;
   if (s.dtype == 0)
-    return cudaLaunchKernelEx(&cfg, step_generic_kernel<__nv_bfloat16>, ds, s,
-                              (const __nv_bfloat16*)q, (const __nv_bfloat16*)k_cache,
-                              (const __nv_bfloat16*)v_cache, (__nv_bfloat16*)o);
-  return cudaLaunchKernelEx(&cfg, step_generic_kernel<float>, ds, s, (const float*)q,
-                            (const float*)k_cache, (const float*)v_cache, (float*)o);
+    return launch_type<__nv_bfloat16>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
+  return launch_type<float>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
 }
 
 }  // namespace rbkv

@@ -139,10 +139,11 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
   const int W = (a.num_blocks + 31) / 32;
   const int wper = (W + C - 1) / C;
   const int w0 = min((int)rank * wper, W), n_words = min(wper, W - w0);
-  // this thread's: sequences [sa, sb) and words [wa, wb) of the CTA's
-  const int ks = (n_seqs + kThreads - 1) / kThreads, kw = (n_words + kThreads - 1) / kThreads;
+  // this thread's sequences [sa, sb) and this warp's words [wa, wb) of the CTA's
+  const int ks = (n_seqs + kThreads - 1) / kThreads;
   const int sa = min(tid * ks, n_seqs), sb = min(sa + ks, n_seqs);
-  const int wa = min(tid * kw, n_words), wb = min(wa + kw, n_words);
+  const int kw = ((n_words + kWarps - 1) / kWarps + 31) & ~31;
+  const int wa = min(warp * kw, n_words), wb = min(wa + kw, n_words);
   const bool on_chip = n_seqs <= kSmemSeqs;
   // bits past the pool's last block count for nothing
   auto pool_word = [&](int w) -> uint32_t {
@@ -163,7 +164,8 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
 #pragma unroll
     for (int x = 0; x < kSums; ++x) mine[x] += v[x];
   }
-  for (int w = wa; w < wb; ++w) mine[kFreeBits] += __popc(pool_word(w0 + w));
+#pragma unroll 4
+  for (int w = wa + lane; w < wb; w += 32) mine[kFreeBits] += __popc(pool_word(w0 + w));
   int32_t at[kSums];       // sums before this thread
 #pragma unroll
   for (int i = 0; i < kSums; ++i) at[i] = mine[i];
@@ -210,7 +212,8 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSums; ++i) at[i] += sh.warp_sum[i][warp] - mine[i];
+  for (int i = 0; i < kFreeBits; ++i) at[i] += sh.warp_sum[i][warp] - mine[i];
+  at[kFreeBits] = sh.warp_sum[kFreeBits][warp];   // before the warp
 
   // ---- the step's totals, and what the CTAs before this one hold ----
   int32_t total[kSums];
@@ -303,25 +306,31 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
   }
 
   // ---- the lowest free ids, taken out of the bitmap ----
-  int32_t k = at[kFreeBits];
-  for (int i = wa; i < wb; ++i) {
-    const int w = w0 + i;
-    uint32_t left = pool_word(w), taken = 0;
-    if (k + __popc(left) <= grow) {
-      taken = left;        // the whole word
-    } else {
-      uint32_t rest = left;
-      for (int n = k; n < grow; ++n) {
-        taken |= rest & (0u - rest);
-        rest &= rest - 1;
+  const bool in_place = a.free_words == a.free_in;
+  int32_t before = at[kFreeBits];
+  for (int i = wa; i < wb; i += 32) {
+    if (before >= grow && in_place) break;      // what is left stays as it is
+    const int w = w0 + i + lane;
+    const bool live = i + lane < wb;
+    const uint32_t word = live ? (uint32_t)a.free_in[w] : 0u;
+    uint32_t taken = 0;
+    if (before < grow) {
+      uint32_t rest = live ? pool_word(w) : 0u;
+      int32_t inc = __popc(rest), n = inc;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int32_t up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
       }
+      for (int32_t k = before + inc - n; rest && k < grow; ++k) {
+        const uint32_t low = rest & (0u - rest);
+        rest ^= low;
+        taken |= low;
+        plan.new_ids[k] = w * 32 + 31 - __clz(low);
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    const int next = k + __popc(left);
-    for (uint32_t rest = taken; rest; rest &= rest - 1)
-      plan.new_ids[k++] = w * 32 + __ffs(rest) - 1;
-    if (a.free_words != a.free_in || taken)
-      a.free_words[w] = (int32_t)((uint32_t)a.free_in[w] & ~taken);
-    k = next;
+    if (live && (taken || !in_place)) a.free_words[w] = (int32_t)(word & ~taken);
   }
 
   // ---- rows past the step's ----
