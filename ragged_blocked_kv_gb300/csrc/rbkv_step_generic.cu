@@ -52,6 +52,12 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                      __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Shared memory: q [kRows][D], each warp's weights [32 keys][kRows], and for
 // the join O [warp][row][D] and (max, sum) [warp][row].
 __host__ __device__ constexpr int smem_floats(int D) {
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int r = 0; r < kRows; ++r) x[r] = 0.f;
       if (off >= 0) {
         const T* kr = k_cache + off;
-#pragma unroll 4
+#pragma unroll 8
         for (int d = 0; d < D; d += 4) {
           const float4 k = load4(kr + d);
 #pragma unroll
@@ -132,19 +138,14 @@ __global__ void __launch_bounds__(kThreads)
         if (r >= ra && r < rb) {
           const int lim = causal ? lim0 + (row0 + r) / g - tok0 : lim0;
           const float sc = off >= 0 && key < lim ? x[r] : -INFINITY;
-          float top = sc;
-#pragma unroll
-          for (int f = 16; f; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
+          const float top = warp_max(sc);
           const float mn = fmaxf(m[r], top);
           // a row with no visible key so far keeps max -inf: its terms are 0
           const float base = mn == -INFINITY ? 0.f : mn;
           const float corr = exp2f(m[r] - base);
           p = exp2f(sc - base);
-          float sum = p;
-#pragma unroll
-          for (int f = 16; f; f >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, f);
           m[r] = mn;
-          l[r] = fmaf(l[r], corr, sum);
+          l[r] = fmaf(l[r], corr, p);       // this lane's keys; summed at the end
 #pragma unroll
           for (int i = 0; i < kPer; ++i) acc[r][i] *= corr;
         }
@@ -154,22 +155,31 @@ __global__ void __launch_bounds__(kThreads)
       // the keys that some row sees (the others' values may be anything)
       const int last = causal ? min(n, lim0 + (row0 + rb - 1) / g - tok0) : n;
       const int count = min(32, last - k0);
-#pragma unroll 2
-      for (int j = 0; j < count; ++j) {
-        const int64_t at = __shfl_sync(0xffffffffu, off, j);
-        if (at < 0) continue;
-        const float4 pa = *reinterpret_cast<const float4*>(p_s + j * kRows);
-        const float4 pb = *reinterpret_cast<const float4*>(p_s + j * kRows + 4);
-        const float w[kRows] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+      // (several value rows in flight: their latency is what a chunk waits for)
+      constexpr int kAhead = 16 / kPer;
+      for (int j0 = 0; j0 < count; j0 += kAhead) {
+        float v[kAhead][kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (i < dpl) {
-            const float v = to_f(v_cache[at + lane + 32 * i]);
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t at = __shfl_sync(0xffffffffu, off, j0 + u);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
-              // (a key past a causal row's limit has weight 0 and a written,
-              // finite or not, value of a later token: skip it, as 0 x inf is NaN)
-              if (w[r] != 0.f) acc[r][i] = fmaf(w[r], v, acc[r][i]);
+          for (int i = 0; i < kPer; ++i)
+            v[u][i] = i < dpl && at >= 0 && j0 + u < count ? to_f(v_cache[at + lane + 32 * i])
+                                                           : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const float4 pa = *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows);
+          const float4 pb = *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows + 4);
+          const float w[kRows] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            // (a key past a causal row's limit has weight 0 and the value of a
+            // later token, finite or not: skip it, as 0 x inf is NaN)
+            if (w[r] != 0.f) {
+#pragma unroll
+              for (int i = 0; i < kPer; ++i) acc[r][i] = fmaf(w[r], v[u][i], acc[r][i]);
+            }
           }
         }
       }
@@ -197,6 +207,8 @@ __global__ void __launch_bounds__(kThreads)
     // ---- join the warps ----
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+      for (int f = 16; f; f >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], f);
       if (lane == 0) {
         join_ml[(warp * kRows + r) * 2] = m[r];
         join_ml[(warp * kRows + r) * 2 + 1] = l[r];
