@@ -94,8 +94,10 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
     float m[kRows], l[kRows], acc[kRows][kPer];
+    int tok[kRows];        // the rows' tokens (rows of the step)
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
+      tok[r] = (row0 + r) / g;
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     // One 32-key chunk for the rows [ra, rb) of the block; row r sees the keys
-    // below lim0 + (token of r - first token).
+    // below lim0 + (token of r - tok0), or all n.
     auto chunk = [&](const int32_t* ids, int k0, int n, int ra, int rb, int lim0, int tok0,
                      bool causal) {
       const int key = k0 + lane;
@@ -118,69 +120,62 @@ __global__ void __launch_bounds__(kThreads)
       float x[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) x[r] = 0.f;
-      if (off >= 0) {
-        const T* kr = k_cache + off;
-#pragma unroll 8
-        for (int d = 0; d < D; d += 4) {
-          const float4 k = load4(kr + d);
+      // (all of a 32-element piece of the key row requested before any of it is used)
+      const T* kr = k_cache + max((int64_t)0, off);
+      for (int d0 = 0; d0 < D; d0 += 32) {
+        float4 k[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) k[u] = load4(kr + d0 + 4 * u);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
-            if (r >= ra && r < rb) {
-              const float4 a = *reinterpret_cast<const float4*>(q_s + r * D + d);
-              x[r] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, x[r]))));
-            }
+            const float4 a = *reinterpret_cast<const float4*>(q_s + r * D + d0 + 4 * u);
+            x[r] = fmaf(a.x, k[u].x, fmaf(a.y, k[u].y, fmaf(a.z, k[u].z, fmaf(a.w, k[u].w, x[r]))));
           }
         }
       }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        float p = 0.f;
-        if (r >= ra && r < rb) {
-          const int lim = causal ? lim0 + (row0 + r) / g - tok0 : lim0;
-          const float sc = off >= 0 && key < lim ? x[r] : -INFINITY;
-          const float top = warp_max(sc);
-          const float mn = fmaxf(m[r], top);
-          // a row with no visible key so far keeps max -inf: its terms are 0
-          const float base = mn == -INFINITY ? 0.f : mn;
-          const float corr = exp2f(m[r] - base);
-          p = exp2f(sc - base);
-          m[r] = mn;
-          l[r] = fmaf(l[r], corr, p);       // this lane's keys; summed at the end
+        // (other sequences' rows see none of these keys: their terms are 0)
+        const int lim = r < ra || r >= rb ? 0 : causal ? lim0 + tok[r] - tok0 : n;
+        const float sc = off >= 0 && key < lim ? x[r] : -INFINITY;
+        const float mn = fmaxf(m[r], warp_max(sc));
+        // a row with no visible key so far keeps max -inf: its terms are 0
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float corr = ptx::ex2(m[r] - base), p = ptx::ex2(sc - base);
+        m[r] = mn;
+        l[r] = fmaf(l[r], corr, p);       // this lane's keys; summed at the end
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) acc[r][i] *= corr;
-        }
+        for (int i = 0; i < kPer; ++i) acc[r][i] *= corr;
         p_s[lane * kRows + r] = p;
       }
       __syncwarp();
-      // the keys that some row sees (the others' values may be anything)
-      const int last = causal ? min(n, lim0 + (row0 + rb - 1) / g - tok0) : n;
-      const int count = min(32, last - k0);
-      // (several value rows in flight: their latency is what a chunk waits for)
+      // several value rows in flight: their latency is what a chunk waits for
+      const int count = min(32, n - k0);
       constexpr int kAhead = 16 / kPer;
       for (int j0 = 0; j0 < count; j0 += kAhead) {
         float v[kAhead][kPer];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int64_t at = __shfl_sync(0xffffffffu, off, j0 + u);
+          // (a key that no row sees has weight 0: any row may stand in)
+          const int64_t at = max((int64_t)0, __shfl_sync(0xffffffffu, off, j0 + u));
+          const T* vr = v_cache + at + lane;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            v[u][i] = i < dpl && at >= 0 && j0 + u < count ? to_f(v_cache[at + lane + 32 * i])
-                                                           : 0.f;
+          for (int i = 0; i < kPer; ++i) v[u][i] = to_f(vr[32 * min(i, dpl - 1)]);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const float4 pa = *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows);
           const float4 pb = *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows + 4);
           const float w[kRows] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+          // (a weight of 0 leaves the sum alone: the value may be another
+          // sequence's or a later token's, finite or not, and 0 x inf is NaN)
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            // (a key past a causal row's limit has weight 0 and the value of a
-            // later token, finite or not: skip it, as 0 x inf is NaN)
-            if (w[r] != 0.f) {
+          for (int r = 0; r < kRows; ++r)
 #pragma unroll
-              for (int i = 0; i < kPer; ++i) acc[r][i] = fmaf(w[r], v[u][i], acc[r][i]);
-            }
-          }
+            for (int i = 0; i < kPer; ++i)
+              acc[r][i] = w[r] != 0.f ? fmaf(w[r], v[u][i], acc[r][i]) : acc[r][i];
         }
       }
       __syncwarp();
@@ -188,8 +183,7 @@ __global__ void __launch_bounds__(kThreads)
 
     int c = 0;      // chunks dealt so far
     for (int k0 = 0; k0 < ds.prefix_len; k0 += 32, ++c)
-      if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, ds.prefix_len,
-                                    0, false);
+      if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, 0, 0, false);
     for (int ra = 0; ra < rows;) {
       // the rows of one sequence: row0 + ra .. row0 + rb - 1
       const int t = (row0 + ra) / g;
