@@ -10,12 +10,15 @@ namespace rbkv {
 // at most this go to the streaming kernel, longer ones to the tile kernel.
 constexpr int kStepPackedRows = 16;
 constexpr int kStepStreamKeys = 16;     // keys per tile of the streaming kernel
-constexpr int kStepPipes = 8;           // its pipelines (warps) per SM
+constexpr int kStepPipes = 4;           // its pipelines (warps) per CTA
 constexpr int kStepTileKeys = 128;      // keys per tile of the tensor-core kernel
 constexpr int kStepTileRows = 128;      // packed query rows per tensor-core tile
 
 // Tokens whose packed rows fill one tensor-core query tile.
 __host__ __device__ __forceinline__ int step_tile_tokens(int g) { return kStepTileRows / g; }
+
+// Shared memory of a tile kernel CTA (beside which a streaming one fits).
+constexpr int kStepTileSmem = 4 * 32768 + 512;
 
 // What a unit of work costs beside its key tiles (queries in, results out), in
 // key tiles of its kernel, for the even cut of the work over the CTAs.
@@ -102,27 +105,26 @@ __host__ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int6
   return total;
 }
 
-// A tiled sequence's new tokens are taken in pairs of tensor-core tiles of
-// `pair` tokens together.  Pair k sees the keys below
-// seen + min(n_new, (k + 1) pair): its key tiles; the line length of the pairs
-// before it; and the line length of all of them.
-__host__ __device__ __forceinline__ int32_t step_pair_tiles(int32_t seen, int32_t n_new,
-                                                            int32_t pair, int32_t k) {
-  const int64_t end = (int64_t)(k + 1) * pair;
+// A tiled sequence's new tokens are taken in query tiles of `tokens` each.
+// Tile k sees the keys below seen + min(n_new, (k + 1) tokens): its key tiles;
+// the line length of the query tiles before it; and that of all of them.
+__host__ __device__ __forceinline__ int32_t step_key_tiles(int32_t seen, int32_t n_new,
+                                                           int32_t tokens, int32_t k) {
+  const int64_t end = (int64_t)(k + 1) * tokens;
   const int64_t keys = seen + (end < n_new ? end : (int64_t)n_new);
   return (int32_t)((keys + kStepTileKeys - 1) / kStepTileKeys);
 }
-__host__ __device__ __forceinline__ int64_t step_len_before(int32_t seen, int32_t pair,
+__host__ __device__ __forceinline__ int64_t step_len_before(int32_t seen, int32_t tokens,
                                                             int32_t k) {
-  // every pair before another one is whole
-  return floor_sum(k, kStepTileKeys, pair, (int64_t)seen + pair + kStepTileKeys - 1) +
+  // every tile before another one is whole
+  return floor_sum(k, kStepTileKeys, tokens, (int64_t)seen + tokens + kStepTileKeys - 1) +
          (int64_t)k * kStepTileUnit;
 }
 __host__ __device__ __forceinline__ int64_t step_seq_len(int32_t seen, int32_t n_new,
-                                                         int32_t pair) {
-  const int32_t pairs = (int32_t)(((int64_t)n_new + pair - 1) / pair);
-  return step_len_before(seen, pair, pairs - 1) +
-         step_pair_tiles(seen, n_new, pair, pairs - 1) + kStepTileUnit;
+                                                         int32_t tokens) {
+  const int32_t tiles = (int32_t)(((int64_t)n_new + tokens - 1) / tokens);
+  return step_len_before(seen, tokens, tiles - 1) +
+         step_key_tiles(seen, n_new, tokens, tiles - 1) + kStepTileUnit;
 }
 
 // What the kernels of a step see.
@@ -152,15 +154,15 @@ __host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, i
 // The units of the streaming kernel: (streamed sequence, KV head), the KV
 // heads of a sequence in order; then, when the whole step has at most
 // kStepPackedRows packed rows, the prefix as one more sequence.
-// The units of the tile kernel: (KV head, pair of query tiles) over the
-// prefix unless it is streamed; then (tiled sequence, KV head, pair).
+// The units of the tile kernel: (KV head, query tile) over the prefix unless it
+// is streamed; then (tiled sequence, KV head, query tile).
 struct StepWork {
   int64_t stream_own, stream_total;
   int64_t tile_prefix, tile_total;
   int32_t rows, streamed;             // query rows; streamed sequences
   int32_t prefix_stream_tiles;        // 16-key tiles of the prefix, when streamed
   int32_t prefix_tile_steps;          // 128-key tiles of the prefix, when tiled
-  int32_t prefix_pairs;               // pairs of query tiles over the prefix
+  int32_t prefix_rows;                // query tiles of a KV head over the prefix
 };
 
 __host__ __device__ __forceinline__ bool step_prefix_streamed(int32_t max_tokens, int32_t g) {
@@ -179,15 +181,15 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
   const int32_t P = T > 0 ? ds.prefix_len : 0;
   w.prefix_stream_tiles = streamed ? (P + kStepStreamKeys - 1) / kStepStreamKeys : 0;
   w.prefix_tile_steps = streamed ? 0 : (int32_t)(((int64_t)P + kStepTileKeys - 1) / kStepTileKeys);
-  const int32_t pair = 2 * step_tile_tokens(s.g);
-  w.prefix_pairs = (T + pair - 1) / pair;
+  const int32_t tokens = step_tile_tokens(s.g);
+  w.prefix_rows = (T + tokens - 1) / tokens;
   w.stream_own = (int64_t)h.w * s.H_kv;
   w.stream_total = w.stream_own;
   if (w.prefix_stream_tiles)
     w.stream_total += (int64_t)(w.prefix_stream_tiles + kStepStreamUnit) * s.H_kv;
   w.tile_prefix = 0;
   if (w.prefix_tile_steps)
-    w.tile_prefix = (int64_t)s.H_kv * w.prefix_pairs * (w.prefix_tile_steps + kStepTileUnit);
+    w.tile_prefix = (int64_t)s.H_kv * w.prefix_rows * (w.prefix_tile_steps + kStepTileUnit);
   w.tile_total = w.tile_prefix + (int64_t)plan.header[kPlanTileLen] * s.H_kv;
   return w;
 }
@@ -197,15 +199,20 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
 struct StepWorkspace {
   float *own_o, *pre_o;         // [max_tokens][H_q][128]
   float *own_lse, *pre_lse;     // [max_tokens][H_q]
-  float *stream_o, *stream_lse; // spill rows [stream grid][kStepPackedRows]
-  float *tile_o, *tile_lse;     // spill rows [tile grid][2 kStepTileRows]
-  int32_t stream_grid, tile_grid;
+  float *stream_o, *stream_lse; // spill rows [stream grid kStepPipes][kStepPackedRows]
+  float *tile_o, *tile_lse;     // spill rows [tile grid][kStepTileRows]
+  int32_t stream_grid, tile_grid;     // CTAs (the streaming kernel's: two per SM)
 };
 
 #ifdef __CUDACC__
-// Pipelines of the streaming kernel that take part.
+// CTAs of the streaming kernel that take part: two per SM, or one beside the
+// tile kernel's CTA where that has work; and the pipelines among them.
+__device__ __forceinline__ int64_t step_stream_ctas(const StepWorkspace& ws,
+                                                    const StepWork& work) {
+  return work.tile_total > 0 ? ws.stream_grid / 2 : ws.stream_grid;
+}
 __device__ __forceinline__ int64_t step_pipes(const StepWorkspace& ws, const StepWork& work) {
-  return min((int64_t)ws.stream_grid, work.stream_total);
+  return min(step_stream_ctas(ws, work) * kStepPipes, work.stream_total);
 }
 #endif
 

@@ -3,7 +3,10 @@
 // keys; every cached K/V byte is read once, so HBM bounds it.
 //
 // The units lie on one line in groups of 16 keys, cut evenly (rbkv_step.h) over
-// eight warps per SM.  Each warp is a pipeline of its own: lane 0 keeps a ring
+// eight warps per SM, in two CTAs - or four in one CTA beside a CTA of the tile
+// kernel, whose tensor-core work then runs under the memory traffic of this
+// one (they share an SM's registers and shared memory by design: 99 and 129
+// KB).  Each warp is a pipeline of its own: lane 0 keeps a ring
 // of three 8 KB groups (16 keys of K and V, one TMA copy each) in flight,
 // and the warp multiplies, exponentiates and accumulates a group at a time:
 //   S^T = K Q^T   (m16n8k16: 16 keys x 8 query rows, one or two such tiles)
@@ -42,7 +45,9 @@ constexpr int kRows = kStepPackedRows;
 constexpr int kSegments = kStages + 2;        // segments that a warp's window can meet
 constexpr int kSmemBytes =
     kWarps * (kStages * kStage + kSegments * 32 + kStages * 8);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024 &&
+              kSmemBytes + kStepTileSmem + 2 * 1024 <= 228 * 1024,
+              "two CTAs per SM, or one beside the tile kernel's");
 constexpr long long kWaitLimit = 4000000000LL;   // ~2 s of SM clock
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -476,7 +481,7 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     step_stream_kernel(const __grid_constant__ Maps maps, DevStep ds, ShapeInfo shp,
                        StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
                        __nv_bfloat16* __restrict__ o, int first) {
@@ -488,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const StepWork work = step_work(ds, shp, plan);
   const int64_t pipes = step_pipes(ws, work);
   // neighbouring parts on different SMs
-  const int64_t pipe = (int64_t)warp * gridDim.x + blockIdx.x;
+  const int64_t ctas = step_stream_ctas(ws, work);
+  const int64_t pipe = blockIdx.x < ctas ? (int64_t)warp * ctas + blockIdx.x : pipes;
   if (ptx::smem_u32(smem_raw) & 1023) {
     // the swizzled layout needs a 1024-byte aligned base
     if (threadIdx.x == 0) atomicCAS(ds.status, 0, kDevBounds);
@@ -547,7 +553,6 @@ constexpr int kJoinWideRows = 32;   // steps of at most this many rows: W = 8
 // Spills of a unit that a row joins: of CTAs [first, first + n).
 struct Spills {
   int first, n;
-  int cut;        // the unit was cut between its tiles
 };
 
 __device__ __forceinline__ int first_cut(int64_t p, int64_t total, int ctas) {
@@ -626,11 +631,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       }
     }
     const StepRow r = plan.rows[t];
-    const int pair = r.token / (2 * tpt), in_pair = r.token - pair * 2 * tpt;
+    const int tile = r.token / tpt;
     if (threadIdx.x < 2 * kHeads) {
       const int kv = kv0 + (threadIdx.x >> 1);
       int64_t begin = 0, total = work.stream_total;
-      int unit = kStepStreamUnit, tiles = 0, seen_tiles = 0, ctas = s_ctas;
+      int unit = kStepStreamUnit, tiles = 0, ctas = s_ctas;
       if (kv >= shp.H_kv) {
         // (past the last head)
       } else if (threadIdx.x & 1) {
@@ -640,32 +645,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         } else if (pre) {
           tiles = work.prefix_tile_steps;
           unit = kStepTileUnit;
-          begin = ((int64_t)kv * work.prefix_pairs + t / (2 * tpt)) * (tiles + unit);
+          begin = ((int64_t)kv * work.prefix_rows + t / tpt) * (tiles + unit);
           total = work.tile_total;
           ctas = t_ctas;
         }
-        seen_tiles = tiles;
       } else if (r.unit >= 0) {
-        seen_tiles = tiles = r.tiles;
+        tiles = r.tiles;
         begin = (int64_t)shp.H_kv * r.cum + (int64_t)kv * (tiles + unit);
       } else {
         const StepSeq e = plan.tiled[-1 - r.unit];
-        const int seen = e.ctx - e.n_new;
-        tiles = step_pair_tiles(seen, e.n_new, 2 * tpt, pair);
-        // key tiles of the row's own query tile
-        const int end = min(e.n_new, (2 * pair + (in_pair < tpt ? 1 : 2)) * tpt);
-        seen_tiles = (seen + end + kStepTileKeys - 1) / kStepTileKeys;
+        tiles = step_key_tiles(e.ctx - e.n_new, e.n_new, tpt, tile);
         unit = kStepTileUnit;
         begin = work.tile_prefix + (int64_t)shp.H_kv * r.cum + (int64_t)kv * r.tiles +
-                step_len_before(seen, 2 * tpt, pair);
+                step_len_before(e.ctx - e.n_new, tpt, tile);
         total = work.tile_total;
         ctas = t_ctas;
       }
-      Spills s = {0, 0, 0};
+      Spills s = {0, 0};
       if (tiles > 0) {
         s.first = first_cut(begin + unit + 1, total, ctas);
-        s.n = max(0, first_cut(begin + unit + seen_tiles, total, ctas) - s.first);
-        s.cut = first_cut(begin + unit + tiles, total, ctas) > s.first;
+        s.n = first_cut(begin + unit + tiles, total, ctas) - s.first;
       }
       spills[threadIdx.x] = s;
     }
@@ -677,19 +676,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       j.add<2>(l2, v2);
       const int n = a.n + p.n;
       if (n > wi) {
-        const int tile_row = in_pair < tpt ? in_pair * g : kStepTileRows + (in_pair - tpt) * g;
-        const int pre_in = t % (2 * tpt);
-        const int pre_row = pre_in < tpt ? pre_in * g : kStepTileRows + (pre_in - tpt) * g;
         const Part mine = r.unit >= 0
             ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + r.token * g + hh,
                    kStepPackedRows}
-            : Part{ws.tile_o, ws.tile_lse, a.first * 2 * kStepTileRows + tile_row + hh,
-                   2 * kStepTileRows};
+            : Part{ws.tile_o, ws.tile_lse,
+                   a.first * kStepTileRows + (r.token - tile * tpt) * g + hh, kStepTileRows};
         const Part theirs = pre_streamed
             ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + t * g + hh,
                    kStepPackedRows}
-            : Part{ws.tile_o, ws.tile_lse, p.first * 2 * kStepTileRows + pre_row + hh,
-                   2 * kStepTileRows};
+            : Part{ws.tile_o, ws.tile_lse, p.first * kStepTileRows + (t % tpt) * g + hh,
+                   kStepTileRows};
         constexpr int kAtOnce = W > 1 ? 8 : 4;
         for (int k0 = wi; k0 < n; k0 += kAtOnce * W) {
           float l[kAtOnce];
@@ -735,7 +731,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         }
       }
       // (a unit that was whole and alone: its kernel wrote O)
-      if (wi == 0 && (pre || a.cut)) {
+      if (wi == 0 && (pre || a.n > 0)) {
         const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
         uint2 out;
         out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
@@ -764,16 +760,16 @@ size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* bas
   };
   const int64_t rows = (int64_t)max_tokens * s.H_q;
   StepWorkspace v;
-  v.stream_grid = kStepPipes * sms;
+  v.stream_grid = 2 * sms;
   v.tile_grid = sms;
   v.own_o = take(rows * 128);
   v.pre_o = take(rows * 128);
   v.own_lse = take(rows);
   v.pre_lse = take(rows);
-  v.stream_o = take((int64_t)v.stream_grid * kStepPackedRows * 128);
-  v.stream_lse = take((int64_t)v.stream_grid * kStepPackedRows);
-  v.tile_o = take((int64_t)v.tile_grid * 2 * kStepTileRows * 128);
-  v.tile_lse = take((int64_t)v.tile_grid * 2 * kStepTileRows);
+  v.stream_o = take((int64_t)v.stream_grid * kStepPipes * kStepPackedRows * 128);
+  v.stream_lse = take((int64_t)v.stream_grid * kStepPipes * kStepPackedRows);
+  v.tile_o = take((int64_t)v.tile_grid * kStepTileRows * 128);
+  v.tile_lse = take((int64_t)v.tile_grid * kStepTileRows);
   if (w) *w = v;
   return at;
 }
@@ -808,7 +804,7 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
     attr_done.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(w.stream_grid / kStepPipes));
+  cfg.gridDim = dim3((unsigned)w.stream_grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;

@@ -64,7 +64,7 @@ __device__ __forceinline__ int32_t measure(const BuildArgs& a, int32_t seen, int
     v[kStreamLen] = (int32_t)((ctx + kStepStreamKeys - 1) / kStepStreamKeys) + kStepStreamUnit;
   } else {
     v[kTiled] = 1;
-    const int64_t len = step_seq_len(seen, n_new, 2 * step_tile_tokens(a.group));
+    const int64_t len = step_seq_len(seen, n_new, step_tile_tokens(a.group));
     if (len >= (int64_t)kMaxLen) return kErrCapacity;
     v[kTileLen] = (int32_t)len;
   }

@@ -61,6 +61,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -159,6 +167,34 @@ __device__ __forceinline__ void tc_mma_ss_k128(uint32_t d_tmem, uint32_t a_lo, u
       "add.u32 a, %1, 1030;\n\tadd.u32 b, %2, 1030;\n\tmov.b64 da, {a, %3};\n\tmov.b64 db, {b, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p1;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// TS over K = 128 with both operands K-major: A (bf16 pairs) in tensor memory,
+// step kk at column a_tmem + 8kk; B with 128-byte swizzle and two 64-column
+// halves 16 KB apart, as in the SS form above.
+__device__ __forceinline__ void tc_mma_ts_kmajor_k128(uint32_t d_tmem, uint32_t a_tmem,
+                                                      uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b32 a, b;\n\t.reg .b64 db;\n\t"
+      "setp.ne.u32 p0, %4, %4;\n\tsetp.eq.u32 p1, %4, %4;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p0;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 2;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 4;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 6;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t"
+      "add.u32 a, %1, 32;\n\tadd.u32 b, %2, 1024;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t"
+      "add.u32 a, %1, 40;\n\tadd.u32 b, %2, 1026;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t"
+      "add.u32 a, %1, 48;\n\tadd.u32 b, %2, 1028;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t"
+      "add.u32 a, %1, 56;\n\tadd.u32 b, %2, 1030;\n\tmov.b64 db, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, p1;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc)
       : "memory");
 }
 
