@@ -18,7 +18,7 @@ constexpr int kStepTileRows = 128;      // packed query rows per tensor-core til
 __host__ __device__ __forceinline__ int step_tile_tokens(int g) { return kStepTileRows / g; }
 
 // Shared memory of a tile kernel CTA (beside which a streaming one fits).
-constexpr int kStepTileSmem = 4 * 32768 + 512;
+constexpr int kStepTileSmem = 4 * 32768 + 1024;
 
 // What a unit of work costs beside its key tiles (queries in, results out), in
 // key tiles of its kernel, for the even cut of the work over the CTAs.

@@ -13,14 +13,24 @@
 // The streaming kernel's memory traffic runs beside this kernel's tensor work
 // on the same SM, so this one keeps to 129 KB of shared memory and half of the
 // registers.  Roles:
-//  - warp 4 (TMA): streams 128-key K and V tiles through a 4-stage ring of
-//    32 KB (128-byte swizzle), in the order K0 K1 V0 K2 V1 K3 ...; lane i
-//    copies box i of a tile (one block, or 128 keys of a larger one);
+//  - warps 4 and 7 (TMA): stream the 128-key tiles of K and of V through a
+//    4-stage ring of 32 KB (128-byte swizzle), in the order K0 K1 V0 K2 V1 K3
+//    ..., one box per block (or 128 keys of a larger one) and half of the head
+//    dim; the lanes hold the block ids, one elected lane copies.  (A copy costs
+//    its thread about 200 cycles: one warp for both could not keep up with a
+//    step of 1600);
 //  - warp 5 (MMA): one elected lane issues S = Q K^T (M=128, N=128 keys,
 //    K=128; Q from tensor memory) into one of two score buffers and
 //    O += P V (P from tensor memory), in the order QK(0) QK(1), then per key
 //    tile j: PV(j) QK(j+2).  The next tile's scores are so computed under the
 //    softmax of the current one;
+//  - warp 6 walks the line and publishes the segments to the other roles (one
+//    copy of that code: the kernel starts with cold instruction caches, and a
+//    second copy cost a segment 4000 cycles); and it reports, with the softmax
+//    threads, that a tile's products may be issued: it has seen V_j and K_j+2
+//    land, so that the issuing thread has one wait per step (a wait costs it
+//    200 to 450 cycles while its products are queued) and the softmax threads
+//    none for the ring;
 //  - warps 0-3 (softmax): thread i owns packed row i = TMEM lane i.  It writes
 //    its row of Q into tensor memory (two Q buffers: the next unit's is
 //    written while the current one's last products run), keeps a running max
@@ -56,10 +66,11 @@ constexpr int kKeys = kStepTileKeys;        // 128 keys per KV tile (MMA N of QK
 constexpr int kStages = 4;                  // ring stages, each one K or one V tile
 constexpr int kHalf = kKeys * 128;          // 16 KB: 128 rows x 64 head dims
 constexpr int kTileBytes = 2 * kHalf;       // 32 KB: 128 rows x 128 head dims
-constexpr int kProducerWarp = 4;
+constexpr int kKeyWarp = 4, kValueWarp = 7;
 constexpr int kMmaWarp = 5;
-// Two warpgroups: the softmax warps, and one with the TMA and MMA warps (its
-// other two warps idle).  Launched at kLaunchRegs a thread, the second gives
+constexpr int kWalkWarp = 6;
+constexpr int kSegments = 8, kAhead = 3;    // published segments, and how far ahead
+// Two warpgroups: the softmax warps, and one with the other roles.  Launched at kLaunchRegs a thread, the second gives
 // back down to kIssueRegs and the first takes kSoftmaxRegs: the shares add up
 // to the launch's total (a larger claim would wait forever), and the launch's
 // total leaves half of an SM's registers to a streaming CTA.
@@ -76,6 +87,20 @@ constexpr long long kWaitLimit = 4000000000LL;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
+// One segment of a unit, as published (n = 0: there are no more).
+struct __align__(16) Segment {
+  const int32_t* table;
+  int kv_head;
+  int row, n_tok;  // first row and tokens of the query tile
+  int pos;         // last key its first token sees (the prefix: every token)
+  int kb, ke;      // key range of the segment
+  int n;           // its key tiles
+  int flags;
+  int pad[2];
+};
+static_assert(sizeof(Segment) == 48, "Segment is 12 int32");
+enum { kPrefix = 1, kHead = 2, kWhole = 4 };
+
 // Each barrier is waited on in order of its phases and can never run two
 // phases ahead of a waiter (the parity of a wait is then unambiguous).
 struct Bars {
@@ -83,32 +108,27 @@ struct Bars {
   uint64_t kv_full[kStages];      // a K or V tile landed (TMA)
   uint64_t kv_empty[kStages];     // the MMAs are done with the stage
   uint64_t s_full[2];             // QK^T of a key tile done, by score buffer
-  uint64_t p_full[2];             // its P written (and V tail rows zeroed)
+  uint64_t p_full[2];             // its P written, V tail rows zeroed, V_j and K_j+2 landed
   uint64_t o_done[2];             // its PV done
   uint64_t o_free;                // a unit's O read: the next unit may overwrite it
   uint64_t drain;                 // every MMA the CTA issued done
+  uint64_t published[kSegments];  // a segment is in its slot
+  Segment segments[kSegments];
   uint32_t tmem_base;
   int abort_flag;
 };
 static_assert(kStages * kTileBytes + (int)sizeof(Bars) <= kStepTileSmem,
               "shared-memory layout overflows its allocation");
 
-// Ring index, from the unit's first, of K_j and V_j of a segment of n tiles.
+// Ring index, from the segment's first, of K_j and V_j of a segment of n tiles.
+// The products read the stages in just this order (QK(0) QK(1) PV(0) QK(2) ...),
+// so stages are released in index order; each producer warp's indices are at
+// most four apart, so when it waits for the release of index i - 4, that of
+// i - 8 is over and the parity of its wait is unambiguous.
 __device__ __forceinline__ uint32_t ring_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ uint32_t ring_v(int j, int n) {
   return j + 1 < n ? 2 * j + 2 : 2 * n - 1;
 }
-
-// One segment of a unit as every role sees it.
-struct Item {
-  const int32_t* table;
-  int kv_head;
-  int row, n_tok;  // first row and tokens of the query tile
-  int pos;         // last key its first token sees (the prefix: every token)
-  int kb, ke;      // key range of the segment
-  int n;           // its key tiles
-  bool prefix, head, whole;
-};
 
 // Walks a CTA's part [x, end) of the line.
 struct Walk {
@@ -116,9 +136,9 @@ struct Walk {
   int unit;              // tiled sequence
 };
 
-__device__ __forceinline__ bool next_item(Walk& w, const DevStep& ds, const ShapeInfo& s,
+__device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const ShapeInfo& s,
                                           const StepPlan& plan, const StepWork& work, int tpt,
-                                          Item& it) {
+                                          Segment& it) {
   while (w.x < w.end) {
     int n;                 // the unit's key tiles
     int64_t unit0;         // its place on the line
@@ -129,7 +149,7 @@ __device__ __forceinline__ bool next_item(Walk& w, const DevStep& ds, const Shap
       unit0 = unit * (n + kStepTileUnit);
       it.kv_head = (int)step_div(unit, work.prefix_rows);
       const int tile = (int)(unit - (int64_t)it.kv_head * work.prefix_rows);
-      it.prefix = true;
+      it.flags = kPrefix;
       it.table = ds.prefix_table;
       it.row = tile * tpt;
       it.n_tok = min(tpt, work.rows - it.row);
@@ -149,7 +169,7 @@ __device__ __forceinline__ bool next_item(Walk& w, const DevStep& ds, const Shap
         unit0 += n + kStepTileUnit;
         n = step_key_tiles(seen, e.n_new, tpt, ++tile);
       }
-      it.prefix = false;
+      it.flags = 0;
       it.table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
       it.row = e.row + tile * tpt;
       it.n_tok = min(tpt, e.n_new - tile * tpt);
@@ -162,14 +182,35 @@ __device__ __forceinline__ bool next_item(Walk& w, const DevStep& ds, const Shap
     const int last = (int)(to < 0 ? 0 : to < n ? to : n);
     w.x = unit0 + n + kStepTileUnit;
     if (first >= last) continue;
-    it.head = first == 0;
-    it.whole = it.head && last == n;
+    it.flags |= (first == 0 ? kHead : 0) | (first == 0 && last == n ? kWhole : 0);
     it.kb = first * kKeys;
     it.ke = (int)min((int64_t)keys, (int64_t)last * kKeys);
     it.n = last - first;
     return true;
   }
+  it.n = 0;
   return false;
+}
+
+// Wait for a phase of a barrier; false when it gave up or another role did.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (*abort_flag || clock64() - t0 > kWaitLimit) return false;
+  }
+  return true;
+}
+
+// A row's 32 floats as 256-bit stores (whole sectors per lane).
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])),
+               "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+               "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
 }
 
 // True in one lane of the (converged) warp.
@@ -210,11 +251,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&bars->q_full[b], 4 * 32);
       ptx::mbar_init(&bars->s_full[b], 1);
-      ptx::mbar_init(&bars->p_full[b], 4 * 32);
+      ptx::mbar_init(&bars->p_full[b], 4 * 32 + 1);
       ptx::mbar_init(&bars->o_done[b], 1);
     }
     ptx::mbar_init(&bars->o_free, 4 * 32);
     ptx::mbar_init(&bars->drain, 1);
+    for (int i = 0; i < kSegments; ++i) ptx::mbar_init(&bars->published[i], 1);
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&bars->kv_full[s], 1);
       ptx::mbar_init(&bars->kv_empty[s], 1);
@@ -226,88 +268,92 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  Walk walk;
-  walk.x = step_cut(blockIdx.x, work.tile_total, ctas);
-  walk.end = step_cut(blockIdx.x + 1, work.tile_total, ctas);
-  walk.unit = 0;
-  if (walk.x >= work.tile_prefix) {
-    // the tiled sequence that holds this CTA's first step
-    const int64_t v = step_div(walk.x - work.tile_prefix, shp.H_kv);
-    int hi = plan.header[kPlanTiled] - 1;
-    while (walk.unit < hi) {
-      const int mid = (walk.unit + hi + 1) >> 1;
-      if (plan.tiled[mid].cum <= v) walk.unit = mid;
-      else hi = mid - 1;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // Every role walks the same segments in the same order.  Ring indices, score
+  // The k-th segment of this CTA; false when there is none (or the wait for it
+  // gave up).
+  auto segment = [&](uint32_t k, Segment& it) -> bool {
+    const bool got =
+        wait_phase(&bars->published[k % kSegments], (k / kSegments) & 1, abort_flag);
+    if (!__all_sync(0xffffffffu, got)) return false;
+    it = bars->segments[k % kSegments];
+    return it.n > 0;
+  };
+
+  // Every role takes the same segments in the same order.  Ring indices, score
   // buffers and barrier phases carry over from segment to segment: `gi` is the
   // ring index of a segment's K_0, `tc0` the number of its first key tile.
   if (warp >= 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == kProducerWarp) {
-      // ---------------------------------------------------------- TMA producer
-      // Lane i copies box i of a tile; a box whose block id is out of range is
-      // skipped (and reported).  Ids are loaded three tiles ahead.
+    if (warp == kKeyWarp || warp == kValueWarp) {
+      // --------------------------------------------------------- TMA producers
+      // Lane i holds the block id of box i of a tile (-2: no such box; one out
+      // of range is skipped and reported).  Ids are loaded a tile ahead, the
+      // next segment's while the last tile of the current one is copied.
+      const bool leader = elect_one();
+      const bool is_k = warp == kKeyWarp;
+      const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
       const int box_rows = B < kKeys ? B : kKeys, boxes = kKeys / box_rows;
-      Item it;
-      uint32_t gi = 0;
-      bool stop = false;
-      while (!stop && next_item(walk, ds, shp, plan, work, tpt, it)) {
-        auto look_up = [&](int j) -> int {
-          const int key = it.kb + j * kKeys + lane * box_rows;
-          return lane < boxes && j < it.n && key < it.ke ? it.table[key / B] : -2;
-        };
-        // one K or V tile: j is the tile, id this lane's box of it (-2: none)
-        auto copy = [&](const CUtensorMap* map, int j, int id, uint32_t index) {
+      auto look_up = [&](const Segment& u, int j) -> int {
+        const int key = u.kb + j * kKeys + lane * box_rows;
+        return lane < boxes && key < u.ke ? u.table[key / B] : -2;
+      };
+      Segment it, nx;
+      uint32_t gi = 0, k = 0;
+      bool ok = true;
+      bool more = segment(0, it);
+      int id = more ? look_up(it, 0) : -2;
+      while (more && ok) {
+        for (int j = 0; ok && j < it.n; ++j) {
+          int id_next = -2;
+          if (j + 1 < it.n) {
+            id_next = look_up(it, j + 1);
+          } else {
+            more = segment(++k, nx);
+            if (more) id_next = look_up(nx, 0);
+          }
+          const uint32_t index = gi + (is_k ? ring_k(j) : ring_v(j, it.n));
           const int st = index % kStages;
-          bool go = !*abort_flag;
-          if (go && index >= (uint32_t)kStages)
-            go = ptx::mbar_wait(&bars->kv_empty[st], ((index / kStages) - 1) & 1, kWaitLimit);
-          if (!__all_sync(0xffffffffu, go)) {
-            if (lane == 0) {
-              ptx::report_wait(ds.status, kDevTimeout, 72, (int)index);
+          if (index >= (uint32_t)kStages)
+            ok = wait_phase(&bars->kv_empty[st], ((index / kStages) - 1) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (leader) {
+              ptx::report_wait(ds.status, kDevTimeout, is_k ? 72 : 71, (int)index);
               *abort_flag = 1;
             }
-            stop = true;
-            return;
+            break;
           }
-          const bool ok = id != -2 && (uint32_t)id < (uint32_t)ds.num_blocks;
-          if (id != -2 && !ok) atomicCAS(ds.status, 0, kDevBounds);
-          const int n = __popc(__ballot_sync(0xffffffffu, ok));
-          if (lane == 0)
-            ptx::mbar_arrive_expect_tx(&bars->kv_full[st], (uint32_t)(n * box_rows * 256));
-          __syncwarp();
-          if (ok) {
-            const int key = it.kb + j * kKeys + lane * box_rows;
-            const int row = (id * shp.H_kv + it.kv_head) * B + key % B;
-            uint8_t* dst = kv_s + st * kTileBytes + lane * box_rows * 128;
-            ptx::tma_load_2d(dst, map, 0, row, &bars->kv_full[st]);
-            ptx::tma_load_2d(dst + kHalf, map, 64, row, &bars->kv_full[st]);
+          const bool good = (uint32_t)id < (uint32_t)ds.num_blocks;
+          const uint32_t mask = __ballot_sync(0xffffffffu, good);
+          if (id != -2 && !good) atomicCAS(ds.status, 0, kDevBounds);
+          if (leader)
+            ptx::mbar_arrive_expect_tx(&bars->kv_full[st],
+                                       (uint32_t)(__popc(mask) * box_rows * 256));
+          // (a box begins a block, but for blocks of more than 128 keys)
+          const int in_block = B > kKeys ? (it.kb + j * kKeys) % B : 0;
+          uint8_t* dst = kv_s + st * kTileBytes;
+          for (int i = 0; i < boxes; ++i) {
+            const int row =
+                (__shfl_sync(0xffffffffu, id, i) * shp.H_kv + it.kv_head) * B + in_block;
+            if (leader && (mask >> i & 1)) {
+              ptx::tma_load_2d(dst + i * box_rows * 128, map, 0, row, &bars->kv_full[st]);
+              ptx::tma_load_2d(dst + kHalf + i * box_rows * 128, map, 64, row,
+                               &bars->kv_full[st]);
+            }
           }
           __syncwarp();
-        };
-        int id0 = look_up(0), id1 = look_up(1), id2 = look_up(2);
-        copy(&tmap_k, 0, id0, gi);
-        if (!stop && it.n > 1) copy(&tmap_k, 1, id1, gi + 1);
-        for (int j = 0; !stop && j < it.n; ++j) {
-          const int id3 = look_up(j + 3);
-          copy(&tmap_v, j, id0, gi + ring_v(j, it.n));
-          if (!stop && j + 2 < it.n) copy(&tmap_k, j + 2, id2, gi + ring_k(j + 2));
-          id0 = id1;
-          id1 = id2;
-          id2 = id3;
+          id = id_next;
         }
-        if (!stop) gi += 2 * it.n;
+        gi += 2 * it.n;
+        it = nx;
       }
-      // every copy must land before the CTA may exit: the softmax warps waited
-      // for each tile of a finished walk; after an abort, wait for the stages
-      if (stop)
+      // every copy must land before the CTA may exit: a finished walk's tiles
+      // were all used; after an abort, wait for both phases of every stage
+      if (!ok)
         for (int st = 0; st < kStages; ++st)
           for (uint32_t ph = 0; ph < 2; ++ph)
             ptx::mbar_wait(&bars->kv_full[st], ph, kWaitLimit / 64);
@@ -354,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // complete (Q or P written, O read) the MMAs that follow are ordered
       // after those accesses with a tcgen05 fence.
       auto wait_bar = [&](uint64_t* bar, uint32_t parity, int where, int index) {
-        const bool got = ptx::mbar_wait(bar, parity, kWaitLimit) && !*abort_flag;
+        const bool got = wait_phase(bar, parity, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           site = where;
@@ -364,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         return true;
       };
-      Item it;
+      Segment it;
       uint32_t gi = 0, tc0 = 0;
-      for (uint32_t k = 0; ok && next_item(walk, ds, shp, plan, work, tpt, it); ++k) {
+      for (uint32_t k = 0; ok && segment(k, it); ++k) {
         if (!wait_bar(&bars->q_full[k & 1], (k >> 1) & 1, 73, (int)k)) break;
         for (int j = 0; ok && j < 2 && j < it.n; ++j) {
           const uint32_t index = gi + ring_k(j);
@@ -374,10 +420,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             break;
           issue_qk(tc0 + j, index, k & 1);
         }
-        // then per key tile j: PV(j) QK(j+2) once its softmax has written P.
-        // The softmax threads have also seen V_j and K_j+2 land before they
-        // report P: a wait of the issuing thread costs 200 to 450 cycles while
-        // its products are queued
+        // then per key tile j: PV(j) QK(j+2) once its softmax has written P and
+        // V_j and K_j+2 have landed (both of which p_full reports)
         for (int j = 0; ok && j < it.n; ++j) {
           const uint32_t t = tc0 + j;
           if (!wait_bar(&bars->p_full[t & 1], (t >> 1) & 1, 75, (int)t)) break;
@@ -397,6 +441,66 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (leader) tc_commit(&bars->drain);
       __syncwarp();
       ptx::mbar_wait(&bars->drain, 0, kWaitLimit);
+    } else if (warp == kWalkWarp) {
+      // ------------------------------------------- the walk, and landed tiles
+      Walk walk;
+      walk.x = step_cut(blockIdx.x, work.tile_total, ctas);
+      walk.end = step_cut(blockIdx.x + 1, work.tile_total, ctas);
+      walk.unit = 0;
+      if (walk.x >= work.tile_prefix) {
+        // the tiled sequence that holds this CTA's first step
+        const int64_t v = step_div(walk.x - work.tile_prefix, shp.H_kv);
+        int hi = plan.header[kPlanTiled] - 1;
+        while (walk.unit < hi) {
+          const int mid = (walk.unit + hi + 1) >> 1;
+          if (plan.tiled[mid].cum <= v) walk.unit = mid;
+          else hi = mid - 1;
+        }
+      }
+      // A slot is written again eight segments later; when a segment's first
+      // tile is handled here the softmax warps have left all but the two
+      // segments before it, so kAhead + 2 slots are in use at most.
+      static_assert(kAhead + 3 <= kSegments, "segment ring");
+      uint32_t n_pub = 0;
+      bool last = false;
+      auto publish = [&] {
+        if (last) return;
+        Segment u;
+        last = !next_segment(walk, ds, shp, plan, work, tpt, u);
+        if (lane == 0) {
+          bars->segments[n_pub % kSegments] = u;
+          ptx::mbar_arrive(&bars->published[n_pub % kSegments]);
+        }
+        ++n_pub;
+      };
+      uint32_t gi = 0, t = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        while (n_pub <= k + kAhead && !last) publish();
+        Segment it;
+        if (!segment(k, it)) break;
+        for (int j = 0; ok && j < it.n; ++j, ++t) {
+          const uint32_t gv = gi + ring_v(j, it.n), gk = gi + ring_k(j + 2);
+          // Once S_j is there, K_j and every tile of smaller ring index but V_j-1
+          // have landed, so the stages of V_j and K_j+2 are in the phase before
+          // the one that is waited for, or in it; and they stay there until P_j is
+          // reported.
+          ok = wait_phase(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag);
+          ok = ok && wait_phase(&bars->kv_full[gv % kStages], (gv / kStages) & 1, abort_flag);
+          if (ok && j + 2 < it.n)
+            ok = wait_phase(&bars->kv_full[gk % kStages], (gk / kStages) & 1, abort_flag);
+          // (not before the barrier's last phase is over: it would count for that)
+          if (ok && t >= 2) ok = wait_phase(&bars->p_full[t & 1], ((t - 2) >> 1) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) ptx::mbar_arrive(&bars->p_full[t & 1]);
+          if (!ok && lane == 0) {
+            ptx::report_wait(ds.status, kDevTimeout, 77, (int)t);
+            *abort_flag = 1;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        gi += 2 * it.n;
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -407,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tok = row / g, hh = row - tok * g;      // its token in the tile, and head
     // this thread's query row -> tensor memory, buffer b; rows past the tile's
     // end are zero
-    auto write_q = [&](const Item& u, uint32_t b) {
+    auto write_q = [&](const Segment& u, uint32_t b) {
       float qv[64];
       uint4* q4 = reinterpret_cast<uint4*>(qv);
       if (tok < u.n_tok) {
@@ -428,18 +532,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t gi = 0, tc0 = 0;
     bool ok = true;
     int site = 0, at = 0;
-    Item it, nx;
-    bool more = next_item(walk, ds, shp, plan, work, tpt, it);
+    Segment it;
+    bool more = segment(0, it);
     if (more) write_q(it, 0);
     for (uint32_t k = 0; more && ok; ++k) {
       // the last key this row sees
-      const int pos = it.prefix ? it.pos : it.pos + tok;
+      const int pos = it.flags & kPrefix ? it.pos : it.pos + tok;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < it.n; ++j) {
         const uint32_t t = tc0 + j;
         // tcgen05.ld/st are warp-collective: every decision below is warp-uniform
-        const bool got = ptx::mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, kWaitLimit);
-        if (!__all_sync(0xffffffffu, got) || __any_sync(0xffffffffu, *abort_flag != 0)) {
+        const bool got = wait_phase(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           site = 81;
           at = (int)t;
@@ -535,20 +639,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float ps =
             ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         l = l * corr + ps;
-        // V_j and K_j+2 have landed (the issuing thread relies on it)
-        const uint32_t gv = gi + ring_v(j, it.n), gk = gi + ring_k(j + 2);
-        bool landed = ptx::mbar_wait(&bars->kv_full[gv % kStages], (gv / kStages) & 1, kWaitLimit);
-        if (landed && j + 2 < it.n)
-          landed = ptx::mbar_wait(&bars->kv_full[gk % kStages], (gk / kStages) & 1, kWaitLimit);
-        if (!__all_sync(0xffffffffu, landed)) {
-          ok = false;
-          site = 82;
-          at = (int)gv;
-          break;
-        }
         if (j == it.n - 1 && (it.ke % kKeys) != 0) {
           // keys past the unit's end may be anything (unwritten cache slots, and
           // 0 * NaN is NaN): their V rows are zeroed
+          const uint32_t gv = gi + ring_v(j, it.n);
+          const bool landed =
+              wait_phase(&bars->kv_full[gv % kStages], (gv / kStages) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, landed)) {
+            ok = false;
+            site = 82;
+            at = (int)gv;
+            break;
+          }
           uint8_t* vt = kv_s + (gv % kStages) * kTileBytes;
           const int valid = it.ke - key0;
           for (int e = row; e < (kKeys - valid) * 16; e += kRows) {
@@ -564,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (!ok) break;
       // the next unit's queries, while this one's last products run
-      more = next_item(walk, ds, shp, plan, work, tpt, nx);
+      Segment nx;
+      more = segment(k + 1, nx);
       if (more) write_q(nx, (k + 1) & 1);
       const uint32_t tl = tc0 + it.n - 1;
       const bool fin = ptx::mbar_wait(&bars->o_done[tl & 1], (tl >> 1) & 1, kWaitLimit);
@@ -579,39 +682,37 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool store = tok < it.n_tok;
       // O itself when nothing is to be joined, the unit's rows of the
       // workspace, or this CTA's spill rows
-      const bool partial = !it.whole || ds.prefix_len > 0;
-      const int64_t slot = it.head ? (int64_t)(it.row + tok) * shp.H_q + it.kv_head * g + hh
-                                   : (int64_t)blockIdx.x * kRows + row;
+      const bool head = it.flags & kHead, pre = it.flags & kPrefix;
+      const bool partial = !(it.flags & kWhole) || ds.prefix_len > 0;
+      const int64_t slot = head ? (int64_t)(it.row + tok) * shp.H_q + it.kv_head * g + hh
+                                : (int64_t)blockIdx.x * kRows + row;
       __nv_bfloat16* orow = o + slot * 128;
-      float* prow = (it.head ? (it.prefix ? ws.pre_o : ws.own_o) : ws.tile_o) + slot * 128;
-      float* plse = it.head ? (it.prefix ? ws.pre_lse : ws.own_lse) : ws.tile_lse;
+      float* prow = (head ? (pre ? ws.pre_o : ws.own_o) : ws.tile_o) + slot * 128;
+      float* plse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.tile_lse;
+      float ov[128];
 #pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) {
-        float ov[32];
-        tmem_ld32(lane_base + kOCol + c4 * 32, ov);
-        tmem_wait_ld();
-        if (store && !partial) {
-#pragma unroll
-          for (int c8 = 0; c8 < 4; ++c8) {
-            uint4 v;
-            v.x = ptx::pack_bf16x2(ov[c8 * 8 + 0] * inv, ov[c8 * 8 + 1] * inv);
-            v.y = ptx::pack_bf16x2(ov[c8 * 8 + 2] * inv, ov[c8 * 8 + 3] * inv);
-            v.z = ptx::pack_bf16x2(ov[c8 * 8 + 4] * inv, ov[c8 * 8 + 5] * inv);
-            v.w = ptx::pack_bf16x2(ov[c8 * 8 + 6] * inv, ov[c8 * 8 + 7] * inv);
-            *reinterpret_cast<uint4*>(orow + c4 * 32 + c8 * 8) = v;
-          }
-        } else if (store) {
-#pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8)
-            *reinterpret_cast<float4*>(prow + c4 * 32 + c8 * 4) =
-                make_float4(ov[c8 * 4 + 0] * inv, ov[c8 * 4 + 1] * inv, ov[c8 * 4 + 2] * inv,
-                            ov[c8 * 4 + 3] * inv);
-        }
-      }
-      if (store && partial) plse[slot] = l > 0.f ? m_ref + log2f(l) : -INFINITY;
+      for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(lane_base + kOCol + c4 * 32, ov + c4 * 32);
+      tmem_wait_ld();
       // O has been read: the next unit's first PV may overwrite it
       tc_fence_before();
       ptx::mbar_arrive(&bars->o_free);
+#pragma unroll
+      for (int c = 0; c < 128; ++c) ov[c] *= inv;
+      if (store && !partial) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          uint4 v;
+          v.x = ptx::pack_bf16x2(ov[c + 0], ov[c + 1]);
+          v.y = ptx::pack_bf16x2(ov[c + 2], ov[c + 3]);
+          v.z = ptx::pack_bf16x2(ov[c + 4], ov[c + 5]);
+          v.w = ptx::pack_bf16x2(ov[c + 6], ov[c + 7]);
+          *reinterpret_cast<uint4*>(orow + c) = v;
+        }
+      } else if (store) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) store8(prow + c, ov + c);
+        plse[slot] = l > 0.f ? m_ref + log2f(l) : -INFINITY;
+      }
       gi += 2 * it.n;
       tc0 += it.n;
       it = nx;
