@@ -146,7 +146,8 @@ struct DevStep {
 // start(c) = floor(c total / G').  A unit is so cut into segments of key tiles.
 // The segment at a unit's first tile writes its result to the unit's own rows
 // of the workspace; a segment that begins inside a unit can only be the first
-// of its CTA, and goes to that CTA's spill rows.
+// of its CTA, and goes to that CTA's spill rows: CTAs c + 1, c + 2, ... where
+// CTA c holds the unit's first tile.
 __host__ __device__ __forceinline__ int64_t step_cut(int64_t c, int64_t total, int64_t ctas) {
   return step_div(c * total, ctas);
 }
@@ -195,24 +196,67 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
 }
 #endif
 
-// The workspace: fp32 partial outputs (head dim 128) and base-2 log-sum-exps.
+// CTAs (or pipelines) whose spill rows hold the rest of a cut unit.
+struct Spills {
+  int32_t first, n;
+};
+
+// The workspace: fp32 partial outputs (head dim 128) and base-2 log-sum-exps,
+// and what is to be joined.  The segment at a unit's first tile fills in the
+// unit's Spills, at the unit's first row (a streamed prefix: row 0).
 struct StepWorkspace {
   float *own_o, *pre_o;         // [max_tokens][H_q][128]
   float *own_lse, *pre_lse;     // [max_tokens][H_q]
   float *stream_o, *stream_lse; // spill rows [stream grid kStepPipes][kStepPackedRows]
   float *tile_o, *tile_lse;     // spill rows [tile grid][kStepTileRows]
+  Spills *own_cut, *pre_cut;    // [max_tokens][H_kv]
   int32_t stream_grid, tile_grid;     // CTAs (the streaming kernel's: two per SM)
 };
 
 #ifdef __CUDACC__
-// CTAs of the streaming kernel that take part: two per SM, or one beside the
-// tile kernel's CTA where that has work; and the pipelines among them.
-__device__ __forceinline__ int64_t step_stream_ctas(const StepWorkspace& ws,
-                                                    const StepWork& work) {
-  return work.tile_total > 0 ? ws.stream_grid / 2 : ws.stream_grid;
-}
-__device__ __forceinline__ int64_t step_pipes(const StepWorkspace& ws, const StepWork& work) {
-  return min(step_stream_ctas(ws, work) * kStepPipes, work.stream_total);
+// The streaming kernel's pipelines: kStepPipes in each of two CTAs per SM.
+// Without tile work both CTAs of an SM run from the start and share its line
+// evenly.  With it, the second one only fits once the tile kernel's CTA has
+// left: the early CTAs take [0, cut) of the line and the late ones the rest,
+// such that both end together.  Let x be the share of the streaming that the
+// early ones do while the tile kernel runs; they do it at about 1.75 ns per
+// 16-key group of the whole line (5.2 TB/s beside the tile kernel), which takes
+// about 1.5 us per step then (1.05 alone) and 4 us to start.  What is left
+// after that is shared evenly: the early ones' part is x + (1 - x) / 2.  (On 512
+// sequences of 256 keys behind 4096 shared ones, with everything given to the
+// early CTAs, the late ones idled for half of 130 us.)
+struct StreamCuts {
+  int64_t cut, total;       // the line
+  int32_t early, late;      // pipelines of [0, cut) and of [cut, total)
+
+  // where pipeline c's part begins
+  __device__ __forceinline__ int64_t at(int32_t c) const {
+    if (c < early) return step_cut(c, cut, early);
+    return c < early + late ? cut + step_cut(c - early, total - cut, late) : total;
+  }
+  // the first pipeline whose part begins at or behind p (0 < p <= total)
+  __device__ __forceinline__ int32_t first(int64_t p) const {
+    if (p <= cut) return (int32_t)step_div(p * early + cut - 1, cut);
+    return early + (int32_t)step_div((p - cut) * late + total - cut - 1, total - cut);
+  }
+};
+
+__device__ __forceinline__ StreamCuts step_stream_cuts(const StepWorkspace& ws,
+                                                       const StepWork& work) {
+  StreamCuts c;
+  const int64_t half = (int64_t)ws.stream_grid / 2 * kStepPipes;
+  c.total = work.stream_total;
+  c.cut = (c.total + 1) / 2;
+  if (work.tile_total > 0) {
+    const int64_t tile_ns = step_div(work.tile_total * 1500, ws.tile_grid) + 4000;
+    const int64_t stream_ns = c.total * 7 / 4;
+    c.cut = tile_ns >= stream_ns
+                ? c.total
+                : c.total / 2 + (int64_t)((float)c.total * 0.5f * ((float)tile_ns / (float)stream_ns));
+  }
+  c.early = (int32_t)(c.cut < half ? c.cut : half);
+  c.late = (int32_t)(c.total - c.cut < half ? c.total - c.cut : half);
+  return c;
 }
 #endif
 

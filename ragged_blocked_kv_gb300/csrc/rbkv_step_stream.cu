@@ -71,7 +71,7 @@ struct __align__(16) Segment {
   int kv_head;
   int group, groups;     // first group of keys, and number of them (0: no more)
   int keys;              // keys of the unit's last row
-  int diag;              // keys of its first row (the prefix: every row sees all)
+  int cuts;              // at a unit's head: pipelines that begin inside it behind this
   int flags;
 };
 static_assert(sizeof(Segment) == 32, "Segment is 8 int32");
@@ -99,6 +99,8 @@ struct Walk {
   StepSeq cur, next;
   const int32_t* table;
   uint32_t seg;          // segments published
+  StreamCuts cuts;
+  int32_t pipe;          // this pipeline
 
   __device__ __forceinline__ int load_ids(const int32_t* t, int from, int n, int lane) const {
     return from + lane < n ? t[from + lane] : 0;
@@ -212,9 +214,11 @@ struct Walk {
       g.group = first;
       g.groups = left;
       g.keys = cur.ctx;
-      g.diag = prefix ? cur.ctx : cur.ctx - cur.n_new + 1;
       g.flags = (prefix ? kPrefix : 0) | (first == 0 ? kHead : 0) |
                 (first == 0 && last == n ? kWhole : 0);
+      // pipelines that begin inside the unit, behind this segment at its head
+      g.cuts = 0;
+      if (first == 0 && last < n) g.cuts = cuts.first(next_x) - (pipe + 1);
       segments[seg % kSegments] = g;      // (every lane the same values)
       ++seg;
       return true;
@@ -329,7 +333,9 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
   for (int i = 0; i < NT; ++i) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      lim[i][e] = min(it.keys, it.diag + (8 * i + c2 + e) / s.g);
+      lim[i][e] = it.flags & kPrefix
+                      ? it.keys
+                      : min(it.keys, it.keys - it.n_tok + 1 + (8 * i + c2 + e) / s.g);
       m[i][e] = -INFINITY;
       l[i][e] = 0.f;
     }
@@ -438,6 +444,9 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
   float* part = head ? (pre ? ws.pre_o : ws.own_o) : ws.stream_o;
   float* lse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.stream_lse;
   const int nrg = it.n_tok * s.g;
+  if (head && lane == 0)
+    (pre ? ws.pre_cut : ws.own_cut)[(int64_t)it.row * s.H_kv + it.kv_head] =
+        Spills{(int32_t)pipe + 1, it.cuts};
   auto place = [&](int r) -> int64_t {
     const int tok = r / s.g;
     return head ? (int64_t)(it.row + tok) * s.H_q + it.kv_head * s.g + (r - tok * s.g)
@@ -491,14 +500,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int64_t pipes = step_pipes(ws, work);
-  // neighbouring parts on different SMs
-  const int64_t ctas = step_stream_ctas(ws, work);
-  const int64_t pipe = blockIdx.x < ctas ? (int64_t)warp * ctas + blockIdx.x : pipes;
+  const StreamCuts cuts = step_stream_cuts(ws, work);
+  // neighbouring parts on different SMs; the second half of the grid is late
+  const int half = ws.stream_grid / 2;
+  const bool late = (int)blockIdx.x >= half;
+  const int mine = warp * half + ((int)blockIdx.x - (late ? half : 0));
+  const int pipe = late ? cuts.early + mine : mine;
+  const bool works = mine < (late ? cuts.late : cuts.early);
   if (ptx::smem_u32(smem_raw) & 1023) {
     // the swizzled layout needs a 1024-byte aligned base
     if (threadIdx.x == 0) atomicCAS(ds.status, 0, kDevBounds);
-  } else if (pipe < pipes) {
+  } else if (works) {
     Ring ring;
     ring.stages = smem_raw + warp * kStages * kStage;
     ring.segments =
@@ -514,8 +526,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     Walk walk;
-    walk.end = step_cut(pipe + 1, work.stream_total, pipes);
-    walk.start(step_cut(pipe, work.stream_total, pipes), ds, shp, plan, work, lane);
+    walk.cuts = cuts;
+    walk.pipe = pipe;
+    walk.end = cuts.at(pipe + 1);
+    walk.start(cuts.at(pipe), ds, shp, plan, work, lane);
     for (int i = 0; i < kStages; ++i)
       if (walk.issue(ring.stages + i * kStage, &ring.full[i], ring.segments, maps, ds, shp, plan,
                      work, lane))
@@ -540,24 +554,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 // The join: W warps per (row, query head), four columns per lane.
 // ---------------------------------------------------------------------------
 // O = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M) over the row's partial
-// outputs: its own part and the prefix's, each with the spills of the CTAs
-// (or pipelines) whose cuts fall inside its unit.  Which those are is a
-// formula: cut c is at floor(c total / G), so the first cut at or behind p is
-// ceil(p G / total).  One thread per KV head and part works them out while the
-// main sources are on their way.  A row has a handful of sources and one warp
-// joins them; a step of few rows over a long prefix has a hundred (every
-// pipeline streamed a piece), and eight warps share them.
+// outputs: its own part and the prefix's, each with the spills of the CTAs (or
+// pipelines) that begin inside its unit, which the segment at the unit's head
+// has written down.  A row has a handful of sources and one warp joins them; a
+// step of few rows over a long prefix has a hundred (every pipeline streamed a
+// piece), and eight warps share them.  Bound by latency, and by the partials'
+// traffic (from L2, they were just written).
 constexpr int kJoinWarps = 8;
 constexpr int kJoinWideRows = 32;   // steps of at most this many rows: W = 8
-
-// Spills of a unit that a row joins: of CTAs [first, first + n).
-struct Spills {
-  int first, n;
-};
-
-__device__ __forceinline__ int first_cut(int64_t p, int64_t total, int ctas) {
-  return (int)step_div(p * ctas + total - 1, total);
-}
 
 // Partial outputs of one part (own or prefix): source k's row.
 struct Part {
@@ -595,12 +599,15 @@ struct Join {
   }
 };
 
+__device__ __forceinline__ int bounded(const Spills& s, int rows) {
+  return s.first >= 0 && s.first <= rows && s.n > 0 && s.n <= rows - s.first ? s.n : 0;
+}
+
 template <int W>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : 4)
     step_combine_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
                         __nv_bfloat16* __restrict__ o) {
   constexpr int kHeads = kJoinWarps / W;      // query heads of a block
-  __shared__ Spills spills[2 * kHeads];       // [KV head of the block][own, prefix]
   __shared__ float4 wide_acc[W > 1 ? kJoinWarps * 32 : 1];
   __shared__ float wide_ml[W > 1 ? kJoinWarps * 2 : 1];
   ptx::pdl_wait_previous();
@@ -610,13 +617,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const bool pre = ds.prefix_len > 0;
   const int h0 = blockIdx.x * kHeads, h = h0 + warp / W, wi = warp % W;
   const bool live = h < shp.H_q;
-  const int kv0 = h0 / g, kvh = h / g;
+  const int kvh = h / g, hh = h - kvh * g;
+  const bool pre_streamed = pre && step_prefix_streamed(ds.max_tokens, g);
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
-  const StepWork work = step_work(ds, shp, plan);
-  const int s_ctas = (int)step_pipes(ws, work);
-  const int t_ctas = (int)min((int64_t)ws.tile_grid, work.tile_total);
-  const bool pre_streamed = work.prefix_stream_tiles > 0;
-  for (int t = blockIdx.y; t < work.rows; t += gridDim.y) {
+  const int T = plan.header[kPlanRows];
+  for (int t = blockIdx.y; t < T; t += gridDim.y) {
     const int64_t w = (int64_t)t * shp.H_q + h;
     // the two main sources, requested before anything that depends on the
     // row's place
@@ -630,61 +635,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         v2[1] = reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane];
       }
     }
-    const StepRow r = plan.rows[t];
-    const int tile = r.token / tpt;
-    if (threadIdx.x < 2 * kHeads) {
-      const int kv = kv0 + (threadIdx.x >> 1);
-      int64_t begin = 0, total = work.stream_total;
-      int unit = kStepStreamUnit, tiles = 0, ctas = s_ctas;
-      if (kv >= shp.H_kv) {
-        // (past the last head)
-      } else if (threadIdx.x & 1) {
-        if (pre_streamed) {
-          tiles = work.prefix_stream_tiles;
-          begin = work.stream_own + (int64_t)kv * (tiles + unit);
-        } else if (pre) {
-          tiles = work.prefix_tile_steps;
-          unit = kStepTileUnit;
-          begin = ((int64_t)kv * work.prefix_rows + t / tpt) * (tiles + unit);
-          total = work.tile_total;
-          ctas = t_ctas;
-        }
-      } else if (r.unit >= 0) {
-        tiles = r.tiles;
-        begin = (int64_t)shp.H_kv * r.cum + (int64_t)kv * (tiles + unit);
-      } else {
-        const StepSeq e = plan.tiled[-1 - r.unit];
-        tiles = step_key_tiles(e.ctx - e.n_new, e.n_new, tpt, tile);
-        unit = kStepTileUnit;
-        begin = work.tile_prefix + (int64_t)shp.H_kv * r.cum + (int64_t)kv * r.tiles +
-                step_len_before(e.ctx - e.n_new, tpt, tile);
-        total = work.tile_total;
-        ctas = t_ctas;
-      }
-      Spills s = {0, 0};
-      if (tiles > 0) {
-        s.first = first_cut(begin + unit + 1, total, ctas);
-        s.n = first_cut(begin + unit + tiles, total, ctas) - s.first;
-      }
-      spills[threadIdx.x] = s;
-    }
-    __syncthreads();
     if (live) {
-      const Spills a = spills[2 * (kvh - kv0)], p = spills[2 * (kvh - kv0) + 1];
-      const int hh = h - kvh * g;
+      Spills a, p = {0, 0};
+      const int pre_in = pre_streamed ? t : t % tpt;      // the row in its prefix unit
+      if (pre) p = ws.pre_cut[(int64_t)(t - pre_in) * shp.H_kv + kvh];
+      const StepRow r = plan.rows[t];
+      const int own_in = r.unit >= 0 ? r.token : r.token % tpt;
+      a = ws.own_cut[(int64_t)(t - own_in) * shp.H_kv + kvh];
+      // (after a wait that gave up, a unit's Spills may not have been written:
+      // nothing outside the spill rows is read then either)
+      a.n = bounded(a, r.unit >= 0 ? ws.stream_grid * kStepPipes : ws.tile_grid);
+      p.n = bounded(p, pre_streamed ? ws.stream_grid * kStepPipes : ws.tile_grid);
       Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       j.add<2>(l2, v2);
       const int n = a.n + p.n;
       if (n > wi) {
         const Part mine = r.unit >= 0
-            ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + r.token * g + hh,
+            ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + own_in * g + hh,
                    kStepPackedRows}
-            : Part{ws.tile_o, ws.tile_lse,
-                   a.first * kStepTileRows + (r.token - tile * tpt) * g + hh, kStepTileRows};
+            : Part{ws.tile_o, ws.tile_lse, a.first * kStepTileRows + own_in * g + hh,
+                   kStepTileRows};
         const Part theirs = pre_streamed
-            ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + t * g + hh,
+            ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + pre_in * g + hh,
                    kStepPackedRows}
-            : Part{ws.tile_o, ws.tile_lse, p.first * kStepTileRows + (t % tpt) * g + hh,
+            : Part{ws.tile_o, ws.tile_lse, p.first * kStepTileRows + pre_in * g + hh,
                    kStepTileRows};
         constexpr int kAtOnce = W > 1 ? 8 : 4;
         for (int k0 = wi; k0 < n; k0 += kAtOnce * W) {
@@ -739,7 +713,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
       }
     }
-    __syncthreads();   // the next row's spills replace these
+    if (W > 1) __syncthreads();   // the next row's sums replace these
   }
 }
 
@@ -770,6 +744,8 @@ size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* bas
   v.stream_lse = take((int64_t)v.stream_grid * kStepPipes * kStepPackedRows);
   v.tile_o = take((int64_t)v.tile_grid * kStepTileRows * 128);
   v.tile_lse = take((int64_t)v.tile_grid * kStepTileRows);
+  v.own_cut = reinterpret_cast<Spills*>(take(2 * (int64_t)max_tokens * s.H_kv));
+  v.pre_cut = reinterpret_cast<Spills*>(take(2 * (int64_t)max_tokens * s.H_kv));
   if (w) *w = v;
   return at;
 }

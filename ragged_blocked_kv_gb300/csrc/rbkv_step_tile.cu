@@ -96,7 +96,8 @@ struct __align__(16) Segment {
   int kb, ke;      // key range of the segment
   int n;           // its key tiles
   int flags;
-  int pad[2];
+  int cuts;        // at a unit's head: CTAs that begin inside the unit behind it
+  int pad;
 };
 static_assert(sizeof(Segment) == 48, "Segment is 12 int32");
 enum { kPrefix = 1, kHead = 2, kWhole = 4 };
@@ -137,8 +138,8 @@ struct Walk {
 };
 
 __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const ShapeInfo& s,
-                                          const StepPlan& plan, const StepWork& work, int tpt,
-                                          Segment& it) {
+                                          const StepPlan& plan, const StepWork& work, int64_t ctas,
+                                             int tpt, Segment& it) {
   while (w.x < w.end) {
     int n;                 // the unit's key tiles
     int64_t unit0;         // its place on the line
@@ -186,6 +187,12 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const S
     it.kb = first * kKeys;
     it.ke = (int)min((int64_t)keys, (int64_t)last * kKeys);
     it.n = last - first;
+    it.cuts = 0;
+    // (CTA c begins at floor(c total / ctas): the first at or behind p is
+    // ceil(p ctas / total))
+    if (first == 0 && last < n)
+      it.cuts = (int)step_div(w.x * ctas + work.tile_total - 1, work.tile_total) -
+                ((int)blockIdx.x + 1);
     return true;
   }
   it.n = 0;
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto publish = [&] {
         if (last) return;
         Segment u;
-        last = !next_segment(walk, ds, shp, plan, work, tpt, u);
+        last = !next_segment(walk, ds, shp, plan, work, ctas, tpt, u);
         if (lane == 0) {
           bars->segments[n_pub % kSegments] = u;
           ptx::mbar_arrive(&bars->published[n_pub % kSegments]);
@@ -687,6 +694,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int64_t slot = head ? (int64_t)(it.row + tok) * shp.H_q + it.kv_head * g + hh
                                 : (int64_t)blockIdx.x * kRows + row;
       __nv_bfloat16* orow = o + slot * 128;
+      if (head && row == 0)
+        (pre ? ws.pre_cut : ws.own_cut)[(int64_t)it.row * shp.H_kv + it.kv_head] =
+            Spills{(int32_t)blockIdx.x + 1, it.cuts};
       float* prow = (head ? (pre ? ws.pre_o : ws.own_o) : ws.tile_o) + slot * 128;
       float* plse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.tile_lse;
       float ov[128];
