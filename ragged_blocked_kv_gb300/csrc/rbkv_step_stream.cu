@@ -101,6 +101,7 @@ struct Walk {
   uint32_t seg;          // segments published
   StreamCuts cuts;
   int32_t pipe;          // this pipeline
+  uint64_t once;         // the L2 policy of the loads
 
   __device__ __forceinline__ int load_ids(const int32_t* t, int from, int n, int lane) const {
     return from + lane < n ? t[from + lane] : 0;
@@ -248,8 +249,8 @@ struct Walk {
       if (lane == 0) {
         ptx::mbar_arrive_expect_tx(full, ok ? kStage : 0);
         if (ok) {
-          ptx::tma_load_4d(stage, &maps.k, row >> 4, full);
-          ptx::tma_load_4d(stage + kGroup, &maps.v, row >> 4, full);
+          ptx::tma_load_4d_hint(stage, &maps.k, row >> 4, full, once);
+          ptx::tma_load_4d_hint(stage + kGroup, &maps.v, row >> 4, full, once);
         }
       }
       if (++sub * kKeys == s.B) {
@@ -528,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     Walk walk;
     walk.cuts = cuts;
     walk.pipe = pipe;
+    // own keys are read once: they are not to push the prefix, the queries and
+    // the partial outputs out of the L2
+    walk.once = ptx::policy_evict_first();
     walk.end = cuts.at(pipe + 1);
     walk.start(cuts.at(pipe), ds, shp, plan, work, lane);
     for (int i = 0; i < kStages; ++i)
