@@ -22,8 +22,8 @@ constexpr int kStepTileSmem = 4 * 32768 + 1024;
 
 // What a unit of work costs beside its key tiles (queries in, results out), in
 // key tiles of its kernel, for the even cut of the work over the CTAs.
-constexpr int kStepStreamUnit = 2;
-constexpr int kStepTileUnit = 2;
+constexpr int kStepStreamUnit = 3;
+constexpr int kStepTileUnit = 5;
 
 // Header words of the plan.
 enum {
