@@ -374,14 +374,14 @@ def _stream(stream):
     return _P(stream.cuda_stream)
 
 
-def _raw_stream(index: int) -> int:
-    """Handle of the current stream of a device (the current one): the short
-    way where torch has it, as a Stream object costs a small step's time."""
+def _device_calls():
+    """(index of the current device, handle of a device's current stream): the
+    short ways where torch has them."""
     import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if get is not None:
-        return get(index)
-    return torch.cuda.current_stream(index).cuda_stream
+    current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                     lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return current, stream
 
 
 def _device(device):
@@ -571,14 +571,22 @@ class StepTables:
                                        self.position, self.slot, self.plan, self.status)))
         self._c, self._t = C.byref(self._cfg), C.byref(self._tables)
         self._i32, self._dt = torch.int32, config.torch_dtype
-        self._on_gpu = self.device.type == "cuda"
+        # (what a call needs, looked up once: a small step takes less time on the
+        # GPU than these look-ups do; -2 matches no tensor's device)
+        self._index = self.device.index if self.device.type == "cuda" else -2
+        self._current, self._raw_stream = _device_calls()
+        L = lib()
+        self._f_build, self._f_append = L.rbkv_step_build, L.rbkv_step_append
+        self._f_attention = L.rbkv_step_attention
+        self._table_shape, self._free_shape = self.block_table.shape, self.free.shape
+        self._seq_shape = self.ctx.shape
         self._q_shape = torch.Size((self.max_tokens, config.num_heads_q, config.head_dim))
         self._kv_shape = torch.Size((self.max_tokens, config.num_heads_kv, config.head_dim))
         self._cache_shape = torch.Size(config.cache_shape())
 
     def _ptr(self, t, name, dtype, shape) -> int:
-        if t.device == self.device and t.dtype is dtype and t.shape == shape and \
-                t.is_contiguous() and self._on_gpu:
+        if t.get_device() == self._index and t.dtype is dtype and t.shape == shape and \
+                t.is_contiguous():
             return t.data_ptr()
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the tables on {self.device}")
@@ -586,11 +594,10 @@ class StepTables:
 
     def _call(self, fn, *args, stream=None) -> None:
         """A library call on the tables' device (the current one or not)."""
-        import torch
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
+        if self._current() != self._index:
+            with _device(self.device):
                 return _check(fn(self._c, self._t, *args, _stream(stream)))
-        st = _raw_stream(self.device.index) if stream is None else _stream(stream)
+        st = self._raw_stream(self._index) if stream is None else _stream(stream)
         status = fn(self._c, self._t, *args, st)
         if status != OK:
             _check(status)
@@ -599,12 +606,12 @@ class StepTables:
         """Sequence s holds ``seen[s]`` tokens and takes ``n_new[s]`` more.
         ``block_table`` / ``free``: read from these instead of the tables' own
         (which are written either way)."""
-        i32, S = self._i32, self.ctx.shape
-        self._call(lib().rbkv_step_build, self._ptr(seen, "seen", i32, S),
+        i32, S = self._i32, self._seq_shape
+        self._call(self._f_build, self._ptr(seen, "seen", i32, S),
                    self._ptr(n_new, "n_new", i32, S),
                    None if block_table is None else
-                   self._ptr(block_table, "block_table", i32, self.block_table.shape),
-                   None if free is None else self._ptr(free, "free", i32, self.free.shape),
+                   self._ptr(block_table, "block_table", i32, self._table_shape),
+                   None if free is None else self._ptr(free, "free", i32, self._free_shape),
                    stream=stream)
         return self
 
@@ -616,7 +623,7 @@ class StepTables:
     def append(self, k_new, v_new, k_cache, v_cache, stream=None) -> None:
         """Scatter the step's K/V rows ([max_tokens][H_kv][D]) into the caches."""
         dt, row, cache = self._dt, self._kv_shape, self._cache_shape
-        self._call(lib().rbkv_step_append, self._ptr(k_new, "k_new", dt, row),
+        self._call(self._f_append, self._ptr(k_new, "k_new", dt, row),
                    self._ptr(v_new, "v_new", dt, row), self._ptr(k_cache, "k_cache", dt, cache),
                    self._ptr(v_cache, "v_cache", dt, cache), stream=stream)
 
@@ -638,14 +645,14 @@ class StepTables:
             table = self._ptr(prefix_table, "prefix_table", self._i32, prefix_table.shape)
         if o is None or workspace is None:
             o, workspace = self._outputs(o, workspace, prefix_len, stream)
-        if workspace.device != self.device:
+        if workspace.get_device() != self._index:
             raise ValueError("workspace is on another device than the tables")
         dt, cache = self._dt, self._cache_shape
-        self._call(lib().rbkv_step_attention, self._ptr(q, "q", dt, self._q_shape),
+        self._call(self._f_attention, self._ptr(q, "q", dt, self._q_shape),
                    self._ptr(k_cache, "k_cache", dt, cache),
                    self._ptr(v_cache, "v_cache", dt, cache), table, prefix_len,
                    self._ptr(o, "o", dt, self._q_shape), workspace.data_ptr(),
-                   workspace.numel() * workspace.element_size(), stream=stream)
+                   workspace.nbytes, stream=stream)
         return o
 
     def _outputs(self, o, workspace, prefix_len, stream):
