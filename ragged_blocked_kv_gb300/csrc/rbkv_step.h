@@ -274,10 +274,9 @@ struct BuildArgs {
 
 cudaError_t launch_step_build(const BuildArgs& a, cudaStream_t st);
 cudaError_t launch_step_release(const BuildArgs& a, const int32_t* done, cudaStream_t st);
-// CUDA-core attention of a step: every type and shape, its packed rows eight to
+// CUDA-core attention of a step: every type and shape, its packed rows a few to
 // a block and the keys of each shared by `splits` blocks (more than one: with
 // a workspace and a second kernel).
-constexpr int kStepGenericRows = 8;
 constexpr int kStepGenericSplits = 32;
 int step_generic_splits(const ShapeInfo& s, int32_t max_tokens, int32_t max_blocks,
                         int32_t prefix_len, int sms);

@@ -1,8 +1,8 @@
 // Attention of a step on the CUDA cores: every type, head dim and block size
 // (fp32 steps, and bf16 shapes off the tensor-core kernels).
 //
-// A block takes eight packed rows (row = token * g + head) of one KV head.
-// Over the prefix all eight see the same keys; behind it each token sees its
+// A block takes eight packed rows (row = token * g + head) of one KV head, or
+// four.  Over the prefix all of them see the same keys; behind it each token sees its
 // own sequence's.  Keys go 32 at a time, one per lane, so that one read of a
 // key row serves all rows (its dot products take q from shared memory as
 // broadcasts); the weights pass through shared memory to the value product,
@@ -27,8 +27,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kStepGenericRows;     // packed rows of a block
-static_assert(kRows == 8, "the weights of a key are read as two float4");
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <class T> __device__ __forceinline__ float to_f(T x);
@@ -58,14 +56,15 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// Shared memory: q [kRows][D], each warp's weights [32 keys][kRows], and for
+// Shared memory: q [rows][D], each warp's weights [32 keys][rows], and for
 // the join O [warp][row][D] and (max, sum) [warp][row].
-__host__ __device__ constexpr int smem_floats(int D) {
-  return kRows * D + kWarps * 32 * kRows + kWarps * kRows * D + kWarps * kRows * 2;
+__host__ __device__ constexpr int smem_floats(int D, int rows) {
+  return rows * D + kWarps * 32 * rows + kWarps * rows * D + kWarps * rows * 2;
 }
 
-// kPer: head-dim elements per lane, D = 32 dpl with dpl <= kPer.
-template <class T, int kPer>
+// kPer: head-dim elements per lane, D = 32 dpl with dpl <= kPer.  kRows: packed
+// rows of a block, 4 or 8.
+template <class T, int kPer, int kRows>
 __global__ void __launch_bounds__(kThreads)
     step_generic_kernel(DevStep ds, ShapeInfo s, const T* __restrict__ q,
                         const T* __restrict__ k_cache, const T* __restrict__ v_cache,
@@ -166,9 +165,11 @@ __global__ void __launch_bounds__(kThreads)
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const float4 pa = *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows);
-          const float4 pb = *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows + 4);
-          const float w[kRows] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+          float w[kRows];
+#pragma unroll
+          for (int r = 0; r < kRows; r += 4)
+            *reinterpret_cast<float4*>(w + r) =
+                *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows + r);
           // (a weight of 0 leaves the sum alone: the value may be another
           // sequence's or a later token's, finite or not, and 0 x inf is NaN)
 #pragma unroll
@@ -274,12 +275,22 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace
 
+namespace {
+// Packed rows of a block: four where eight would leave SMs without one (74
+// blocks of eight rows, fp32: 20.9 us; 148 of four: half the dot products per
+// key and twice the blocks).
+int rows_of(const ShapeInfo& s, int32_t max_tokens, int sms) {
+  return ((int64_t)max_tokens * s.g + 7) / 8 * s.H_kv < sms ? 4 : 8;
+}
+}  // namespace
+
 // Blocks that share a block of rows: as many as bring the grid near two blocks
 // per SM, at most one per 256 keys of the prefix or of the longest sequence
 // the tables hold (a split costs a second launch).
 int step_generic_splits(const ShapeInfo& s, int32_t max_tokens, int32_t max_blocks,
                         int32_t prefix_len, int sms) {
-  const int64_t units = ((int64_t)max_tokens * s.g + kRows - 1) / kRows * s.H_kv;
+  const int rows = rows_of(s, max_tokens, sms);
+  const int64_t units = ((int64_t)max_tokens * s.g + rows - 1) / rows * s.H_kv;
   const int64_t keys = (int64_t)prefix_len + (int64_t)max_blocks * s.B;
   const int64_t n = std::min<int64_t>(2 * (int64_t)sms / units, keys / 256);
   return (int)std::max<int64_t>(1, std::min<int64_t>(n, kStepGenericSplits));
@@ -292,11 +303,11 @@ size_t step_generic_workspace(const ShapeInfo& s, int32_t max_tokens, int splits
 
 namespace {
 
-template <class T, int kPer>
+template <class T, int kPer, int kRows>
 cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, const void* k_cache,
                         const void* v_cache, void* o, float* part_o, float* part_lse, int splits,
                         int sms, cudaStream_t st) {
-  const int bytes = smem_floats(s.D) * 4;
+  const int bytes = smem_floats(s.D, kRows) * 4;
   // the shared-memory limit is raised once per device
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
@@ -304,9 +315,9 @@ cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, co
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(step_generic_kernel<T, kPer>,
+    e = cudaFuncSetAttribute(step_generic_kernel<T, kPer, kRows>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem_floats(kPer * 32) * 4);
+                             smem_floats(kPer * 32, kRows) * 4);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
@@ -322,7 +333,7 @@ cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, step_generic_kernel<T, kPer>, ds, s, (const T*)q,
+  e = cudaLaunchKernelEx(&cfg, step_generic_kernel<T, kPer, kRows>, ds, s, (const T*)q,
                          (const T*)k_cache, (const T*)v_cache, (T*)o, part_o, part_lse, splits);
   if (e != cudaSuccess || splits == 1) return e;
   const int64_t warps = (int64_t)ds.max_tokens * s.H_q;
@@ -337,11 +348,11 @@ template <class T>
 cudaError_t launch_type(const DevStep& ds, const ShapeInfo& s, const void* q, const void* k_cache,
                         const void* v_cache, void* o, float* po, float* pl, int splits, int sms,
                         cudaStream_t st) {
-  if (s.D <= 64)
-    return launch_rows<T, 2>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
-  if (s.D <= 128)
-    return launch_rows<T, 4>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
-  return launch_rows<T, 8>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
+  const bool few = rows_of(s, ds.max_tokens, sms) == 4;
+  auto fn = s.D <= 64    ? (few ? launch_rows<T, 2, 4> : launch_rows<T, 2, 8>)
+            : s.D <= 128 ? (few ? launch_rows<T, 4, 4> : launch_rows<T, 4, 8>)
+                         : (few ? launch_rows<T, 8, 4> : launch_rows<T, 8, 8>);
+  return fn(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
 }
 
 }  // namespace
