@@ -518,7 +518,8 @@ int64_t rbkv_step_plan_ints(int32_t num_seqs, int32_t max_tokens);
  * the step are read (NULL: t->block_table / t->free_words, in place).  seen
  * may be t->ctx when the block table is built in place.
  * All or nothing: a negative length (RBKV_ERR_INVALID), more rows than
- * max_tokens or a sequence beyond max_blocks (RBKV_ERR_WORKSPACE) or too few
+ * max_tokens, a sequence beyond max_blocks or 2^30 tokens
+ * (RBKV_ERR_WORKSPACE) or too few
  * free blocks (RBKV_ERR_NO_BLOCKS) is recorded in the status words, and the
  * step is empty: no rows, ctx = seen, table and free bits as they were.  A
  * block id outside the pool in a table is recorded as
@@ -551,8 +552,9 @@ size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables*
  * over the prefix's keys 0 .. prefix_len - 1 (block prefix_table[i / B], slot
  * i % B) and the keys 0 .. position[r] of the row's sequence.  q, o:
  * [max_tokens][H_q][D]; rows past the step's rows are not written.
- * prefix_len >= 0 (prefix_table may be NULL at 0: paged attention of the
- * step).  workspace: rbkv_step_workspace_bytes, 256-byte aligned, not used by
+ * prefix_len in [0, 2^30] (prefix_table may be NULL at 0: paged attention of
+ * the step).  What a row does not see does not reach it, finite or not: slots
+ * past a length, later tokens, other sequences.  workspace: rbkv_step_workspace_bytes, 256-byte aligned, not used by
  * other work until this call's kernels end (calls that overlap, and graphs
  * that run at the same time, need one each).
  * A block id outside the pool is skipped and recorded in the status words.

@@ -97,22 +97,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int
       : "memory");
 }
 
-// The same from a 4-D tensor, at (0, 0, 0, w).
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int32_t w,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // An L2 policy for data that is read once: its lines are the first to leave.
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
+// tma_load_2d from a 4-D tensor, at (0, 0, 0, w), with an L2 policy.
 __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m, int32_t w,
                                                  uint64_t* bar, uint64_t policy) {
   asm volatile(

@@ -179,7 +179,8 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
     return invalid("tensors must be 16-byte aligned");
   if (q == o) return invalid("o must not be q");
-  if (prefix_len < 0) return invalid("prefix_len must be >= 0");
+  if (prefix_len < 0 || prefix_len > 1 << 30)
+    return invalid("prefix_len must be in [0, 2^30]");
   if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4)))
     return invalid("a prefix needs a 4-byte aligned block list");
   if (!aligned(workspace, 256)) return invalid("workspace must be 256-byte aligned");

@@ -46,7 +46,7 @@ static_assert(sizeof(StepSeq) == 32, "StepSeq is 8 int32");
 // A query row: unit >= 0: entry of the streamed list; else -1 - unit: entry of
 // the tiled list.  token: its index among its sequence's new tokens.
 struct StepRow {
-  int32_t unit, token, cum, tiles;
+  int32_t unit, token, pad[2];
 };
 static_assert(sizeof(StepRow) == 16, "StepRow is 4 int32");
 
@@ -56,8 +56,8 @@ struct StepPlan {
   StepRow* rows;        // [max_tokens]
   StepSeq* streamed;    // [S], in sequence order
   StepSeq* tiled;       // [S], in sequence order
-  StepRow* of_seq;      // [S] scratch: unit, cum and tiles of a sequence; token is
-                        // the rank of its first new block
+  StepRow* of_seq;      // [S] scratch: unit of a sequence; token is the rank of its
+                        // first new block
   int32_t* new_ids;     // [max_tokens] scratch: the new block ids, by rank
 };
 
@@ -193,6 +193,28 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
     w.tile_prefix = (int64_t)s.H_kv * w.prefix_rows * (w.prefix_tile_steps + kStepTileUnit);
   w.tile_total = w.tile_prefix + (int64_t)plan.header[kPlanTileLen] * s.H_kv;
   return w;
+}
+#endif
+
+#ifdef __CUDACC__
+// 0xffff over each of two bf16 that is an infinity or NaN.
+//
+// A row must not see the values of later tokens of its sequence, and in a
+// matrix product a weight of 0 does not hide one that is not finite.  Where
+// some rows of a unit see a key and others do not, the kernels look for such
+// values, zero them in shared memory and add them as they are to the rows that
+// see them (their weights are positive: the sums are what they would be).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+         ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+// Zeroes those of 8 bf16; true if there were any.
+__device__ __forceinline__ bool zero_nonfinite(uint4* p) {
+  const uint4 w = *p;
+  const uint4 m = make_uint4(nonfinite2(w.x), nonfinite2(w.y), nonfinite2(w.z), nonfinite2(w.w));
+  if (!(m.x | m.y | m.z | m.w)) return false;
+  *p = make_uint4(w.x & ~m.x, w.y & ~m.y, w.z & ~m.z, w.w & ~m.w);
+  return true;
 }
 #endif
 

@@ -306,6 +306,39 @@ __device__ __forceinline__ void load_q(uint32_t (&qb)[NT][8][2], const Segment& 
   }
 }
 
+// Moves a group's non-finite values, if there are any, from V (in shared
+// memory) to the accumulators of the rows that see them: lane's rows 8 i + 2
+// (lane % 4) + e, dims 16 t + lane / 4 (+ 8).
+template <int NT>
+__device__ __forceinline__ void add_nonfinite(uint8_t* v, int key0, const int (&lim)[NT][2],
+                                              float (&acc)[NT][8][4], int lane) {
+  bool any = false;
+#pragma unroll
+  for (int e = 0; e < kGroup / 16; e += 32) {
+    const uint4 w = *reinterpret_cast<const uint4*>(v + (e + lane) * 16);
+    any |= (nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w)) != 0;
+  }
+  if (!__any_sync(0xffffffffu, any)) return;
+#pragma unroll 1
+  for (int key = 0; key < kKeys; ++key) {
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const uint32_t w = *reinterpret_cast<const uint16_t*>(v + group_off(key, 8 * u) +
+                                                            (lane >> 2) * 2);
+      if (nonfinite2(w)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (key0 + key < lim[i][e]) acc[i][u / 2][(u & 1) * 2 + e] += __uint_as_float(w << 16);
+      }
+    }
+  }
+  __syncwarp();
+  for (int e = lane; e < kGroup / 16; e += 32) zero_nonfinite(reinterpret_cast<uint4*>(v) + e);
+  __syncwarp();
+}
+
 // A warp's ring.
 struct Ring {
   uint8_t* stages;
@@ -343,6 +376,8 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
 #pragma unroll
     for (int t = 0; t < 8; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
   }
+  // keys that every row of the unit sees
+  const int all_see = it.flags & kPrefix ? it.keys : it.keys - it.n_tok + 1;
   // ldmatrix rows of this lane: K as [key][dim] tiles, V transposed
   const int k_key = (lane & 7) + ((lane >> 3) & 1) * 8, k_d = (lane >> 4) * 8;
   const int v_key = (lane & 7) + (lane >> 4) * 8, v_d = ((lane >> 3) & 1) * 8;
@@ -422,6 +457,8 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
       pb[i][0] = transpose8(ptx::pack_bf16x2(sc[i][0], sc[i][1]));
       pb[i][1] = transpose8(ptx::pack_bf16x2(sc[i][2], sc[i][3]));
     }
+    if (key0 + kKeys > all_see && all_see < it.keys)
+      add_nonfinite<NT>(stage + kGroup, key0, lim, acc, lane);
     // O^T += V^T P^T: 8 tiles of 16 head dims
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -764,8 +801,8 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
     e = make_cache_tmap(&maps.k, k_cache, rows, s.D, s.B);
     if (e == cudaSuccess) e = make_cache_tmap(&maps.v, v_cache, rows, s.D, s.B);
   } else {
-    e = make_group_tmap(&maps.k, k_cache, rows, 1);
-    if (e == cudaSuccess) e = make_group_tmap(&maps.v, v_cache, rows, 1);
+    e = make_group_tmap(&maps.k, k_cache, rows);
+    if (e == cudaSuccess) e = make_group_tmap(&maps.v, v_cache, rows);
   }
   if (e != cudaSuccess) return e;
   // the shared-memory limit is raised once per device

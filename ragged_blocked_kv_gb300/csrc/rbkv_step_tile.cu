@@ -70,10 +70,11 @@ constexpr int kKeyWarp = 4, kValueWarp = 7;
 constexpr int kMmaWarp = 5;
 constexpr int kWalkWarp = 6;
 constexpr int kSegments = 8, kAhead = 3;    // published segments, and how far ahead
-// Two warpgroups: the softmax warps, and one with the other roles.  Launched at kLaunchRegs a thread, the second gives
-// back down to kIssueRegs and the first takes kSoftmaxRegs: the shares add up
-// to the launch's total (a larger claim would wait forever), and the launch's
-// total leaves half of an SM's registers to a streaming CTA.
+// Two warpgroups: the softmax warps, and one with the other roles.  Launched at
+// kLaunchRegs a thread, the second gives back down to kIssueRegs and the first
+// takes kSoftmaxRegs: the shares add up to the launch's total (a larger claim
+// would wait forever), and the launch's total leaves half of an SM's registers
+// to a streaming CTA.
 constexpr int kThreads = 256;
 constexpr int kLaunchRegs = 128;
 constexpr int kIssueRegs = 48;
@@ -117,6 +118,10 @@ struct Bars {
   Segment segments[kSegments];
   uint32_t tmem_base;
   int abort_flag;
+  // k + 1 of the last segment k that held non-finite values of keys which some
+  // of its rows see, by k & 1 (every softmax warp has stored segment k before
+  // any of them reports a P of k + 1, hence before segment k + 2 has scores)
+  volatile uint32_t nonfinite[2];
 };
 static_assert(kStages * kTileBytes + (int)sizeof(Bars) <= kStepTileSmem,
               "shared-memory layout overflows its allocation");
@@ -138,8 +143,8 @@ struct Walk {
 };
 
 __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const ShapeInfo& s,
-                                          const StepPlan& plan, const StepWork& work, int64_t ctas,
-                                             int tpt, Segment& it) {
+                                             const StepPlan& plan, const StepWork& work,
+                                             int64_t ctas, int tpt, Segment& it) {
   while (w.x < w.end) {
     int n;                 // the unit's key tiles
     int64_t unit0;         // its place on the line
@@ -234,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     step_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
                      StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
-                     __nv_bfloat16* __restrict__ o, int first) {
+                     const __nv_bfloat16* __restrict__ v_cache, __nv_bfloat16* __restrict__ o,
+                     int first) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (first) ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
@@ -269,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(&bars->kv_empty[s], 1);
     }
     bars->abort_flag = 0;
+    bars->nonfinite[0] = bars->nonfinite[1] = 0;
     ptx::fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -545,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (uint32_t k = 0; more && ok; ++k) {
       // the last key this row sees
       const int pos = it.flags & kPrefix ? it.pos : it.pos + tok;
+      const int all_see = it.pos + 1;        // keys that every row sees
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < it.n; ++j) {
         const uint32_t t = tc0 + j;
@@ -646,9 +654,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float ps =
             ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         l = l * corr + ps;
-        if (j == it.n - 1 && (it.ke % kKeys) != 0) {
+        const bool ragged = all_see < it.ke && key0 + kKeys > all_see;
+        if (ragged || (j == it.n - 1 && (it.ke % kKeys) != 0)) {
           // keys past the unit's end may be anything (unwritten cache slots, and
-          // 0 * NaN is NaN): their V rows are zeroed
+          // 0 * NaN is NaN): their V rows are zeroed.  So are non-finite values
+          // of keys that some rows do not see; the epilogue looks them up.
           const uint32_t gv = gi + ring_v(j, it.n);
           const bool landed =
               wait_phase(&bars->kv_full[gv % kStages], (gv / kStages) & 1, abort_flag);
@@ -659,12 +669,20 @@ __global__ void __launch_bounds__(kThreads, 2)
             break;
           }
           uint8_t* vt = kv_s + (gv % kStages) * kTileBytes;
-          const int valid = it.ke - key0;
+          const int valid = min(it.ke - key0, kKeys);
           for (int e = row; e < (kKeys - valid) * 16; e += kRows) {
             const int key = valid + e / 16, c = e % 16;
             *reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + key * 128 + ((c & 7) << 4)) =
                 make_uint4(0, 0, 0, 0);
           }
+          const int from = ragged ? max(all_see - key0, 0) : valid;
+          bool found = false;
+          for (int e = row; e < (valid - from) * 16; e += kRows) {
+            const int key = from + e / 16, c = e % 16;
+            found |= zero_nonfinite(reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + key * 128 +
+                                                             ((c & 7) << 4)));
+          }
+          if (found) bars->nonfinite[k & 1] = k + 1;
           // the PV MMAs read these rows through the async proxy
           ptx::fence_proxy_async_smem();
         }
@@ -708,6 +726,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_arrive(&bars->o_free);
 #pragma unroll
       for (int c = 0; c < 128; ++c) ov[c] *= inv;
+      if (bars->nonfinite[k & 1] == k + 1) {
+        // (written before the last P was reported, so before its product)
+        for (int key = max(it.kb, all_see); key < min(it.ke, pos + 1); ++key) {
+          const int blk = it.table[key / B];
+          if ((uint32_t)blk >= (uint32_t)ds.num_blocks) continue;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              v_cache + (((int64_t)blk * shp.H_kv + it.kv_head) * B + key % B) * 128);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint4 x = src[c];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t bad = w[i] & nonfinite2(w[i]);
+              ov[8 * c + 2 * i] += __uint_as_float(bad << 16);
+              ov[8 * c + 2 * i + 1] += __uint_as_float(bad & 0xffff0000u);
+            }
+          }
+        }
+      }
       if (store && !partial) {
 #pragma unroll
         for (int c = 0; c < 128; c += 8) {
@@ -786,7 +824,8 @@ cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWo
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_tile_kernel, tk, tv, ds, s, w, (const __nv_bfloat16*)q,
+  return cudaLaunchKernelEx(&cfg, step_tile_kernel, tk, tv, ds, s, w,
+                            (const __nv_bfloat16*)q, (const __nv_bfloat16*)v_cache,
                             (__nv_bfloat16*)o, first ? 1 : 0);
 }
 

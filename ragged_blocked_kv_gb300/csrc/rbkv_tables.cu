@@ -29,6 +29,8 @@ constexpr int kOneSeqs = 2048, kOneBlocks = 131072, kOneRows = 8192;
 constexpr int kSmemSeqs = 2048;       // sequences of a CTA whose offsets stay on chip
 
 constexpr int32_t kErrInvalid = -1, kErrNoBlocks = -2, kErrCapacity = -6;
+// Tokens of a sequence, at most.
+constexpr uint32_t kMaxTokens = 1u << 30;
 // Lengths of the work lines of one KV head, and rows, stay below this.
 constexpr float kMaxLen = 1073741824.f;
 
@@ -53,7 +55,7 @@ __device__ __forceinline__ int32_t measure(const BuildArgs& a, int32_t seen, int
   for (int i = 0; i < kSums; ++i) v[i] = 0;
   if (seen < 0 || n_new < 0) return kErrInvalid;
   const uint32_t ctx = (uint32_t)seen + (uint32_t)n_new, B = (uint32_t)a.block_size;
-  if (ctx > 0x7fffffffu || n_new > a.max_tokens) return kErrCapacity;
+  if (ctx > kMaxTokens || n_new > a.max_tokens) return kErrCapacity;
   const uint32_t need = (ctx + B - 1) / B;
   if (need > (uint32_t)a.max_blocks) return kErrCapacity;
   v[kTokens] = n_new;
@@ -271,17 +273,17 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
     measure(a, seen, n_new, v);
     a.ctx[s] = seen + n_new;
     a.q_start[s] = at[kTokens];
-    StepRow of = {0, at[kGrow], 0, 0};
+    StepRow of = {0, at[kGrow], {0, 0}};
     StepSeq e = {s, at[kTokens], n_new, seen + n_new, 0, 0, {0, 0}};
     if (v[kStreamed]) {
       of.unit = at[kStreamed];
-      of.cum = e.cum = at[kStreamLen];
-      of.tiles = e.tiles = v[kStreamLen] - kStepStreamUnit;
+      e.cum = at[kStreamLen];
+      e.tiles = v[kStreamLen] - kStepStreamUnit;
       plan.streamed[of.unit] = e;
     } else if (v[kTiled]) {
       of.unit = -1 - at[kTiled];
-      of.cum = e.cum = at[kTileLen];
-      of.tiles = e.tiles = v[kTileLen];
+      e.cum = at[kTileLen];
+      e.tiles = v[kTileLen];
       plan.tiled[at[kTiled]] = e;
     }
     if (on_chip) {

@@ -144,9 +144,10 @@ def test_a_serving_loop_of_steps(rbkv):
 
 # ---- append and attention --------------------------------------------------------
 def _case(rbkv, hq, hkv, D, block, dtype, prefix, seen, n_new, pad=0, seed=0, fill=None,
-          scale=1.0):
+          scale=1.0, change=None):
     """A built and appended step with its caches; `fill` in every slot that no
-    token has written (the step's own rows are written by the append)."""
+    token has written (the step's own rows are written by the append);
+    `change(q, k_new, v_new)` may alter the step's rows first."""
     rng = np.random.default_rng(seed)
     seen, n_new = np.asarray(seen), np.asarray(n_new)
     S = len(seen)
@@ -175,6 +176,8 @@ def _case(rbkv, hq, hkv, D, block, dtype, prefix, seen, n_new, pad=0, seed=0, fi
         kc[~live[:, None].expand(-1, hkv, -1)] = fill
         vc[~live[:, None].expand(-1, hkv, -1)] = fill
     q, kn, vn = normal(T, hq, D), normal(T, hkv, D), normal(T, hkv, D)
+    if change is not None:
+        change(q, kn, vn)
     t = rbkv.StepTables(cfg, S, max_blocks, T)
     t.build(i32(seen), i32(n_new), block_table=i32(table), free=i32(free_words(free)))
     kd, vd = kc.cuda(), vc.cuda()
@@ -237,6 +240,82 @@ def test_attention_borders_of_tiles(rbkv, shape, prefix, own):
 @pytest.mark.parametrize("fill", [float("inf"), -3.0e38, float("nan")])
 def test_unwritten_slots_do_not_matter(rbkv, shape, fill):
     _check(rbkv, *shape, 77, *MIXED, pad=3, fill=fill)
+
+
+# (sequence, token, value) of the step below: non-finite values of new tokens
+POKES = [(0, 0, float("inf")), (0, 150, float("nan")), (0, 299, float("-inf")),
+         (1, 1, float("nan")), (1, 2, float("inf")), (2, 0, float("inf")),
+         (3, 20, float("inf")), (3, 21, float("-inf")), (4, 7, float("inf")),
+         (4, 15, float("nan"))]
+POKED = ([70, 0, 5, 130, 1000, 9], [300, 3, 1, 40, 16, 1])
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (8, 8, 128, 16, "bf16"),
+                                   (8, 4, 128, 8, "bf16"), (16, 1, 128, 128, "bf16"),
+                                   (8, 2, 64, 16, "bf16"), (8, 2, 32, 5, "f32")], ids=str)
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_later_values_do_not_reach_earlier_rows(rbkv, shape, prefix):
+    """Infinities and NaN in V of new tokens: the rows that see them have them
+    at that head dim, every other element is what it is without them."""
+    hq, hkv, D, block, dtype = shape
+    starts = np.concatenate([[0], np.cumsum(POKED[1])])
+
+    def change(q, kn, vn):
+        for i, (s, tok, value) in enumerate(POKES):
+            vn[starts[s] + tok, i % hkv, 3 * i:3 * i + 2] = value
+        vn[starts[4] + 9, 0] = float("nan")              # a whole row
+
+    t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, prefix, *POKED, pad=5, seed=3,
+                                                  change=change)
+    o = t.attention(q.cuda(), kd, vd, prefix_table=i32(ids) if prefix else None,
+                    prefix_len=prefix).cpu()[:rows].double()
+    t.device_status()
+    g = hq // hkv
+    added = torch.zeros(rows, hq, D, dtype=torch.float64)
+    for s in range(len(POKED[0])):
+        a, b = int(starts[s]), int(starts[s + 1])
+        for r in range(a, b):
+            block_of, off = divmod(int(want.slot[r]), block)
+            v = vc[block_of, :, off].double()
+            v = torch.where(torch.isfinite(v), 0.0, v).repeat_interleave(g, 0)
+            added[r:b] += v
+    ref = reference(want, q, kc, torch.where(torch.isfinite(vc), vc, torch.zeros((), dtype=vc.dtype)),
+                    ids, prefix)
+    finite = added == 0
+    err = (o - ref[0]).abs()
+    assert (err[finite] <= error_bound(ref, D, dtype)[finite]).all()
+    assert torch.equal(torch.isnan(o), torch.isnan(added))
+    infinite = torch.isinf(added)
+    assert torch.equal(o[infinite], added[infinite]) and 0 < int(infinite.sum())
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (8, 8, 128, 16, "bf16"),
+                                   (8, 2, 32, 5, "f32")], ids=str)
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_a_nan_key_or_query_reaches_its_rows_only(rbkv, shape, prefix):
+    hq, hkv, D, block, dtype = shape
+    starts = np.concatenate([[0], np.cumsum(POKED[1])])
+    g = hq // hkv
+    bad = torch.zeros(int(starts[-1]), hq, dtype=torch.bool)
+    for s, tok in [(0, 130), (1, 1), (3, 39), (4, 8)]:
+        bad[starts[s] + tok:starts[s + 1], g:2 * g] = True      # those who see key head 1
+    bad[starts[5], 0] = bad[starts[0] + 17, 1] = True           # queries
+
+    def change(q, kn, vn):
+        for s, tok in [(0, 130), (1, 1), (3, 39), (4, 8)]:
+            kn[starts[s] + tok, 1, 5] = float("nan")
+        q[starts[5], 0, 2] = q[starts[0] + 17, 1, D - 1] = float("nan")
+
+    t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, prefix, *POKED, pad=5, seed=4,
+                                                  change=change)
+    o = t.attention(q.cuda(), kd, vd, prefix_table=i32(ids) if prefix else None,
+                    prefix_len=prefix).cpu()[:rows].double()
+    t.device_status()
+    assert torch.isnan(o[bad]).all()
+    clean = [torch.nan_to_num(x.float()).to(x.dtype) for x in (q, kc)]
+    ref = reference(want, clean[0], clean[1], vc, ids, prefix)
+    err = (o - ref[0]).abs()
+    assert (err[~bad] <= error_bound(ref, D, dtype)[~bad]).all()
 
 
 @pytest.mark.parametrize("hq,hkv,decodes,prefix,own", [
