@@ -592,17 +592,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ---------------------------------------------------------------------------
-// The join: W warps per (row, query head), four columns per lane.
+// The join: W warps to a (row, query head), or V of them to a warp.
 // ---------------------------------------------------------------------------
 // O = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M) over the row's partial
 // outputs: its own part and the prefix's, each with the spills of the CTAs (or
 // pipelines) that begin inside its unit, which the segment at the unit's head
-// has written down.  A row has a handful of sources and one warp joins them; a
-// step of few rows over a long prefix has a hundred (every pipeline streamed a
-// piece), and eight warps share them.  Bound by latency, and by the partials'
-// traffic (from L2, they were just written).
+// has written down.  The partials come from the L2, they were just written; the
+// chain of dependent loads (place, spills, their rows) bounds a step of few
+// rows, the instructions of finding the sources one of many.  So a step of at
+// most 32 rows, which may have a hundred sources to a row (every pipeline
+// streamed a piece of a long prefix), gives a row eight warps; one whose rows
+// all fit the SMs at once, a warp each; and a larger one has four rows in each
+// warp, which find their sources together: 512 rows of 32 heads 6.0 us (10.0
+// with a warp each, 6.6 with two rows to a warp), 1088 rows 12.5 us (17.1,
+// 13.5); a step of 64 rows takes 68.4 us with a warp each and 71.6 with four.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinBlocks = 4;      // blocks per SM
 constexpr int kJoinWideRows = 32;   // steps of at most this many rows: W = 8
+constexpr int kJoinVecs = 4;        // rows of a warp in steps of many rows
 
 // Partial outputs of one part (own or prefix): source k's row.
 struct Part {
@@ -610,13 +617,15 @@ struct Part {
   int row, stride;
 };
 
+// V float4 per lane: columns 4 (lane + i lanes) .. + 3, i < V.
+template <int V>
 struct Join {
   float M, L;
-  float4 acc;
+  float4 acc[V];
   // N more sources (missing ones and those without a visible key have
   // log-sum-exp -inf)
   template <int N>
-  __device__ __forceinline__ void add(const float (&l)[N], const float4 (&v)[N]) {
+  __device__ __forceinline__ void add(const float (&l)[N], const float4 (&v)[N][V]) {
     float m = M;
 #pragma unroll
     for (int u = 0; u < N; ++u) m = fmaxf(m, l[u]);
@@ -624,18 +633,24 @@ struct Join {
     const float keep = ptx::ex2(M - base);
     M = m;
     L *= keep;
-    acc.x *= keep;
-    acc.y *= keep;
-    acc.z *= keep;
-    acc.w *= keep;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      acc[i].x *= keep;
+      acc[i].y *= keep;
+      acc[i].z *= keep;
+      acc[i].w *= keep;
+    }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const float w = ptx::ex2(l[u] - base);
       L += w;
-      acc.x = fmaf(w, v[u].x, acc.x);
-      acc.y = fmaf(w, v[u].y, acc.y);
-      acc.z = fmaf(w, v[u].z, acc.z);
-      acc.w = fmaf(w, v[u].w, acc.w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        acc[i].x = fmaf(w, v[u][i].x, acc[i].x);
+        acc[i].y = fmaf(w, v[u][i].y, acc[i].y);
+        acc[i].z = fmaf(w, v[u][i].z, acc[i].z);
+        acc[i].w = fmaf(w, v[u][i].w, acc[i].w);
+      }
     }
   }
 };
@@ -644,20 +659,22 @@ __device__ __forceinline__ int bounded(const Spills& s, int rows) {
   return s.first >= 0 && s.first <= rows && s.n > 0 && s.n <= rows - s.first ? s.n : 0;
 }
 
-template <int W>
-__global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : 4)
+template <int W, int V>
+__global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : kJoinBlocks)
     step_combine_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
                         __nv_bfloat16* __restrict__ o) {
-  constexpr int kHeads = kJoinWarps / W;      // query heads of a block
+  static_assert(W == 1 || V == 1, "several warps to a row, or several rows to a warp");
+  constexpr int kLanes = 32 / V;                         // of a row
+  constexpr int kHeads = kJoinWarps * V / W;             // query heads of a block
   __shared__ float4 wide_acc[W > 1 ? kJoinWarps * 32 : 1];
   __shared__ float wide_ml[W > 1 ? kJoinWarps * 2 : 1];
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x % kLanes;
   const int g = shp.g, tpt = step_tile_tokens(g);
   const bool pre = ds.prefix_len > 0;
-  const int h0 = blockIdx.x * kHeads, h = h0 + warp / W, wi = warp % W;
-  const bool live = h < shp.H_q;
+  const int h = blockIdx.x * kHeads + threadIdx.x / (kLanes * W), wi = warp % W;
+  if (h >= shp.H_q) return;      // (W = 8: the block is one head, in range)
   const int kvh = h / g, hh = h - kvh * g;
   const bool pre_streamed = pre && step_prefix_streamed(ds.max_tokens, g);
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
@@ -667,91 +684,105 @@ __global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : 4)
     // the two main sources, requested before anything that depends on the
     // row's place
     float l2[2] = {-INFINITY, -INFINITY};
-    float4 v2[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (live && wi == 0) {
+    float4 v2[2][V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v2[0][i] = v2[1][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (wi == 0) {
       l2[0] = ws.own_lse[w];
-      v2[0] = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        v2[0][i] = reinterpret_cast<const float4*>(ws.own_o + w * 128)[lane + i * kLanes];
       if (pre) {
         l2[1] = ws.pre_lse[w];
-        v2[1] = reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          v2[1][i] = reinterpret_cast<const float4*>(ws.pre_o + w * 128)[lane + i * kLanes];
       }
     }
-    if (live) {
-      Spills a, p = {0, 0};
-      const int pre_in = pre_streamed ? t : t % tpt;      // the row in its prefix unit
-      if (pre) p = ws.pre_cut[(int64_t)(t - pre_in) * shp.H_kv + kvh];
-      const StepRow r = plan.rows[t];
-      const int own_in = r.unit >= 0 ? r.token : r.token % tpt;
-      a = ws.own_cut[(int64_t)(t - own_in) * shp.H_kv + kvh];
-      // (after a wait that gave up, a unit's Spills may not have been written:
-      // nothing outside the spill rows is read then either)
-      a.n = bounded(a, r.unit >= 0 ? ws.stream_grid * kStepPipes : ws.tile_grid);
-      p.n = bounded(p, pre_streamed ? ws.stream_grid * kStepPipes : ws.tile_grid);
-      Join j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      j.add<2>(l2, v2);
-      const int n = a.n + p.n;
-      if (n > wi) {
-        const Part mine = r.unit >= 0
-            ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + own_in * g + hh,
-                   kStepPackedRows}
-            : Part{ws.tile_o, ws.tile_lse, a.first * kStepTileRows + own_in * g + hh,
-                   kStepTileRows};
-        const Part theirs = pre_streamed
-            ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + pre_in * g + hh,
-                   kStepPackedRows}
-            : Part{ws.tile_o, ws.tile_lse, p.first * kStepTileRows + pre_in * g + hh,
-                   kStepTileRows};
-        constexpr int kAtOnce = W > 1 ? 8 : 4;
-        for (int k0 = wi; k0 < n; k0 += kAtOnce * W) {
-          float l[kAtOnce];
-          float4 v[kAtOnce];
+    Spills a, p = {0, 0};
+    const int pre_in = pre_streamed ? t : t % tpt;      // the row in its prefix unit
+    if (pre) p = ws.pre_cut[(int64_t)(t - pre_in) * shp.H_kv + kvh];
+    const StepRow r = plan.rows[t];
+    const int own_in = r.unit >= 0 ? r.token : r.token % tpt;
+    a = ws.own_cut[(int64_t)(t - own_in) * shp.H_kv + kvh];
+    // (after a wait that gave up, a unit's Spills may not have been written:
+    // nothing outside the spill rows is read then either)
+    a.n = bounded(a, r.unit >= 0 ? ws.stream_grid * kStepPipes : ws.tile_grid);
+    p.n = bounded(p, pre_streamed ? ws.stream_grid * kStepPipes : ws.tile_grid);
+    Join<V> j;
+    j.M = -INFINITY;
+    j.L = 0.f;
 #pragma unroll
-          for (int u = 0; u < kAtOnce; ++u) {
-            const int k = k0 + u * W;
-            l[u] = -INFINITY;
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k < n) {
-              const bool m = k < a.n;
-              const int row = m ? mine.row + k * mine.stride
-                                : theirs.row + (k - a.n) * theirs.stride;
-              l[u] = (m ? mine.lse : theirs.lse)[row];
-              v[u] = reinterpret_cast<const float4*>((m ? mine.o : theirs.o) +
-                                                     (int64_t)row * 128)[lane];
-            }
-          }
-          j.add<kAtOnce>(l, v);
-        }
-      }
-      if (W > 1) {
-        wide_acc[threadIdx.x] = j.acc;
-        if (lane == 0) {
-          wide_ml[warp * 2] = j.M;
-          wide_ml[warp * 2 + 1] = j.L;
-        }
-        __syncthreads();       // (W = 8: the block is one head, live as a whole)
-        if (wi == 0) {
+    for (int i = 0; i < V; ++i) j.acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    j.template add<2>(l2, v2);
+    const int n = a.n + p.n;
+    if (n > wi) {
+      const Part mine = r.unit >= 0
+          ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + own_in * g + hh,
+                 kStepPackedRows}
+          : Part{ws.tile_o, ws.tile_lse, a.first * kStepTileRows + own_in * g + hh,
+                 kStepTileRows};
+      const Part theirs = pre_streamed
+          ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + pre_in * g + hh,
+                 kStepPackedRows}
+          : Part{ws.tile_o, ws.tile_lse, p.first * kStepTileRows + pre_in * g + hh,
+                 kStepTileRows};
+      constexpr int kAtOnce = W > 1 ? 8 : 4 / V;
+      for (int k0 = wi; k0 < n; k0 += kAtOnce * W) {
+        float l[kAtOnce];
+        float4 v[kAtOnce][V];
 #pragma unroll
-          for (int x = 1; x < W; ++x) {
-            float m = wide_ml[x * 2], base = fmaxf(j.M, m);
-            base = base == -INFINITY ? 0.f : base;
-            const float keep = ptx::ex2(j.M - base), f = ptx::ex2(m - base);
-            const float4 v = wide_acc[x * 32 + lane];
-            j.M = fmaxf(j.M, m);
-            j.L = j.L * keep + wide_ml[x * 2 + 1] * f;
-            j.acc.x = j.acc.x * keep + v.x * f;
-            j.acc.y = j.acc.y * keep + v.y * f;
-            j.acc.z = j.acc.z * keep + v.z * f;
-            j.acc.w = j.acc.w * keep + v.w * f;
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int k = k0 + u * W;
+          l[u] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < n) {
+            const bool m = k < a.n;
+            const int row = m ? mine.row + k * mine.stride
+                              : theirs.row + (k - a.n) * theirs.stride;
+            l[u] = (m ? mine.lse : theirs.lse)[row];
+            const float4* from =
+                reinterpret_cast<const float4*>((m ? mine.o : theirs.o) + (int64_t)row * 128);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[u][i] = from[lane + i * kLanes];
           }
         }
+        j.template add<kAtOnce>(l, v);
       }
-      // (a unit that was whole and alone: its kernel wrote O)
-      if (wi == 0 && (pre || a.n > 0)) {
-        const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
+    }
+    if constexpr (W > 1) {
+      wide_acc[threadIdx.x] = j.acc[0];
+      if (lane == 0) {
+        wide_ml[warp * 2] = j.M;
+        wide_ml[warp * 2 + 1] = j.L;
+      }
+      __syncthreads();
+      if (wi == 0) {
+#pragma unroll
+        for (int x = 1; x < W; ++x) {
+          float m = wide_ml[x * 2], base = fmaxf(j.M, m);
+          base = base == -INFINITY ? 0.f : base;
+          const float keep = ptx::ex2(j.M - base), f = ptx::ex2(m - base);
+          const float4 v = wide_acc[x * 32 + lane];
+          j.M = fmaxf(j.M, m);
+          j.L = j.L * keep + wide_ml[x * 2 + 1] * f;
+          j.acc[0].x = j.acc[0].x * keep + v.x * f;
+          j.acc[0].y = j.acc[0].y * keep + v.y * f;
+          j.acc[0].z = j.acc[0].z * keep + v.z * f;
+          j.acc[0].w = j.acc[0].w * keep + v.w * f;
+        }
+      }
+    }
+    // (a unit that was whole and alone: its kernel wrote O)
+    if (wi == 0 && (pre || a.n > 0)) {
+      const float inv = j.L > 0.f ? 1.f / j.L : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
         uint2 out;
-        out.x = ptx::pack_bf16x2(j.acc.x * inv, j.acc.y * inv);
-        out.y = ptx::pack_bf16x2(j.acc.z * inv, j.acc.w * inv);
-        reinterpret_cast<uint2*>(o + w * 128)[lane] = out;
+        out.x = ptx::pack_bf16x2(j.acc[i].x * inv, j.acc[i].y * inv);
+        out.y = ptx::pack_bf16x2(j.acc[i].z * inv, j.acc[i].w * inv);
+        reinterpret_cast<uint2*>(o + w * 128)[lane + i * kLanes] = out;
       }
     }
     if (W > 1) __syncthreads();   // the next row's sums replace these
@@ -837,7 +868,9 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
 cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                                 void* o, cudaStream_t st) {
   const bool wide = ds.max_tokens <= kJoinWideRows;
-  const int heads = wide ? 1 : kJoinWarps;
+  // one row per warp while all of them fit the SMs at once
+  const bool few = (int64_t)ds.max_tokens * s.H_q <= (int64_t)w.tile_grid * kJoinBlocks * kJoinWarps;
+  const int heads = wide ? 1 : kJoinWarps * (few ? 1 : kJoinVecs);
   const int chunks = (s.H_q + heads - 1) / heads;
   const int rows = std::min(ds.max_tokens, std::max(1, w.tile_grid * 16 / chunks));
   cudaLaunchConfig_t cfg = {};
@@ -849,7 +882,9 @@ cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const Ste
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wide ? step_combine_kernel<kJoinWarps> : step_combine_kernel<1>,
+  return cudaLaunchKernelEx(&cfg,
+                            wide ? step_combine_kernel<kJoinWarps, 1>
+                                 : few ? step_combine_kernel<1, 1> : step_combine_kernel<1, kJoinVecs>,
                             ds, s, w, (__nv_bfloat16*)o);
 }
 
