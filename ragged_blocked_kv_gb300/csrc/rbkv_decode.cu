@@ -516,19 +516,6 @@ cudaError_t make_cache_tmap(CUtensorMap* m, const void* cache, int64_t rows, int
   return make_tmap_2d(m, cache, rows, head_dim, box_rows);
 }
 
-cudaError_t make_group_tmap(CUtensorMap* m, const void* cache, int64_t rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  cuuint64_t dims[4] = {64, 16, 2, (cuuint64_t)(rows / 16)};
-  cuuint64_t strides[3] = {256, 128, 4096};
-  cuuint32_t box[4] = {64, 16, 2, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 int decode_ctas_per_sm(const ShapeInfo& s) {
   // two CTAs fit when each leaves room for the other (228 KB per SM, 1 KB
   // reserved per CTA; 160 threads x at most 204 registers each)

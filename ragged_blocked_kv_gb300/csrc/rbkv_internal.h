@@ -162,10 +162,6 @@ int decode_ctas_per_sm(const ShapeInfo& s);
 // rows of head_dim elements, boxes of 64 columns x box_rows rows, 128 B swizzle.
 cudaError_t make_cache_tmap(::CUtensorMap_st* m, const void* cache, int64_t rows,
                             int head_dim, int box_rows);
-// A bf16 cache of head dim 128 as a 4-D tensor {64 columns, 16 rows, 2 halves,
-// rows / 16}: a box of one 16-row group lands as [half][16 rows] of 128 bytes,
-// 128 B swizzle - both halves of the head dim in one copy.
-cudaError_t make_group_tmap(::CUtensorMap_st* m, const void* cache, int64_t rows);
 // Any row-major bf16 [rows][cols] matrix, same box width and swizzle.
 cudaError_t make_tmap_2d(::CUtensorMap_st* m, const void* ptr, int64_t rows, int64_t cols,
                          int box_rows);

@@ -103,16 +103,6 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-// tma_load_2d from a 4-D tensor, at (0, 0, 0, w), with an L2 policy.
-__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m, int32_t w,
-                                                 uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(w), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
 // Order this thread's earlier generic-proxy shared-memory accesses before
 // later async-proxy accesses (TMA writes, tensor-core reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -5,28 +5,28 @@
 // The units lie on one line in groups of 16 keys, cut evenly (rbkv_step.h) over
 // eight warps per SM, in two CTAs - or four in one CTA beside a CTA of the tile
 // kernel, whose tensor-core work then runs under the memory traffic of this
-// one (they share an SM's registers and shared memory by design: 99 and 129
-// KB).  Each warp is a pipeline of its own: lane 0 keeps a ring
-// of three 8 KB groups (16 keys of K and V, one TMA copy each) in flight,
-// and the warp multiplies, exponentiates and accumulates a group at a time:
+// one (they share an SM's registers and shared memory by design: 98 and 130
+// KB).  Each warp is a pipeline of its own: it keeps a ring of three 8 KB groups
+// (16 keys of K and V, 16 bytes per lane and copy) in flight, and multiplies,
+// exponentiates and accumulates a group at a time:
 //   S^T = K Q^T   (m16n8k16: 16 keys x 8 query rows, one or two such tiles)
 //   P^T = exp2(S^T - running maximum of the row), rounded to bf16
 //   O^T += V^T P^T (16 head dims x 8 rows per MMA)
 // with the keys and head dims on the MMAs' 16-row side, so a group of 4 or 8
 // heads wastes at most half of the narrow side, where Q on the 16-row side
 // would waste three quarters.  No warp waits for another: no merge, no block
-// barrier; 128 KB in flight per SM cover the latency.  (Four warps sharing
+// barrier; 192 KB in flight per SM cover the latency.  (Four warps sharing
 // 64-key tiles of a common ring, merged per unit, held 5.2 TB/s on 512
-// sequences of 256 keys: the merge idled the ring.)
-// Every wait is bounded; on timeout the kernel records RBKV_ERR_TIMEOUT and
-// the warp drains its copies and returns.
+// sequences of 256 keys: the merge idled the ring.)  The copies are the lanes'
+// own (cp.async): as one bulk tensor copy per group they took 99 us for those
+// 512 sequences instead of 93 (5.8 TB/s), and held up the tile kernel's tensor
+// copies on the same SM: 137 instead of 127 us for both.
 #include <algorithm>
 #include <atomic>
 
 #include "rbkv_step.h"
 #include "rbkv_ptx.cuh"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,11 +44,10 @@ constexpr int kStage = 2 * kGroup;            // K + V
 constexpr int kRows = kStepPackedRows;
 constexpr int kSegments = kStages + 2;        // segments that a warp's window can meet
 constexpr int kSmemBytes =
-    kWarps * (kStages * kStage + kSegments * 32 + kStages * 8);
+    kWarps * (kStages * kStage + kSegments * 32);
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024 &&
               kSmemBytes + kStepTileSmem + 2 * 1024 <= 228 * 1024,
               "two CTAs per SM, or one beside the tile kernel's");
-constexpr long long kWaitLimit = 4000000000LL;   // ~2 s of SM clock
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Byte offset, inside a group, of the 16-byte chunk holding elements d..d+7
@@ -77,11 +76,19 @@ struct __align__(16) Segment {
 static_assert(sizeof(Segment) == 32, "Segment is 8 int32");
 enum { kPrefix = 1, kHead = 2, kWhole = 4 };
 
-// The caches as tensor maps: boxes of 16 keys, both halves (8-key blocks: 8
-// keys and one half).
-struct Maps {
-  CUtensorMap k, v;
-};
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(live ? 16 : 0), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // A warp's walk over its part [x, end) of the line, one group per issue().
 // Every lane holds the same state; block ids are held 32 to a warp.  Units
@@ -102,6 +109,7 @@ struct Walk {
   StreamCuts cuts;
   int32_t pipe;          // this pipeline
   uint64_t once;         // the L2 policy of the loads
+  const __nv_bfloat16 *k_cache, *v_cache;
 
   __device__ __forceinline__ int load_ids(const int32_t* t, int from, int n, int lane) const {
     return from + lane < n ? t[from + lane] : 0;
@@ -236,52 +244,47 @@ struct Walk {
     return __shfl_sync(0xffffffffu, ids, e - window);
   }
 
-  // Loads the next group into `stage`; false when the part has ended.
-  __device__ __forceinline__ bool issue(uint8_t* stage, uint64_t* full, Segment* segments,
-                                        const Maps& maps, const DevStep& ds, const ShapeInfo& s,
-                                        const StepPlan& plan, const StepWork& work, int lane) {
+  // Loads the next group into `stage`; false when the part has ended.  Lane l
+  // copies the 16-byte chunk l % 16 of rows l / 16, + 2, ...; rows past the
+  // unit's last key are zero (unwritten cache slots: 0 * V has to be 0).
+  __device__ __forceinline__ bool issue(uint8_t* stage, Segment* segments, const DevStep& ds,
+                                        const ShapeInfo& s, const StepPlan& plan,
+                                        const StepWork& work, int lane) {
     if (left == 0 && !advance(segments, ds, s, plan, work, lane)) return false;
     --left;
-    const int blk = id_at(entry, s, lane);
-    bool ok = (uint32_t)blk < (uint32_t)ds.num_blocks;
-    const int row = (blk * s.H_kv + kv_head) * s.B + sub * kKeys;
-    if (s.B >= kKeys) {
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(full, ok ? kStage : 0);
-        if (ok) {
-          ptx::tma_load_4d_hint(stage, &maps.k, row >> 4, full, once);
-          ptx::tma_load_4d_hint(stage + kGroup, &maps.v, row >> 4, full, once);
-        }
+    const int c = lane & 15, r0 = lane >> 4;
+    const uint32_t dst = ptx::smem_u32(stage) + (c >> 3) * kHalf + r0 * 128;
+    const int keys = cur.ctx - entry * s.B - sub * kKeys;     // of the unit, from here
+    bool bad = false;
+    auto half = [&](int blk, int row_in_block, int first) {   // eight rows
+      const bool ok = (uint32_t)blk < (uint32_t)ds.num_blocks;
+      bad |= !ok;
+      const int64_t at =
+          (((int64_t)(ok ? blk : 0) * s.H_kv + kv_head) * s.B + row_in_block + r0) * 128 + c * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t to = dst + (first + 2 * i) * 128 + ((((c & 7) ^ r0) ^ (2 * i)) << 4);
+        const bool live = ok && first + 2 * i + r0 < keys;
+        copy16(to, k_cache + at + i * 256, live, once);
+        copy16(to + kGroup, v_cache + at + i * 256, live, once);
       }
+    };
+    const int blk = id_at(entry, s, lane);
+    if (s.B >= kKeys) {
+      half(blk, sub * kKeys, 0);
+      half(blk, sub * kKeys + 8, 8);
       if (++sub * kKeys == s.B) {
         sub = 0;
         ++entry;
       }
     } else {
       // 8-key blocks: a group is two of them, or one at the unit's end
-      const bool two = entry + 1 < entries(cur.ctx, s.B);
-      const int blk1 = two ? id_at(entry + 1, s, lane) : 0;
-      const bool ok1 = (uint32_t)blk1 < (uint32_t)ds.num_blocks;
-      const int row1 = (blk1 * s.H_kv + kv_head) * s.B;
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(full, (ok ? kStage / 2 : 0) + (two && ok1 ? kStage / 2 : 0));
-        if (ok) {
-          ptx::tma_load_2d(stage, &maps.k, 0, row, full);
-          ptx::tma_load_2d(stage + kHalf, &maps.k, 64, row, full);
-          ptx::tma_load_2d(stage + kGroup, &maps.v, 0, row, full);
-          ptx::tma_load_2d(stage + kGroup + kHalf, &maps.v, 64, row, full);
-        }
-        if (two && ok1) {
-          ptx::tma_load_2d(stage + 1024, &maps.k, 0, row1, full);
-          ptx::tma_load_2d(stage + kHalf + 1024, &maps.k, 64, row1, full);
-          ptx::tma_load_2d(stage + kGroup + 1024, &maps.v, 0, row1, full);
-          ptx::tma_load_2d(stage + kGroup + kHalf + 1024, &maps.v, 64, row1, full);
-        }
-      }
-      ok = ok && ok1;
+      const int blk1 = keys > 8 ? id_at(entry + 1, s, lane) : blk;
+      half(blk, 0, 0);
+      half(blk1, 0, 8);
       entry += 2;
     }
-    if (!ok && lane == 0) atomicCAS(ds.status, 0, kDevBounds);
+    if (bad && lane == 0) atomicCAS(ds.status, 0, kDevBounds);
     return true;
   }
 };
@@ -342,17 +345,15 @@ __device__ __forceinline__ void add_nonfinite(uint8_t* v, int key0, const int (&
 // A warp's ring.
 struct Ring {
   uint8_t* stages;
-  uint64_t* full;
   Segment* segments;
-  uint32_t issued, taken;
-  bool failed;
+  uint32_t taken;
 };
 
 // Works through one segment: NT tiles of 8 packed rows.
 template <int NT>
 __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk& walk,
-                                            const Maps& maps, const DevStep& ds,
-                                            const ShapeInfo& s, const StepPlan& plan,
+                                            const DevStep& ds, const ShapeInfo& s,
+                                            const StepPlan& plan,
                                             const StepWork& work, const StepWorkspace& ws,
                                             const __nv_bfloat16* q, __nv_bfloat16* o,
                                             int64_t pipe, int lane) {
@@ -384,26 +385,11 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
 
   for (int j = 0; j < it.groups; ++j) {
     const int st = ring.taken % kStages;
-    if (!ptx::mbar_wait(&ring.full[st], (ring.taken / kStages) & 1, kWaitLimit)) {
-      if (lane == 0) ptx::report_wait(ds.status, kDevTimeout, 62, (int)ring.taken);
-      ring.failed = true;
-    }
-    ring.failed = __any_sync(0xffffffffu, ring.failed);
-    if (ring.failed) return;
+    copies_wait<kStages - 1>();
+    __syncwarp();
     const int key0 = (it.group + j) * kKeys;
     uint8_t* stage = ring.stages + st * kStage;
     const uint32_t kt = ptx::smem_u32(stage), vt = kt + kGroup;
-    if (key0 + kKeys > it.keys) {
-      // rows past the unit's last key may hold anything (unwritten cache
-      // slots): zero those of V so 0 * V stays 0
-      const int from = it.keys - key0;
-      for (int e = lane; e < (kKeys - from) * 16; e += 32) {
-        const int key = from + e / 16, c = e % 16;
-        *reinterpret_cast<uint4*>(stage + kGroup + (c >> 3) * kHalf + key * 128 +
-                                  ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-      }
-      __syncwarp();
-    }
     // S^T = K Q^T, the head dim in two chains of MMAs
     float sc[NT][4], sd[NT][4];
 #pragma unroll
@@ -470,9 +456,8 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
     ++ring.taken;
     __syncwarp();
     // the stage is free: the next group of the part
-    if (lane == 0) ptx::fence_proxy_async_smem();
-    if (walk.issue(stage, &ring.full[st], ring.segments, maps, ds, s, plan, work, lane))
-      ++ring.issued;
+    walk.issue(stage, ring.segments, ds, s, plan, work, lane);
+    copies_commit();
   }
 
   // ---- the segment's result: O itself when nothing is to be joined, the
@@ -529,9 +514,11 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
 }
 
 __global__ void __launch_bounds__(kThreads, 2)
-    step_stream_kernel(const __grid_constant__ Maps maps, DevStep ds, ShapeInfo shp,
-                       StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
-                       __nv_bfloat16* __restrict__ o, int first) {
+    step_stream_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
+                       const __nv_bfloat16* __restrict__ q,
+                       const __nv_bfloat16* __restrict__ k_cache,
+                       const __nv_bfloat16* __restrict__ v_cache, __nv_bfloat16* __restrict__ o,
+                       int first) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (first) ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
@@ -545,48 +532,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int mine = warp * half + ((int)blockIdx.x - (late ? half : 0));
   const int pipe = late ? cuts.early + mine : mine;
   const bool works = mine < (late ? cuts.late : cuts.early);
-  if (ptx::smem_u32(smem_raw) & 1023) {
-    // the swizzled layout needs a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicCAS(ds.status, 0, kDevBounds);
-  } else if (works) {
+  if (works) {
     Ring ring;
     ring.stages = smem_raw + warp * kStages * kStage;
     ring.segments =
         reinterpret_cast<Segment*>(smem_raw + kWarps * kStages * kStage) + warp * kSegments;
-    ring.full = reinterpret_cast<uint64_t*>(smem_raw + kWarps * (kStages * kStage +
-                                                                 kSegments * 32)) +
-                warp * kStages;
-    ring.issued = ring.taken = 0;
-    ring.failed = false;
-    if (lane == 0) {
-      for (int i = 0; i < kStages; ++i) ptx::mbar_init(&ring.full[i], 1);
-      ptx::fence_barrier_init();
-    }
-    __syncwarp();
+    ring.taken = 0;
     Walk walk;
     walk.cuts = cuts;
     walk.pipe = pipe;
     // own keys are read once: they are not to push the prefix, the queries and
     // the partial outputs out of the L2
     walk.once = ptx::policy_evict_first();
+    walk.k_cache = k_cache;
+    walk.v_cache = v_cache;
     walk.end = cuts.at(pipe + 1);
     walk.start(cuts.at(pipe), ds, shp, plan, work, lane);
-    for (int i = 0; i < kStages; ++i)
-      if (walk.issue(ring.stages + i * kStage, &ring.full[i], ring.segments, maps, ds, shp, plan,
-                     work, lane))
-        ++ring.issued;
+    for (int i = 0; i < kStages; ++i) {
+      walk.issue(ring.stages + i * kStage, ring.segments, ds, shp, plan, work, lane);
+      copies_commit();
+    }
     __syncwarp();
-    for (uint32_t n = 0; n < walk.seg && !ring.failed; ++n) {
+    for (uint32_t n = 0; n < walk.seg; ++n) {
       const Segment it = ring.segments[n % kSegments];
       if (it.n_tok * shp.g <= 8)
-        run_segment<1>(it, ring, walk, maps, ds, shp, plan, work, ws, q, o, pipe, lane);
+        run_segment<1>(it, ring, walk, ds, shp, plan, work, ws, q, o, pipe, lane);
       else
-        run_segment<2>(it, ring, walk, maps, ds, shp, plan, work, ws, q, o, pipe, lane);
+        run_segment<2>(it, ring, walk, ds, shp, plan, work, ws, q, o, pipe, lane);
       __syncwarp();
     }
-    // after a timeout: copies in flight must land before the CTA exits
-    for (; ring.failed && ring.taken < ring.issued; ++ring.taken)
-      ptx::mbar_wait(&ring.full[ring.taken % kStages], (ring.taken / kStages) & 1, kWaitLimit);
   }
   ptx::pdl_wait_previous();   // the grid's completion covers its predecessor
 }
@@ -825,17 +799,7 @@ size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* bas
 cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                                const void* q, const void* k_cache, const void* v_cache, void* o,
                                bool first, cudaStream_t st) {
-  const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
-  Maps maps;
   cudaError_t e;
-  if (s.B < kKeys) {
-    e = make_cache_tmap(&maps.k, k_cache, rows, s.D, s.B);
-    if (e == cudaSuccess) e = make_cache_tmap(&maps.v, v_cache, rows, s.D, s.B);
-  } else {
-    e = make_group_tmap(&maps.k, k_cache, rows);
-    if (e == cudaSuccess) e = make_group_tmap(&maps.v, v_cache, rows);
-  }
-  if (e != cudaSuccess) return e;
   // the shared-memory limit is raised once per device
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
@@ -861,7 +825,8 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_stream_kernel, maps, ds, s, w, (const __nv_bfloat16*)q,
+  return cudaLaunchKernelEx(&cfg, step_stream_kernel, ds, s, w, (const __nv_bfloat16*)q,
+                            (const __nv_bfloat16*)k_cache, (const __nv_bfloat16*)v_cache,
                             (__nv_bfloat16*)o, first ? 1 : 0);
 }
 
