@@ -279,8 +279,8 @@ def test_later_values_do_not_reach_earlier_rows(rbkv, shape, prefix):
             v = vc[block_of, :, off].double()
             v = torch.where(torch.isfinite(v), 0.0, v).repeat_interleave(g, 0)
             added[r:b] += v
-    ref = reference(want, q, kc, torch.where(torch.isfinite(vc), vc, torch.zeros((), dtype=vc.dtype)),
-                    ids, prefix)
+    finite_v = torch.where(torch.isfinite(vc), vc, torch.zeros((), dtype=vc.dtype))
+    ref = reference(want, q, kc, finite_v, ids, prefix)
     finite = added == 0
     err = (o - ref[0]).abs()
     assert (err[finite] <= error_bound(ref, D, dtype)[finite]).all()
@@ -363,6 +363,108 @@ def test_repeats_are_bit_identical(rbkv):
         ws.fill_(fill)
         again = t.attention(q.cuda(), kd, vd, prefix_table=i32(ids), prefix_len=900, workspace=ws)
         assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("hq,hkv,T", [(16, 1, 1), (17, 1, 1), (8, 1, 2), (9, 1, 2), (64, 1, 1),
+                                      (4, 4, 16), (4, 4, 17), (64, 1, 3)])
+@pytest.mark.parametrize("prefix", [0, 400])
+def test_steps_around_sixteen_packed_rows(rbkv, hq, hkv, T, prefix):
+    """Where the prefix goes from the streaming kernel to the tile kernel; the
+    rows as single tokens and as one sequence's."""
+    _check(rbkv, hq, hkv, 128, 32, "bf16", prefix, [40 + 3 * i for i in range(T)], [1] * T)
+    _check(rbkv, hq, hkv, 128, 32, "bf16", prefix, [40, 0], [T, 0], seed=1)
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (4, 4, 128, 16, "bf16"),
+                                   (8, 2, 64, 16, "f32")], ids=str)
+def test_a_step_of_idle_slots_writes_nothing(rbkv, shape):
+    for pad in (3, 40):                          # few rows and many
+        t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, 70, [5, 0, 300], [0, 0, 0],
+                                                      pad=pad)
+        assert rows == 0
+        o = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+        t.attention(q.cuda(), kd, vd, prefix_table=i32(ids), prefix_len=70, o=o)
+        t.device_status()
+        assert (o == 7.0).all()
+
+
+def test_attention_of_many_sequences(rbkv):
+    """Tables of thousands of sequences (several CTAs build them), with prompts
+    among the single tokens and idle slots."""
+    rng = np.random.default_rng(9)
+    n_new = rng.choice([0, 1, 1, 1, 3], 2100)
+    n_new[[5, 700, 2099]] = [180, 65, 33]
+    _check(rbkv, 4, 1, 128, 16, "bf16", 130, rng.integers(0, 40, 2100), n_new, pad=5)
+    _check(rbkv, 2, 1, 32, 16, "f32", 30, rng.integers(0, 20, 2100), np.minimum(n_new, 3), pad=5)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
+def test_blocks_far_into_a_large_cache(rbkv, dtype, D):
+    """Offsets past 2^31 elements: a step whose blocks lie at the end of the
+    cache against the same step at the start of a small one."""
+    hq, hkv, B, P, S = 16, 8, 64, 150, 4
+    seen, n_new = np.array([70, 0, 200, 5]), np.array([1, 90, 1, 3])
+    T, held, max_blocks = int(n_new.sum()), -(-(seen + n_new) // B), 5
+    gen = torch.Generator().manual_seed(1)
+    outs, far = [], (1 << 31) // (hkv * B * D) + 100
+    for first in (0, far):
+        cfg = _cfg(rbkv, hq, hkv, D, B, dtype, first + 20)
+        dt = cfg.torch_dtype
+        kc, vc = (torch.empty(cfg.cache_shape(), dtype=dt, device="cuda") for _ in range(2))
+        assert first == 0 or kc.numel() > 1 << 31
+        gen.manual_seed(1)
+        for c in (kc, vc):
+            c[first:] = torch.randn(20, hkv, B, D, generator=gen).to(dt).cuda()
+        q, kn, vn = (torch.randn(T, h, D, generator=gen).to(dt).cuda() for h in (hq, hkv, hkv))
+        table = np.full((S, max_blocks), -1)
+        free = np.zeros(first + 20, bool)
+        at = first + 3                                   # (three blocks hold the prefix)
+        for s in range(S):
+            n = -(-seen[s] // B)
+            table[s, :n] = range(at, at + n)
+            at += n
+        free[at:at + int(held.sum())] = True
+        t = rbkv.StepTables(cfg, S, max_blocks, T)
+        t.build(i32(seen), i32(n_new), block_table=i32(table), free=i32(free_words(free)))
+        t.append(kn, vn, kc, vc)
+        outs.append(t.attention(q, kc, vc, prefix_table=i32(range(first, first + 3)),
+                                prefix_len=P).cpu())
+        t.device_status()
+        del kc, vc
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+
+
+def test_tensors_at_sixteen_byte_addresses(rbkv):
+    """Inputs and outputs that begin 16 bytes into their storage."""
+    def shifted(x):
+        n = 16 // x.element_size()
+        y = torch.empty(x.numel() + n, dtype=x.dtype, device="cuda")[n:].view(x.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x)
+
+    for shape in ((32, 8, 128, 64, "bf16"), (8, 2, 64, 16, "f32")):
+        t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, 333, *MIXED)
+        o = t.attention(q.cuda(), kd, vd, prefix_table=i32(ids), prefix_len=333)
+        p = t.attention(shifted(q), shifted(kd), shifted(vd), prefix_table=i32(ids),
+                        prefix_len=333, o=shifted(torch.zeros_like(q)))
+        t.device_status()
+        assert torch.equal(o[:rows], p[:rows])
+
+
+def test_the_longest_sequence(rbkv):
+    """2^30 tokens are the limit of a sequence (256-token blocks)."""
+    B, n = 256, 1 << 22
+    t = rbkv.StepTables(_cfg(rbkv, block=B, blocks=n), 2, n, 4)
+    t.block_table.copy_(torch.arange(n, dtype=torch.int32, device="cuda").expand(2, n))
+    t.free.zero_()
+    t.build(i32([(1 << 30) - 1, 7]), i32([1, 2]))
+    assert t.ctx.tolist() == [1 << 30, 9] and t.slot.tolist() == [(1 << 30) - 1, 7, 8, -1]
+    t.device_status()
+    t.build(t.ctx, i32([1, 0]))
+    assert t.q_start.tolist() == [0, 0, 0] and t.ctx.tolist() == [1 << 30, 9]
+    with pytest.raises(rbkv.RbkvError) as e:
+        t.device_status()
+    assert e.value.status == WORKSPACE
 
 
 def test_bad_prefix_ids_are_reported(rbkv):

@@ -80,8 +80,8 @@ def test_attention_refusals(rbkv):
         return L.rbkv_step_attention(C.byref(cfg), C.byref(t), q, k, v, ids, n, o, ws, size, None)
 
     for bad in ({"q": None}, {"k": None}, {"v": None}, {"o": None}, {"q": FAKE + 8},
-                {"k": FAKE + 4}, {"v": FAKE + 2}, {"o": FAKE + 8}, {"n": -1}, {"ids": None},
-                {"ids": FAKE + 2}, {"q": FAKE + 4096}, {"ws": FAKE + 16}):
+                {"k": FAKE + 4}, {"v": FAKE + 2}, {"o": FAKE + 8}, {"n": -1},
+                {"n": (1 << 30) + 1}, {"ids": None}, {"ids": FAKE + 2}, {"q": FAKE + 4096}, {"ws": FAKE + 16}):
         assert call(**bad) == INVALID, bad
 
 
