@@ -17,7 +17,10 @@
 // would waste three quarters.  No warp waits for another: no merge, no block
 // barrier; 192 KB in flight per SM cover the latency.  (Four warps sharing
 // 64-key tiles of a common ring, merged per unit, held 5.2 TB/s on 512
-// sequences of 256 keys: the merge idled the ring.)  The copies are the lanes'
+// sequences of 256 keys: the merge idled the ring.)  Beside the tile kernel the
+// two contend for the SM's issue slots, not for the memory: with its
+// arithmetic left out the whole step took 102 instead of 127 us, and half of
+// the tile kernel's operand bytes made no difference.  The copies are the lanes'
 // own (cp.async): as one bulk tensor copy per group they took 99 us for those
 // 512 sequences instead of 93 (5.8 TB/s), and held up the tile kernel's tensor
 // copies on the same SM: 137 instead of 127 us for both.
@@ -574,15 +577,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 // has written down.  The partials come from the L2, they were just written; the
 // chain of dependent loads (place, spills, their rows) bounds a step of few
 // rows, the instructions of finding the sources one of many.  So a step of at
-// most 32 rows, which may have a hundred sources to a row (every pipeline
-// streamed a piece of a long prefix), gives a row eight warps; one whose rows
-// all fit the SMs at once, a warp each; and a larger one has four rows in each
+// most 16 rows, which may have a hundred sources to a row (every pipeline
+// streamed a piece of a long prefix), gives a row eight warps (a whole step of
+// 1, 4, 8, 16 rows behind 4096 keys: 10.3, 12.6, 14.8, 18.0 us; with a warp
+// each 29.6, 31.9, 16.9, 18.0; 32 rows 28.0 and 27.6); one whose rows all fit
+// the SMs at once, a warp each; and a larger one has four rows in each
 // warp, which find their sources together: 512 rows of 32 heads 6.0 us (10.0
 // with a warp each, 6.6 with two rows to a warp), 1088 rows 12.5 us (17.1,
 // 13.5); a step of 64 rows takes 68.4 us with a warp each and 71.6 with four.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinBlocks = 4;      // blocks per SM
-constexpr int kJoinWideRows = 32;   // steps of at most this many rows: W = 8
+constexpr int kJoinWideRows = 16;   // steps of at most this many rows: W = 8
 constexpr int kJoinVecs = 4;        // rows of a warp in steps of many rows
 
 // Partial outputs of one part (own or prefix): source k's row.
@@ -834,7 +839,8 @@ cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const Ste
                                 void* o, cudaStream_t st) {
   const bool wide = ds.max_tokens <= kJoinWideRows;
   // one row per warp while all of them fit the SMs at once
-  const bool few = (int64_t)ds.max_tokens * s.H_q <= (int64_t)w.tile_grid * kJoinBlocks * kJoinWarps;
+  const bool few =
+      (int64_t)ds.max_tokens * s.H_q <= (int64_t)w.tile_grid * kJoinBlocks * kJoinWarps;
   const int heads = wide ? 1 : kJoinWarps * (few ? 1 : kJoinVecs);
   const int chunks = (s.H_q + heads - 1) / heads;
   const int rows = std::min(ds.max_tokens, std::max(1, w.tile_grid * 16 / chunks));
@@ -847,10 +853,10 @@ cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const Ste
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg,
-                            wide ? step_combine_kernel<kJoinWarps, 1>
-                                 : few ? step_combine_kernel<1, 1> : step_combine_kernel<1, kJoinVecs>,
-                            ds, s, w, (__nv_bfloat16*)o);
+  auto kernel = wide  ? step_combine_kernel<kJoinWarps, 1>
+                : few ? step_combine_kernel<1, 1>
+                      : step_combine_kernel<1, kJoinVecs>;
+  return cudaLaunchKernelEx(&cfg, kernel, ds, s, w, (__nv_bfloat16*)o);
 }
 
 }  // namespace rbkv

@@ -42,6 +42,13 @@
 // Tensor memory (512 columns x 128 lanes): scores 0 [0,128), scores 1
 // [128,256), O [256,384), Q 0 [384,448), Q 1 [448,512).  Registers move from
 // the second warpgroup to the first (setmaxnreg).
+//
+// Bound by the chain of a key tile: 1950 cycles (wait for S 270, read it 230,
+// maximum 270, exponentials and P 930, report 200), of which the two products
+// take about 1270 of the tensor pipe; 7000 cycles to start and 4500 to 8000 per
+// unit.  Alone, 512 rows of 32 heads behind 4096 keys (34 GFLOP) take 33.5 us,
+// 1.03 PFLOP/s and 54% of the library's best product; 64 rows of 64 heads
+// behind 15999 keys 38 us.  (Tensor pipe 39% active; issue 31%.)
 // Every wait is bounded; on timeout the kernel records RBKV_ERR_TIMEOUT, lets
 // its copies and MMAs drain (bounded), frees its tensor memory and returns.
 #include <algorithm>

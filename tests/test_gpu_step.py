@@ -30,7 +30,8 @@ TABLES = [
     # seqs, longest, most new tokens, block, spare blocks, spare rows
     (1, 0, 1, 16, 1, 0), (1, 5, 1, 1, 3, 2), (3, 40, 0, 8, 0, 5), (17, 300, 1, 64, 9, 0),
     (33, 90, 7, 16, 100, 12), (100, 1000, 3, 128, 31, 1), (513, 700, 1, 16, 1000, 0),
-    (7, 50, 900, 16, 5, 3), (4100, 60, 2, 16, 40000, 77), (9000, 3, 1, 5, 20, 1)]
+    (7, 50, 900, 16, 5, 3), (400, 9000, 2, 16, 200000, 3), (1500, 30, 3, 16, 70, 4),
+    (4100, 60, 2, 16, 40000, 77), (9000, 3, 1, 5, 20, 1)]
 
 
 @pytest.mark.parametrize("S,longest,most,block,spare,rows", TABLES)
