@@ -288,7 +288,9 @@ int rows_of(const ShapeInfo& s, int32_t max_tokens, int sms) {
 
 // Blocks that share a block of rows: as many as bring the grid near two blocks
 // per SM, at most one per 256 keys of the prefix or of the longest sequence
-// the tables hold (a split costs a second launch).
+// the tables hold (a split costs a second launch).  One row of 8 heads, dim 64,
+// behind 2000 keys: 23.6 us with splits, 50.3 without; 32 rows 36.8 and 57.3;
+// behind 333 keys the rule gives none.
 int step_generic_splits(const ShapeInfo& s, int32_t max_tokens, int32_t max_blocks,
                         int32_t prefix_len, int sms) {
   const int rows = rows_of(s, max_tokens, sms);
