@@ -64,6 +64,45 @@ def test_tables_against_oracle(rbkv, S, longest, most, block, spare, rows, in_pl
     t.device_status()
 
 
+@pytest.mark.parametrize("S", [40, 1500])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_captured_tables(rbkv, S, in_place):
+    """A captured build and release, replayed over other lengths (one CTA, and
+    a cluster)."""
+    rng = np.random.default_rng(S)
+    B, max_blocks, T, blocks = 8, 12, 3 * S, 9 * S
+    t = rbkv.StepTables(_cfg(rbkv, block=B, blocks=blocks), S, max_blocks, T)
+    seen, n_new, done = (torch.zeros(S, dtype=torch.int32, device="cuda") for _ in range(3))
+    src, bits = torch.empty_like(t.block_table), torch.empty_like(t.free)
+
+    def step():
+        t.build(seen, n_new, **({} if in_place else {"block_table": src, "free": bits}))
+        t.release(done)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        lengths, new = rng.integers(0, 60, S), rng.integers(0, 4, S)
+        table, free, _ = random_batch(rng, lengths, B, max_blocks, blocks)
+        seen.copy_(i32(lengths))
+        n_new.copy_(i32(new))
+        for mine, given, value in ((t.block_table, src, table), (t.free, bits, free_words(free))):
+            (mine if in_place else given).copy_(i32(value))
+        gone = rng.random(S) < 0.3
+        done.copy_(i32(gone))
+        graph.replay()
+        want = oracle.step.build(lengths, new, table, free, B, T)
+        assert want.status == 0
+        for s in np.flatnonzero(gone):
+            for c in range(-(-int(want.ctx[s]) // B)):
+                want.free[want.table[s, c]] = True
+        want.ctx[gone] = 0
+        _equal(t, want)
+    t.device_status()
+
+
 @pytest.mark.parametrize("seen,n_new,T,status", [
     ([3, -1, 5], [1, 1, 1], 8, INVALID), ([3, 1, 0], [1, -2, 1], 8, INVALID),
     ([0, 0, 0], [5, 4, 0], 8, WORKSPACE), ([12, 0, 0], [1, 0, 0], 8, WORKSPACE),
