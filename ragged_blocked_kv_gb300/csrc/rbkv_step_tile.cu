@@ -43,10 +43,12 @@
 // [128,256), O [256,384), Q 0 [384,448), Q 1 [448,512).  Registers move from
 // the second warpgroup to the first (setmaxnreg).
 //
-// Bound by the chain of a key tile: 1950 cycles (wait for S 270, read it 230,
-// maximum 270, exponentials and P 930, report 200), of which the two products
-// take about 1270 of the tensor pipe; 7000 cycles to start and 4500 to 8000 per
-// unit.  Alone, 512 rows of 32 heads behind 4096 keys (34 GFLOP) take 33.5 us,
+// Bound by two chains of a key tile of nearly the same length, 1900 cycles: the
+// softmax (see S 280 or more, read it 220, maximum 270, exponentials and P 980)
+// and the ring (K_j+2 takes the stage that QK(j) releases: 330 until its
+// producer wakes, 850 for its four copies, 650 until they land); the two
+// products take 1180 of the tensor pipe.  Besides, 7000 cycles to start and 4500
+// to 8000 per unit.  Alone, 512 rows of 32 heads behind 4096 keys (34 GFLOP) take 33.5 us,
 // 1.03 PFLOP/s and 54% of the library's best product; 64 rows of 64 heads
 // behind 15999 keys 38 us.  (Tensor pipe 39% active; issue 31%.)
 // Every wait is bounded; on timeout the kernel records RBKV_ERR_TIMEOUT, lets
