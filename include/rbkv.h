@@ -557,7 +557,8 @@ size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables*
  * past a length, later tokens, other sequences.  workspace: rbkv_step_workspace_bytes, 256-byte aligned, not used by
  * other work until this call's kernels end (calls that overlap, and graphs
  * that run at the same time, need one each).
- * A block id outside the pool is skipped and recorded in the status words.
+ * The keys of a block id outside the pool are left out of the sums (a row that
+ * has no others is 0), and the id is recorded in the status words.
  * Errors: RBKV_ERR_INVALID, RBKV_ERR_UNSUPPORTED, RBKV_ERR_WORKSPACE,
  * RBKV_ERR_CUDA. */
 rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* t, const void* q,

@@ -109,6 +109,8 @@ struct Walk {
   StepSeq cur, next;
   const int32_t* table;
   uint32_t seg;          // segments published
+  uint32_t missing;      // two bits per issue(), the latest lowest: halves of the
+                         // group whose block id is outside the pool
   StreamCuts cuts;
   int32_t pipe;          // this pipeline
   uint64_t once;         // the L2 policy of the loads
@@ -162,6 +164,7 @@ struct Walk {
     next_x = x;
     left = 0;
     seg = 0;
+    missing = 0;
     window = -1;
     ids_next = 0;
     if (unit < work.streamed && kv_head == s.H_kv - 1) prefetch(ds, s, work, lane);
@@ -247,21 +250,22 @@ struct Walk {
     return __shfl_sync(0xffffffffu, ids, e - window);
   }
 
-  // Loads the next group into `stage`; false when the part has ended.  Lane l
-  // copies the 16-byte chunk l % 16 of rows l / 16, + 2, ...; rows past the
-  // unit's last key are zero (unwritten cache slots: 0 * V has to be 0).
-  __device__ __forceinline__ bool issue(uint8_t* stage, Segment* segments, const DevStep& ds,
+  // Loads the next group into `stage`, if the part has one.  Lane l copies the
+  // 16-byte chunk l % 16 of rows l / 16, + 2, ...; rows past the unit's last key
+  // are zero (unwritten cache slots: 0 * V has to be 0), and so are those of a
+  // block id outside the pool, whose scores are then taken for -inf.
+  __device__ __forceinline__ void issue(uint8_t* stage, Segment* segments, const DevStep& ds,
                                         const ShapeInfo& s, const StepPlan& plan,
                                         const StepWork& work, int lane) {
-    if (left == 0 && !advance(segments, ds, s, plan, work, lane)) return false;
+    missing <<= 2;
+    if (left == 0 && !advance(segments, ds, s, plan, work, lane)) return;
     --left;
     const int c = lane & 15, r0 = lane >> 4;
     const uint32_t dst = ptx::smem_u32(stage) + (c >> 3) * kHalf + r0 * 128;
     const int keys = cur.ctx - entry * s.B - sub * kKeys;     // of the unit, from here
-    bool bad = false;
     auto half = [&](int blk, int row_in_block, int first) {   // eight rows
       const bool ok = (uint32_t)blk < (uint32_t)ds.num_blocks;
-      bad |= !ok;
+      missing |= ok ? 0u : first ? 2u : 1u;
       const int64_t at =
           (((int64_t)(ok ? blk : 0) * s.H_kv + kv_head) * s.B + row_in_block + r0) * 128 + c * 8;
 #pragma unroll
@@ -287,8 +291,7 @@ struct Walk {
       half(blk1, 0, 8);
       entry += 2;
     }
-    if (bad && lane == 0) atomicCAS(ds.status, 0, kDevBounds);
-    return true;
+    if ((missing & 3) && lane == 0) atomicCAS(ds.status, 0, kDevBounds);
   }
 };
 
@@ -409,6 +412,18 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
         ptx::mma_bf16_16816(sc[i], a, qb[i][kk][0], qb[i][kk][1]);
         ptx::mma_bf16_16816(sd[i], b, qb[i][kk + 1][0], qb[i][kk + 1][1]);
       }
+    }
+    // (as many groups have been issued as the ring has stages, this one first)
+    const uint32_t missing = walk.missing >> (2 * (kStages - 1)) & 3;
+    if (missing) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (missing & (x < 2 ? 1 : 2)) {
+            sc[i][x] = -INFINITY;
+            sd[i][x] = 0.f;
+          }
     }
     uint32_t pb[NT][2];
 #pragma unroll

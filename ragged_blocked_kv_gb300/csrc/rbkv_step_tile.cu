@@ -127,6 +127,8 @@ struct Bars {
   Segment segments[kSegments];
   uint32_t tmem_base;
   int abort_flag;
+  // a block id outside the pool has been met (set before its K tile lands)
+  volatile int missing;
   // k + 1 of the last segment k that held non-finite values of keys which some
   // of its rows see, by k & 1 (every softmax warp has stored segment k before
   // any of them reports a P of k + 1, hence before segment k + 2 has scores)
@@ -244,6 +246,20 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// Scores -inf, in tensor memory, for the keys of a tile that have no block.
+// (Not inlined, and called from the branch of a wait that gave up: elsewhere in
+// the softmax loop these few instructions, which never run otherwise, made a step
+// of 512 rows behind 4096 keys take 134 to 137 us instead of 127; so, 129.)
+__device__ __noinline__ void hide_keys(uint32_t s_col, const int32_t* table, int key0, int ke,
+                                       int B, int num_blocks) {
+  const int lane = threadIdx.x & 31, key = key0 + lane * 8;   // blocks are of 8 keys or more
+  const bool none =
+      lane < kKeys / 8 && key < ke && (uint32_t)table[key / B] >= (uint32_t)num_blocks;
+  for (uint32_t m = __ballot_sync(0xffffffffu, none); m; m &= m - 1)
+    tmem_fill8(s_col + 8 * (__ffs(m) - 1), -INFINITY);
+  tmem_wait_st();
+}
+
 __global__ void __launch_bounds__(kThreads, 2)
     step_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
@@ -283,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(&bars->kv_full[s], 1);
       ptx::mbar_init(&bars->kv_empty[s], 1);
     }
-    bars->abort_flag = 0;
+    bars->abort_flag = bars->missing = 0;
     bars->nonfinite[0] = bars->nonfinite[1] = 0;
     ptx::fence_barrier_init();
   }
@@ -313,16 +329,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == kKeyWarp || warp == kValueWarp) {
       // --------------------------------------------------------- TMA producers
-      // Lane i holds the block id of box i of a tile (-2: no such box; one out
-      // of range is skipped and reported).  Ids are loaded a tile ahead, the
-      // next segment's while the last tile of the current one is copied.
+      // Lane i holds the block id of box i of a tile; -2: no such box; -1: an id
+      // outside the pool, which is reported.  (Id -1 makes rows in front of the
+      // cache: the copy fills the box with zeros, and the softmax threads take
+      // its scores for -inf.)  Ids are loaded a tile ahead, the next segment's
+      // while the last tile of the current one is copied.
       const bool leader = elect_one();
       const bool is_k = warp == kKeyWarp;
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
       const int box_rows = B < kKeys ? B : kKeys, boxes = kKeys / box_rows;
       auto look_up = [&](const Segment& u, int j) -> int {
         const int key = u.kb + j * kKeys + lane * box_rows;
-        return lane < boxes && key < u.ke ? u.table[key / B] : -2;
+        if (lane >= boxes || key >= u.ke) return -2;
+        const int blk = u.table[key / B];
+        return (uint32_t)blk < (uint32_t)ds.num_blocks ? blk : -1;
       };
       Segment it, nx;
       uint32_t gi = 0, k = 0;
@@ -350,9 +370,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             break;
           }
-          const bool good = (uint32_t)id < (uint32_t)ds.num_blocks;
-          const uint32_t mask = __ballot_sync(0xffffffffu, good);
-          if (id != -2 && !good) atomicCAS(ds.status, 0, kDevBounds);
+          const uint32_t mask = __ballot_sync(0xffffffffu, id != -2);
+          if (__any_sync(0xffffffffu, id == -1) && leader) {
+            atomicCAS(ds.status, 0, kDevBounds);
+            bars->missing = 1;
+          }
           if (leader)
             ptx::mbar_arrive_expect_tx(&bars->kv_full[st],
                                        (uint32_t)(__popc(mask) * box_rows * 256));
@@ -567,15 +589,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t t = tc0 + j;
         // tcgen05.ld/st are warp-collective: every decision below is warp-uniform
         const bool got = wait_phase(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          site = 81;
-          at = (int)t;
-          break;
-        }
-        tc_fence_after();
         const uint32_t s_col = lane_base + (t & 1) * kKeys;   // S of the tile; then its P
         const int key0 = it.kb + j * kKeys;
+        // (a block id outside the pool is noted before its K tile lands)
+        if (!__all_sync(0xffffffffu, got && !bars->missing)) {
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            site = 81;
+            at = (int)t;
+            break;
+          }
+          tc_fence_after();
+          hide_keys(s_col, it.table, key0, it.ke, B, ds.num_blocks);
+        }
+        tc_fence_after();
         // this row sees the tile's first `lim` keys: those <= its position and
         // before the unit's end (a prefix of the key tile, possibly empty or all)
         const int lim = min(pos + 1, it.ke) - key0;
