@@ -109,8 +109,7 @@ struct Walk {
   StepSeq cur, next;
   const int32_t* table;
   uint32_t seg;          // segments published
-  uint32_t missing;      // two bits per issue(), the latest lowest: halves of the
-                         // group whose block id is outside the pool
+  bool missing;          // a block id outside the pool has been met
   StreamCuts cuts;
   int32_t pipe;          // this pipeline
   uint64_t once;         // the L2 policy of the loads
@@ -164,7 +163,7 @@ struct Walk {
     next_x = x;
     left = 0;
     seg = 0;
-    missing = 0;
+    missing = false;
     window = -1;
     ids_next = 0;
     if (unit < work.streamed && kv_head == s.H_kv - 1) prefetch(ds, s, work, lane);
@@ -257,15 +256,15 @@ struct Walk {
   __device__ __forceinline__ void issue(uint8_t* stage, Segment* segments, const DevStep& ds,
                                         const ShapeInfo& s, const StepPlan& plan,
                                         const StepWork& work, int lane) {
-    missing <<= 2;
     if (left == 0 && !advance(segments, ds, s, plan, work, lane)) return;
     --left;
     const int c = lane & 15, r0 = lane >> 4;
     const uint32_t dst = ptx::smem_u32(stage) + (c >> 3) * kHalf + r0 * 128;
     const int keys = cur.ctx - entry * s.B - sub * kKeys;     // of the unit, from here
+    bool bad = false;
     auto half = [&](int blk, int row_in_block, int first) {   // eight rows
       const bool ok = (uint32_t)blk < (uint32_t)ds.num_blocks;
-      missing |= ok ? 0u : first ? 2u : 1u;
+      bad |= !ok;
       const int64_t at =
           (((int64_t)(ok ? blk : 0) * s.H_kv + kv_head) * s.B + row_in_block + r0) * 128 + c * 8;
 #pragma unroll
@@ -291,7 +290,10 @@ struct Walk {
       half(blk1, 0, 8);
       entry += 2;
     }
-    if ((missing & 3) && lane == 0) atomicCAS(ds.status, 0, kDevBounds);
+    if (bad) {
+      missing = true;
+      if (lane == 0) atomicCAS(ds.status, 0, kDevBounds);
+    }
   }
 };
 
@@ -413,17 +415,22 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
         ptx::mma_bf16_16816(sd[i], b, qb[i][kk + 1][0], qb[i][kk + 1][1]);
       }
     }
-    // (as many groups have been issued as the ring has stages, this one first)
-    const uint32_t missing = walk.missing >> (2 * (kStages - 1)) & 3;
-    if (missing) {
+    // keys without a block (this group's or one issued later has some)
+    if (walk.missing) {
+      const int32_t* table = ds.prefix_table;
+      if (!(it.flags & kPrefix))
+        table = ds.block_table +
+                (int64_t)plan.streamed[plan.rows[it.row].unit].seq * ds.max_blocks;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int half = 0; half < 2; ++half) {
+        const int key = key0 + 8 * half;
+        if (key >= it.keys || (uint32_t)table[key / s.B] < (uint32_t)ds.num_blocks) continue;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (missing & (x < 2 ? 1 : 2)) {
-            sc[i][x] = -INFINITY;
-            sd[i][x] = 0.f;
-          }
+        for (int i = 0; i < NT; ++i) {
+          sc[i][2 * half] = sc[i][2 * half + 1] = -INFINITY;
+          sd[i][2 * half] = sd[i][2 * half + 1] = 0.f;
+        }
+      }
     }
     uint32_t pb[NT][2];
 #pragma unroll

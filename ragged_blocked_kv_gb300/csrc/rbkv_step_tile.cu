@@ -351,6 +351,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       int id = more ? look_up(it, 0) : -2;
       while (more && ok) {
         for (int j = 0; ok && j < it.n; ++j) {
+          if (id == -1) {
+            atomicCAS(ds.status, 0, kDevBounds);
+            bars->missing = 1;
+          }
+          __syncwarp();
           int id_next = -2;
           if (j + 1 < it.n) {
             id_next = look_up(it, j + 1);
@@ -371,10 +376,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             break;
           }
           const uint32_t mask = __ballot_sync(0xffffffffu, id != -2);
-          if (__any_sync(0xffffffffu, id == -1) && leader) {
-            atomicCAS(ds.status, 0, kDevBounds);
-            bars->missing = 1;
-          }
           if (leader)
             ptx::mbar_arrive_expect_tx(&bars->kv_full[st],
                                        (uint32_t)(__popc(mask) * box_rows * 256));
