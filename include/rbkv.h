@@ -491,7 +491,12 @@ rbkv_status rbkv_frame_device_status(rbkv_frame* f, rbkv_stream stream);
 
 /* The arrays of a step, all in device memory, owned by the caller.  They stay
  * valid for any number of layers until the next build.  Two steps in flight
- * at once (two streams, two graphs) need tables of their own. */
+ * at once (two streams, two graphs) need tables of their own.
+ * A step is built for one block size, one number of query heads per KV head
+ * (the append needs the block size only) and the sizes below.  The calls that
+ * follow may be given other configurations (other KV heads, head dims, types),
+ * but where one of these differs, or for the release the pool, they do nothing
+ * and record RBKV_ERR_INVALID in the status words. */
 typedef struct {
   int32_t num_seqs;        /* S: request slots (an idle slot takes no tokens) */
   int32_t max_blocks;      /* entries of one row of block_table */
@@ -567,8 +572,8 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
                                 void* workspace, size_t workspace_bytes, rbkv_stream stream);
 
 /* Wait for `stream`, then read and clear the status words: RBKV_OK or the
- * first error since they were last read (see rbkv_step_build; also
- * RBKV_ERR_TIMEOUT, as rbkv_pass_device_status). */
+ * first error since they were last read (see rbkv_step_build and
+ * rbkv_step_tables; also RBKV_ERR_TIMEOUT, as rbkv_pass_device_status). */
 rbkv_status rbkv_step_device_status(const rbkv_step_tables* t, rbkv_stream stream);
 
 /* ---- the rest of a decoder layer: tensor-core GEMM and RMSNorm --------------

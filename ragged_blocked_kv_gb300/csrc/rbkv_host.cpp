@@ -1206,7 +1206,9 @@ rbkv_status read_device_status(void* dev, cudaStream_t st) {
   if (word == RBKV_ERR_NO_BLOCKS) return fail(RBKV_ERR_NO_BLOCKS, "the step needs more blocks than are free");
   if (word == RBKV_ERR_WORKSPACE)
     return fail(RBKV_ERR_WORKSPACE, "the step exceeds max_tokens or max_blocks of its tables");
-  if (word == RBKV_ERR_INVALID) return fail(RBKV_ERR_INVALID, "the step has a negative length");
+  if (word == RBKV_ERR_INVALID)
+    return fail(RBKV_ERR_INVALID, "the step has a negative length, or was built for another "
+                                  "configuration or for tables of other sizes");
   if (word == kDevTimeout)
     return fail(RBKV_ERR_TIMEOUT, "a bounded device wait gave up (site " + std::to_string(words[1]) +
                                       ", index " + std::to_string(words[2]) + ", block " +

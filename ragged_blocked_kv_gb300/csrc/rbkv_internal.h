@@ -114,6 +114,10 @@ struct DevPass {
   // device array {num_tokens, n_decode, n_generic, n_chunk (items), n_combine}.
   // Null for a plain pass.
   const int32_t* counts;
+  // A step built on the device (rbkv_step_*): {block size, rows of its arrays}
+  // that it was built for, to be compared with what it is used with.  Null
+  // otherwise.
+  const int32_t* built_for[2];
 };
 
 enum { kCountTokens = 0, kCountDecode = 1, kCountGeneric = 2, kCountChunk = 3, kCountCombine = 4 };
@@ -142,6 +146,7 @@ inline size_t partial_lse_bytes(int32_t n_parts, const ShapeInfo& s) {
 }
 
 // Status codes written by kernels (same values as rbkv_status).
+constexpr int32_t kDevInvalid = -1;
 constexpr int32_t kDevBounds = -4;
 constexpr int32_t kDevTimeout = -7;
 

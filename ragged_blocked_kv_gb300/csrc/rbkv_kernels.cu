@@ -67,6 +67,11 @@ __global__ void __launch_bounds__(kAppendThreads)
   const uint32_t per_tok = (uint32_t)H_kv * (uint32_t)vec_per_row;
   const uint32_t half = (uint32_t)pass_count(dp, kCountTokens, dp.num_tokens) * per_tok;
   const uint32_t total = 2 * half;
+  if (dp.built_for[0] &&
+      (*dp.built_for[0] != B || *dp.built_for[1] != dp.num_tokens)) {
+    if (threadIdx.x == 0 && total > 0) report(dp.status, kDevInvalid);
+    return;
+  }
   for (uint32_t i0 = blockIdx.x * kAppendThreads + threadIdx.x; i0 < total;
        i0 += kAppendUnroll * stride) {
     uint4 val[kAppendUnroll];

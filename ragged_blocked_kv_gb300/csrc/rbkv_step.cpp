@@ -151,7 +151,9 @@ rbkv_status rbkv_step_append(const rbkv_config* cfg, const rbkv_step_tables* t,
   dp.slot = t->slot;
   dp.num_tokens = t->max_tokens;
   dp.num_blocks = cfg->num_blocks;
-  dp.counts = t->q_start + t->num_seqs;   // the step's row count
+  dp.counts = t->plan + kPlanRows;
+  dp.built_for[0] = t->plan + kPlanBlock;
+  dp.built_for[1] = t->plan + kPlanTokens;
   cudaError_t e = launch_kv_append(dp, s, k_new, v_new, k_cache, v_cache, (cudaStream_t)stream,
                                    true);
   if (e != cudaSuccess) return cuda_fail(e, "step append launch");

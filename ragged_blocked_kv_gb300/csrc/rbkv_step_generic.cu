@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads)
   float* p_s = smem + kRows * D + warp * 32 * kRows;
   float* join_o = smem + kRows * D + kWarps * 32 * kRows;
   float* join_ml = join_o + kWarps * kRows * D;
-  const int T_rows = plan.header[kPlanRows];
+  const int T_rows = step_rows(ds, s, plan);
   const int n_rows = T_rows * g;               // packed rows of a KV head
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int stride = kWarps * splits, mine = split * kWarps + warp;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(128)
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const int lane = threadIdx.x & 31, D = s.D;
-  const int64_t rows = (int64_t)plan.header[kPlanRows] * s.H_q;
+  const int64_t rows = (int64_t)step_rows(ds, s, plan) * s.H_q;
   const int64_t all = (int64_t)ds.max_tokens * s.H_q;
   for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); w < rows;
        w += (int64_t)gridDim.x * 4) {

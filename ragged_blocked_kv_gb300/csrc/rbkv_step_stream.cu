@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : kJoinBlocks)
   const int kvh = h / g, hh = h - kvh * g;
   const bool pre_streamed = pre && step_prefix_streamed(ds.max_tokens, g);
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
-  const int T = plan.header[kPlanRows];
+  const int T = step_rows(ds, shp, plan);
   for (int t = blockIdx.y; t < T; t += gridDim.y) {
     const int64_t w = (int64_t)t * shp.H_q + h;
     // the two main sources, requested before anything that depends on the

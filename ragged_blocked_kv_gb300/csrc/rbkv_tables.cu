@@ -35,7 +35,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kOneSeqs = 1024, kOneBlocks = 524288, kOneRows = 8192;
 constexpr int kSmemSeqs = 2048;       // sequences of a CTA whose offsets stay on chip
 
-constexpr int32_t kErrInvalid = -1, kErrNoBlocks = -2, kErrCapacity = -6;
+constexpr int32_t kErrInvalid = kDevInvalid, kErrNoBlocks = -2, kErrCapacity = -6;
 // Tokens of a sequence, at most.
 constexpr uint32_t kMaxTokens = 1u << 30;
 // Lengths of the work lines of one KV head, and rows, stay below this.
@@ -311,6 +311,12 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
     plan.header[kPlanTiled] = ok ? total[kTiled] : 0;
     plan.header[kPlanStreamLen] = ok ? total[kStreamLen] : 0;
     plan.header[kPlanTileLen] = ok ? total[kTileLen] : 0;
+    plan.header[kPlanGroup] = a.group;
+    plan.header[kPlanBlock] = B;
+    plan.header[kPlanSeqs] = S;
+    plan.header[kPlanTokens] = a.max_tokens;
+    plan.header[kPlanMaxBlocks] = a.max_blocks;
+    plan.header[kPlanPool] = a.num_blocks;
     if (!ok) atomicCAS(a.status, 0, err);
   }
 
@@ -394,6 +400,13 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
 __global__ void __launch_bounds__(256)
     release_kernel(BuildArgs a, const int32_t* __restrict__ done) {
   const int s = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  const int32_t* h = a.plan;
+  if (h[kPlanBlock] != 0 &&      // (0: no step has been built yet)
+      (h[kPlanBlock] != a.block_size || h[kPlanSeqs] != a.num_seqs ||
+       h[kPlanMaxBlocks] != a.max_blocks || h[kPlanPool] != a.num_blocks)) {
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, kErrInvalid);
+    return;
+  }
   if (s >= a.num_seqs || done[s] == 0) return;
   const int32_t ctx = a.ctx[s];
   int32_t held, need;
