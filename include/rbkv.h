@@ -559,8 +559,11 @@ size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables*
  * [max_tokens][H_q][D]; rows past the step's rows are not written.
  * prefix_len in [0, 2^30] (prefix_table may be NULL at 0: paged attention of
  * the step).  What a row does not see does not reach it, finite or not: slots
- * past a length, later tokens, other sequences.  workspace: rbkv_step_workspace_bytes, 256-byte aligned, not used by
- * other work until this call's kernels end (calls that overlap, and graphs
+ * past a length, later tokens, other sequences.  A value that is not finite
+ * reaches every row that sees it (as itself or as NaN, where its weight
+ * underflows to 0); a row whose scores are all -inf is 0, as in the pass's
+ * attention.  workspace: rbkv_step_workspace_bytes, 256-byte aligned, not used
+ * by other work until this call's kernels end (calls that overlap, and graphs
  * that run at the same time, need one each).
  * The keys of a block id outside the pool are left out of the sums (a row that
  * has no others is 0), and the id is recorded in the status words.

@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kThreads)
       for (int r = 0; r < kRows; ++r) {
         // (other sequences' rows see none of these keys: their terms are 0)
         const int lim = r < ra || r >= rb ? 0 : causal ? lim0 + tok[r] - tok0 : n;
-        const float sc = off >= 0 && key < lim ? x[r] : -INFINITY;
+        const bool sees = off >= 0 && key < lim;
+        const float sc = sees ? x[r] : -INFINITY;
         const float mn = fmaxf(m[r], warp_max(sc));
         // a row with no visible key so far keeps max -inf: its terms are 0
         const float base = mn == -INFINITY ? 0.f : mn;
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kThreads)
         l[r] = fmaf(l[r], corr, p);       // this lane's keys; summed at the end
 #pragma unroll
         for (int i = 0; i < kPer; ++i) acc[r][i] *= corr;
-        p_s[lane * kRows + r] = p;
+        p_s[lane * kRows + r] = sees ? p : -1.f;
       }
       __syncwarp();
       // several value rows in flight: their latency is what a chunk waits for
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads)
         float v[kAhead][kPer];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          // (a key that no row sees has weight 0: any row may stand in)
+          // (a key that no row sees is left out below: any row may stand in)
           const int64_t at = max((int64_t)0, __shfl_sync(0xffffffffu, off, j0 + u));
           const T* vr = v_cache + at + lane;
 #pragma unroll
@@ -172,13 +173,15 @@ __global__ void __launch_bounds__(kThreads)
           for (int r = 0; r < kRows; r += 4)
             *reinterpret_cast<float4*>(w + r) =
                 *reinterpret_cast<const float4*>(p_s + (j0 + u) * kRows + r);
-          // (a weight of 0 leaves the sum alone: the value may be another
-          // sequence's or a later token's, finite or not, and 0 x inf is NaN)
+          // (a weight of -1 leaves the sum alone: the row does not see the key, whose
+          // value may be another sequence's or a later token's, finite or not; one
+          // that underflowed to 0 does not: a value that is not finite reaches
+          // every row that sees it)
 #pragma unroll
           for (int r = 0; r < kRows; ++r)
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              acc[r][i] = w[r] != 0.f ? fmaf(w[r], v[u][i], acc[r][i]) : acc[r][i];
+              acc[r][i] = w[r] < 0.f ? acc[r][i] : fmaf(w[r], v[u][i], acc[r][i]);
         }
       }
       __syncwarp();
