@@ -647,6 +647,8 @@ class StepTables:
             o, workspace = self._outputs(o, workspace, prefix_len, stream)
         if workspace.get_device() != self._index:
             raise ValueError("workspace is on another device than the tables")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         dt, cache = self._dt, self._cache_shape
         self._call(self._f_attention, self._ptr(q, "q", dt, self._q_shape),
                    self._ptr(k_cache, "k_cache", dt, cache),

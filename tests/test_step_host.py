@@ -185,3 +185,14 @@ def test_reference_and_oracle_attention(prefix):
         moved = oracle.step.Step(0, st.q_start, st.ctx + prefix, whole, [], st.position + prefix,
                                  st.slot)
         assert torch.allclose(reference(moved, q, kc, vc, [], 0)[0], ref, atol=1e-12)
+
+
+def test_a_strided_workspace_is_refused(rbkv):
+    """Its bytes are not the ones behind its address (an expanded one has one)."""
+    cfg = rbkv.Config(8, 2, 64, 16, "f32", 33)
+    t = rbkv.StepTables(cfg, 4, 8, 16, device="cpu")
+    t._index = -1                                # (a CPU tensor's: past the device check)
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 20),
+               torch.empty(1 << 10, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="contiguous"):
+            t.attention(None, None, None, o=torch.empty(0), workspace=ws)
