@@ -389,6 +389,13 @@ def _device(device):
     return torch.cuda.device(device)
 
 
+def _int32(x: int, name: str) -> int:
+    """(ctypes would cut it off)"""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits")
+    return x
+
+
 def _dev_ptr(t, name, dtype, shape):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -548,6 +555,8 @@ class StepTables:
         self.config = config
         self.num_seqs, self.max_blocks = int(num_seqs), int(max_blocks)
         self.max_tokens = int(max_tokens)
+        for x in (self.num_seqs, self.max_blocks, self.max_tokens):
+            _int32(x, "num_seqs, max_blocks and max_tokens")
         ints = int(lib().rbkv_step_plan_ints(self.num_seqs, self.max_tokens))
         if ints == 0 or self.max_blocks < 1 or config.num_blocks < 1:
             raise ValueError("num_seqs, max_blocks, max_tokens and num_blocks must be >= 1")
@@ -628,15 +637,16 @@ class StepTables:
                    self._ptr(v_cache, "v_cache", dt, cache), stream=stream)
 
     def workspace_bytes(self, prefix_len: int = 0) -> int:
+        prefix_len = _int32(int(prefix_len), "prefix_len")
         with _device(self.device):
-            return int(lib().rbkv_step_workspace_bytes(self._c, self._t, int(prefix_len)))
+            return int(lib().rbkv_step_workspace_bytes(self._c, self._t, prefix_len))
 
     def attention(self, q, k_cache, v_cache, prefix_table=None, prefix_len: int = 0, o=None,
                   workspace=None, stream=None):
         """Every row attends the prefix and its sequence's keys up to its own;
         returns O ([max_tokens][H_q][D]; rows past the step's are left as they
         were)."""
-        prefix_len = int(prefix_len)
+        prefix_len = _int32(int(prefix_len), "prefix_len")
         table = None
         if prefix_table is not None:
             if prefix_table.dim() != 1 or \

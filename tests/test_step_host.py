@@ -196,3 +196,22 @@ def test_a_strided_workspace_is_refused(rbkv):
                torch.empty(1 << 10, 2, dtype=torch.uint8)[:, 0]):
         with pytest.raises(ValueError, match="contiguous"):
             t.attention(None, None, None, o=torch.empty(0), workspace=ws)
+
+
+@pytest.mark.parametrize("sizes", [(2 ** 32 + 4, 8, 16), (4, 2 ** 32 + 8, 16), (4, 8, 2 ** 32 + 16),
+                                   (2 ** 31, 8, 16), (4, 8, 2 ** 31)])
+def test_sizes_past_32_bits_are_refused(rbkv, sizes):
+    """(meta: nothing is allocated where they were taken for small ones)"""
+    cfg = rbkv.Config(8, 2, 64, 16, "f32", 33)
+    with pytest.raises(ValueError, match="32 bits"):
+        rbkv.StepTables(cfg, *sizes, device="meta")
+
+
+@pytest.mark.parametrize("prefix_len", [2 ** 32, 2 ** 31, -2 ** 32 + 5])
+def test_prefix_lengths_past_32_bits_are_refused(rbkv, prefix_len):
+    t = rbkv.StepTables(rbkv.Config(8, 2, 64, 16, "f32", 33), 4, 8, 16, device="cpu")
+    with pytest.raises(ValueError, match="32 bits"):
+        t.workspace_bytes(prefix_len)
+    with pytest.raises(ValueError, match="32 bits"):
+        t.attention(None, None, None, prefix_len=prefix_len, o=torch.empty(0),
+                    workspace=torch.empty(0))
