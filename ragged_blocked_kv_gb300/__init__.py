@@ -526,6 +526,18 @@ class Frame:
             pass
 
 
+def _held(name: str):
+    """A tensor whose address the library holds: changed in place, not replaced."""
+    key = "_" + name
+
+    def set_(self, value):
+        if getattr(self, key, value) is not value:
+            raise AttributeError(f"{name} cannot be replaced: write into it (copy_, fill_, ...)")
+        self.__dict__[key] = value
+
+    return property(lambda self: self.__dict__[key], set_)
+
+
 class StepTables:
     """Block tables, slots and the attention plan of a step, on the GPU.
 
@@ -546,8 +558,13 @@ class StepTables:
     [num_seqs + 1], ``ctx`` [num_seqs] (0 at first), ``position`` and ``slot``
     [max_tokens] (-1 past the step's rows).  Lengths, tables and positions
     count a sequence's own tokens, not the prefix.  A step that does not fit
-    is empty and ``device_status`` says why.
+    is empty and ``device_status`` says why.  The arrays are written in place
+    (``t.free.copy_(...)``): the library holds their addresses.
     """
+
+    block_table, free, q_start = _held("block_table"), _held("free"), _held("q_start")
+    ctx, position, slot = _held("ctx"), _held("position"), _held("slot")
+    plan, status = _held("plan"), _held("status")
 
     def __init__(self, config: Config, num_seqs: int, max_blocks: int, max_tokens: int,
                  device="cuda"):

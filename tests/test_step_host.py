@@ -215,3 +215,22 @@ def test_prefix_lengths_past_32_bits_are_refused(rbkv, prefix_len):
     with pytest.raises(ValueError, match="32 bits"):
         t.attention(None, None, None, prefix_len=prefix_len, o=torch.empty(0),
                     workspace=torch.empty(0))
+
+
+def test_the_arrays_cannot_be_replaced(rbkv):
+    """The library holds their addresses: another tensor under the name would
+    not be used, and would free the memory that is."""
+    t = rbkv.StepTables(rbkv.Config(8, 2, 64, 16, "f32", 33), 4, 8, 16, device="cpu")
+    for name in ("block_table", "free", "q_start", "ctx", "position", "slot", "plan", "status"):
+        held = getattr(t, name)
+        with pytest.raises(AttributeError):
+            setattr(t, name, held.clone())
+        assert getattr(t, name) is held
+    t.free &= 1                                  # in place: the same tensor
+    assert t.free.tolist() == [1, 1]
+    before = t.ctx
+    t.ctx += 3
+    assert t.ctx is before and t.ctx.tolist() == [3, 3, 3, 3]
+    for name in ("free", "ctx"):
+        with pytest.raises(AttributeError):
+            delattr(t, name)
