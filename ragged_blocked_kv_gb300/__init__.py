@@ -526,18 +526,6 @@ class Frame:
             pass
 
 
-def _held(name: str):
-    """A tensor whose address the library holds: changed in place, not replaced."""
-    key = "_" + name
-
-    def set_(self, value):
-        if getattr(self, key, value) is not value:
-            raise AttributeError(f"{name} cannot be replaced: write into it (copy_, fill_, ...)")
-        self.__dict__[key] = value
-
-    return property(lambda self: self.__dict__[key], set_)
-
-
 class StepTables:
     """Block tables, slots and the attention plan of a step, on the GPU.
 
@@ -562,9 +550,19 @@ class StepTables:
     (``t.free.copy_(...)``): the library holds their addresses.
     """
 
-    block_table, free, q_start = _held("block_table"), _held("free"), _held("q_start")
-    ctx, position, slot = _held("ctx"), _held("position"), _held("slot")
-    plan, status = _held("plan"), _held("status")
+    _HELD = frozenset(("block_table", "free", "q_start", "ctx", "position", "slot", "plan",
+                       "status"))
+
+    def __setattr__(self, name, value):
+        # (plain attributes, for fast reads: a small step's time is the host's)
+        if name in self._HELD and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} cannot be replaced: write into it (copy_, fill_, ...)")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._HELD:
+            raise AttributeError(f"{name} cannot be deleted")
+        object.__delattr__(self, name)
 
     def __init__(self, config: Config, num_seqs: int, max_blocks: int, max_tokens: int,
                  device="cuda"):
