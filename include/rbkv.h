@@ -521,7 +521,8 @@ int64_t rbkv_step_plan_ints(int32_t num_seqs, int32_t max_tokens);
  * first, in sequence order (the composer's rule), and they leave the free
  * bits.  table_in / free_in: where the block table and the free bits before
  * the step are read (NULL: t->block_table / t->free_words, in place).  seen
- * may be t->ctx when the block table is built in place.
+ * may be t->ctx when the block table is built in place; otherwise no input may
+ * overlap an array that the step writes.
  * All or nothing: a negative length (RBKV_ERR_INVALID), more rows than
  * max_tokens, a sequence beyond max_blocks or 2^30 tokens
  * (RBKV_ERR_WORKSPACE) or too few
@@ -556,7 +557,8 @@ size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables*
  *   O[r][h][:] = sum_i softmax_i(Q[r][h] . K[i] / sqrt(D)) V[i]
  * over the prefix's keys 0 .. prefix_len - 1 (block prefix_table[i / B], slot
  * i % B) and the keys 0 .. position[r] of the row's sequence.  q, o:
- * [max_tokens][H_q][D]; rows past the step's rows are not written.
+ * [max_tokens][H_q][D], apart from one another; rows past the step's rows are
+ * not written.
  * prefix_len in [0, 2^30] (prefix_table may be NULL at 0: paged attention of
  * the step).  What a row does not see does not reach it, finite or not: slots
  * past a length, later tokens, other sequences.  A value that is not finite

@@ -18,6 +18,11 @@ rbkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(RBKV_ERR_CUDA, (std::string(what) + ": " + cudaGetErrorString(e)).c_str());
 }
 
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 rbkv_status check_tables(const rbkv_config* c, const rbkv_step_tables* t) {
@@ -38,6 +43,20 @@ rbkv_status check_tables(const rbkv_config* c, const rbkv_step_tables* t) {
     return invalid("table arrays must be 4-byte aligned");
   if (!aligned(t->plan, 16)) return invalid("plan must be 16-byte aligned");
   return RBKV_OK;
+}
+
+// Whether the n int32 at p meet an array that a build writes, other than the
+// one (of the same length) that they may be read from in place.
+bool written_by_build(const rbkv_step_tables* t, int32_t num_blocks, const void* p, int64_t n,
+                      const void* in_place) {
+  if (p == in_place) return false;
+  const int64_t S = t->num_seqs, T = t->max_tokens;
+  return overlap(p, 4 * n, t->block_table, 4 * S * t->max_blocks) ||
+         overlap(p, 4 * n, t->free_words, 4 * (((int64_t)num_blocks + 31) / 32)) ||
+         overlap(p, 4 * n, t->q_start, 4 * (S + 1)) || overlap(p, 4 * n, t->ctx, 4 * S) ||
+         overlap(p, 4 * n, t->position, 4 * T) || overlap(p, 4 * n, t->slot, 4 * T) ||
+         overlap(p, 4 * n, t->plan, 4 * step_plan_ints(S, T)) ||
+         overlap(p, 4 * n, t->status, 16);
 }
 
 BuildArgs build_args(const rbkv_config* c, const rbkv_step_tables* t) {
@@ -109,8 +128,12 @@ rbkv_status rbkv_step_build(const rbkv_config* cfg, const rbkv_step_tables* t,
   a.n_new = n_new;
   if (table_in) a.table_in = table_in;
   if (free_in) a.free_in = free_in;
-  if (n_new == t->ctx || n_new == t->q_start || seen == t->q_start)
-    return invalid("n_new and seen must not be written by the step");
+  const int64_t S = t->num_seqs, pool = cfg->num_blocks;
+  if (written_by_build(t, cfg->num_blocks, seen, S, t->ctx) ||
+      written_by_build(t, cfg->num_blocks, n_new, S, nullptr) ||
+      written_by_build(t, cfg->num_blocks, a.table_in, S * t->max_blocks, t->block_table) ||
+      written_by_build(t, cfg->num_blocks, a.free_in, (pool + 31) / 32, t->free_words))
+    return invalid("an input overlaps an array that the step writes");
   if (seen == t->ctx && a.table_in != a.table)
     return invalid("seen may be the tables' ctx only when the block table is built in place");
   cudaError_t e = launch_step_build(a, (cudaStream_t)stream);
@@ -125,7 +148,10 @@ rbkv_status rbkv_step_release(const rbkv_config* cfg, const rbkv_step_tables* t,
   rbkv_status st = check_tables(cfg, t);
   if (st != RBKV_OK) return st;
   if (!done || !aligned(done, 4)) return invalid("done must be a 4-byte aligned array");
-  if (done == t->ctx) return invalid("done must not be the tables' ctx");
+  const int64_t S = t->num_seqs;
+  if (overlap(done, 4 * S, t->ctx, 4 * S) || overlap(done, 4 * S, t->status, 16) ||
+      overlap(done, 4 * S, t->free_words, 4 * (((int64_t)cfg->num_blocks + 31) / 32)))
+    return invalid("done overlaps an array that the release writes");
   cudaError_t e = launch_step_release(build_args(cfg, t), done, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "step release launch");
   note_launches(1);
@@ -206,6 +232,12 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
   const size_t need = workspace_of(s, t, prefix_len, sms);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
+  const int64_t q_bytes =
+      (int64_t)t->max_tokens * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
+  if (overlap(q, q_bytes, o, q_bytes)) return invalid("o overlaps q");
+  if (need > 0 && (overlap(workspace, (int64_t)need, q, q_bytes) ||
+                   overlap(workspace, (int64_t)need, o, q_bytes)))
+    return invalid("workspace overlaps q or o");
   if (!step_fast_supported(s)) {
     const int splits = step_generic_splits(s, t->max_tokens, t->max_blocks, prefix_len, sms);
     e = launch_step_generic(ds, s, q, k_cache, v_cache, o, workspace, splits, sms, cs);

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from step_harness import error_bound, i32, reference
-from test_gpu_step import INVALID, MIXED, _case
+from test_gpu_step import INVALID, MIXED, WORKSPACE, _case
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,47 @@ def test_before_the_first_step(rbkv):
     t.release(i32([0, 1, 0]))
     t.device_status()
     assert t.free.tolist() == [1 << 5] and t.ctx.tolist() == [0, 0, 0]
+
+
+def test_an_output_over_the_queries_is_refused(rbkv):
+    t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, 8, 2, 64, 16, "f32", 20, [3, 0], [1, 40])
+    both = torch.cat([q, q[:1]]).cuda()
+    before = both.clone()
+    for x, o in ((both[:-1], both[1:]), (both[1:], both[:-1])):
+        with pytest.raises(rbkv.RbkvError) as e:
+            t.attention(x, kd, vd, prefix_table=i32(ids), prefix_len=20, o=o)
+        assert e.value.status == INVALID
+    need = t.workspace_bytes(20)
+    if need:
+        with pytest.raises(rbkv.RbkvError):
+            t.attention(both[:-1], kd, vd, prefix_table=i32(ids), prefix_len=20,
+                        workspace=both.view(torch.uint8))
+    torch.cuda.synchronize()
+    assert torch.equal(both, before)
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (8, 2, 64, 16, "f32")], ids=str)
+def test_a_workspace_is_needed_and_kept_apart(rbkv, shape):
+    """One row behind a long prefix takes a workspace on every route: none, one
+    that is too small and one that holds an operand are refused."""
+    t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, 3000, [300], [1])
+    need, qc, idc = t.workspace_bytes(3000), q.cuda(), i32(ids)
+    assert need > 0
+    L, cfg = rbkv.lib(), t.config._c()
+    ws, o = torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.full_like(qc, 7.0)
+
+    def call(ws, size, q=qc, o=o):
+        return L.rbkv_step_attention(C.byref(cfg), C.byref(t._tables), q.data_ptr(),
+                                     kd.data_ptr(), vd.data_ptr(), idc.data_ptr(), 3000,
+                                     o.data_ptr(), ws, size, None)
+
+    assert call(None, 0) == WORKSPACE and call(ws.data_ptr(), need - 1) == WORKSPACE
+    inside = ws[need // 2 // 256 * 256:][:qc.nbytes].view(qc.dtype).view(qc.shape)
+    assert call(ws.data_ptr(), need, q=inside) == INVALID
+    assert call(ws.data_ptr(), need, o=inside) == INVALID
+    torch.cuda.synchronize()
+    assert (o == 7.0).all() and (ws == 0).all()
+    assert call(ws.data_ptr(), need) == 0
+    t.device_status()
+    ref = reference(want, q, kc, vc, ids, 3000)
+    assert ((o.cpu().double() - ref[0]).abs() <= error_bound(ref, shape[2], shape[4])).all()

@@ -234,3 +234,45 @@ def test_the_arrays_cannot_be_replaced(rbkv):
     for name in ("free", "ctx"):
         with pytest.raises(AttributeError):
             delattr(t, name)
+
+
+def _apart(rbkv, S=4, max_blocks=8, T=16):
+    """Tables whose arrays lie a megabyte apart, and addresses that are free."""
+    at = [FAKE + (i << 20) for i in range(12)]
+    return rbkv._StepTables(S, max_blocks, T, *at[:8]), at[8:]
+
+
+# (a table array, bytes into it): where an input would be overwritten by the step
+OVERLAPS = [("q_start", 4), ("q_start", 16), ("ctx", 4), ("ctx", -12), ("position", 0),
+            ("position", 60), ("slot", 8), ("plan", 16), ("status", 12), ("free_words", 0),
+            ("block_table", 124)]
+
+
+@pytest.mark.parametrize("name,at", OVERLAPS)
+def test_inputs_that_a_step_would_overwrite_are_refused(rbkv, name, at):
+    t, (a, b, c, d) = _apart(rbkv)
+    where = getattr(t, name) + at
+    for args in ((where, a), (a, where)):
+        assert _build(rbkv, t=t, seen=args[0], n_new=args[1]) == INVALID
+        assert b"overlap" in rbkv.lib().rbkv_last_error()
+    if name != "free_words" and at >= 0:                     # (one word of free bits)
+        assert _build(rbkv, t=t, seen=a, n_new=b, free=where) == INVALID
+        assert b"overlap" in rbkv.lib().rbkv_last_error()
+    assert _build(rbkv, t=t, seen=a, n_new=b, table=where) == INVALID
+    assert b"overlap" in rbkv.lib().rbkv_last_error()
+    cfg = _cfg(rbkv)
+    if name in ("ctx", "free_words", "status"):
+        assert rbkv.lib().rbkv_step_release(C.byref(cfg), C.byref(t), where, None) == INVALID
+        assert b"overlap" in rbkv.lib().rbkv_last_error()
+
+
+def test_arrays_in_place_are_not_overlaps(rbkv):
+    """(without a GPU the launch fails: any other status than INVALID will do)"""
+    t, (a, b, c, d) = _apart(rbkv)
+    if torch.cuda.is_available():
+        pytest.skip("would launch with made-up addresses")
+    for kw in ({"seen": t.ctx, "n_new": a}, {"seen": a, "n_new": a},
+               {"seen": t.ctx, "n_new": b, "table": t.block_table, "free": t.free_words},
+               {"seen": t.ctx + 16, "n_new": t.ctx - 16},              # next to it
+               {"seen": a, "n_new": b, "table": c, "free": d}):
+        assert _build(rbkv, t=t, **kw) != INVALID, kw
