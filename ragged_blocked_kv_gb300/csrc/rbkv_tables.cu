@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const int per = (S + C - 1) / C;
   const int s0 = min((int)rank * per, S), n_seqs = min(per, S - s0);
-  const int W = (a.num_blocks + 31) / 32;
+  const int W = (a.num_blocks - 1) / 32 + 1;      // (num_blocks + 31 may pass 2^31)
   const int wper = (W + C - 1) / C;
   const int w0 = min((int)rank * wper, W), n_words = min(wper, W - w0);
   // this thread's sequences [sa, sb) and this warp's words [wa, wb) of the CTA's
