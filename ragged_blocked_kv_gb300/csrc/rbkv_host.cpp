@@ -1193,12 +1193,14 @@ rbkv_status rbkv_ragged_attention(rbkv_pass* p, const void* q, const void* k_cac
 
 namespace {
 
-// Wait for `st`, then read and clear the four device status words at `dev`.
+// Wait for `st`, then read and clear the four device status words at `dev` (on
+// that stream too: what is launched there next comes after the clearing, and
+// work of other streams is not waited for).
 rbkv_status read_device_status(void* dev, cudaStream_t st) {
   int32_t words[4] = {0, 0, 0, 0};
-  cudaError_t e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess) e = cudaMemcpy(words, dev, sizeof(words), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess) e = cudaMemset(dev, 0, sizeof(words));
+  cudaError_t e = cudaMemcpyAsync(words, dev, sizeof(words), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(dev, 0, sizeof(words), st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "device status read");
   const int32_t word = words[0];
   if (word == kDevBounds) return fail(RBKV_ERR_DEVICE_BOUNDS, "a kernel met an out-of-range block id");

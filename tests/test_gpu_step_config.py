@@ -184,3 +184,20 @@ def test_a_workspace_is_needed_and_kept_apart(rbkv, shape):
     t.device_status()
     ref = reference(want, q, kc, vc, ids, 3000)
     assert ((o.cpu().double() - ref[0]).abs() <= error_bound(ref, shape[2], shape[4])).all()
+
+
+def test_status_is_read_and_cleared_in_its_stream_order(rbkv):
+    """A step that fails right behind a status read on a side stream: the words
+    are cleared before its kernel, not after it."""
+    t = rbkv.StepTables(rbkv.Config(8, 2, 64, 16, "f32", 8), 1, 4, 4)
+    bad, good, one = i32([-1]), i32([0]), i32([1])
+    side, busy = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(200):
+        busy.add_(1.0)                           # the default stream has work of its own
+        t.build(bad, one, stream=side)
+        with pytest.raises(rbkv.RbkvError) as e:
+            t.device_status(stream=side)
+        assert e.value.status == INVALID, i
+    t.build(good, one, stream=side)
+    t.device_status(stream=side)
