@@ -247,7 +247,7 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
     step_workspace(s, t->max_tokens, sms, workspace, &w);
     // a step of at most 16 packed rows has no work for the tile kernel
     const bool tiles = !step_prefix_streamed(t->max_tokens, s.g);
-    if (tiles) e = launch_step_tile(ds, s, w, q, k_cache, v_cache, o, true, cs);
+    if (tiles) e = launch_step_tile(ds, s, w, q, k_cache, v_cache, o, cs);
     if (e == cudaSuccess)
       e = launch_step_stream(ds, s, w, q, k_cache, v_cache, o, !tiles, cs);
     if (e == cudaSuccess) e = launch_step_combine(ds, s, w, o, cs);

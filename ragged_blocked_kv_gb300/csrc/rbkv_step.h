@@ -186,7 +186,7 @@ __host__ __device__ __forceinline__ bool step_prefix_streamed(int32_t max_tokens
 // built for another group or block size or for tables of other sizes (its
 // lengths and lists would lead out of the tables).
 __device__ __forceinline__ int32_t step_rows(const DevStep& ds, const ShapeInfo& s,
-                                             const StepPlan& plan, int4* first = nullptr,
+                                             const StepPlan& plan, int4* head = nullptr,
                                              int32_t* tile_len = nullptr) {
   // (one round trip for all of it)
   int4 a = *reinterpret_cast<const int4*>(plan.header);
@@ -201,7 +201,7 @@ __device__ __forceinline__ int32_t step_rows(const DevStep& ds, const ShapeInfo&
     a = make_int4(0, 0, 0, 0);
     b.x = 0;
   }
-  if (first) *first = a;
+  if (head) *head = a;
   if (tile_len) *tile_len = b.x;
   return a.x;
 }
@@ -341,12 +341,13 @@ size_t step_generic_workspace(const ShapeInfo& s, int32_t max_tokens, int splits
 cudaError_t launch_step_generic(const DevStep& ds, const ShapeInfo& s, const void* q,
                                 const void* k_cache, const void* v_cache, void* o,
                                 void* workspace, int splits, int sms, cudaStream_t st);
-// The fast path's three kernels.  The first one launched of the first two
-// waits for the stream's previous kernel (`first`); the other starts beside
-// it and waits for it before ending; the combine waits for both.
+// The fast path's three kernels.  The tile kernel, where there is one, is
+// launched first and waits for the stream's previous kernel; the streaming
+// kernel starts beside it and waits for it before ending, or is the `first`
+// one itself; the combine waits for both.
 cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                              const void* q, const void* k_cache, const void* v_cache, void* o,
-                             bool first, cudaStream_t st);
+                             cudaStream_t st);
 cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                                const void* q, const void* k_cache, const void* v_cache, void* o,
                                bool first, cudaStream_t st);

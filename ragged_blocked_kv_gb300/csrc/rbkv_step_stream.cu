@@ -122,7 +122,7 @@ struct Walk {
   __device__ __forceinline__ int entries(int keys, int B) const { return (keys + B - 1) / B; }
 
   __device__ __forceinline__ void enter(const DevStep& ds, const ShapeInfo& s,
-                                        const StepPlan& plan, const StepWork& work) {
+                                        const StepWork& work) {
     if (unit < work.streamed) {
       unit0 = (int64_t)s.H_kv * cur.cum + (int64_t)kv_head * (cur.tiles + kStepStreamUnit);
       table = ds.block_table + (int64_t)cur.seq * ds.max_blocks;
@@ -159,7 +159,7 @@ struct Walk {
       len = cur.tiles + kStepStreamUnit;
     }
     kv_head = (int)step_div(x - base, len);
-    enter(ds, s, plan, work);
+    enter(ds, s, work);
     next_x = x;
     left = 0;
     seg = 0;
@@ -189,7 +189,7 @@ struct Walk {
           cur = next;
           moved = true;
         }
-        enter(ds, s, plan, work);
+        enter(ds, s, work);
         if (moved) {
           window = -1;
           if (unit < work.streamed) {

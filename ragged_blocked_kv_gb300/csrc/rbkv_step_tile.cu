@@ -264,10 +264,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     step_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
                      StepWorkspace ws, const __nv_bfloat16* __restrict__ q,
-                     const __nv_bfloat16* __restrict__ v_cache, __nv_bfloat16* __restrict__ o,
-                     int first) {
+                     const __nv_bfloat16* __restrict__ v_cache, __nv_bfloat16* __restrict__ o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (first) ptx::pdl_wait_previous();
+  ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
@@ -275,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   if ((ptx::smem_u32(smem_raw) & 1023) || blockIdx.x >= ctas) {
     // (the swizzled operand layouts need a 1024-byte aligned base)
     if (threadIdx.x == 0 && blockIdx.x < ctas) atomicCAS(ds.status, 0, kDevBounds);
-    ptx::pdl_wait_previous();   // the grid's completion still covers its predecessor
     return;
   }
   uint8_t* kv_s = smem_raw;                      // [kStages][kTileBytes]
@@ -816,14 +814,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (!first) ptx::pdl_wait_previous();
 }
 
 }  // namespace
 
 cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                              const void* q, const void* k_cache, const void* v_cache, void* o,
-                             bool first, cudaStream_t st) {
+                             cudaStream_t st) {
   const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
   const int box_rows = s.B < kKeys ? s.B : kKeys;
   CUtensorMap tk, tv;
@@ -863,7 +860,7 @@ cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWo
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, step_tile_kernel, tk, tv, ds, s, w,
                             (const __nv_bfloat16*)q, (const __nv_bfloat16*)v_cache,
-                            (__nv_bfloat16*)o, first ? 1 : 0);
+                            (__nv_bfloat16*)o);
 }
 
 }  // namespace rbkv
