@@ -182,36 +182,34 @@ __host__ __device__ __forceinline__ bool step_prefix_streamed(int32_t max_tokens
 }
 
 #ifdef __CUDACC__
-// The step's rows; 0, and RBKV_ERR_INVALID in the status words, where it was
-// built for another group or block size or for tables of other sizes (its
-// lengths and lists would lead out of the tables).
-__device__ __forceinline__ int32_t step_rows(const DevStep& ds, const ShapeInfo& s,
-                                             const StepPlan& plan, int4* head = nullptr,
-                                             int32_t* tile_len = nullptr) {
-  // (one round trip for all of it)
-  int4 a = *reinterpret_cast<const int4*>(plan.header);
-  int4 b = *reinterpret_cast<const int4*>(plan.header + 4);
+// Whether the step was built for what it is used with: else its lengths and
+// lists would lead out of the tables.
+__device__ __forceinline__ bool step_matches(const DevStep& ds, const ShapeInfo& s,
+                                             const StepPlan& plan) {
+  static_assert(kPlanGroup == 5 && kPlanBlock == 6 && kPlanSeqs == 7 && kPlanTokens == 8 &&
+                    kPlanMaxBlocks == 9, "the header's second and third vector");
+  const int4 b = *reinterpret_cast<const int4*>(plan.header + 4);
   const int2 c = *reinterpret_cast<const int2*>(plan.header + 8);
-  static_assert(kPlanRows == 0 && kPlanStreamed == 1 && kPlanStreamLen == 3 && kPlanTileLen == 4 &&
-                    kPlanGroup == 5 && kPlanBlock == 6 && kPlanSeqs == 7 && kPlanTokens == 8 &&
-                    kPlanMaxBlocks == 9, "the header in vectors");
-  if (((b.y ^ s.g) | (b.z ^ s.B) | (b.w ^ ds.num_seqs) | (c.x ^ ds.max_tokens) |
-       (c.y ^ ds.max_blocks)) != 0) {
-    if (a.x > 0 && threadIdx.x == 0) atomicCAS(ds.status, 0, kDevInvalid);
-    a = make_int4(0, 0, 0, 0);
-    b.x = 0;
-  }
-  if (head) *head = a;
-  if (tile_len) *tile_len = b.x;
-  return a.x;
+  // (no short cuts: all of it in one round trip)
+  return ((b.y ^ s.g) | (b.z ^ s.B) | (b.w ^ ds.num_seqs) | (c.x ^ ds.max_tokens) |
+          (c.y ^ ds.max_blocks)) == 0;
+}
+// The step's rows; 0, and RBKV_ERR_INVALID in the status words, where it was
+// built for something else.  (The tile and the streaming kernel leave the report
+// to the join.)
+__device__ __forceinline__ int32_t step_rows(const DevStep& ds, const ShapeInfo& s,
+                                             const StepPlan& plan) {
+  const int32_t rows = plan.header[kPlanRows];
+  if (step_matches(ds, s, plan)) return rows;
+  if (rows > 0 && threadIdx.x == 0) atomicCAS(ds.status, 0, kDevInvalid);
+  return 0;
 }
 
 __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo& s,
                                               const StepPlan& plan) {
   StepWork w;
-  int4 h;
-  int32_t tile_len;
-  const int32_t T = step_rows(ds, s, plan, &h, &tile_len);
+  const int4 h = *reinterpret_cast<const int4*>(plan.header);
+  const int32_t T = h.x;
   w.rows = T;
   w.streamed = h.y;
   const bool streamed = step_prefix_streamed(ds.max_tokens, s.g);
@@ -227,7 +225,7 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
   w.tile_prefix = 0;
   if (w.prefix_tile_steps)
     w.tile_prefix = (int64_t)s.H_kv * w.prefix_rows * (w.prefix_tile_steps + kStepTileUnit);
-  w.tile_total = w.tile_prefix + (int64_t)tile_len * s.H_kv;
+  w.tile_total = w.tile_prefix + (int64_t)plan.header[kPlanTileLen] * s.H_kv;
   return w;
 }
 #endif

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const bool late = (int)blockIdx.x >= half;
   const int mine = warp * half + ((int)blockIdx.x - (late ? half : 0));
   const int pipe = late ? cuts.early + mine : mine;
-  const bool works = mine < (late ? cuts.late : cuts.early);
+  const bool works = step_matches(ds, shp, plan) && mine < (late ? cuts.late : cuts.early);
   if (works) {
     Ring ring;
     ring.stages = smem_raw + warp * kStages * kStage;

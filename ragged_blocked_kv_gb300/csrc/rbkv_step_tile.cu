@@ -246,6 +246,13 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// A block id outside the pool has been met.  (Not inlined: in the producers' loop
+// these few instructions cost a percent of the kernel.)
+__device__ __noinline__ void note_missing(Bars* bars, int32_t* status) {
+  atomicCAS(status, 0, kDevBounds);
+  bars->missing = 1;
+}
+
 // Scores -inf, in tensor memory, for the keys of a tile that have no block.
 // (Not inlined, and called from the branch of a wait that gave up: elsewhere in
 // the softmax loop these few instructions, which never run otherwise, made a step
@@ -271,9 +278,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
   const int64_t ctas = min((int64_t)gridDim.x, work.tile_total);
-  if ((ptx::smem_u32(smem_raw) & 1023) || blockIdx.x >= ctas) {
+  if (blockIdx.x >= ctas || !step_matches(ds, shp, plan)) return;
+  if (ptx::smem_u32(smem_raw) & 1023) {
     // (the swizzled operand layouts need a 1024-byte aligned base)
-    if (threadIdx.x == 0 && blockIdx.x < ctas) atomicCAS(ds.status, 0, kDevBounds);
+    if (threadIdx.x == 0) atomicCAS(ds.status, 0, kDevBounds);
     return;
   }
   uint8_t* kv_s = smem_raw;                      // [kStages][kTileBytes]
@@ -349,10 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       int id = more ? look_up(it, 0) : -2;
       while (more && ok) {
         for (int j = 0; ok && j < it.n; ++j) {
-          if (id == -1) {
-            atomicCAS(ds.status, 0, kDevBounds);
-            bars->missing = 1;
-          }
+          if (__any_sync(0xffffffffu, id == -1)) note_missing(bars, ds.status);
           __syncwarp();
           int id_next = -2;
           if (j + 1 < it.n) {
