@@ -509,7 +509,8 @@ typedef struct {
   int32_t* ctx;            /* [S] out: tokens cached after the step */
   int32_t* position;       /* [max_tokens] out: position in the sequence; -1 past the rows */
   int32_t* slot;           /* [max_tokens] out: block * B + offset; -1 past the rows */
-  int32_t* plan;           /* [rbkv_step_plan_ints] opaque, 16-byte aligned */
+  int32_t* plan;           /* [rbkv_step_plan_ints] opaque, 16-byte aligned, zero
+                              at first */
   int32_t* status;         /* [4] zero at first; see rbkv_step_device_status */
 } rbkv_step_tables;
 
