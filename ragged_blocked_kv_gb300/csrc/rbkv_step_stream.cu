@@ -549,6 +549,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+  if (!step_matches(ds, shp, plan)) {
+    ptx::pdl_wait_previous();
+    return;
+  }
   const StepWork work = step_work(ds, shp, plan);
   const StreamCuts cuts = step_stream_cuts(ws, work);
   // neighbouring parts on different SMs; the second half of the grid is late
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const bool late = (int)blockIdx.x >= half;
   const int mine = warp * half + ((int)blockIdx.x - (late ? half : 0));
   const int pipe = late ? cuts.early + mine : mine;
-  const bool works = step_matches(ds, shp, plan) && mine < (late ? cuts.late : cuts.early);
+  const bool works = mine < (late ? cuts.late : cuts.early);
   if (works) {
     Ring ring;
     ring.stages = smem_raw + warp * kStages * kStage;

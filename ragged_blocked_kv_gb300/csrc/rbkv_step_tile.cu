@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int64_t ctas = min((int64_t)gridDim.x, work.tile_total);
-  if (blockIdx.x >= ctas || !step_matches(ds, shp, plan)) return;
+  const int64_t ctas = step_matches(ds, shp, plan) ? min((int64_t)gridDim.x, work.tile_total) : 0;
+  if (blockIdx.x >= ctas) return;
   if (ptx::smem_u32(smem_raw) & 1023) {
     // (the swizzled operand layouts need a 1024-byte aligned base)
     if (threadIdx.x == 0) atomicCAS(ds.status, 0, kDevBounds);
