@@ -547,7 +547,9 @@ class StepTables:
     [max_tokens] (-1 past the step's rows).  Lengths, tables and positions
     count a sequence's own tokens, not the prefix.  A step that does not fit
     is empty and ``device_status`` says why.  The arrays are written in place
-    (``t.free.copy_(...)``): the library holds their addresses.
+    (``t.free.copy_(...)``): the library holds their addresses.  A call with
+    ``stream`` does not keep its tensors: they have to live until that stream's
+    work is over.
     """
 
     _HELD = frozenset(("block_table", "free", "q_start", "ctx", "position", "slot", "plan",

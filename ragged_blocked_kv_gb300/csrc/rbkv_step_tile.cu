@@ -256,7 +256,7 @@ __device__ __noinline__ void note_missing(Bars* bars, int32_t* status) {
 // Scores -inf, in tensor memory, for the keys of a tile that have no block.
 // (Not inlined, and called from the branch of a wait that gave up: elsewhere in
 // the softmax loop these few instructions, which never run otherwise, made a step
-// of 512 rows behind 4096 keys take 134 to 137 us instead of 127; so, 129.)
+// of 512 rows behind 4096 keys take 134 to 137 us instead of 127; so, 128.)
 __device__ __noinline__ void hide_keys(uint32_t s_col, const int32_t* table, int key0, int ke,
                                        int B, int num_blocks) {
   const int lane = threadIdx.x & 31, key = key0 + lane * 8;   // blocks are of 8 keys or more
