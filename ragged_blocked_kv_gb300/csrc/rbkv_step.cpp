@@ -189,7 +189,7 @@ rbkv_status rbkv_step_append(const rbkv_config* cfg, const rbkv_step_tables* t,
 
 size_t rbkv_step_workspace_bytes(const rbkv_config* cfg, const rbkv_step_tables* t,
                                  int32_t prefix_len) {
-  if (check_tables(cfg, t) != RBKV_OK || prefix_len < 0) return 0;
+  if (check_tables(cfg, t) != RBKV_OK || prefix_len < 0 || prefix_len > 1 << 30) return 0;
   const ShapeInfo s = shape(cfg);
   int sms = 0;
   if (num_sms(&sms) != cudaSuccess) return 0;

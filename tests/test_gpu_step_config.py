@@ -201,3 +201,9 @@ def test_status_is_read_and_cleared_in_its_stream_order(rbkv):
         assert e.value.status == INVALID, i
     t.build(good, one, stream=side)
     t.device_status(stream=side)
+
+
+def test_workspace_bytes_of_refused_prefixes(rbkv):
+    t = rbkv.StepTables(rbkv.Config(32, 8, 128, 64, "bf16", 8), 2, 4, 40)
+    assert t.workspace_bytes(0) > 0 and t.workspace_bytes(1 << 30) > 0
+    assert t.workspace_bytes(-1) == 0 and t.workspace_bytes((1 << 30) + 1) == 0
