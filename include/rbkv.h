@@ -276,6 +276,29 @@ rbkv_status rbkv_kv_append(rbkv_pass* p, const void* k_new, const void* v_new,
  * split.  Makes the plan for the current device if not made yet. */
 size_t rbkv_attention_workspace_bytes(rbkv_pass* p);
 
+/* A rotary position embedding.  Pair i of the first rotary_dim elements of a
+ * head - elements i and i + rotary_dim / 2, or 2 i and 2 i + 1 when interleaved -
+ * is rotated by the angle position * turns[i] / 2^64 turns and multiplied by
+ * `scale`; the other elements stay as they are.  The angle is exact up to the
+ * table's own rounding at any position: the product is taken modulo 2^64.
+ * turns: rotary_dim / 2 entries in device memory, 8-byte aligned. */
+typedef struct {
+  const uint64_t* turns;
+  int32_t rotary_dim;    /* even, 2 .. head_dim */
+  int32_t interleaved;   /* 0 or 1 */
+  float scale;
+} rbkv_rotary;
+
+/* rbkv_kv_append with the rotation on the way: k_cache receives the rotated
+ * keys, v_cache the values, and q_out ([T][H_q][D]) the rotated queries, all
+ * by the rows' positions in their sequences (fp32 arithmetic, each output
+ * rounded once).  q_out may be q; it must not overlap it in part, or any other
+ * tensor of the call.  16-byte aligned tensors.
+ * Errors: as rbkv_kv_append, and RBKV_ERR_INVALID for a bad rotary. */
+rbkv_status rbkv_kv_append_rotary(rbkv_pass* p, const rbkv_rotary* rotary, const void* q,
+                                  void* q_out, const void* k_new, const void* v_new,
+                                  void* k_cache, void* v_cache, rbkv_stream stream);
+
 /* Ragged causal attention of every pass row (FastGen guide, "Dynamic SplitKV
  * Attention" and Step 3's reference operator; exact softmax attention):
  *   O[t][h][:] = sum_{i<=p} softmax_i(Q[t][h] . K_s[i] / sqrt(D)) V_s[i]
@@ -455,6 +478,12 @@ rbkv_status rbkv_frame_load(rbkv_frame* f, rbkv_pass* p, rbkv_stream stream);
 rbkv_status rbkv_frame_kv_append(rbkv_frame* f, const void* k_new, const void* v_new,
                                  void* k_cache, void* v_cache, rbkv_stream stream);
 
+/* rbkv_kv_append_rotary for the pass loaded last: q and q_out are
+ * [max_tokens][H_q][D] (rows past the pass's are neither read nor written). */
+rbkv_status rbkv_frame_kv_append_rotary(rbkv_frame* f, const rbkv_rotary* rotary, const void* q,
+                                        void* q_out, const void* k_new, const void* v_new,
+                                        void* k_cache, void* v_cache, rbkv_stream stream);
+
 /* Workspace bytes rbkv_frame_attention needs (for max_parts partial slots). */
 size_t rbkv_frame_workspace_bytes(const rbkv_frame* f);
 
@@ -581,6 +610,95 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
  * first error since they were last read (see rbkv_step_build and
  * rbkv_step_tables; also RBKV_ERR_TIMEOUT, as rbkv_pass_device_status). */
 rbkv_status rbkv_step_device_status(const rbkv_step_tables* t, rbkv_stream stream);
+
+/* ---- drafted tokens ------------------------------------------------------------
+ *
+ * A step may verify drafted tokens: a sequence's new tokens then form a tree,
+ * several candidate continuations at once, whose tokens see the prefix, the
+ * sequence's cached tokens, and those tokens of the tree that they follow.  Once
+ * a token has been chosen at each of them, the path that the choices agree with
+ * is kept and the rest is given back.  Per step: rbkv_step_build,
+ * rbkv_step_draft_plan, rbkv_step_draft_accept; per layer:
+ * rbkv_step_append_rotary (or rbkv_step_append), rbkv_step_attention_draft and,
+ * after the acceptance, rbkv_step_draft_compact.  No call copies to or from the
+ * host, so that a drafting loop can be captured as a CUDA graph. */
+
+/* Tokens of a tree, at most; longer runs of new tokens are chains (prompt
+ * chunks). */
+#define RBKV_DRAFT_TOKENS 128
+
+/* The arrays of a step's drafted tokens, in device memory, owned by the caller.
+ * As a step's tables, they stay valid until the next build. */
+typedef struct {
+  int32_t* place;        /* [max_tokens] out of the plan: position in the sequence once the
+                            path to the token is kept (tokens cached before the step, plus
+                            the token's depth in its tree); -1 past the rows */
+  int32_t* ancestors;    /* [max_tokens][4] out of the plan, 16-byte aligned: bit i of word
+                            w set = the token is, or follows, token 32 w + i of its
+                            sequence's new ones; 0 for chains of more than
+                            RBKV_DRAFT_TOKENS and past the rows */
+  int32_t* path;         /* [max_tokens] out of the acceptance: entry q_start[s] + d is the
+                            row of the d-th kept token of sequence s; -1 elsewhere */
+  int32_t* accepted;     /* [num_seqs] out: kept tokens of the step (0 of an idle slot) */
+  int32_t* next_token;   /* [num_seqs] out: the token chosen at the last kept one (-1) */
+} rbkv_step_draft;
+
+/* Plan the trees of the step built last.  parent: [max_tokens], for every row
+ * the index, among its sequence's new tokens, of the token that it follows:
+ * before its own, or -1 for none (it sees cached tokens only).  A sequence with
+ * another value, or with more than RBKV_DRAFT_TOKENS new tokens that are not a
+ * chain (0 -1, 1 0, 2 1, ...), is recorded as RBKV_ERR_INVALID in the status
+ * words and taken as a chain.
+ * Errors of the call: RBKV_ERR_INVALID, RBKV_ERR_UNSUPPORTED, RBKV_ERR_CUDA. */
+rbkv_status rbkv_step_draft_plan(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                 const rbkv_step_draft* d, const int32_t* parent,
+                                 rbkv_stream stream);
+
+/* rbkv_step_append with the rotation on the way, as rbkv_kv_append_rotary, by
+ * the positions prefix_len + position[r], or prefix_len + place[r] when d is
+ * not NULL (the trees must have been planned: else nothing is written and
+ * RBKV_ERR_INVALID recorded).  q, q_out: [max_tokens][H_q][D]; rows past the
+ * step's are neither read nor written. */
+rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                    const rbkv_step_draft* d, const rbkv_rotary* rotary,
+                                    int32_t prefix_len, const void* q, void* q_out,
+                                    const void* k_new, const void* v_new, void* k_cache,
+                                    void* v_cache, rbkv_stream stream);
+
+/* rbkv_step_attention where a row sees the prefix's keys, those of its
+ * sequence's tokens cached before the step, and those of its ancestors and
+ * itself.  Same workspace; the trees must have been planned (else nothing is
+ * written and RBKV_ERR_INVALID recorded). */
+rbkv_status rbkv_step_attention_draft(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                      const rbkv_step_draft* d, const void* q,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* prefix_table, int32_t prefix_len, void* o,
+                                      void* workspace, size_t workspace_bytes,
+                                      rbkv_stream stream);
+
+/* Keep a path of every tree: tokens[r] is the token of row r, chosen[r] the one
+ * chosen to follow it.  The first given[s] new tokens of sequence s (in [1,
+ * new tokens]; NULL: 1 each) are kept as they are; from the last of them the
+ * path goes on to the lowest child whose token is the chosen one, until there
+ * is none.  Writes path, accepted and next_token, sets ctx[s] to the tokens
+ * cached before the step plus the kept ones, and returns the blocks behind them
+ * to the free bits.  The slots and the tables of the step stay as they are
+ * until the next build.  given out of range is recorded as RBKV_ERR_INVALID and
+ * taken for the nearest allowed; so is a step whose trees were not planned,
+ * which is left alone.  A second call for the same step has to come before any
+ * other call that takes blocks. */
+rbkv_status rbkv_step_draft_accept(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                   const rbkv_step_draft* d, const int32_t* tokens,
+                                   const int32_t* chosen, const int32_t* given,
+                                   rbkv_stream stream);
+
+/* Move the kept tokens' rows of a layer's caches to the slots that follow the
+ * sequence's cached tokens: once per layer, after the acceptance and before the
+ * next build (without an acceptance nothing is moved and RBKV_ERR_INVALID
+ * recorded). */
+rbkv_status rbkv_step_draft_compact(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                    const rbkv_step_draft* d, void* k_cache, void* v_cache,
+                                    rbkv_stream stream);
 
 /* ---- the rest of a decoder layer: tensor-core GEMM and RMSNorm --------------
  *

@@ -31,6 +31,9 @@ What it computes, plainly and slowly:
 * ``step``       - a step built from device-side lengths (tables, slots) and
   attention over a shared prefix and a sequence's own keys, in plain loops.
 
+* ``draft``      - a step's drafted tokens (trees, the kept path, the move of its
+  rows) and rotary positions, in plain loops.
+
 Pins (tests marked ``not gpu``): the tiny configuration's worked pass, budget
 and conservation invariants, brute force on tiny inputs, closed forms,
 PyTorch's scaled-dot-product attention as an independent library special case,
@@ -40,7 +43,7 @@ block ids, parity unpinned (only that rule and the pool invariants - distinct
 ids, ceil(ctx / B) held per sequence, all-or-nothing - hold them).
 """
 from .composer import Composer, PassMeta, InvalidRequest, NoBlocks, budget_for_latency, latency_at  # noqa: F401
-from . import router, step  # noqa: F401
+from . import draft, router, step  # noqa: F401
 from .cache import BlockedCache, kv_append  # noqa: F401
 from .attention import (  # noqa: F401
     widen,

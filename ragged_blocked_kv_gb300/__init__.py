@@ -16,6 +16,7 @@ is missing, importing the names below raises.
 from __future__ import annotations
 
 import ctypes as C
+import math
 from dataclasses import dataclass
 from pathlib import Path
 from typing import List, Optional, Sequence, Tuple
@@ -77,6 +78,15 @@ class _StepTables(C.Structure):
                                    "slot", "plan", "status")]
 
 
+class _StepDraft(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("place", "ancestors", "path", "accepted", "next_token")]
+
+
+class _Rotary(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("scale", C.c_float)]
+
+
 # Every symbol include/rbkv.h declares, with (restype, argtypes).
 _P = C.c_void_p
 SIGNATURES = {
@@ -102,6 +112,7 @@ SIGNATURES = {
     "rbkv_pass_plan_for_sms": (C.c_int, [_P, C.c_int32, C.POINTER(_PlanInfo)]),
     "rbkv_pass_destroy": (None, [_P]),
     "rbkv_kv_append": (C.c_int, [_P, _P, _P, _P, _P, _P]),
+    "rbkv_kv_append_rotary": (C.c_int, [_P, C.POINTER(_Rotary), _P, _P, _P, _P, _P, _P, _P]),
     "rbkv_attention_workspace_bytes": (C.c_size_t, [_P]),
     "rbkv_ragged_attention": (C.c_int, [_P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "rbkv_pass_device_status": (C.c_int, [_P, _P]),
@@ -111,6 +122,8 @@ SIGNATURES = {
     "rbkv_frame_destroy": (None, [_P]),
     "rbkv_frame_load": (C.c_int, [_P, _P, _P]),
     "rbkv_frame_kv_append": (C.c_int, [_P, _P, _P, _P, _P, _P]),
+    "rbkv_frame_kv_append_rotary": (C.c_int, [_P, C.POINTER(_Rotary), _P, _P, _P, _P, _P, _P,
+                                              _P]),
     "rbkv_frame_workspace_bytes": (C.c_size_t, [_P]),
     "rbkv_frame_attention": (C.c_int, [_P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "rbkv_frame_device_status": (C.c_int, [_P, _P]),
@@ -136,6 +149,18 @@ SIGNATURES = {
                                                C.c_int32]),
     "rbkv_step_attention": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables), _P, _P, _P, _P,
                                       C.c_int32, _P, _P, C.c_size_t, _P]),
+    "rbkv_step_draft_plan": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables),
+                                       C.POINTER(_StepDraft), _P, _P]),
+    "rbkv_step_append_rotary": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables),
+                                          C.POINTER(_StepDraft), C.POINTER(_Rotary), C.c_int32,
+                                          _P, _P, _P, _P, _P, _P, _P]),
+    "rbkv_step_attention_draft": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables),
+                                            C.POINTER(_StepDraft), _P, _P, _P, _P, C.c_int32, _P,
+                                            _P, C.c_size_t, _P]),
+    "rbkv_step_draft_accept": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables),
+                                         C.POINTER(_StepDraft), _P, _P, _P, _P]),
+    "rbkv_step_draft_compact": (C.c_int, [C.POINTER(_Config), C.POINTER(_StepTables),
+                                          C.POINTER(_StepDraft), _P, _P, _P]),
     "rbkv_step_device_status": (C.c_int, [C.POINTER(_StepTables), _P]),
     "rbkv_router_create": (C.c_int, [C.c_int32, C.POINTER(_P)]),
     "rbkv_router_destroy": (None, [_P]),
@@ -421,6 +446,99 @@ def kv_append(p: Pass, k_new, v_new, k_cache, v_cache, stream=None) -> None:
                                 _stream(stream)))
 
 
+class Rotary:
+    """A rotary position embedding: the table of its angles per position, on the GPU.
+
+    Pair i of a head's first ``rotary_dim`` elements (i and i + rotary_dim / 2 for
+    ``layout="half"``, 2 i and 2 i + 1 for ``"interleaved"``) turns by position *
+    theta_i, theta_i = base ** (-2 i / rotary_dim), and is multiplied by ``scale``;
+    the other elements stay.  ``scaling`` stretches contexts by ``factor``:
+    "linear" divides every theta_i; "base" raises the base to base * factor **
+    (rotary_dim / (rotary_dim - 2)); "parts" divides those pairs that turn less than
+    ``low`` times over ``original_length`` positions, leaves those that turn more than
+    ``high`` times, and blends in between.  ``inv_freq``: the theta_i themselves
+    (fp64 values) instead.
+
+        rope = Rotary(128, base=500000.0)
+        q = t.append_rotary(rope, q, k_new, v_new, k_cache, v_cache)
+
+    Angles are kept as 64-bit fractions of a turn: far positions lose nothing.  The
+    table is written by the stream that is current here, in the constructor.
+    """
+
+    LAYOUTS = {"half": 0, "interleaved": 1}
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, original_length: int = 0,
+                 low: float = 1.0, high: float = 32.0, scale: float = 1.0, inv_freq=None,
+                 device="cuda"):
+        import torch
+        self.rotary_dim, self.layout, self.scale = int(rotary_dim), layout, float(scale)
+        if self.rotary_dim < 2 or self.rotary_dim % 2 or self.rotary_dim > 256:
+            raise ValueError("rotary_dim must be even, in [2, 256]")
+        if layout not in self.LAYOUTS:
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        if inv_freq is not None:
+            theta = np.asarray(inv_freq, np.float64)
+            if theta.shape != (self.rotary_dim // 2,) or not np.isfinite(theta).all():
+                raise ValueError("inv_freq must be rotary_dim / 2 finite values")
+            if scaling != "none":
+                raise ValueError("inv_freq takes no scaling")
+        else:
+            theta = self._theta(float(base), scaling, float(factor), original_length, low, high)
+        self.inv_freq = theta
+        turns = [round(math.ldexp(float(x) / (2 * math.pi), 64)) % 2 ** 64 for x in theta]
+        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns],
+                                  dtype=torch.int64, device=device)
+        self._c = C.byref(_Rotary(self.turns.data_ptr(), self.rotary_dim, self.LAYOUTS[layout],
+                                  self.scale))
+
+    def _theta(self, base, scaling, factor, original_length, low, high):
+        R = self.rotary_dim
+        if not (base > 0 and factor > 0 and math.isfinite(base) and math.isfinite(factor)):
+            raise ValueError("base and factor must be positive")
+        if scaling == "base":
+            base = base * factor ** (R / max(R - 2, 1))
+        theta = base ** (-np.arange(0, R, 2, dtype=np.float64) / R)
+        if scaling == "linear":
+            theta = theta / factor
+        elif scaling == "parts":
+            if original_length < 1 or not high > low:
+                raise ValueError("'parts' needs original_length >= 1 and high > low")
+            turned = original_length * theta / (2 * math.pi)
+            keep = np.clip((turned - low) / (high - low), 0.0, 1.0)
+            theta = theta * (keep + (1.0 - keep) / factor)
+        elif scaling not in ("none", "base"):
+            raise ValueError("scaling must be 'none', 'linear', 'base' or 'parts'")
+        return theta
+
+    def _on(self, device):
+        if self.turns.device != device:
+            raise ValueError(f"rotary is on {self.turns.device}, the call on {device}")
+        return self._c
+
+
+def kv_append_rotary(p: Pass, rotary: Rotary, q, k_new, v_new, k_cache, v_cache, q_out=None,
+                     stream=None):
+    """``kv_append`` with the rotation on the way: rotated keys and the values into the
+    caches, rotated queries into ``q_out`` (which may be ``q``), by the rows' positions
+    in their sequences; returns ``q_out`` ``[T][H_q][D]``."""
+    import torch
+    c = p.config
+    T, dt = p.num_tokens, c.torch_dtype
+    row, qshape = (T, c.num_heads_kv, c.head_dim), (T, c.num_heads_q, c.head_dim)
+    if q_out is None:
+        q_out = torch.empty(qshape, dtype=dt, device=q.device)
+    _check(lib().rbkv_kv_append_rotary(p._h, rotary._on(q.device), _dev_ptr(q, "q", dt, qshape),
+                                       _dev_ptr(q_out, "q_out", dt, qshape),
+                                       _dev_ptr(k_new, "k_new", dt, row),
+                                       _dev_ptr(v_new, "v_new", dt, row),
+                                       _dev_ptr(k_cache, "k_cache", dt, c.cache_shape()),
+                                       _dev_ptr(v_cache, "v_cache", dt, c.cache_shape()),
+                                       _stream(stream)))
+    return q_out
+
+
 def ragged_attention(p: Pass, q, k_cache, v_cache, o=None, workspace=None, stream=None):
     """Ragged causal attention of every pass row; returns O ``[T][H_q][D]``."""
     import torch
@@ -500,6 +618,24 @@ class Frame:
                                           _dev_ptr(v_cache, "v_cache", dt, c.cache_shape()),
                                           _stream(stream)))
 
+    def kv_append_rotary(self, rotary: Rotary, q, k_new, v_new, k_cache, v_cache, q_out=None,
+                         stream=None):
+        """``kv_append_rotary`` of the loaded pass; returns ``q_out`` ([max_tokens][H_q][D];
+        rows past the pass's are left as they were)."""
+        import torch
+        c = self.config
+        dt = c.torch_dtype
+        row = (self.max_tokens, c.num_heads_kv, c.head_dim)
+        qshape = (self.max_tokens, c.num_heads_q, c.head_dim)
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=dt, device=q.device)
+        _check(lib().rbkv_frame_kv_append_rotary(
+            self._h, rotary._on(q.device), _dev_ptr(q, "q", dt, qshape),
+            _dev_ptr(q_out, "q_out", dt, qshape), _dev_ptr(k_new, "k_new", dt, row),
+            _dev_ptr(v_new, "v_new", dt, row), _dev_ptr(k_cache, "k_cache", dt, c.cache_shape()),
+            _dev_ptr(v_cache, "v_cache", dt, c.cache_shape()), _stream(stream)))
+        return q_out
+
     def attention(self, q, k_cache, v_cache, o, workspace, stream=None) -> None:
         c = self.config
         dt = c.torch_dtype
@@ -526,7 +662,24 @@ class Frame:
             pass
 
 
-class StepTables:
+class _Arrays:
+    """An object whose device arrays the library holds by address."""
+
+    _HELD = frozenset()
+
+    def __setattr__(self, name, value):
+        # (plain attributes, for fast reads: a small step's time is the host's)
+        if name in self._HELD and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} cannot be replaced: write into it (copy_, fill_, ...)")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._HELD:
+            raise AttributeError(f"{name} cannot be deleted")
+        object.__delattr__(self, name)
+
+
+class StepTables(_Arrays):
     """Block tables, slots and the attention plan of a step, on the GPU.
 
     ``build`` makes them from device-side lengths, with no host work and no
@@ -541,6 +694,9 @@ class StepTables:
         t.attention(q, k_cache, v_cache, prefix_table=ids, prefix_len=n, o=o, workspace=ws)
         t.release(done)                              # finished requests' blocks
 
+    ``append_rotary`` rotates queries and keys on the way; ``StepDraft`` adds
+    trees of drafted tokens.
+
     Arrays (int32, device memory): ``block_table`` [num_seqs][max_blocks],
     ``free`` (one bit per block, set = free; all free at first), ``q_start``
     [num_seqs + 1], ``ctx`` [num_seqs] (0 at first), ``position`` and ``slot``
@@ -554,17 +710,6 @@ class StepTables:
 
     _HELD = frozenset(("block_table", "free", "q_start", "ctx", "position", "slot", "plan",
                        "status"))
-
-    def __setattr__(self, name, value):
-        # (plain attributes, for fast reads: a small step's time is the host's)
-        if name in self._HELD and self.__dict__.get(name, value) is not value:
-            raise AttributeError(f"{name} cannot be replaced: write into it (copy_, fill_, ...)")
-        object.__setattr__(self, name, value)
-
-    def __delattr__(self, name):
-        if name in self._HELD:
-            raise AttributeError(f"{name} cannot be deleted")
-        object.__delattr__(self, name)
 
     def __init__(self, config: Config, num_seqs: int, max_blocks: int, max_tokens: int,
                  device="cuda"):
@@ -604,6 +749,8 @@ class StepTables:
         L = lib()
         self._f_build, self._f_append = L.rbkv_step_build, L.rbkv_step_append
         self._f_attention = L.rbkv_step_attention
+        self._f_append_rotary, self._f_draft = L.rbkv_step_append_rotary, \
+            L.rbkv_step_attention_draft
         self._table_shape, self._free_shape = self.block_table.shape, self.free.shape
         self._seq_shape = self.ctx.shape
         self._q_shape = torch.Size((self.max_tokens, config.num_heads_q, config.head_dim))
@@ -653,16 +800,41 @@ class StepTables:
                    self._ptr(v_new, "v_new", dt, row), self._ptr(k_cache, "k_cache", dt, cache),
                    self._ptr(v_cache, "v_cache", dt, cache), stream=stream)
 
+    def append_rotary(self, rotary: Rotary, q, k_new, v_new, k_cache, v_cache, q_out=None,
+                      prefix_len: int = 0, draft: Optional["StepDraft"] = None, stream=None):
+        """``append`` with the rotation on the way, by the positions prefix_len +
+        ``position`` (prefix_len + ``draft.place`` with drafted tokens): rotated keys
+        and the values into the caches, rotated queries into ``q_out``, which may be
+        ``q`` (rows past the step's are left as they were); returns ``q_out``."""
+        prefix_len = _int32(int(prefix_len), "prefix_len")
+        if q_out is None:
+            q_out = self._outputs(None, q, 0, stream)[0]
+        dt, row, cache = self._dt, self._kv_shape, self._cache_shape
+        self._call(self._f_append_rotary, self._drafted(draft), rotary._on(self.device),
+                   prefix_len, self._ptr(q, "q", dt, self._q_shape),
+                   self._ptr(q_out, "q_out", dt, self._q_shape),
+                   self._ptr(k_new, "k_new", dt, row), self._ptr(v_new, "v_new", dt, row),
+                   self._ptr(k_cache, "k_cache", dt, cache),
+                   self._ptr(v_cache, "v_cache", dt, cache), stream=stream)
+        return q_out
+
+    def _drafted(self, draft):
+        if draft is None:
+            return None
+        if draft.tables is not self:
+            raise ValueError("draft belongs to other tables")
+        return draft._d
+
     def workspace_bytes(self, prefix_len: int = 0) -> int:
         prefix_len = _int32(int(prefix_len), "prefix_len")
         with _device(self.device):
             return int(lib().rbkv_step_workspace_bytes(self._c, self._t, prefix_len))
 
     def attention(self, q, k_cache, v_cache, prefix_table=None, prefix_len: int = 0, o=None,
-                  workspace=None, stream=None):
-        """Every row attends the prefix and its sequence's keys up to its own;
-        returns O ([max_tokens][H_q][D]; rows past the step's are left as they
-        were)."""
+                  workspace=None, stream=None, draft: Optional["StepDraft"] = None):
+        """Every row attends the prefix and its sequence's keys up to its own (with
+        ``draft``: those cached before the step, its ancestors' and its own); returns O
+        ([max_tokens][H_q][D]; rows past the step's are left as they were)."""
         prefix_len = _int32(int(prefix_len), "prefix_len")
         table = None
         if prefix_table is not None:
@@ -677,11 +849,13 @@ class StepTables:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         dt, cache = self._dt, self._cache_shape
-        self._call(self._f_attention, self._ptr(q, "q", dt, self._q_shape),
-                   self._ptr(k_cache, "k_cache", dt, cache),
-                   self._ptr(v_cache, "v_cache", dt, cache), table, prefix_len,
-                   self._ptr(o, "o", dt, self._q_shape), workspace.data_ptr(),
-                   workspace.nbytes, stream=stream)
+        args = (self._ptr(q, "q", dt, self._q_shape), self._ptr(k_cache, "k_cache", dt, cache),
+                self._ptr(v_cache, "v_cache", dt, cache), table, prefix_len,
+                self._ptr(o, "o", dt, self._q_shape), workspace.data_ptr(), workspace.nbytes)
+        if draft is None:
+            self._call(self._f_attention, *args, stream=stream)
+        else:
+            self._call(self._f_draft, self._drafted(draft), *args, stream=stream)
         return o
 
     def _outputs(self, o, workspace, prefix_len, stream):
@@ -701,6 +875,76 @@ class StepTables:
     def device_status(self, stream=None) -> None:
         with _device(self.device):
             _check(lib().rbkv_step_device_status(self._t, _stream(stream)))
+
+
+class StepDraft(_Arrays):
+    """Drafted tokens of a step: a tree of candidate tokens per sequence, attended at
+    once, of which one path is kept.  One step of a drafting loop, captured or not::
+
+        d = StepDraft(t)                                  # t: StepTables
+        t.build(t.ctx, n_new)                             # new tokens: the trees'
+        d.plan(parent)                                    # parent: int32 [max_tokens]
+        q = t.append_rotary(rope, q, k_new, v_new, k_cache, v_cache, draft=d)   # per layer
+        t.attention(q, k_cache, v_cache, o=o, workspace=ws, draft=d)
+        d.accept(tokens, chosen)                          # t.ctx, t.free: cut back
+        d.compact(k_cache, v_cache)                       # per layer
+
+    ``parent[r]``: the index, among its sequence's new tokens, of the token that row r
+    follows (before its own; -1: none).  Trees have at most 128 tokens; longer runs of
+    new tokens are chains, as prompt chunks are.  A bad tree is taken as a chain and
+    ``t.device_status`` says so.
+
+    Arrays (int32, device memory, written in place): ``place`` [max_tokens] (position
+    of a token once its path is kept; -1 past the rows) and ``ancestors``
+    [max_tokens][4] (bit i of word w: the token is, or follows, token 32 w + i) are the
+    plan's; ``path`` [max_tokens] (entry q_start[s] + d: row of the d-th kept token of
+    sequence s; else -1), ``accepted`` and ``next_token`` [num_seqs] the acceptance's.
+    """
+
+    _HELD = frozenset(("place", "ancestors", "path", "accepted", "next_token", "tables"))
+
+    def __init__(self, tables: StepTables):
+        import torch
+        self.tables = t = tables
+
+        def full(value, *shape):
+            return torch.full(shape, value, dtype=torch.int32, device=t.device)
+
+        self.place, self.path = full(-1, t.max_tokens), full(-1, t.max_tokens)
+        self.ancestors = full(0, t.max_tokens, 4)
+        self.accepted, self.next_token = full(0, t.num_seqs), full(-1, t.num_seqs)
+        self._d = C.byref(_StepDraft(*(x.data_ptr() for x in (
+            self.place, self.ancestors, self.path, self.accepted, self.next_token))))
+        L = lib()
+        self._f_plan, self._f_accept = L.rbkv_step_draft_plan, L.rbkv_step_draft_accept
+        self._f_compact = L.rbkv_step_draft_compact
+        self._rows = t.position.shape
+
+    def plan(self, parent, stream=None) -> "StepDraft":
+        """Work out the trees of the step built last."""
+        t = self.tables
+        t._call(self._f_plan, self._d, t._ptr(parent, "parent", t._i32, self._rows),
+                stream=stream)
+        return self
+
+    def accept(self, tokens, chosen, given=None, stream=None) -> "StepDraft":
+        """Keep a path of every tree.  ``tokens[r]``: the token of row r; ``chosen[r]``:
+        the one chosen to follow it; ``given[s]`` (1 each): leading new tokens of
+        sequence s that are not drafted (a prompt chunk: all of them).  From the last
+        given token the path goes on to the lowest child that is the chosen token.
+        Cuts ``t.ctx`` back to the kept tokens and frees the blocks behind them."""
+        t, i32 = self.tables, self.tables._i32
+        t._call(self._f_accept, self._d, t._ptr(tokens, "tokens", i32, self._rows),
+                t._ptr(chosen, "chosen", i32, self._rows),
+                None if given is None else t._ptr(given, "given", i32, t._seq_shape),
+                stream=stream)
+        return self
+
+    def compact(self, k_cache, v_cache, stream=None) -> None:
+        """Move the kept tokens' rows of a layer's caches together."""
+        t = self.tables
+        t._call(self._f_compact, self._d, t._ptr(k_cache, "k_cache", t._dt, t._cache_shape),
+                t._ptr(v_cache, "v_cache", t._dt, t._cache_shape), stream=stream)
 
 
 def budget_for_latency(tokens, latency, bound: float) -> int:
@@ -857,5 +1101,5 @@ class Router:
             pass
 
 
-__all__ = ["gemm", "gemm_qkv", "gemm_workspace_bytes", "rmsnorm", "Router", "Frame", "StepTables", "budget_for_latency", "seq_states", "SeqStates", "ragged_attention_noalloc", "kernel_launches", "profile_enable", "profile_reset", "profile_read", "Config", "Composer", "Pass", "PassMeta", "kv_append", "ragged_attention",
+__all__ = ["gemm", "gemm_qkv", "gemm_workspace_bytes", "rmsnorm", "Router", "Frame", "StepTables", "StepDraft", "Rotary", "kv_append_rotary", "budget_for_latency", "seq_states", "SeqStates", "ragged_attention_noalloc", "kernel_launches", "profile_enable", "profile_reset", "profile_read", "Config", "Composer", "Pass", "PassMeta", "kv_append", "ragged_attention",
            "RbkvError", "NoBlocksError", "lib", "library_path", "SIGNATURES"]

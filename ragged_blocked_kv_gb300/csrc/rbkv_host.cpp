@@ -672,6 +672,12 @@ rbkv_status ensure_plan(rbkv_pass* p) {
 }
 
 
+// Position of every pass row in its sequence.
+void fill_positions(const rbkv_pass& p, int32_t* out) {
+  for (size_t i = 0; i < p.seen.size(); ++i)
+    for (int32_t j = 0; j < p.n_new[i]; ++j) out[p.q_start[i] + j] = p.seen[i] + j;
+}
+
 // Plan (if needed), pack and upload the metadata on `st`; order `st` after
 // the upload when it is another stream.
 rbkv_status ensure_device(rbkv_pass* p, cudaStream_t st) {
@@ -688,6 +694,7 @@ rbkv_status ensure_device(rbkv_pass* p, cudaStream_t st) {
       return off;
     };
     const size_t o_slot = section(p->slot.size() * 4);
+    const size_t o_pos = section(p->slot.size() * 4);
     const size_t o_blocks = section(p->block_ids.size() * 4);
     const size_t o_dec = section(pl.decode.size() * sizeof(WorkItem));
     const size_t o_gen = section(pl.generic.size() * sizeof(WorkItem));
@@ -704,6 +711,7 @@ rbkv_status ensure_device(rbkv_pass* p, cudaStream_t st) {
       if (n) std::memcpy(hw + off, src, n);
     };
     fill(o_slot, p->slot.data(), p->slot.size() * 4);
+    fill_positions(*p, hw + o_pos);
     fill(o_blocks, p->block_ids.data(), p->block_ids.size() * 4);
     fill(o_dec, pl.decode.data(), pl.decode.size() * sizeof(WorkItem));
     fill(o_gen, pl.generic.data(), pl.generic.size() * sizeof(WorkItem));
@@ -731,6 +739,7 @@ rbkv_status ensure_device(rbkv_pass* p, cudaStream_t st) {
     DevPass& dp = p->dp;
     dp.status = base;
     dp.slot = base + o_slot;
+    dp.position = base + o_pos;
     dp.block_ids = base + o_blocks;
     dp.decode_items = (const WorkItem*)(base + o_dec);
     dp.generic_items = (const WorkItem*)(base + o_gen);
@@ -1133,6 +1142,27 @@ rbkv_status rbkv_kv_append(rbkv_pass* p, const void* k_new, const void* v_new, v
   return RBKV_OK;
 }
 
+rbkv_status rbkv_kv_append_rotary(rbkv_pass* p, const rbkv_rotary* rotary, const void* q,
+                                  void* q_out, const void* k_new, const void* v_new,
+                                  void* k_cache, void* v_cache, rbkv_stream stream) {
+  rbkv::NvtxRange nvtx_range("rbkv_kv_append_rotary");
+  if (!p) return fail(RBKV_ERR_INVALID, "pass is NULL");
+  if (p->slot.empty()) return RBKV_OK;
+  rbkv_status rs = check_append_rotary(&p->cfg, rotary, (int64_t)p->slot.size(), q, q_out, k_new,
+                                       v_new, k_cache, v_cache);
+  if (rs != RBKV_OK) return rs;
+  cudaStream_t st = (cudaStream_t)stream;
+  rs = ensure_device(p, st);
+  if (rs != RBKV_OK) return rs;
+  const ShapeInfo s = shape_of(p->cfg);
+  cudaError_t e = launch_counted(RBKV_KERNEL_KV_APPEND, st, [&] {
+    return launch_append_rotary(p->dp, s, *rotary, 0, q, q_out, k_new, v_new, k_cache, v_cache,
+                                st, !g_prof.on);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_rotary launch");
+  return RBKV_OK;
+}
+
 size_t rbkv_attention_workspace_bytes(rbkv_pass* p) {
   if (!p || ensure_plan(p) != RBKV_OK) return 0;
   return workspace_bytes_of(*p);
@@ -1246,7 +1276,7 @@ struct rbkv_frame {
   int sms = 0;
   int32_t* dev = nullptr;   // device words: status[4] | counts[8] | sections
   size_t words = 0;
-  size_t o_slot = 0, o_blocks = 0, o_dec = 0, o_chunk = 0, o_items = 0, o_comb = 0;
+  size_t o_slot = 0, o_pos = 0, o_blocks = 0, o_dec = 0, o_chunk = 0, o_items = 0, o_comb = 0;
   int32_t max_items = 0;   // chunk work items: max_chunk_tiles x num_heads_q
   static constexpr int kStages = 4;
   int32_t* host[kStages] = {};   // pinned staging, same layout
@@ -1323,6 +1353,7 @@ rbkv_status rbkv_frame_create(const rbkv_config* cfg, const rbkv_frame_caps* cap
   f->sms = sms;
   size_t w = 12;  // status words, counts
   f->o_slot = w;   w = align4(w + (size_t)c.max_tokens);
+  f->o_pos = w;    w = align4(w + (size_t)c.max_tokens);
   f->o_blocks = w; w = align4(w + (size_t)c.max_blocks);
   f->o_dec = w;    w = align4(w + (size_t)c.max_decode_items * (sizeof(WorkItem) / 4));
   f->o_chunk = w;  w = align4(w + (size_t)c.max_chunk_tiles * (sizeof(ChunkTile) / 4));
@@ -1344,6 +1375,7 @@ rbkv_status rbkv_frame_create(const rbkv_config* cfg, const rbkv_frame_caps* cap
   dp.status = base;
   dp.counts = base + 4;
   dp.slot = base + f->o_slot;
+  dp.position = base + f->o_pos;
   dp.block_ids = base + f->o_blocks;
   dp.decode_items = (const WorkItem*)(base + f->o_dec);
   dp.generic_items = nullptr;
@@ -1425,10 +1457,11 @@ rbkv_status rbkv_frame_load(rbkv_frame* f, rbkv_pass* p, rbkv_stream stream) {
   size_t head_end = 12;
   if (pl) {
     std::memcpy(h + f->o_slot, p->slot.data(), p->slot.size() * 4);
+    fill_positions(*p, h + f->o_pos);
     std::memcpy(h + f->o_blocks, p->block_ids.data(), p->block_ids.size() * 4);
     head_end = f->o_blocks + p->block_ids.size();
   }
-  // counts, slots and block tables in one copy (not the status words), then
+  // counts, slots, positions and block tables in one copy (not the status words), then
   // the used part of each work list
   e = cudaMemcpyAsync(f->dev + 4, h + 4, (head_end - 4) * 4, cudaMemcpyHostToDevice, st);
   auto section = [&](size_t off, const void* src, size_t bytes) {
@@ -1458,6 +1491,24 @@ rbkv_status rbkv_frame_kv_append(rbkv_frame* f, const void* k_new, const void* v
     return launch_kv_append(f->dp, s, k_new, v_new, k_cache, v_cache, st, !g_prof.on);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return RBKV_OK;
+}
+
+rbkv_status rbkv_frame_kv_append_rotary(rbkv_frame* f, const rbkv_rotary* rotary, const void* q,
+                                        void* q_out, const void* k_new, const void* v_new,
+                                        void* k_cache, void* v_cache, rbkv_stream stream) {
+  rbkv::NvtxRange nvtx_range("rbkv_frame_kv_append_rotary");
+  if (!f) return fail(RBKV_ERR_INVALID, "frame is NULL");
+  rbkv_status rs = check_append_rotary(&f->cfg, rotary, f->caps.max_tokens, q, q_out, k_new,
+                                       v_new, k_cache, v_cache);
+  if (rs != RBKV_OK) return rs;
+  cudaStream_t st = (cudaStream_t)stream;
+  const ShapeInfo s = shape_of(f->cfg);
+  cudaError_t e = launch_counted(RBKV_KERNEL_KV_APPEND, st, [&] {
+    return launch_append_rotary(f->dp, s, *rotary, 0, q, q_out, k_new, v_new, k_cache, v_cache,
+                                st, !g_prof.on);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_rotary launch");
   return RBKV_OK;
 }
 

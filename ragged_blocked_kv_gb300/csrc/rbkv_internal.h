@@ -92,6 +92,7 @@ static_assert(sizeof(ChunkItem) == 32, "ChunkItem is 8 int32");
 struct DevPass {
   int32_t* status;                 // device status words (rbkv_status code, wait site, ...)
   const int32_t* slot;             // [T]
+  const int32_t* position;         // [T]
   const int32_t* block_ids;        // all block tables
   const WorkItem* decode_items;    // fast decode path
   const WorkItem* generic_items;   // CUDA-core path
@@ -115,9 +116,9 @@ struct DevPass {
   // Null for a plain pass.
   const int32_t* counts;
   // A step built on the device (rbkv_step_*): {block size, rows of its arrays}
-  // that it was built for, to be compared with what it is used with.  Null
-  // otherwise.
-  const int32_t* built_for[2];
+  // that it was built for, to be compared with what it is used with; and for
+  // drafted tokens whether their trees were planned.  Null otherwise.
+  const int32_t* built_for[3];
 };
 
 enum { kCountTokens = 0, kCountDecode = 1, kCountGeneric = 2, kCountChunk = 3, kCountCombine = 4 };
@@ -181,6 +182,16 @@ cudaError_t launch_kv_append(const DevPass& dp, const ShapeInfo& s, const void* 
 // kernel that may overlap its predecessor and waits for it before storing.
 cudaError_t launch_meta_upload(const void* src, void* dst, size_t bytes, cudaStream_t st,
                                bool overlap_previous);
+// The append with a rotation on the way, by the positions offset + position[t]
+// (rbkv_rotary.cu).
+cudaError_t launch_append_rotary(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r,
+                                 int32_t offset, const void* q, void* q_out, const void* k_new,
+                                 const void* v_new, void* k_cache, void* v_cache, cudaStream_t st,
+                                 bool overlap_previous);
+// Checks of its arguments, for `rows` rows.
+rbkv_status check_append_rotary(const rbkv_config* c, const rbkv_rotary* r, int64_t rows,
+                                const void* q, const void* q_out, const void* k_new,
+                                const void* v_new, const void* k_cache, const void* v_cache);
 cudaError_t launch_generic_attention(const DevPass& dp, const ShapeInfo& s, const void* q,
                                      const void* k_cache, const void* v_cache, void* o,
                                      float* part_o, float* part_lse, cudaStream_t st);

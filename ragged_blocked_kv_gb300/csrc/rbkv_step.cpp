@@ -104,6 +104,136 @@ size_t workspace_of(const ShapeInfo& s, const rbkv_step_tables* t, int32_t prefi
   return step_generic_workspace(s, t->max_tokens, splits);
 }
 
+rbkv_status check_draft(const rbkv_config* c, const rbkv_step_tables* t,
+                        const rbkv_step_draft* d) {
+  rbkv_status st = check_tables(c, t);
+  if (st != RBKV_OK) return st;
+  if (!d) return invalid("draft is NULL");
+  if (!d->place || !d->ancestors || !d->path || !d->accepted || !d->next_token)
+    return invalid("NULL draft array");
+  if (!aligned(d->ancestors, 16)) return invalid("ancestors must be 16-byte aligned");
+  if (!aligned(d->place, 4) || !aligned(d->path, 4) || !aligned(d->accepted, 4) ||
+      !aligned(d->next_token, 4))
+    return invalid("draft arrays must be 4-byte aligned");
+  return RBKV_OK;
+}
+
+DraftArgs draft_args(const rbkv_config* c, const rbkv_step_tables* t, const rbkv_step_draft* d) {
+  DraftArgs a = {};
+  a.num_seqs = t->num_seqs;
+  a.max_blocks = t->max_blocks;
+  a.max_tokens = t->max_tokens;
+  a.num_blocks = c->num_blocks;
+  a.block_size = c->block_size;
+  a.q_start = t->q_start;
+  a.position = t->position;
+  a.slot = t->slot;
+  a.table = t->block_table;
+  a.ctx = t->ctx;
+  a.free_words = t->free_words;
+  a.plan = t->plan;
+  a.status = t->status;
+  a.place = d->place;
+  a.ancestors = d->ancestors;
+  a.path = d->path;
+  a.accepted = d->accepted;
+  a.next_token = d->next_token;
+  return a;
+}
+
+// Whether the n int32 at p meet an array that a draft call writes or that a
+// build writes (which its calls read).
+bool written_by_draft(const rbkv_config* c, const rbkv_step_tables* t, const rbkv_step_draft* d,
+                      const void* p, int64_t n) {
+  const int64_t S = t->num_seqs, T = t->max_tokens;
+  return written_by_build(t, c->num_blocks, p, n, nullptr) || overlap(p, 4 * n, d->place, 4 * T) ||
+         overlap(p, 4 * n, d->ancestors, 16 * T) || overlap(p, 4 * n, d->path, 4 * T) ||
+         overlap(p, 4 * n, d->accepted, 4 * S) || overlap(p, 4 * n, d->next_token, 4 * S);
+}
+
+DevPass append_pass(const rbkv_config* c, const rbkv_step_tables* t) {
+  DevPass dp = {};
+  dp.status = t->status;
+  dp.slot = t->slot;
+  dp.position = t->position;
+  dp.num_tokens = t->max_tokens;
+  dp.num_blocks = c->num_blocks;
+  dp.counts = t->plan + kPlanRows;
+  dp.built_for[0] = t->plan + kPlanBlock;
+  dp.built_for[1] = t->plan + kPlanTokens;
+  return dp;
+}
+
+// rbkv_step_attention, with drafted tokens or (d null) without.
+rbkv_status step_attention(const rbkv_config* cfg, const rbkv_step_tables* t,
+                           const rbkv_step_draft* d, const void* q, const void* k_cache,
+                           const void* v_cache, const int32_t* prefix_table, int32_t prefix_len,
+                           void* o, void* workspace, size_t workspace_bytes, rbkv_stream stream) {
+  rbkv_status st = check_tables(cfg, t);
+  if (st != RBKV_OK) return st;
+  if (!q || !k_cache || !v_cache || !o) return invalid("NULL tensor");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
+    return invalid("tensors must be 16-byte aligned");
+  if (q == o) return invalid("o must not be q");
+  if (prefix_len < 0 || prefix_len > 1 << 30)
+    return invalid("prefix_len must be in [0, 2^30]");
+  if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4)))
+    return invalid("a prefix needs a 4-byte aligned block list");
+  if (!aligned(workspace, 256)) return invalid("workspace must be 256-byte aligned");
+  DevStep ds = {};
+  ds.num_seqs = t->num_seqs;
+  ds.max_blocks = t->max_blocks;
+  ds.max_tokens = t->max_tokens;
+  ds.num_blocks = cfg->num_blocks;
+  ds.block_table = t->block_table;
+  ds.q_start = t->q_start;
+  ds.ctx = t->ctx;
+  ds.plan = t->plan;
+  ds.status = t->status;
+  ds.prefix_table = prefix_table;
+  ds.prefix_len = prefix_len;
+  if (d) {
+    ds.place = d->place;
+    ds.ancestors = (const uint4*)d->ancestors;
+  }
+  const ShapeInfo s = shape(cfg);
+  const int64_t T = t->max_tokens;
+  const int64_t q_bytes = T * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
+  if (overlap(q, q_bytes, o, q_bytes)) return invalid("o overlaps q");
+  if (d && (overlap(o, q_bytes, d->place, 4 * T) || overlap(o, q_bytes, d->ancestors, 16 * T)))
+    return invalid("o overlaps the drafted tokens' arrays");
+  const cudaStream_t cs = (cudaStream_t)stream;
+  int sms = 0;
+  cudaError_t e = num_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  const size_t need = workspace_of(s, t, prefix_len, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
+  if (need > 0 && (overlap(workspace, (int64_t)need, q, q_bytes) ||
+                   overlap(workspace, (int64_t)need, o, q_bytes)))
+    return invalid("workspace overlaps q or o");
+  if (d && need > 0 && (overlap(workspace, (int64_t)need, d->place, 4 * T) ||
+                        overlap(workspace, (int64_t)need, d->ancestors, 16 * T)))
+    return invalid("workspace overlaps the drafted tokens' arrays");
+  if (!step_fast_supported(s)) {
+    const int splits = step_generic_splits(s, t->max_tokens, t->max_blocks, prefix_len, sms);
+    e = launch_step_generic(ds, s, q, k_cache, v_cache, o, workspace, splits, sms, cs);
+    if (e == cudaSuccess) note_launches(splits > 1 ? 2 : 1);
+  } else {
+    StepWorkspace w;
+    step_workspace(s, t->max_tokens, sms, workspace, &w);
+    // a step of at most 16 packed rows has no work for the tile kernel
+    const bool tiles = !step_prefix_streamed(t->max_tokens, s.g);
+    if (tiles) e = launch_step_tile(ds, s, w, q, k_cache, v_cache, o, cs);
+    if (e == cudaSuccess)
+      e = launch_step_stream(ds, s, w, q, k_cache, v_cache, o, !tiles, cs);
+    if (e == cudaSuccess) e = launch_step_combine(ds, s, w, o, cs);
+    if (e == cudaSuccess) note_launches(tiles ? 3 : 2);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "step attention launch");
+  return RBKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -172,16 +302,8 @@ rbkv_status rbkv_step_append(const rbkv_config* cfg, const rbkv_step_tables* t,
   const int64_t vec = (int64_t)s.D * (s.dtype == RBKV_BF16 ? 2 : 4) / 16;
   if (2 * (int64_t)t->max_tokens * s.H_kv * vec >= (int64_t)1 << 31)
     return fail(RBKV_ERR_UNSUPPORTED, "max_tokens too large for one append");
-  DevPass dp = {};
-  dp.status = t->status;
-  dp.slot = t->slot;
-  dp.num_tokens = t->max_tokens;
-  dp.num_blocks = cfg->num_blocks;
-  dp.counts = t->plan + kPlanRows;
-  dp.built_for[0] = t->plan + kPlanBlock;
-  dp.built_for[1] = t->plan + kPlanTokens;
-  cudaError_t e = launch_kv_append(dp, s, k_new, v_new, k_cache, v_cache, (cudaStream_t)stream,
-                                   true);
+  cudaError_t e = launch_kv_append(append_pass(cfg, t), s, k_new, v_new, k_cache, v_cache,
+                                   (cudaStream_t)stream, true);
   if (e != cudaSuccess) return cuda_fail(e, "step append launch");
   note_launches(1);
   return RBKV_OK;
@@ -201,59 +323,108 @@ rbkv_status rbkv_step_attention(const rbkv_config* cfg, const rbkv_step_tables* 
                                 const int32_t* prefix_table, int32_t prefix_len, void* o,
                                 void* workspace, size_t workspace_bytes, rbkv_stream stream) {
   NvtxRange nvtx_range("rbkv_step_attention");
-  rbkv_status st = check_tables(cfg, t);
+  return step_attention(cfg, t, nullptr, q, k_cache, v_cache, prefix_table, prefix_len, o,
+                        workspace, workspace_bytes, stream);
+}
+
+rbkv_status rbkv_step_attention_draft(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                      const rbkv_step_draft* d, const void* q,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* prefix_table, int32_t prefix_len, void* o,
+                                      void* workspace, size_t workspace_bytes,
+                                      rbkv_stream stream) {
+  NvtxRange nvtx_range("rbkv_step_attention_draft");
+  rbkv_status st = check_draft(cfg, t, d);
   if (st != RBKV_OK) return st;
-  if (!q || !k_cache || !v_cache || !o) return invalid("NULL tensor");
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
-    return invalid("tensors must be 16-byte aligned");
-  if (q == o) return invalid("o must not be q");
-  if (prefix_len < 0 || prefix_len > 1 << 30)
-    return invalid("prefix_len must be in [0, 2^30]");
-  if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4)))
-    return invalid("a prefix needs a 4-byte aligned block list");
-  if (!aligned(workspace, 256)) return invalid("workspace must be 256-byte aligned");
-  DevStep ds = {};
-  ds.num_seqs = t->num_seqs;
-  ds.max_blocks = t->max_blocks;
-  ds.max_tokens = t->max_tokens;
-  ds.num_blocks = cfg->num_blocks;
-  ds.block_table = t->block_table;
-  ds.q_start = t->q_start;
-  ds.ctx = t->ctx;
-  ds.plan = t->plan;
-  ds.status = t->status;
-  ds.prefix_table = prefix_table;
-  ds.prefix_len = prefix_len;
+  return step_attention(cfg, t, d, q, k_cache, v_cache, prefix_table, prefix_len, o, workspace,
+                        workspace_bytes, stream);
+}
+
+rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                    const rbkv_step_draft* d, const rbkv_rotary* rotary,
+                                    int32_t prefix_len, const void* q, void* q_out,
+                                    const void* k_new, const void* v_new, void* k_cache,
+                                    void* v_cache, rbkv_stream stream) {
+  NvtxRange nvtx_range("rbkv_step_append_rotary");
+  rbkv_status st = d ? check_draft(cfg, t, d) : check_tables(cfg, t);
+  if (st != RBKV_OK) return st;
+  if (prefix_len < 0 || prefix_len > 1 << 30) return invalid("prefix_len must be in [0, 2^30]");
+  st = check_append_rotary(cfg, rotary, t->max_tokens, q, q_out, k_new, v_new, k_cache, v_cache);
+  if (st != RBKV_OK) return st;
   const ShapeInfo s = shape(cfg);
-  const cudaStream_t cs = (cudaStream_t)stream;
-  int sms = 0;
-  cudaError_t e = num_sms(&sms);
-  if (e != cudaSuccess) return cuda_fail(e, "device query");
-  const size_t need = workspace_of(s, t, prefix_len, sms);
-  if (need > 0 && (!workspace || workspace_bytes < need))
-    return fail(RBKV_ERR_WORKSPACE, "workspace missing or too small");
-  const int64_t q_bytes =
-      (int64_t)t->max_tokens * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
-  if (overlap(q, q_bytes, o, q_bytes)) return invalid("o overlaps q");
-  if (need > 0 && (overlap(workspace, (int64_t)need, q, q_bytes) ||
-                   overlap(workspace, (int64_t)need, o, q_bytes)))
-    return invalid("workspace overlaps q or o");
-  if (!step_fast_supported(s)) {
-    const int splits = step_generic_splits(s, t->max_tokens, t->max_blocks, prefix_len, sms);
-    e = launch_step_generic(ds, s, q, k_cache, v_cache, o, workspace, splits, sms, cs);
-    if (e == cudaSuccess) note_launches(splits > 1 ? 2 : 1);
-  } else {
-    StepWorkspace w;
-    step_workspace(s, t->max_tokens, sms, workspace, &w);
-    // a step of at most 16 packed rows has no work for the tile kernel
-    const bool tiles = !step_prefix_streamed(t->max_tokens, s.g);
-    if (tiles) e = launch_step_tile(ds, s, w, q, k_cache, v_cache, o, cs);
-    if (e == cudaSuccess)
-      e = launch_step_stream(ds, s, w, q, k_cache, v_cache, o, !tiles, cs);
-    if (e == cudaSuccess) e = launch_step_combine(ds, s, w, o, cs);
-    if (e == cudaSuccess) note_launches(tiles ? 3 : 2);
+  const int64_t T = t->max_tokens;
+  const int64_t q_bytes = T * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
+  if (overlap(q_out, q_bytes, t->slot, 4 * T) || overlap(q_out, q_bytes, t->position, 4 * T) ||
+      overlap(q_out, q_bytes, t->plan, 4 * step_plan_ints(t->num_seqs, T)) ||
+      (d && overlap(q_out, q_bytes, d->place, 4 * T)))
+    return invalid("q_out overlaps an array that the call reads");
+  DevPass dp = append_pass(cfg, t);
+  if (d) {
+    dp.position = d->place;
+    dp.built_for[2] = t->plan + kPlanDraft;
   }
-  if (e != cudaSuccess) return cuda_fail(e, "step attention launch");
+  cudaError_t e = launch_append_rotary(dp, s, *rotary, prefix_len, q, q_out, k_new, v_new, k_cache,
+                                       v_cache, (cudaStream_t)stream, true);
+  if (e != cudaSuccess) return cuda_fail(e, "step append_rotary launch");
+  note_launches(1);
+  return RBKV_OK;
+}
+
+rbkv_status rbkv_step_draft_plan(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                 const rbkv_step_draft* d, const int32_t* parent,
+                                 rbkv_stream stream) {
+  NvtxRange nvtx_range("rbkv_step_draft_plan");
+  rbkv_status st = check_draft(cfg, t, d);
+  if (st != RBKV_OK) return st;
+  if (!parent || !aligned(parent, 4)) return invalid("parent must be a 4-byte aligned array");
+  if (written_by_draft(cfg, t, d, parent, t->max_tokens))
+    return invalid("parent overlaps an array of the step");
+  DraftArgs a = draft_args(cfg, t, d);
+  a.parent = parent;
+  cudaError_t e = launch_draft_plan(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "draft plan launch");
+  note_launches(1);
+  return RBKV_OK;
+}
+
+rbkv_status rbkv_step_draft_accept(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                   const rbkv_step_draft* d, const int32_t* tokens,
+                                   const int32_t* chosen, const int32_t* given,
+                                   rbkv_stream stream) {
+  NvtxRange nvtx_range("rbkv_step_draft_accept");
+  rbkv_status st = check_draft(cfg, t, d);
+  if (st != RBKV_OK) return st;
+  if (!tokens || !chosen) return invalid("tokens and chosen must not be NULL");
+  if (!aligned(tokens, 4) || !aligned(chosen, 4) || !aligned(given, 4))
+    return invalid("arrays must be 4-byte aligned");
+  if (written_by_draft(cfg, t, d, tokens, t->max_tokens) ||
+      written_by_draft(cfg, t, d, chosen, t->max_tokens) ||
+      (given && written_by_draft(cfg, t, d, given, t->num_seqs)))
+    return invalid("an input overlaps an array of the step");
+  DraftArgs a = draft_args(cfg, t, d);
+  a.tokens = tokens;
+  a.chosen = chosen;
+  a.given = given;
+  cudaError_t e = launch_draft_accept(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "draft accept launch");
+  note_launches(1);
+  return RBKV_OK;
+}
+
+rbkv_status rbkv_step_draft_compact(const rbkv_config* cfg, const rbkv_step_tables* t,
+                                    const rbkv_step_draft* d, void* k_cache, void* v_cache,
+                                    rbkv_stream stream) {
+  NvtxRange nvtx_range("rbkv_step_draft_compact");
+  rbkv_status st = check_draft(cfg, t, d);
+  if (st != RBKV_OK) return st;
+  if (!k_cache || !v_cache) return invalid("NULL tensor");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return invalid("tensors must be 16-byte aligned");
+  cudaError_t e =
+      launch_draft_compact(draft_args(cfg, t, d), shape(cfg), k_cache, v_cache,
+                           (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "draft compact launch");
+  note_launches(1);
   return RBKV_OK;
 }
 

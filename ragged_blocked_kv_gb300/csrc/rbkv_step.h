@@ -14,6 +14,9 @@ constexpr int kStepPipes = 4;           // its pipelines (warps) per CTA
 constexpr int kStepTileKeys = 128;      // keys per tile of the tensor-core kernel
 constexpr int kStepTileRows = 128;      // packed query rows per tensor-core tile
 
+// Drafted tokens of a sequence, at most (a set of ancestors is four words).
+constexpr int kStepTreeTokens = RBKV_DRAFT_TOKENS;
+
 // Tokens whose packed rows fill one tensor-core query tile.
 __host__ __device__ __forceinline__ int step_tile_tokens(int g) { return kStepTileRows / g; }
 
@@ -40,8 +43,10 @@ enum {
   kPlanTokens = 8,
   kPlanMaxBlocks = 9,
   kPlanPool = 10,       // blocks of the pool
+  kPlanDraft = 11,      // what has been done to the step's drafted tokens since the build
   kPlanHeader = 16
 };
+enum { kDraftPlanned = 1, kDraftAccepted = 2 };
 
 // A sequence of a kernel's work list.  cum: line length before it, for one KV
 // head; tiles: 16-key tiles (streamed) or line length (tiled).
@@ -145,6 +150,9 @@ struct DevStep {
   int32_t* status;
   const int32_t* prefix_table;
   int32_t prefix_len;
+  // drafted tokens (null: every row sees its sequence's earlier ones)
+  const int32_t* place;         // [max_tokens]
+  const uint4* ancestors;       // [max_tokens]
 };
 
 // Work is cut evenly over the CTAs of a persistent grid.  A kernel's units lie
@@ -190,6 +198,8 @@ __device__ __forceinline__ bool step_matches(const DevStep& ds, const ShapeInfo&
                     kPlanMaxBlocks == 9, "the header's second and third vector");
   const int4 b = *reinterpret_cast<const int4*>(plan.header + 4);
   const int2 c = *reinterpret_cast<const int2*>(plan.header + 8);
+  // (drafted tokens whose trees have not been planned since the build)
+  if (ds.place && plan.header[kPlanDraft] == 0) return false;
   // (no short cuts: all of it in one round trip)
   return ((b.y ^ s.g) | (b.z ^ s.B) | (b.w ^ ds.num_seqs) | (c.x ^ ds.max_tokens) |
           (c.y ^ ds.max_blocks)) == 0;
@@ -231,6 +241,36 @@ __device__ __forceinline__ StepWork step_work(const DevStep& ds, const ShapeInfo
 #endif
 
 #ifdef __CUDACC__
+// Drafted tokens: what the row of token `token` of a sequence sees of its own
+// keys.  A row sees a run of keys from the first, up to key `last`, and of those
+// behind it the keys seen + i with bit i of its ancestors: a row that follows all
+// tokens before it (its depth is its index) sees them as one run, any other the
+// tokens cached before the step.  (Sequences of more than kStepTreeTokens new
+// tokens are chains, all runs.)
+__device__ __forceinline__ bool draft_is_run(const DevStep& ds, int row, int seen, int token) {
+  return ds.place[row] - seen == token;
+}
+// Words of the ancestors' set moved down by `by` bits (up, where negative).
+__device__ __forceinline__ void draft_window(const uint4& set, int by, uint32_t (&w)[4]) {
+  const uint32_t m[4] = {set.x, set.y, set.z, set.w};
+  const int words = by >> 5, bits = by & 31;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if (y == x + words) lo = m[y];
+      if (y == x + words + 1) hi = m[y];
+    }
+    w[x] = __funnelshift_r(lo, hi, bits);
+  }
+}
+// Bit i of a set (none outside it).
+__device__ __forceinline__ bool draft_bit(const uint4& set, int i) {
+  const uint32_t w = i < 64 ? (i < 32 ? set.x : set.y) : (i < 96 ? set.z : set.w);
+  return (uint32_t)i < (uint32_t)kStepTreeTokens && (w >> (i & 31) & 1u);
+}
+
 // 0xffff over each of two bf16 that is an infinity or NaN.
 //
 // A row must not see the values of later tokens of its sequence, and in a
@@ -326,6 +366,19 @@ struct BuildArgs {
   const int32_t *seen, *n_new, *table_in, *free_in;
   int32_t *table, *free_words, *q_start, *ctx, *position, *slot, *plan, *status;
 };
+
+// Drafted tokens (rbkv_draft.cu).
+struct DraftArgs {
+  int32_t num_seqs, max_blocks, max_tokens, num_blocks, block_size;
+  const int32_t *q_start, *position, *slot, *table;
+  int32_t *ctx, *free_words, *plan, *status;
+  const int32_t *parent, *tokens, *chosen, *given;
+  int32_t *place, *ancestors, *path, *accepted, *next_token;
+};
+cudaError_t launch_draft_plan(const DraftArgs& a, cudaStream_t st);
+cudaError_t launch_draft_accept(const DraftArgs& a, cudaStream_t st);
+cudaError_t launch_draft_compact(const DraftArgs& a, const ShapeInfo& s, void* k_cache,
+                                 void* v_cache, cudaStream_t st);
 
 cudaError_t launch_step_build(const BuildArgs& a, cudaStream_t st);
 cudaError_t launch_step_release(const BuildArgs& a, const int32_t* done, cudaStream_t st);

@@ -66,7 +66,7 @@ __host__ __device__ constexpr int smem_floats(int D, int rows) {
 
 // kPer: head-dim elements per lane, D = 32 dpl with dpl <= kPer.  kRows: packed
 // rows of a block, 4 or 8.
-template <class T, int kPer, int kRows>
+template <class T, int kPer, int kRows, bool kDraft>
 __global__ void __launch_bounds__(kThreads)
     step_generic_kernel(DevStep ds, ShapeInfo s, const T* __restrict__ q,
                         const T* __restrict__ k_cache, const T* __restrict__ v_cache,
@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     // One 32-key chunk for the rows [ra, rb) of the block; row r sees the keys
-    // below lim0 + (token of r - tok0), or all n.
+    // below lim0 + (token of r - tok0), or all n.  tree >= 0 (drafted tokens): the
+    // keys below it, and those behind it of its ancestors.
     auto chunk = [&](const int32_t* ids, int k0, int n, int ra, int rb, int lim0, int tok0,
-                     bool causal) {
+                     bool causal, int tree) {
       const int key = k0 + lane;
       int64_t off = -1;
       if (key < n) {
@@ -140,7 +141,12 @@ __global__ void __launch_bounds__(kThreads)
       for (int r = 0; r < kRows; ++r) {
         // (other sequences' rows see none of these keys: their terms are 0)
         const int lim = r < ra || r >= rb ? 0 : causal ? lim0 + tok[r] - tok0 : n;
-        const bool sees = off >= 0 && key < lim;
+        bool sees = off >= 0 && key < lim;
+        if constexpr (kDraft) {
+          // (every row's word of the set is requested, wherever the row is used)
+          if (tree >= 0 && k0 + 32 > tree && r >= ra && r < rb)
+            sees = off >= 0 && (key < tree || draft_bit(ds.ancestors[tok[r]], key - tree));
+        }
         const float sc = sees ? x[r] : -INFINITY;
         const float mn = fmaxf(m[r], warp_max(sc));
         // a row with no visible key so far keeps max -inf: its terms are 0
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kThreads)
 
     int c = 0;      // chunks dealt so far
     for (int k0 = 0; k0 < ds.prefix_len; k0 += 32, ++c)
-      if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, 0, 0, false);
+      if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, 0, 0, false, -1);
     for (int ra = 0; ra < rows;) {
       // the rows of one sequence: row0 + ra .. row0 + rb - 1
       const int t = (row0 + ra) / g;
@@ -199,8 +205,9 @@ __global__ void __launch_bounds__(kThreads)
       const int lim0 = e.ctx - e.n_new + info.token + 1;      // keys that token t sees
       const int n = lim0 + (row0 + rb - 1) / g - t;           // and the last one
       const int32_t* table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
+      const int tree = kDraft && e.n_new <= kStepTreeTokens ? e.ctx - e.n_new : -1;
       for (int k0 = 0; k0 < n; k0 += 32, ++c)
-        if (c % stride == mine) chunk(table, k0, n, ra, rb, lim0, t, true);
+        if (c % stride == mine) chunk(table, k0, n, ra, rb, lim0, t, true, tree);
       ra = rb;
     }
 
@@ -310,7 +317,7 @@ size_t step_generic_workspace(const ShapeInfo& s, int32_t max_tokens, int splits
 
 namespace {
 
-template <class T, int kPer, int kRows>
+template <class T, int kPer, int kRows, bool kDraft>
 cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, const void* k_cache,
                         const void* v_cache, void* o, float* part_o, float* part_lse, int splits,
                         int sms, cudaStream_t st) {
@@ -322,7 +329,7 @@ cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, co
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(step_generic_kernel<T, kPer, kRows>,
+    e = cudaFuncSetAttribute(step_generic_kernel<T, kPer, kRows, kDraft>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem_floats(kPer * 32, kRows) * 4);
     if (e != cudaSuccess) return e;
@@ -340,7 +347,7 @@ cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, step_generic_kernel<T, kPer, kRows>, ds, s, (const T*)q,
+  e = cudaLaunchKernelEx(&cfg, step_generic_kernel<T, kPer, kRows, kDraft>, ds, s, (const T*)q,
                          (const T*)k_cache, (const T*)v_cache, (T*)o, part_o, part_lse, splits);
   if (e != cudaSuccess || splits == 1) return e;
   const int64_t warps = (int64_t)ds.max_tokens * s.H_q;
@@ -351,14 +358,14 @@ cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, co
                             (const float*)part_lse, (T*)o, splits);
 }
 
-template <class T>
+template <class T, bool kDraft>
 cudaError_t launch_type(const DevStep& ds, const ShapeInfo& s, const void* q, const void* k_cache,
                         const void* v_cache, void* o, float* po, float* pl, int splits, int sms,
                         cudaStream_t st) {
   const bool few = rows_of(s, ds.max_tokens, sms) == 4;
-  auto fn = s.D <= 64    ? (few ? launch_rows<T, 2, 4> : launch_rows<T, 2, 8>)
-            : s.D <= 128 ? (few ? launch_rows<T, 4, 4> : launch_rows<T, 4, 8>)
-                         : (few ? launch_rows<T, 8, 4> : launch_rows<T, 8, 8>);
+  auto fn = s.D <= 64    ? (few ? launch_rows<T, 2, 4, kDraft> : launch_rows<T, 2, 8, kDraft>)
+            : s.D <= 128 ? (few ? launch_rows<T, 4, 4, kDraft> : launch_rows<T, 4, 8, kDraft>)
+                         : (few ? launch_rows<T, 8, 4, kDraft> : launch_rows<T, 8, 8, kDraft>);
   return fn(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
 }
 
@@ -369,9 +376,10 @@ cudaError_t launch_step_generic(const DevStep& ds, const ShapeInfo& s, const voi
                                 void* workspace, int splits, int sms, cudaStream_t st) {
   float* po = (float*)workspace;
   float* pl = po ? po + (size_t)splits * ds.max_tokens * s.H_q * s.D : nullptr;
-  if (s.dtype == 0)
-    return launch_type<__nv_bfloat16>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
-  return launch_type<float>(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
+  auto fn = s.dtype == 0
+                ? (ds.place ? launch_type<__nv_bfloat16, true> : launch_type<__nv_bfloat16, false>)
+                : (ds.place ? launch_type<float, true> : launch_type<float, false>);
+  return fn(ds, s, q, k_cache, v_cache, o, po, pl, splits, sms, st);
 }
 
 }  // namespace rbkv

@@ -320,8 +320,9 @@ __device__ __forceinline__ void load_q(uint32_t (&qb)[NT][8][2], const Segment& 
 // Moves a group's non-finite values, if there are any, from V (in shared
 // memory) to the accumulators of the rows that see them: lane's rows 8 i + 2
 // (lane % 4) + e, dims 16 t + lane / 4 (+ 8).
-template <int NT>
+template <int NT, bool kDraft>
 __device__ __forceinline__ void add_nonfinite(uint8_t* v, int key0, const int (&lim)[NT][2],
+                                              const uint32_t (&own)[NT][2],
                                               float (&acc)[NT][8][4], int lane) {
   bool any = false;
 #pragma unroll
@@ -341,7 +342,8 @@ __device__ __forceinline__ void add_nonfinite(uint8_t* v, int key0, const int (&
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (key0 + key < lim[i][e]) acc[i][u / 2][(u & 1) * 2 + e] += __uint_as_float(w << 16);
+            if (key0 + key < lim[i][e] || (kDraft && (own[i][e] >> key & 1u)))
+              acc[i][u / 2][(u & 1) * 2 + e] += __uint_as_float(w << 16);
       }
     }
   }
@@ -358,7 +360,7 @@ struct Ring {
 };
 
 // Works through one segment: NT tiles of 8 packed rows.
-template <int NT>
+template <int NT, bool kDraft>
 __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk& walk,
                                             const DevStep& ds, const ShapeInfo& s,
                                             const StepPlan& plan,
@@ -386,7 +388,20 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
     for (int t = 0; t < 8; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
   }
   // keys that every row of the unit sees
-  const int all_see = it.flags & kPrefix ? it.keys : it.keys - it.n_tok + 1;
+  const bool tree = kDraft && !(it.flags & kPrefix);
+  const int seen = it.keys - it.n_tok;
+  const int all_see = it.flags & kPrefix ? it.keys : tree ? seen : seen + 1;
+  if (tree) {
+    // a row that does not follow every token before it sees the cached keys, and
+    // then those of its ancestors
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = (8 * i + c2 + e) / s.g;
+        if (tok < it.n_tok && !draft_is_run(ds, it.row + tok, seen, tok)) lim[i][e] = seen;
+      }
+  }
   // ldmatrix rows of this lane: K as [key][dim] tiles, V transposed
   const int k_key = (lane & 7) + ((lane >> 3) & 1) * 8, k_d = (lane >> 4) * 8;
   const int v_key = (lane & 7) + (lane >> 4) * 8, v_d = ((lane >> 3) & 1) * 8;
@@ -433,6 +448,22 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
       }
     }
     uint32_t pb[NT][2];
+    // bit k: key key0 + k is that of an ancestor (at most 16 tokens: one word; looked
+    // up in the one or two groups that hold them)
+    uint32_t own[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) own[i][0] = own[i][1] = 0;
+    if (tree && key0 + kKeys > seen) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tok = (8 * i + c2 + e) / s.g;
+          const uint32_t w = tok < it.n_tok ? ds.ancestors[it.row + tok].x & 0xffffu : 0u;
+          const int by = key0 - seen;             // -15 .. 15
+          own[i][e] = by >= 0 ? w >> by : w << -by;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -440,8 +471,13 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
         // rows' scores of keys kr and kr + 8, masked; the row's maximum over
         // the eight lanes that share it
         float x = (sc[i][e] + sd[i][e]) * qk_scale, y = (sc[i][2 + e] + sd[i][2 + e]) * qk_scale;
-        x = key0 + kr < lim[i][e] ? x : -INFINITY;
-        y = key0 + kr + 8 < lim[i][e] ? y : -INFINITY;
+        bool sees_x = key0 + kr < lim[i][e], sees_y = key0 + kr + 8 < lim[i][e];
+        if (kDraft) {
+          sees_x |= own[i][e] >> kr & 1u;
+          sees_y |= own[i][e] >> (kr + 8) & 1u;
+        }
+        x = sees_x ? x : -INFINITY;
+        y = sees_y ? y : -INFINITY;
         float top = fmaxf(x, y);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
@@ -469,7 +505,7 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
       pb[i][1] = transpose8(ptx::pack_bf16x2(sc[i][2], sc[i][3]));
     }
     if (key0 + kKeys > all_see && all_see < it.keys)
-      add_nonfinite<NT>(stage + kGroup, key0, lim, acc, lane);
+      add_nonfinite<NT, kDraft>(stage + kGroup, key0, lim, own, acc, lane);
     // O^T += V^T P^T: 8 tiles of 16 head dims
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -538,6 +574,7 @@ __device__ __forceinline__ void run_segment(const Segment& it, Ring& ring, Walk&
   }
 }
 
+template <bool kDraft>
 __global__ void __launch_bounds__(kThreads, 2)
     step_stream_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
                        const __nv_bfloat16* __restrict__ q,
@@ -585,9 +622,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (uint32_t n = 0; n < walk.seg; ++n) {
       const Segment it = ring.segments[n % kSegments];
       if (it.n_tok * shp.g <= 8)
-        run_segment<1>(it, ring, walk, ds, shp, plan, work, ws, q, o, pipe, lane);
+        run_segment<1, kDraft>(it, ring, walk, ds, shp, plan, work, ws, q, o, pipe, lane);
       else
-        run_segment<2>(it, ring, walk, ds, shp, plan, work, ws, q, o, pipe, lane);
+        run_segment<2, kDraft>(it, ring, walk, ds, shp, plan, work, ws, q, o, pipe, lane);
       __syncwarp();
     }
   }
@@ -827,9 +864,11 @@ size_t step_workspace(const ShapeInfo& s, int32_t max_tokens, int sms, void* bas
   return at;
 }
 
-cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
-                               const void* q, const void* k_cache, const void* v_cache, void* o,
-                               bool first, cudaStream_t st) {
+namespace {
+template <bool kDraft>
+cudaError_t launch_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                          const void* q, const void* k_cache, const void* v_cache, void* o,
+                          bool first, cudaStream_t st) {
   cudaError_t e;
   // the shared-memory limit is raised once per device
   static std::atomic<uint64_t> attr_done{0};
@@ -838,10 +877,11 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(step_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes);
+    e = cudaFuncSetAttribute(step_stream_kernel<kDraft>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(step_stream_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(step_stream_kernel<kDraft>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
@@ -856,9 +896,17 @@ cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const Step
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_stream_kernel, ds, s, w, (const __nv_bfloat16*)q,
+  return cudaLaunchKernelEx(&cfg, step_stream_kernel<kDraft>, ds, s, w, (const __nv_bfloat16*)q,
                             (const __nv_bfloat16*)k_cache, (const __nv_bfloat16*)v_cache,
                             (__nv_bfloat16*)o, first ? 1 : 0);
+}
+}  // namespace
+
+cudaError_t launch_step_stream(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                               const void* q, const void* k_cache, const void* v_cache, void* o,
+                               bool first, cudaStream_t st) {
+  return (ds.place ? launch_stream<true> : launch_stream<false>)(ds, s, w, q, k_cache, v_cache, o,
+                                                                 first, st);
 }
 
 cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,

@@ -107,7 +107,7 @@ struct __align__(16) Segment {
   int n;           // its key tiles
   int flags;
   int cuts;        // at a unit's head: CTAs that begin inside the unit behind it
-  int pad;
+  int tree;        // drafted tokens: keys in front of the tree; -1: rows see runs of keys
 };
 static_assert(sizeof(Segment) == 48, "Segment is 12 int32");
 enum { kPrefix = 1, kHead = 2, kWhole = 4 };
@@ -153,6 +153,7 @@ struct Walk {
   int unit;              // tiled sequence
 };
 
+template <bool kDraft>
 __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const ShapeInfo& s,
                                              const StepPlan& plan, const StepWork& work,
                                              int64_t ctas, int tpt, Segment& it) {
@@ -171,6 +172,7 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const S
       it.row = tile * tpt;
       it.n_tok = min(tpt, work.rows - it.row);
       it.pos = ds.prefix_len - 1;
+      it.tree = -1;
       keys = ds.prefix_len;
     } else {
       StepSeq e = plan.tiled[w.unit];
@@ -191,6 +193,7 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const S
       it.row = e.row + tile * tpt;
       it.n_tok = min(tpt, e.n_new - tile * tpt);
       it.pos = seen + tile * tpt;
+      it.tree = kDraft && e.n_new <= kStepTreeTokens ? seen : -1;
       keys = it.pos + it.n_tok;
     }
     // the unit's tiles [first, last) of this segment
@@ -267,6 +270,29 @@ __device__ __noinline__ void hide_keys(uint32_t s_col, const int32_t* table, int
   tmem_wait_st();
 }
 
+// Scores -inf, in tensor memory, of what a drafted row does not see: it sees the
+// tile's first `lim` keys and those whose bits its ancestors' set has (null: none),
+// bit `by` being the tile's first key.  (In tensor memory and not inlined: as a mask
+// over the softmax's registers it spilled 540 bytes, and only a unit's last tile or
+// two need it.)
+__device__ __noinline__ void hide_others(uint32_t s_col, const uint4* set, int by, int lim) {
+  uint32_t own[4];
+  draft_window(set ? *set : make_uint4(0, 0, 0, 0), by, own);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int run = lim - 32 * x;
+    const uint32_t sees = own[x] | (run <= 0 ? 0u : run >= 32 ? ~0u : (1u << run) - 1u);
+    float v[32];
+    tmem_ld32(s_col + 32 * x, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = sees >> c & 1u ? v[c] : -INFINITY;
+    tmem_st32(s_col + 32 * x, v);
+  }
+  tmem_wait_st();
+}
+
+template <bool kDraft>
 __global__ void __launch_bounds__(kThreads, 2)
     step_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
@@ -515,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto publish = [&] {
         if (last) return;
         Segment u;
-        last = !next_segment(walk, ds, shp, plan, work, ctas, tpt, u);
+        last = !next_segment<kDraft>(walk, ds, shp, plan, work, ctas, tpt, u);
         if (lane == 0) {
           bars->segments[n_pub % kSegments] = u;
           ptx::mbar_arrive(&bars->published[n_pub % kSegments]);
@@ -586,8 +612,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (more) write_q(it, 0);
     for (uint32_t k = 0; more && ok; ++k) {
       // the last key this row sees
-      const int pos = it.flags & kPrefix ? it.pos : it.pos + tok;
-      const int all_see = it.pos + 1;        // keys that every row sees
+      int pos = it.flags & kPrefix ? it.pos : it.pos + tok;
+      int all_see = it.pos + 1;              // keys that every row sees
+      if constexpr (kDraft) {
+        if (it.tree >= 0) {
+          all_see = it.tree;
+          if (tok < it.n_tok &&
+              !draft_is_run(ds, it.row + tok, it.tree, it.pos + tok - it.tree))
+            pos = it.tree - 1;               // and then its ancestors
+        }
+      }
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < it.n; ++j) {
         const uint32_t t = tc0 + j;
@@ -609,7 +643,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         // this row sees the tile's first `lim` keys: those <= its position and
         // before the unit's end (a prefix of the key tile, possibly empty or all)
-        const int lim = min(pos + 1, it.ke) - key0;
+        int lim = min(pos + 1, it.ke) - key0;
+        if (kDraft && it.tree >= 0 && key0 + kKeys > it.tree) {
+          hide_others(s_col, pos < it.tree ? ds.ancestors + it.row + tok : nullptr,
+                      key0 - it.tree, lim);
+          lim = kKeys;
+        }
         const bool full = __all_sync(0xffffffffu, lim >= kKeys);
         // the whole row of scores in one round trip (four loads, one wait)
         float sc[128];
@@ -768,7 +807,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int c = 0; c < 128; ++c) ov[c] *= inv;
       if (bars->nonfinite[k & 1] == k + 1) {
         // (written before the last P was reported, so before its product)
-        for (int key = max(it.kb, all_see); key < min(it.ke, pos + 1); ++key) {
+        const int end = kDraft && it.tree >= 0 ? it.ke : min(it.ke, pos + 1);
+        for (int key = max(it.kb, all_see); key < end; ++key) {
+          if (kDraft && key > pos &&
+              (pos >= it.tree || !draft_bit(ds.ancestors[it.row + tok], key - it.tree)))
+            continue;
           const int blk = it.table[key / B];
           if ((uint32_t)blk >= (uint32_t)ds.num_blocks) continue;
           const uint4* src = reinterpret_cast<const uint4*>(
@@ -823,9 +866,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
-cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
-                             const void* q, const void* k_cache, const void* v_cache, void* o,
-                             cudaStream_t st) {
+namespace {
+template <bool kDraft>
+cudaError_t launch(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w, const void* q,
+                   const void* k_cache, const void* v_cache, void* o, cudaStream_t st) {
   const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
   const int box_rows = s.B < kKeys ? s.B : kKeys;
   CUtensorMap tk, tv;
@@ -842,13 +886,14 @@ cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWo
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, step_tile_kernel);
+    e = cudaFuncGetAttributes(&fa, step_tile_kernel<kDraft>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(step_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(step_tile_kernel<kDraft>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kStepTileSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(step_tile_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(step_tile_kernel<kDraft>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
@@ -863,9 +908,16 @@ cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWo
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_tile_kernel, tk, tv, ds, s, w,
+  return cudaLaunchKernelEx(&cfg, step_tile_kernel<kDraft>, tk, tv, ds, s, w,
                             (const __nv_bfloat16*)q, (const __nv_bfloat16*)v_cache,
                             (__nv_bfloat16*)o);
+}
+}  // namespace
+
+cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
+                             const void* q, const void* k_cache, const void* v_cache, void* o,
+                             cudaStream_t st) {
+  return (ds.place ? launch<true> : launch<false>)(ds, s, w, q, k_cache, v_cache, o, st);
 }
 
 }  // namespace rbkv

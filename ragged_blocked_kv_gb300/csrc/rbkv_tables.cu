@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
     plan.header[kPlanTokens] = a.max_tokens;
     plan.header[kPlanMaxBlocks] = a.max_blocks;
     plan.header[kPlanPool] = a.num_blocks;
+    plan.header[kPlanDraft] = 0;
     if (!ok) atomicCAS(a.status, 0, err);
   }
 

@@ -5,7 +5,7 @@ ragged attention).
 DeepSpeed-FastGen paper summary page, idea I1: a pass's latency follows its
 token count; the layer's projections are that token-proportional work.  The
 layer is a Llama-2-7B decoder layer (pre-RMSNorm, QKV and output projections,
-SwiGLU MLP, residuals; rotary embeddings left out), random bf16 weights.
+SwiGLU MLP, residuals; rotary positions where ``rotary`` is given), random bf16 weights.
 
 Weights as stored here: ``w_qkv`` [(H_q + 2 H_kv) D][hidden] (Q rows, then K,
 then V), ``w_o`` [hidden][H_q D], ``w_gu`` [2 ffn][hidden] with the gate and
@@ -64,11 +64,13 @@ class DecoderLayer:
     """One layer's weights and its forward pass over a composed pass."""
 
     def __init__(self, rbkv, weights: dict, num_heads_q: int, num_heads_kv: int, head_dim: int,
-                 eps: float = 1e-5):
+                 eps: float = 1e-5, rotary=None):
+        """``rotary``: an ``rbkv.Rotary`` that turns queries and keys (else none)."""
         self.rbkv = rbkv
         self.w = weights
         self.hq, self.hkv, self.d = num_heads_q, num_heads_kv, head_dim
         self.eps = eps
+        self.rotary = rotary
 
     def buffers(self, max_tokens: int, device: str = "cuda") -> dict:
         """Fixed activation buffers of max_tokens rows (for forward_into)."""
@@ -101,8 +103,8 @@ class DecoderLayer:
 
     def forward_into(self, x, out, buf: dict, attend, rows: int, stream=None) -> None:
         """The layer on the first `rows` rows of fixed buffers: x -> out, with
-        attend(q, k, v, o) running the KV append and attention (a plain pass
-        or a frame); allocates nothing, so it can be captured in a graph."""
+        attend(q, k, v, o) running the KV append (with the rotation, where positions
+        are rotary: self.rotary) and attention (a plain pass or a frame); allocates nothing, so it can be captured in a graph."""
         rb, w = self.rbkv, self.w
         T = rows
         a, h, b, act = buf["a"][:T], buf["h"][:T], buf["b"][:T], buf["act"][:T]
@@ -122,13 +124,18 @@ class DecoderLayer:
     def forward(self, p, x, k_cache, v_cache, workspace=None, stream=None,
                 status=None) -> dict:
         """x: [T][hidden] bf16 for the pass's rows; appends the pass's K and V
-        to the caches and returns the layer's output and intermediates."""
+        to the caches and returns the layer's output and intermediates (with
+        rotary positions the rotated queries, and the keys as projected)."""
         rb, w = self.rbkv, self.w
         T, hidden = x.shape
         a = rb.rmsnorm(x, w["g_attn"], eps=self.eps, stream=stream)
         q, k, v = rb.gemm_qkv(a, w["w_qkv"], self.hq, self.hkv, self.d, status=status,
                               stream=stream)
-        rb.kv_append(p, k, v, k_cache, v_cache, stream=stream)
+        if self.rotary is None:
+            rb.kv_append(p, k, v, k_cache, v_cache, stream=stream)
+        else:
+            rb.kv_append_rotary(p, self.rotary, q, k, v, k_cache, v_cache, q_out=q,
+                                stream=stream)
         o = rb.ragged_attention(p, q, k_cache, v_cache, workspace=workspace, stream=stream)
         h = rb.gemm(o.view(T, self.hq * self.d), w["w_o"], residual=x, epilogue="residual",
                     status=status, stream=stream)
