@@ -641,6 +641,7 @@ typedef struct {
                             row of the d-th kept token of sequence s; -1 elsewhere */
   int32_t* accepted;     /* [num_seqs] out: kept tokens of the step (0 of an idle slot) */
   int32_t* next_token;   /* [num_seqs] out: the token chosen at the last kept one (-1) */
+  int32_t* work;         /* [num_seqs + 1][4] opaque, 16-byte aligned, zero at first */
 } rbkv_step_draft;
 
 /* Plan the trees of the step built last.  parent: [max_tokens], for every row

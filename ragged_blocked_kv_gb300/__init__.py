@@ -79,7 +79,8 @@ class _StepTables(C.Structure):
 
 
 class _StepDraft(C.Structure):
-    _fields_ = [(n, C.c_void_p) for n in ("place", "ancestors", "path", "accepted", "next_token")]
+    _fields_ = [(n, C.c_void_p) for n in ("place", "ancestors", "path", "accepted", "next_token",
+                                          "work")]
 
 
 class _Rotary(C.Structure):
@@ -901,7 +902,7 @@ class StepDraft(_Arrays):
     sequence s; else -1), ``accepted`` and ``next_token`` [num_seqs] the acceptance's.
     """
 
-    _HELD = frozenset(("place", "ancestors", "path", "accepted", "next_token", "tables"))
+    _HELD = frozenset(("place", "ancestors", "path", "accepted", "next_token", "work", "tables"))
 
     def __init__(self, tables: StepTables):
         import torch
@@ -913,8 +914,9 @@ class StepDraft(_Arrays):
         self.place, self.path = full(-1, t.max_tokens), full(-1, t.max_tokens)
         self.ancestors = full(0, t.max_tokens, 4)
         self.accepted, self.next_token = full(0, t.num_seqs), full(-1, t.num_seqs)
+        self.work = full(0, t.num_seqs + 1, 4)
         self._d = C.byref(_StepDraft(*(x.data_ptr() for x in (
-            self.place, self.ancestors, self.path, self.accepted, self.next_token))))
+            self.place, self.ancestors, self.path, self.accepted, self.next_token, self.work))))
         L = lib()
         self._f_plan, self._f_accept = L.rbkv_step_draft_plan, L.rbkv_step_draft_accept
         self._f_compact = L.rbkv_step_draft_compact

@@ -11,7 +11,12 @@
 // Acceptance: from the last given token, the lowest child whose token is the
 // one chosen, until there is none.  (i is a child of c when c is the highest bit
 // of A(i) below i.)  A warp holds a sequence's tree in registers, four tokens to a
-// lane, and a step of the walk is a broadcast, four compares and votes.
+// lane.  Let M be the tokens that are the choice at their parents; then the path
+// holds those tokens that follow the last given one and have no ancestor behind it
+// outside M - all of them at once, in votes.  Only where siblings are alike does
+// that find more than a path (a token on it is then not the parent of the next), and
+// the path is walked, a broadcast, four compares and votes to a step: of 256 trees
+// of up to 60 tokens, chains among them, 15 us, where the votes take 5.
 //
 // Move: kept token d of a sequence lies in the slot of token p_d >= d, and
 // goes to the slot of token d.  p rises, so a row is never written before it has
@@ -36,13 +41,74 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 // Whether the step was built for these tables; else, if it has rows, it is
 // recorded as RBKV_ERR_INVALID.  `stage`: what must have been done to its trees.
+enum { kBuilt, kPlanned, kAccepted };
 __device__ __forceinline__ bool usable(const DraftArgs& a, const StepPlan& plan, int stage) {
   const int32_t* h = plan.header;
+  const StepLanes* done = reinterpret_cast<const StepLanes*>(a.work);
   const bool ok = h[kPlanSeqs] == a.num_seqs && h[kPlanTokens] == a.max_tokens &&
                   h[kPlanMaxBlocks] == a.max_blocks && h[kPlanBlock] == a.block_size &&
-                  h[kPlanPool] == a.num_blocks && h[kPlanDraft] >= stage;
+                  h[kPlanPool] == a.num_blocks &&
+                  (stage < kPlanned || done->single_cum == h[kPlanSerial]) &&
+                  (stage < kAccepted || done->pair_cum == h[kPlanSerial]);
   if (!ok && threadIdx.x == 0 && h[kPlanRows] > 0) atomicCAS(a.status, 0, kDevInvalid);
   return ok;
+}
+
+// The tiled sequences' places on the tile kernel's road: a scan over them, a run of
+// sequences to a thread.
+__device__ __forceinline__ void plan_lanes(const DraftArgs& a, const StepPlan& plan) {
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ int sums[2][kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  StepLanes* out = reinterpret_cast<StepLanes*>(a.work);
+  const int n = plan.header[kPlanTiled], tokens = step_tile_tokens(plan.header[kPlanGroup]);
+  const int per = (n + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  auto lengths = [&](int i, int& single, int& pair) {
+    const StepSeq e = plan.tiled[i];
+    const int seen = e.ctx - e.n_new, pairs = step_pairs(seen, e.n_new, tokens);
+    single = step_singles_len(seen, e.n_new, tokens, pairs);
+    pair = step_pairs_len(seen, e.n_new, tokens, pairs);
+  };
+  int mine[2] = {0, 0}, at[2];
+  for (int i = i0; i < i1; ++i) {
+    int single, pair;
+    lengths(i, single, pair);
+    mine[0] += single;
+    mine[1] += pair;
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    at[x] = mine[x];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int up = __shfl_up_sync(kAll, at[x], off);
+      if (lane >= off) at[x] += up;
+    }
+    if (lane == 31) sums[x][warp] = at[x];
+  }
+  __syncthreads();
+  int total[2] = {0, 0};
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    at[x] -= mine[x];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at[x] += sums[x][w];
+      total[x] += sums[x][w];
+    }
+  }
+  for (int i = i0; i < i1; ++i) {
+    StepLanes e;
+    lengths(i, e.single_len, e.pair_len);
+    e.single_cum = at[0];
+    e.pair_cum = at[1];
+    out[1 + i] = e;
+    at[0] += e.single_len;
+    at[1] += e.pair_len;
+  }
+  const int serial = plan.header[kPlanSerial];
+  if (tid == 0) out[0] = StepLanes{serial, total[0], ~serial, total[1]};
 }
 
 __global__ void __launch_bounds__(kPlanThreads) draft_plan_kernel(DraftArgs a) {
@@ -51,17 +117,21 @@ __global__ void __launch_bounds__(kPlanThreads) draft_plan_kernel(DraftArgs a) {
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(a.plan, a.num_seqs, a.max_tokens);
-  if (!usable(a, plan, 0)) return;
+  if (!usable(a, plan, kBuilt)) return;
   const int tid = threadIdx.x;
-  if (blockIdx.x == 0 && tid == 0) plan.header[kPlanDraft] = kDraftPlanned;
+  if (blockIdx.x == gridDim.x - 1) {      // (one block more than the trees')
+    plan_lanes(a, plan);
+    return;
+  }
+  const int blocks = gridDim.x - 1;
   const int T = plan.header[kPlanRows];
   uint4* sets = reinterpret_cast<uint4*>(a.ancestors);
   for (int64_t r = T + (int64_t)blockIdx.x * kPlanThreads + tid; r < a.max_tokens;
-       r += (int64_t)gridDim.x * kPlanThreads) {
+       r += (int64_t)blocks * kPlanThreads) {
     a.place[r] = -1;
     sets[r] = make_uint4(0, 0, 0, 0);
   }
-  for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+  for (int s = blockIdx.x; s < a.num_seqs; s += blocks) {
     const int q0 = a.q_start[s], n = a.q_start[s + 1] - q0;
     if (n == 0) continue;
     const int seen = a.position[q0];
@@ -125,9 +195,10 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) draft_accept_kernel(DraftAr
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(a.plan, a.num_seqs, a.max_tokens);
-  if (!usable(a, plan, kDraftPlanned)) return;
+  if (!usable(a, plan, kPlanned)) return;
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0) plan.header[kPlanDraft] = kDraftAccepted;
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    reinterpret_cast<StepLanes*>(a.work)->pair_cum = plan.header[kPlanSerial];
   const int T = plan.header[kPlanRows];
   for (int64_t r = T + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.max_tokens;
        r += (int64_t)gridDim.x * blockDim.x)
@@ -152,43 +223,107 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) draft_accept_kernel(DraftAr
     if (n <= kNodes) {
       // token lane + 32 x of the tree, its parent, and the token chosen there
       int parent[4], token[4], chosen[4], path[4];
+      uint4 set[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int i = lane + 32 * x;
         parent[x] = -1;
         token[x] = chosen[x] = 0;
         path[x] = i;
+        set[x] = make_uint4(0, 0, 0, 0);
         if (i < n) {
-          parent[x] = parent_of(reinterpret_cast<const uint4*>(a.ancestors)[q0 + i], i);
+          set[x] = reinterpret_cast<const uint4*>(a.ancestors)[q0 + i];
+          parent[x] = parent_of(set[x], i);
           token[x] = a.tokens[q0 + i];
           chosen[x] = a.chosen[q0 + i];
         }
       }
-      while (true) {
-        int want = chosen[0];
-#pragma unroll
-        for (int x = 1; x < 4; ++x)
-          if ((cur >> 5) == x) want = chosen[x];
-        want = __shfl_sync(kAll, want, cur & 31);
-        next = want;
-        int child = -1;
-#pragma unroll
-        for (int x = 3; x >= 0; --x) {
-          if (32 * x >= n) continue;
-          const uint32_t v = __ballot_sync(kAll, parent[x] == cur && token[x] == want);
-          if (v) child = 32 * x + __ffs(v) - 1;
-        }
-        if (child < 0) break;
-        cur = child;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (lane + 32 * x == kept) path[x] = child;
-        ++kept;
-      }
+      // M, and the path
+      const int words = (n + 31) >> 5;
+      uint32_t good[4], on[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int i = lane + 32 * x;
-        if (i < n) a.path[q0 + i] = i < kept ? q0 + path[x] : -1;
+        good[x] = on[x] = 0;
+        if (x >= words) continue;
+        int want = 0;
+#pragma unroll
+        for (int y = 0; y <= x; ++y) {
+          const int c = __shfl_sync(kAll, chosen[y], parent[x] & 31);
+          if ((parent[x] >> 5) == y) want = c;
+        }
+        good[x] = __ballot_sync(kAll, parent[x] >= 0 && token[x] == want);
+      }
+      int before = cur;                  // the path's last token so far
+      bool single = true;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (x >= words) continue;
+        const uint32_t w[4] = {set[x].x, set[x].y, set[x].z, set[x].w};
+        bool follows = false, all = true;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int from = given - 32 * y;         // bits of this word that are given
+          const uint32_t behind = from <= 0 ? kAll : from >= 32 ? 0u : kAll << from;
+          if ((cur >> 5) == y) follows = w[y] >> (cur & 31) & 1u;
+          all &= (w[y] & behind & ~good[y]) == 0;
+        }
+        on[x] = __ballot_sync(kAll, lane + 32 * x >= given && follows && all);
+        // each token's parent has to be the one before it
+        const uint32_t below = on[x] & ((1u << lane) - 1u);
+        const int last = below ? 32 * x + 31 - __clz(below) : before;
+        single &= !(on[x] >> lane & 1u) || parent[x] == last;
+        if (on[x]) before = 32 * x + 31 - __clz(on[x]);
+      }
+      if (__all_sync(kAll, single)) {
+        // token i of the path's tokens goes to place kept + its rank among them
+        int rank = given;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (x >= words) continue;
+          if (lane + 32 * x < given) a.path[q0 + lane + 32 * x] = q0 + lane + 32 * x;
+          if (on[x] >> lane & 1u)
+            a.path[q0 + rank + __popc(on[x] & ((1u << lane) - 1u))] = q0 + lane + 32 * x;
+          rank += __popc(on[x]);
+        }
+        kept = rank;
+        cur = before;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = lane + 32 * x;
+          if (i >= kept && i < n) a.path[q0 + i] = -1;
+        }
+        next = chosen[0];
+#pragma unroll
+        for (int x = 1; x < 4; ++x)
+          if ((cur >> 5) == x) next = chosen[x];
+        next = __shfl_sync(kAll, next, cur & 31);
+      } else {
+        while (true) {
+          int want = chosen[0];
+#pragma unroll
+          for (int x = 1; x < 4; ++x)
+            if ((cur >> 5) == x) want = chosen[x];
+          want = __shfl_sync(kAll, want, cur & 31);
+          next = want;
+          int child = -1;
+#pragma unroll
+          for (int x = 3; x >= 0; --x) {
+            if (32 * x >= n) continue;
+            const uint32_t v = __ballot_sync(kAll, parent[x] == cur && token[x] == want);
+            if (v) child = 32 * x + __ffs(v) - 1;
+          }
+          if (child < 0) break;
+          cur = child;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (lane + 32 * x == kept) path[x] = child;
+          ++kept;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = lane + 32 * x;
+          if (i < n) a.path[q0 + i] = i < kept ? q0 + path[x] : -1;
+        }
       }
     } else {
       // a chain: up to the first token that is not the one chosen before it
@@ -233,7 +368,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   ptx::pdl_wait_previous();
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(a.plan, a.num_seqs, a.max_tokens);
-  if (!usable(a, plan, kDraftAccepted)) return;
+  if (!usable(a, plan, kAccepted)) return;
   const int lane = threadIdx.x & 31;
   const int per = H_kv * vec_per_row;
   const int column = blockIdx.x * kMoveThreads + threadIdx.x;
@@ -305,7 +440,7 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t
 
 cudaError_t launch_draft_plan(const DraftArgs& a, cudaStream_t st) {
   const int blocks = std::min(a.num_seqs, 1 << 16);
-  return launch(draft_plan_kernel, dim3((unsigned)blocks), kPlanThreads, st, a);
+  return launch(draft_plan_kernel, dim3((unsigned)blocks + 1), kPlanThreads, st, a);
 }
 
 cudaError_t launch_draft_accept(const DraftArgs& a, cudaStream_t st) {

@@ -1240,7 +1240,9 @@ rbkv_status read_device_status(void* dev, cudaStream_t st) {
     return fail(RBKV_ERR_WORKSPACE, "the step exceeds max_tokens or max_blocks of its tables");
   if (word == RBKV_ERR_INVALID)
     return fail(RBKV_ERR_INVALID, "the step has a negative length, or was built for another "
-                                  "configuration or for tables of other sizes");
+                                  "configuration or for tables of other sizes; or a tree or a "
+                                  "count of given tokens is out of range, or a draft was used "
+                                  "before its plan or its acceptance");
   if (word == kDevTimeout)
     return fail(RBKV_ERR_TIMEOUT, "a bounded device wait gave up (site " + std::to_string(words[1]) +
                                       ", index " + std::to_string(words[2]) + ", block " +

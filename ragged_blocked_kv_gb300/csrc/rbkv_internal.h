@@ -117,8 +117,8 @@ struct DevPass {
   const int32_t* counts;
   // A step built on the device (rbkv_step_*): {block size, rows of its arrays}
   // that it was built for, to be compared with what it is used with; and for
-  // drafted tokens whether their trees were planned.  Null otherwise.
-  const int32_t* built_for[3];
+  // drafted tokens the serials of the build and of their plan.  Null otherwise.
+  const int32_t* built_for[4];
 };
 
 enum { kCountTokens = 0, kCountDecode = 1, kCountGeneric = 2, kCountChunk = 3, kCountCombine = 4 };

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x;
   if (dp.built_for[0] &&
       (*dp.built_for[0] != h.block || *dp.built_for[1] != dp.num_tokens ||
-       (dp.built_for[2] && *dp.built_for[2] == 0))) {
+       (dp.built_for[2] && *dp.built_for[2] != *dp.built_for[3]))) {
     if (tid == 0 && rows > 0) atomicCAS(dp.status, 0, kDevInvalid);
     return;
   }

@@ -109,9 +109,10 @@ rbkv_status check_draft(const rbkv_config* c, const rbkv_step_tables* t,
   rbkv_status st = check_tables(c, t);
   if (st != RBKV_OK) return st;
   if (!d) return invalid("draft is NULL");
-  if (!d->place || !d->ancestors || !d->path || !d->accepted || !d->next_token)
+  if (!d->place || !d->ancestors || !d->path || !d->accepted || !d->next_token || !d->work)
     return invalid("NULL draft array");
-  if (!aligned(d->ancestors, 16)) return invalid("ancestors must be 16-byte aligned");
+  if (!aligned(d->ancestors, 16) || !aligned(d->work, 16))
+    return invalid("ancestors and work must be 16-byte aligned");
   if (!aligned(d->place, 4) || !aligned(d->path, 4) || !aligned(d->accepted, 4) ||
       !aligned(d->next_token, 4))
     return invalid("draft arrays must be 4-byte aligned");
@@ -138,6 +139,7 @@ DraftArgs draft_args(const rbkv_config* c, const rbkv_step_tables* t, const rbkv
   a.path = d->path;
   a.accepted = d->accepted;
   a.next_token = d->next_token;
+  a.work = d->work;
   return a;
 }
 
@@ -148,7 +150,8 @@ bool written_by_draft(const rbkv_config* c, const rbkv_step_tables* t, const rbk
   const int64_t S = t->num_seqs, T = t->max_tokens;
   return written_by_build(t, c->num_blocks, p, n, nullptr) || overlap(p, 4 * n, d->place, 4 * T) ||
          overlap(p, 4 * n, d->ancestors, 16 * T) || overlap(p, 4 * n, d->path, 4 * T) ||
-         overlap(p, 4 * n, d->accepted, 4 * S) || overlap(p, 4 * n, d->next_token, 4 * S);
+         overlap(p, 4 * n, d->accepted, 4 * S) || overlap(p, 4 * n, d->next_token, 4 * S) ||
+         overlap(p, 4 * n, d->work, 16 * (S + 1));
 }
 
 DevPass append_pass(const rbkv_config* c, const rbkv_step_tables* t) {
@@ -195,12 +198,14 @@ rbkv_status step_attention(const rbkv_config* cfg, const rbkv_step_tables* t,
   if (d) {
     ds.place = d->place;
     ds.ancestors = (const uint4*)d->ancestors;
+    ds.work = (const StepLanes*)d->work;
   }
   const ShapeInfo s = shape(cfg);
   const int64_t T = t->max_tokens;
   const int64_t q_bytes = T * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
   if (overlap(q, q_bytes, o, q_bytes)) return invalid("o overlaps q");
-  if (d && (overlap(o, q_bytes, d->place, 4 * T) || overlap(o, q_bytes, d->ancestors, 16 * T)))
+  if (d && (overlap(o, q_bytes, d->place, 4 * T) || overlap(o, q_bytes, d->ancestors, 16 * T) ||
+            overlap(o, q_bytes, d->work, 16 * ((int64_t)t->num_seqs + 1))))
     return invalid("o overlaps the drafted tokens' arrays");
   const cudaStream_t cs = (cudaStream_t)stream;
   int sms = 0;
@@ -212,8 +217,10 @@ rbkv_status step_attention(const rbkv_config* cfg, const rbkv_step_tables* t,
   if (need > 0 && (overlap(workspace, (int64_t)need, q, q_bytes) ||
                    overlap(workspace, (int64_t)need, o, q_bytes)))
     return invalid("workspace overlaps q or o");
-  if (d && need > 0 && (overlap(workspace, (int64_t)need, d->place, 4 * T) ||
-                        overlap(workspace, (int64_t)need, d->ancestors, 16 * T)))
+  if (d && need > 0 &&
+      (overlap(workspace, (int64_t)need, d->place, 4 * T) ||
+       overlap(workspace, (int64_t)need, d->ancestors, 16 * T) ||
+       overlap(workspace, (int64_t)need, d->work, 16 * ((int64_t)t->num_seqs + 1))))
     return invalid("workspace overlaps the drafted tokens' arrays");
   if (!step_fast_supported(s)) {
     const int splits = step_generic_splits(s, t->max_tokens, t->max_blocks, prefix_len, sms);
@@ -356,12 +363,13 @@ rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tabl
   const int64_t q_bytes = T * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
   if (overlap(q_out, q_bytes, t->slot, 4 * T) || overlap(q_out, q_bytes, t->position, 4 * T) ||
       overlap(q_out, q_bytes, t->plan, 4 * step_plan_ints(t->num_seqs, T)) ||
-      (d && overlap(q_out, q_bytes, d->place, 4 * T)))
+      (d && (overlap(q_out, q_bytes, d->place, 4 * T) || overlap(q_out, q_bytes, d->work, 16))))
     return invalid("q_out overlaps an array that the call reads");
   DevPass dp = append_pass(cfg, t);
   if (d) {
     dp.position = d->place;
-    dp.built_for[2] = t->plan + kPlanDraft;
+    dp.built_for[2] = t->plan + kPlanSerial;
+    dp.built_for[3] = d->work;
   }
   cudaError_t e = launch_append_rotary(dp, s, *rotary, prefix_len, q, q_out, k_new, v_new, k_cache,
                                        v_cache, (cudaStream_t)stream, true);

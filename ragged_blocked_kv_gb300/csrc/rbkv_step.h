@@ -27,6 +27,8 @@ constexpr int kStepTileSmem = 4 * 32768 + 1024;
 // key tiles of its kernel, for the even cut of the work over the CTAs.
 constexpr int kStepStreamUnit = 3;
 constexpr int kStepTileUnit = 5;
+// Key tiles of a sequence from which on its query tiles are walked in pairs.
+constexpr int kStepPairTiles = 8;
 
 // Header words of the plan.
 enum {
@@ -43,10 +45,9 @@ enum {
   kPlanTokens = 8,
   kPlanMaxBlocks = 9,
   kPlanPool = 10,       // blocks of the pool
-  kPlanDraft = 11,      // what has been done to the step's drafted tokens since the build
+  kPlanSerial = 11,     // builds so far
   kPlanHeader = 16
 };
-enum { kDraftPlanned = 1, kDraftAccepted = 2 };
 
 // A sequence of a kernel's work list.  cum: line length before it, for one KV
 // head; tiles: 16-key tiles (streamed) or line length (tiled).
@@ -140,6 +141,53 @@ __host__ __device__ __forceinline__ int64_t step_seq_len(int32_t seen, int32_t n
          step_key_tiles(seen, n_new, tokens, tiles - 1) + kStepTileUnit;
 }
 
+// Drafted tokens: where a tiled sequence's units lie on the tile kernel's road.
+//
+// Query tiles of one sequence and KV head read the same keys, and one after the
+// other on the line above they read them again from HBM: between two reads of a
+// key lies what all CTAs read in the time of a unit (a tree of 64 tokens in groups
+// of 4 behind 32768 keys: 260 MB for 137).  So two neighbouring query tiles are a
+// pair, walked side by side by a pair of CTAs.  The road has one place for a step
+// of both lanes: first, two to a place, the steps of units of one tile (over the
+// prefix, and a sequence's last tile where their number is odd), then those of the
+// pairs, as long as the second tile's.  A pair of CTAs takes an even cut of it;
+// of the single units' steps in its part the first CTA walks the first half.
+// (Entry 0 of the list holds the totals as lengths, the serial of the build that
+// the trees were planned for as single_cum, and of the one whose paths were taken
+// as pair_cum.)
+struct __align__(16) StepLanes {
+  int32_t single_cum, single_len;     // for one KV head, as StepSeq's
+  int32_t pair_cum, pair_len;
+};
+static_assert(sizeof(StepLanes) == 16, "StepLanes is 4 int32");
+
+// Pairs of a sequence, and their places and the steps of its other units, for one
+// KV head.  Tiles of few keys are left single: what a unit reads is then still in
+// the L2 when the next one does.
+__host__ __device__ __forceinline__ int32_t step_pairs(int32_t seen, int32_t n_new,
+                                                       int32_t tokens) {
+  const int32_t tiles = (int32_t)(((int64_t)n_new + tokens - 1) / tokens);
+  return step_key_tiles(seen, n_new, tokens, tiles - 1) >= kStepPairTiles ? tiles / 2 : 0;
+}
+__host__ __device__ __forceinline__ int32_t step_singles_len(int32_t seen, int32_t n_new,
+                                                             int32_t tokens, int32_t pairs) {
+  const int32_t tiles = (int32_t)(((int64_t)n_new + tokens - 1) / tokens);
+  if (pairs == 0) return step_seq_len(seen, n_new, tokens);
+  return tiles & 1 ? step_key_tiles(seen, n_new, tokens, tiles - 1) + kStepTileUnit : 0;
+}
+__host__ __device__ __forceinline__ int32_t step_pairs_len(int32_t seen, int32_t n_new,
+                                                           int32_t tokens, int32_t pairs) {
+  if (pairs == 0) return 0;
+  // every pair before the last is whole
+  return (int32_t)(floor_sum(pairs - 1, kStepTileKeys, 2 * tokens,
+                             (int64_t)seen + 2 * tokens + kStepTileKeys - 1) +
+                   step_key_tiles(seen, n_new, tokens, 2 * pairs - 1) +
+                   (int64_t)pairs * kStepTileUnit);
+}
+
+// A unit's spills are every CTA's that follows, or every other one's.
+constexpr int32_t kSpillsApart = 1 << 30;
+
 // What the kernels of a step see.
 struct DevStep {
   int32_t num_seqs, max_blocks, max_tokens, num_blocks;
@@ -153,6 +201,7 @@ struct DevStep {
   // drafted tokens (null: every row sees its sequence's earlier ones)
   const int32_t* place;         // [max_tokens]
   const uint4* ancestors;       // [max_tokens]
+  const StepLanes* work;        // [num_seqs + 1]: totals, then the tiled sequences
 };
 
 // Work is cut evenly over the CTAs of a persistent grid.  A kernel's units lie
@@ -198,11 +247,12 @@ __device__ __forceinline__ bool step_matches(const DevStep& ds, const ShapeInfo&
                     kPlanMaxBlocks == 9, "the header's second and third vector");
   const int4 b = *reinterpret_cast<const int4*>(plan.header + 4);
   const int2 c = *reinterpret_cast<const int2*>(plan.header + 8);
-  // (drafted tokens whose trees have not been planned since the build)
-  if (ds.place && plan.header[kPlanDraft] == 0) return false;
+  // (drafted tokens: whether their trees were planned for this build)
+  int32_t stale = 0;
+  if (ds.place) stale = ds.work[0].single_cum ^ plan.header[kPlanSerial];
   // (no short cuts: all of it in one round trip)
   return ((b.y ^ s.g) | (b.z ^ s.B) | (b.w ^ ds.num_seqs) | (c.x ^ ds.max_tokens) |
-          (c.y ^ ds.max_blocks)) == 0;
+          (c.y ^ ds.max_blocks) | stale) == 0;
 }
 // The step's rows; 0, and RBKV_ERR_INVALID in the status words, where it was
 // built for something else.  (The tile and the streaming kernel leave the report
@@ -373,7 +423,7 @@ struct DraftArgs {
   const int32_t *q_start, *position, *slot, *table;
   int32_t *ctx, *free_words, *plan, *status;
   const int32_t *parent, *tokens, *chosen, *given;
-  int32_t *place, *ancestors, *path, *accepted, *next_token;
+  int32_t *place, *ancestors, *path, *accepted, *next_token, *work;
 };
 cudaError_t launch_draft_plan(const DraftArgs& a, cudaStream_t st);
 cudaError_t launch_draft_accept(const DraftArgs& a, cudaStream_t st);

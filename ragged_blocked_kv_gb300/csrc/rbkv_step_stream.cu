@@ -701,7 +701,7 @@ __device__ __forceinline__ int bounded(const Spills& s, int rows) {
   return s.first >= 0 && s.first <= rows && s.n > 0 && s.n <= rows - s.first ? s.n : 0;
 }
 
-template <int W, int V>
+template <int W, int V, bool kDraft>
 __global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : kJoinBlocks)
     step_combine_kernel(DevStep ds, ShapeInfo shp, StepWorkspace ws,
                         __nv_bfloat16* __restrict__ o) {
@@ -749,6 +749,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : kJoinBlocks)
     a = ws.own_cut[(int64_t)(t - own_in) * shp.H_kv + kvh];
     // (after a wait that gave up, a unit's Spills may not have been written:
     // nothing outside the spill rows is read then either)
+    int apart = 1;           // (CTAs from one spill of a unit to the next)
+    if constexpr (kDraft) {
+      if (a.n & kSpillsApart) {
+        apart = 2;
+        a.n &= ~kSpillsApart;
+        // (the last one's place, as below)
+        if (a.n > 0 && 2 * a.n - 1 > ws.tile_grid - a.first) a.n = 0;
+      }
+    }
     a.n = bounded(a, r.unit >= 0 ? ws.stream_grid * kStepPipes : ws.tile_grid);
     p.n = bounded(p, pre_streamed ? ws.stream_grid * kStepPipes : ws.tile_grid);
     Join<V> j;
@@ -763,7 +772,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : kJoinBlocks)
           ? Part{ws.stream_o, ws.stream_lse, a.first * kStepPackedRows + own_in * g + hh,
                  kStepPackedRows}
           : Part{ws.tile_o, ws.tile_lse, a.first * kStepTileRows + own_in * g + hh,
-                 kStepTileRows};
+                 kStepTileRows * apart};
       const Part theirs = pre_streamed
           ? Part{ws.stream_o, ws.stream_lse, p.first * kStepPackedRows + pre_in * g + hh,
                  kStepPackedRows}
@@ -927,9 +936,12 @@ cudaError_t launch_step_combine(const DevStep& ds, const ShapeInfo& s, const Ste
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = wide  ? step_combine_kernel<kJoinWarps, 1>
-                : few ? step_combine_kernel<1, 1>
-                      : step_combine_kernel<1, kJoinVecs>;
+  auto kernel = ds.place ? (wide  ? step_combine_kernel<kJoinWarps, 1, true>
+                            : few ? step_combine_kernel<1, 1, true>
+                                  : step_combine_kernel<1, kJoinVecs, true>)
+                         : (wide  ? step_combine_kernel<kJoinWarps, 1, false>
+                            : few ? step_combine_kernel<1, 1, false>
+                                  : step_combine_kernel<1, kJoinVecs, false>);
   return cudaLaunchKernelEx(&cfg, kernel, ds, s, w, (__nv_bfloat16*)o);
 }
 

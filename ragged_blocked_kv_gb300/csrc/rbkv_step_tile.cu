@@ -112,6 +112,35 @@ struct __align__(16) Segment {
 static_assert(sizeof(Segment) == 48, "Segment is 12 int32");
 enum { kPrefix = 1, kHead = 2, kWhole = 4 };
 
+// Drafted tokens: the road of the step (see StepLanes), and a CTA's walk over its
+// lane of its pair's part: single units' steps [x, end), then pairs' places [px, pend).
+struct Road {
+  int64_t single, half, total, pairs;      // steps of single units, their places, all; CTA pairs
+  __device__ __forceinline__ int64_t cut(int64_t i) const { return step_cut(i, total, pairs); }
+  // where the single units' steps of CTA c begin
+  __device__ __forceinline__ int64_t begin(int c) const {
+    const int64_t u = min(cut(c >> 1), half);
+    return c & 1 ? u + min(cut((c >> 1) + 1), half) : 2 * u;
+  }
+};
+struct LaneWalk {
+  int64_t x, end, px, pend;
+  int unit;                  // tiled sequence, and its entries
+  bool in_pairs;
+  StepLanes lanes;
+  StepSeq seq;
+};
+
+// What a lane's walk needs, in shared memory, where one thread walks.  (In registers
+// it spilled what the warp needs for reporting landed tiles.)
+struct Lane {
+  DevStep ds;
+  ShapeInfo s;
+  StepWork work;
+  Road road;
+  LaneWalk walk;
+};
+
 // Each barrier is waited on in order of its phases and can never run two
 // phases ahead of a waiter (the parity of a wait is then unambiguous).
 struct Bars {
@@ -127,6 +156,7 @@ struct Bars {
   Segment segments[kSegments];
   uint32_t tmem_base;
   int abort_flag;
+  Lane lane;                      // drafted tokens
   // a block id outside the pool has been met (set before its K tile lands)
   volatile int missing;
   // k + 1 of the last segment k that held non-finite values of keys which some
@@ -172,7 +202,7 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const S
       it.row = tile * tpt;
       it.n_tok = min(tpt, work.rows - it.row);
       it.pos = ds.prefix_len - 1;
-      it.tree = -1;
+      if (kDraft) it.tree = -1;
       keys = ds.prefix_len;
     } else {
       StepSeq e = plan.tiled[w.unit];
@@ -193,7 +223,7 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const S
       it.row = e.row + tile * tpt;
       it.n_tok = min(tpt, e.n_new - tile * tpt);
       it.pos = seen + tile * tpt;
-      it.tree = kDraft && e.n_new <= kStepTreeTokens ? seen : -1;
+      if (kDraft) it.tree = e.n_new <= kStepTreeTokens ? seen : -1;
       keys = it.pos + it.n_tok;
     }
     // the unit's tiles [first, last) of this segment
@@ -212,6 +242,170 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DevStep& ds, const S
     if (first == 0 && last < n)
       it.cuts = (int)step_div(w.x * ctas + work.tile_total - 1, work.tile_total) -
                 ((int)blockIdx.x + 1);
+    return true;
+  }
+  it.n = 0;
+  return false;
+}
+
+__device__ __forceinline__ Road draft_road(const DevStep& ds, const ShapeInfo& s,
+                                           const StepWork& work) {
+  const StepLanes all = ds.work[0];
+  Road r;
+  r.single = work.tile_prefix + (int64_t)s.H_kv * all.single_len;
+  r.half = (r.single + 1) / 2;
+  r.total = r.half + (int64_t)s.H_kv * all.pair_len;
+  r.pairs = min((int64_t)gridDim.x / 2, r.total);
+  return r;
+}
+// The last of the tiled sequences whose place is at or before v.
+template <class F>
+__device__ __forceinline__ int last_at(int n, int64_t v, F cum) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum(mid) <= v) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void enter_unit(LaneWalk& w, const DevStep& ds, const StepPlan& plan,
+                                           int unit) {
+  w.unit = unit;
+  w.lanes = ds.work[1 + unit];
+  w.seq = plan.tiled[unit];
+}
+
+__device__ __forceinline__ void start_lane(Lane* lane) {
+  LaneWalk& w = lane->walk;
+  const DevStep& ds = lane->ds;
+  const ShapeInfo& s = lane->s;
+  const StepWork& work = lane->work;
+  const Road& road = lane->road;
+  const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+  const int c = (int)blockIdx.x, n = plan.header[kPlanTiled];
+  w.x = road.begin(c);
+  w.end = min(road.begin(c + 1), road.single);
+  w.px = max(road.cut(c >> 1), road.half) - road.half;
+  w.pend = max(road.cut((c >> 1) + 1), road.half) - road.half;
+  w.unit = -1;
+  w.in_pairs = false;
+  const StepLanes* lanes = ds.work + 1;
+  if (w.end > max(w.x, work.tile_prefix))
+    enter_unit(w, ds, plan,
+               last_at(n, step_div(max(w.x - work.tile_prefix, (int64_t)0), s.H_kv),
+                       [&](int i) { return lanes[i].single_cum; }));
+}
+
+__device__ __forceinline__ bool next_segment(Lane* lane, Segment* to) {
+  LaneWalk& w = lane->walk;
+  const DevStep& ds = lane->ds;
+  const ShapeInfo& s = lane->s;
+  const StepWork& work = lane->work;
+  const Road& road = lane->road;
+  const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+  const int tpt = step_tile_tokens(s.g);
+  Segment& it = *to;
+  // a query tile of a tiled sequence; returns its key tiles
+  auto own_tile = [&](int tile) -> int {
+    const StepSeq& e = w.seq;
+    const int seen = e.ctx - e.n_new;
+    it.flags = 0;
+    it.table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
+    it.row = e.row + tile * tpt;
+    it.n_tok = min(tpt, e.n_new - tile * tpt);
+    it.pos = seen + tile * tpt;
+    it.tree = e.n_new <= kStepTreeTokens ? seen : -1;
+    it.ke = it.pos + it.n_tok;
+    return step_key_tiles(seen, e.n_new, tpt, tile);
+  };
+  // its key tiles [first, last) of n for this segment
+  auto publish = [&](int first, int last, int n) {
+    it.flags |= (first == 0 ? kHead : 0) | (first == 0 && last == n ? kWhole : 0);
+    it.kb = first * kKeys;
+    it.ke = (int)min((int64_t)it.ke, (int64_t)last * kKeys);
+    it.n = last - first;
+    it.cuts = 0;
+  };
+  auto clamp = [](int64_t v, int n) { return (int)(v < 0 ? 0 : v < n ? v : n); };
+  while (w.x < w.end) {
+    int n;
+    int64_t unit0;
+    if (w.x < work.tile_prefix) {
+      n = work.prefix_tile_steps;
+      const int64_t unit = step_div(w.x, n + kStepTileUnit);
+      unit0 = unit * (n + kStepTileUnit);
+      it.kv_head = (int)step_div(unit, work.prefix_rows);
+      const int tile = (int)(unit - (int64_t)it.kv_head * work.prefix_rows);
+      it.flags = kPrefix;
+      it.table = ds.prefix_table;
+      it.row = tile * tpt;
+      it.n_tok = min(tpt, work.rows - it.row);
+      it.pos = ds.prefix_len - 1;
+      it.tree = -1;
+      it.ke = ds.prefix_len;
+    } else {
+      const int64_t v = w.x - work.tile_prefix;
+      while (v >= (int64_t)s.H_kv * ((int64_t)w.lanes.single_cum + w.lanes.single_len))
+        enter_unit(w, ds, plan, w.unit + 1);
+      const int64_t base = (int64_t)s.H_kv * w.lanes.single_cum;
+      it.kv_head = (int)step_div(v - base, w.lanes.single_len);
+      unit0 = work.tile_prefix + base + (int64_t)it.kv_head * w.lanes.single_len;
+      const int seen = w.seq.ctx - w.seq.n_new;
+      int tile = 2 * step_pairs(seen, w.seq.n_new, tpt);
+      n = step_key_tiles(seen, w.seq.n_new, tpt, tile);
+      while (w.x - unit0 >= n + kStepTileUnit) {
+        unit0 += n + kStepTileUnit;
+        n = step_key_tiles(seen, w.seq.n_new, tpt, ++tile);
+      }
+      own_tile(tile);
+    }
+    const int64_t key0 = unit0 + kStepTileUnit;
+    const int first = clamp(w.x - key0, n), last = clamp(w.end - key0, n);
+    w.x = key0 + n;
+    if (first >= last) continue;
+    publish(first, last, n);
+    if (first == 0 && last < n) {
+      // CTAs that begin in front of the unit's end: the first that does not
+      int lo = (int)blockIdx.x + 1, hi = 2 * (int)road.pairs;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (road.begin(mid) >= w.x) hi = mid;
+        else lo = mid + 1;
+      }
+      it.cuts = lo - ((int)blockIdx.x + 1);
+    }
+    return true;
+  }
+  while (w.px < w.pend) {
+    if (!w.in_pairs) {
+      w.in_pairs = true;
+      enter_unit(w, ds, plan, last_at(plan.header[kPlanTiled], step_div(w.px, s.H_kv),
+                                      [&](int i) { return ds.work[1 + i].pair_cum; }));
+    }
+    while (w.px >= (int64_t)s.H_kv * ((int64_t)w.lanes.pair_cum + w.lanes.pair_len))
+      enter_unit(w, ds, plan, w.unit + 1);
+    const int64_t base = (int64_t)s.H_kv * w.lanes.pair_cum;
+    it.kv_head = (int)step_div(w.px - base, w.lanes.pair_len);
+    int64_t unit0 = base + (int64_t)it.kv_head * w.lanes.pair_len;
+    const int seen = w.seq.ctx - w.seq.n_new;
+    int pair = 0, both = step_key_tiles(seen, w.seq.n_new, tpt, 1);
+    while (w.px - unit0 >= both + kStepTileUnit) {
+      unit0 += both + kStepTileUnit;
+      both = step_key_tiles(seen, w.seq.n_new, tpt, 2 * ++pair + 1);
+    }
+    // (the first tile of a pair may have fewer keys: its lane is empty behind them)
+    const int n = own_tile(2 * pair + ((int)blockIdx.x & 1));
+    const int64_t key0 = unit0 + kStepTileUnit;
+    const int first = clamp(w.px - key0, n), last = clamp(w.pend - key0, n);
+    w.px = key0 + both;
+    if (first >= last) continue;
+    publish(first, last, n);
+    // pairs that begin in front of this tile's end
+    if (first == 0 && last < n)
+      it.cuts = ((int)step_div((key0 + n + road.half) * road.pairs + road.total - 1, road.total) -
+                 (((int)blockIdx.x >> 1) + 1)) | kSpillsApart;
     return true;
   }
   it.n = 0;
@@ -292,7 +486,8 @@ __device__ __noinline__ void hide_others(uint32_t s_col, const uint4* set, int b
   tmem_wait_st();
 }
 
-template <bool kDraft>
+// kDraft: drafted tokens; kLanes: with a road of lanes.
+template <bool kDraft, bool kLanes>
 __global__ void __launch_bounds__(kThreads, 2)
     step_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, DevStep ds, ShapeInfo shp,
@@ -303,7 +498,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int64_t ctas = step_matches(ds, shp, plan) ? min((int64_t)gridDim.x, work.tile_total) : 0;
+  const int64_t ctas = !step_matches(ds, shp, plan) ? 0
+                       : kLanes ? 2 * draft_road(ds, shp, work).pairs
+                                : min((int64_t)gridDim.x, work.tile_total);
   if (blockIdx.x >= ctas) return;
   if (ptx::smem_u32(smem_raw) & 1023) {
     // (the swizzled operand layouts need a 1024-byte aligned base)
@@ -519,10 +716,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp == kWalkWarp) {
       // ------------------------------------------- the walk, and landed tiles
       Walk walk;
+      if (kLanes && lane == 0) {
+        bars->lane.ds = ds;
+        bars->lane.s = shp;
+        bars->lane.work = work;
+        bars->lane.road = draft_road(ds, shp, work);
+        start_lane(&bars->lane);
+      }
       walk.x = step_cut(blockIdx.x, work.tile_total, ctas);
       walk.end = step_cut(blockIdx.x + 1, work.tile_total, ctas);
       walk.unit = 0;
-      if (walk.x >= work.tile_prefix) {
+      if (!kLanes && walk.x >= work.tile_prefix) {
         // the tiled sequence that holds this CTA's first step
         const int64_t v = step_div(walk.x - work.tile_prefix, shp.H_kv);
         int hi = plan.header[kPlanTiled] - 1;
@@ -540,12 +744,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool last = false;
       auto publish = [&] {
         if (last) return;
-        Segment u;
-        last = !next_segment<kDraft>(walk, ds, shp, plan, work, ctas, tpt, u);
-        if (lane == 0) {
-          bars->segments[n_pub % kSegments] = u;
-          ptx::mbar_arrive(&bars->published[n_pub % kSegments]);
+        Segment& slot = bars->segments[n_pub % kSegments];
+        if constexpr (kLanes) {
+          int more = 0;
+          if (lane == 0) more = next_segment(&bars->lane, &slot);
+          last = __shfl_sync(0xffffffffu, more, 0) == 0;
+        } else {
+          Segment u;
+          last = !next_segment<kDraft>(walk, ds, shp, plan, work, ctas, tpt, u);
+          if (lane == 0) slot = u;
         }
+        if (lane == 0) ptx::mbar_arrive(&bars->published[n_pub % kSegments]);
         ++n_pub;
       };
       uint32_t gi = 0, t = 0;
@@ -607,9 +816,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t gi = 0, tc0 = 0;
     bool ok = true;
     int site = 0, at = 0;
+    // drafted tokens: this row's place (looked up with its queries)
+    auto place_of = [&](const Segment& u) {
+      return kDraft && u.tree >= 0 && tok < u.n_tok ? ds.place[u.row + tok] : 0;
+    };
     Segment it;
     bool more = segment(0, it);
-    if (more) write_q(it, 0);
+    int place = 0;
+    if (more) {
+      place = place_of(it);
+      write_q(it, 0);
+    }
     for (uint32_t k = 0; more && ok; ++k) {
       // the last key this row sees
       int pos = it.flags & kPrefix ? it.pos : it.pos + tok;
@@ -617,8 +834,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if constexpr (kDraft) {
         if (it.tree >= 0) {
           all_see = it.tree;
-          if (tok < it.n_tok &&
-              !draft_is_run(ds, it.row + tok, it.tree, it.pos + tok - it.tree))
+          if (tok < it.n_tok && place != it.pos + tok)
             pos = it.tree - 1;               // and then its ancestors
         }
       }
@@ -772,7 +988,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       // the next unit's queries, while this one's last products run
       Segment nx;
       more = segment(k + 1, nx);
-      if (more) write_q(nx, (k + 1) & 1);
+      if (more) {
+        place = place_of(nx);
+        write_q(nx, (k + 1) & 1);
+      }
       const uint32_t tl = tc0 + it.n - 1;
       const bool fin = ptx::mbar_wait(&bars->o_done[tl & 1], (tl >> 1) & 1, kWaitLimit);
       if (!__all_sync(0xffffffffu, fin)) {
@@ -793,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __nv_bfloat16* orow = o + slot * 128;
       if (head && row == 0)
         (pre ? ws.pre_cut : ws.own_cut)[(int64_t)it.row * shp.H_kv + it.kv_head] =
-            Spills{(int32_t)blockIdx.x + 1, it.cuts};
+            Spills{(int32_t)blockIdx.x + (kDraft && (it.cuts & kSpillsApart) ? 2 : 1), it.cuts};
       float* prow = (head ? (pre ? ws.pre_o : ws.own_o) : ws.tile_o) + slot * 128;
       float* plse = head ? (pre ? ws.pre_lse : ws.own_lse) : ws.tile_lse;
       float ov[128];
@@ -867,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 }  // namespace
 
 namespace {
-template <bool kDraft>
+template <bool kDraft, bool kLanes>
 cudaError_t launch(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w, const void* q,
                    const void* k_cache, const void* v_cache, void* o, cudaStream_t st) {
   const int64_t rows = (int64_t)ds.num_blocks * s.H_kv * s.B;
@@ -886,13 +1105,13 @@ cudaError_t launch(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, step_tile_kernel<kDraft>);
+    e = cudaFuncGetAttributes(&fa, step_tile_kernel<kDraft, kLanes>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(step_tile_kernel<kDraft>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kStepTileSmem);
+    e = cudaFuncSetAttribute(step_tile_kernel<kDraft, kLanes>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kStepTileSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(step_tile_kernel<kDraft>,
+      e = cudaFuncSetAttribute(step_tile_kernel<kDraft, kLanes>,
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
@@ -908,7 +1127,7 @@ cudaError_t launch(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_tile_kernel<kDraft>, tk, tv, ds, s, w,
+  return cudaLaunchKernelEx(&cfg, step_tile_kernel<kDraft, kLanes>, tk, tv, ds, s, w,
                             (const __nv_bfloat16*)q, (const __nv_bfloat16*)v_cache,
                             (__nv_bfloat16*)o);
 }
@@ -917,7 +1136,15 @@ cudaError_t launch(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w
 cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWorkspace& w,
                              const void* q, const void* k_cache, const void* v_cache, void* o,
                              cudaStream_t st) {
-  return (ds.place ? launch<true> : launch<false>)(ds, s, w, q, k_cache, v_cache, o, st);
+  // Pairs of query tiles pay where a sequence has more than one and keys enough for
+  // the second one's to be read from HBM again (64 trees of 64 tokens, groups of 4:
+  // 221 us without, 187 with, behind 2200 keys, 134 and 129 behind 1100); the walk of
+  // the lanes costs the others (behind 300, 84.5 and 88.5), and what the tables can
+  // hold is all the host knows.
+  const bool lanes = ds.place && (int64_t)ds.max_tokens * s.g > kRows &&
+                     (int64_t)ds.max_blocks * s.B >= 2 * kStepPairTiles * kKeys;
+  auto fn = !ds.place ? launch<false, false> : lanes ? launch<true, true> : launch<true, false>;
+  return fn(ds, s, w, q, k_cache, v_cache, o, st);
 }
 
 }  // namespace rbkv

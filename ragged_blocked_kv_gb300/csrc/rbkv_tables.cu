@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
     return left >= 32 ? x : x & ((1u << left) - 1u);
   };
 
+  const int32_t serial = rank == 0 && tid == 0 ? plan.header[kPlanSerial] : 0;
+
   // ---- the thread's sums, and their scan over the block ----
   int32_t mine[kSums], err = 0;
   float big = 0.f;
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) build_kernel(BuildArgs a) {
     plan.header[kPlanTokens] = a.max_tokens;
     plan.header[kPlanMaxBlocks] = a.max_blocks;
     plan.header[kPlanPool] = a.num_blocks;
-    plan.header[kPlanDraft] = 0;
+    plan.header[kPlanSerial] = serial + 1;
     if (!ok) atomicCAS(a.status, 0, err);
   }
 

@@ -17,7 +17,7 @@ FAR = 1 << 32            # (fake addresses far enough apart not to overlap)
 
 
 def _draft(rbkv, **change):
-    d = rbkv._StepDraft(*(FAR + (i << 20) for i in range(5)))
+    d = rbkv._StepDraft(*(FAR + (i << 20) for i in range(6)))
     for k, v in change.items():
         setattr(d, k, v)
     return d
@@ -82,7 +82,7 @@ def test_draft_refusals(rbkv):
 
     for bad in (None, *(_draft(rbkv, **x) for x in (
             {"place": None}, {"ancestors": None}, {"path": None}, {"accepted": None},
-            {"next_token": None}, {"ancestors": FAR + 4}, {"place": FAR + 2}, {"path": FAR + 1},
+            {"next_token": None}, {"work": None}, {"work": FAR + 8}, {"ancestors": FAR + 4}, {"place": FAR + 2}, {"path": FAR + 1},
             {"accepted": FAR + 2}, {"next_token": FAR + 3}))):
         assert calls(bad) == [INVALID] * 4
     assert calls(_draft(rbkv), _tables(rbkv, num_seqs=0)) == [INVALID] * 4
@@ -90,7 +90,8 @@ def test_draft_refusals(rbkv):
     a, place = 9 * FAR, FAR
     assert L.rbkv_step_draft_plan(c, tt, d, None, None) == INVALID
     assert L.rbkv_step_draft_plan(c, tt, d, a + 2, None) == INVALID
-    for at in (place, place + (1 << 20), place + (2 << 20), place + (4 << 20) + 8, FAKE):
+    for at in (place, place + (1 << 20), place + (2 << 20), place + (4 << 20) + 8,
+               place + (5 << 20) + 16, FAKE):
         assert L.rbkv_step_draft_plan(c, tt, d, at, None) == INVALID, hex(at)
         assert L.rbkv_step_draft_accept(c, tt, d, at, a, None, None) == INVALID
         assert L.rbkv_step_draft_accept(c, tt, d, a, at, None, None) == INVALID

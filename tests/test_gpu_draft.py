@@ -284,11 +284,31 @@ def test_calls_out_of_order(rbkv):
     ctx, free = t.ctx.clone(), t.free.clone()
     refused(lambda: t.attention(qd, kd, vd, o=o, draft=d))
     refused(lambda: d.accept(tok, tok))
+    d.plan(i32([-1, -1, 0] + [0] * (t.max_tokens - 3)))
+    t.device_status()
+    late = rbkv.StepDraft(t)                             # (planned by another: not by this one)
+    refused(lambda: t.attention(qd, kd, vd, o=o, draft=late))
+    refused(lambda: late.accept(tok, tok))
     # f32 shapes, on the CUDA cores
     t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, 8, 2, 64, 16, "f32", 0, [5, 40], [6, 4])
     d, o = rbkv.StepDraft(t), torch.full_like(q, 7.0, device="cuda")
     t.attention(q.cuda(), kd, vd, o=o, draft=d)
     assert _status(rbkv, t) == INVALID and (o == 7.0).all()
+
+
+WIDE = ([1000, 30, 2000, 70, 0, 3000, 128, 640], [128, 100, 64, 33, 500, 65, 97, 1])
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (16, 1, 128, 16, "bf16"),
+                                   (10, 2, 128, 32, "bf16"), (64, 1, 128, 128, "bf16"),
+                                   (7, 7, 128, 8, "bf16")], ids=str)
+@pytest.mark.parametrize("prefix", [0, 900])
+@pytest.mark.parametrize("batch", [WIDE, ([5000], [128]), ([0, 9000], [128, 90]),
+                                   ([300] * 40, [70] * 40)], ids=["wide", "one", "two", "many"])
+def test_several_query_tiles_per_sequence(rbkv, shape, prefix, batch):
+    """Odd and even numbers of query tiles, of different lengths, over few and many keys."""
+    t, d, want, parent, q, kc, vc, ids, rows, o = _attend(rbkv, shape, prefix, batch, seed=11)
+    _check(want, parent, q, kc, vc, ids, prefix, rows, o, shape)
 
 
 # ---- acceptance ------------------------------------------------------------------
