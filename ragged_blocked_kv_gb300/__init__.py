@@ -493,6 +493,7 @@ class Rotary:
                                   dtype=torch.int64, device=device)
         self._c = C.byref(_Rotary(self.turns.data_ptr(), self.rotary_dim, self.LAYOUTS[layout],
                                   self.scale))
+        self._device = self.turns.device
 
     def _theta(self, base, scaling, factor, original_length, low, high):
         R = self.rotary_dim
@@ -514,8 +515,8 @@ class Rotary:
         return theta
 
     def _on(self, device):
-        if self.turns.device != device:
-            raise ValueError(f"rotary is on {self.turns.device}, the call on {device}")
+        if self._device != device:
+            raise ValueError(f"rotary is on {self._device}, the call on {device}")
         return self._c
 
 

@@ -12,11 +12,17 @@
 // before it.
 //
 // A block takes a row: a thread each works out one pair's sine and cosine into
-// shared memory, for all heads, while its first vectors are on their way; then
-// every thread rotates units of two 16-byte vectors that hold both elements of
-// their pairs (so that q_out may be q).  Values and the elements behind R are
-// units that are only copied.  Where R / 2 elements are not whole vectors a unit
-// is one pair (kVec = 1).
+// shared memory, for all heads, while its first vectors are on their way.  A unit
+// is two 16-byte vectors that hold both elements of their pairs (so that q_out may
+// be q); a thread has the same units' column in every few heads, and so keeps its
+// pairs' turns in registers.  Values and the elements behind R are only copied.
+// Where R / 2 elements are not whole vectors a unit is one pair (kVec = 1).
+//
+// Bound by memory and, in few rows, by the call: 2048 rows of 32 and 8 heads of
+// 128, bf16, 50 MB, 10.6 us (4.8 TB/s with the launch; the copy alone would take
+// 7.4), 16 rows 6.9 (the host's time).  With the turns read from shared memory for
+// every unit 12.4 us, all of a unit's elements as fp32 at once 11.8, four units in
+// flight instead of three (48 heads are three to a thread) 12.8, two 12.2.
 #include <algorithm>
 #include <cstring>
 #include <string>
@@ -32,70 +38,95 @@ namespace rbkv {
 namespace {
 
 constexpr int kThreads = 128;       // at least the pairs of a head: 256 / 2
-constexpr int kUnroll = 4;          // units of a thread in flight
+constexpr int kUnroll = 3;          // units of a thread in flight
 
-// kVec elements as one word, and as fp32.
-template <class T, int kVec> struct Pack;
-template <> struct Pack<__nv_bfloat16, 8> {
-  using Raw = uint4;
-  static __device__ __forceinline__ void open(const Raw& r, float* x) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// (x, y) turned by an angle of cosine t.x and sine t.y.
+__device__ __forceinline__ void turn(float& x, float& y, const float2& t) {
+  const float u = x * t.x - y * t.y;
+  y = y * t.x + x * t.y;
+  x = u;
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A unit: two words of kVec elements, whose pairs lie across the words ("half") or
+// side by side in them, and the turns of its kVec pairs.  (A few elements at a time:
+// all of a unit's as fp32 at once took registers that the loads in flight need.)
+template <class T, int kVec> struct Unit;
+template <> struct Unit<__nv_bfloat16, 8> {
+  using Word = uint4;
+  static __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* t, bool beside) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (beside) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int i = 0; i < 8; ++i) {
+        float x = low(w[i]), y = high(w[i]);
+        turn(x, y, t[i]);
+        w[i] = ptx::pack_bf16x2(x, y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x0 = low(w[i]), x1 = high(w[i]), y0 = low(w[4 + i]), y1 = high(w[4 + i]);
+        turn(x0, y0, t[2 * i]);
+        turn(x1, y1, t[2 * i + 1]);
+        w[i] = ptx::pack_bf16x2(x0, x1);
+        w[4 + i] = ptx::pack_bf16x2(y0, y1);
+      }
     }
-  }
-  static __device__ __forceinline__ Raw close(const float* x) {
-    return make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
-                      ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
   }
 };
-template <> struct Pack<float, 4> {
-  using Raw = uint4;
-  static __device__ __forceinline__ void open(const Raw& r, float* x) {
-    x[0] = __uint_as_float(r.x);
-    x[1] = __uint_as_float(r.y);
-    x[2] = __uint_as_float(r.z);
-    x[3] = __uint_as_float(r.w);
-  }
-  static __device__ __forceinline__ Raw close(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
+template <> struct Unit<float, 4> {
+  using Word = float4;
+  static __device__ __forceinline__ void rotate(float4& a, float4& b, const float2* t,
+                                                bool beside) {
+    turn(a.x, beside ? a.y : b.x, t[0]);
+    turn(beside ? a.z : a.y, beside ? a.w : b.y, t[1]);
+    turn(beside ? b.x : a.z, beside ? b.y : b.z, t[2]);
+    turn(beside ? b.z : a.w, b.w, t[3]);
   }
 };
-template <> struct Pack<__nv_bfloat16, 1> {
-  using Raw = uint16_t;
-  static __device__ __forceinline__ void open(const Raw& r, float* x) {
-    x[0] = __uint_as_float((uint32_t)r << 16);
-  }
-  static __device__ __forceinline__ Raw close(const float* x) {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+template <> struct Unit<__nv_bfloat16, 1> {
+  using Word = uint16_t;
+  static __device__ __forceinline__ void rotate(uint16_t& a, uint16_t& b, const float2* t, bool) {
+    float x = low(a), y = low(b);
+    turn(x, y, t[0]);
+    a = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    b = __bfloat16_as_ushort(__float2bfloat16_rn(y));
   }
 };
-template <> struct Pack<float, 1> {
-  using Raw = uint32_t;
-  static __device__ __forceinline__ void open(const Raw& r, float* x) {
-    x[0] = __uint_as_float(r);
+template <> struct Unit<float, 1> {
+  using Word = float;
+  static __device__ __forceinline__ void rotate(float& a, float& b, const float2* t, bool) {
+    turn(a, b, t[0]);
   }
-  static __device__ __forceinline__ Raw close(const float* x) { return __float_as_uint(x[0]); }
 };
 
 struct Heads {
   int32_t q, kv, dim, block;
-  uint32_t per, inverse;       // units per head, and ceil(2^32 / per)
+  int32_t per;                 // units per head,
   int32_t rotating;            // of which hold pairs
 };
 
+// Where pair p's turn lies in shared memory: a thread reads the kVec pairs of its
+// column 16 bytes at a time, and eight columns' pieces then fall into different banks.
+template <int kVec>
+__device__ __forceinline__ int turn_at(int p) {
+  const int col = p / kVec, e = p % kVec;
+  const int flip = kVec == 8 ? (col >> 1) & 3 : kVec == 4 ? (col >> 2) & 1 : 0;
+  return col * kVec + (e ^ (flip << 1));
+}
+
 template <class T, int kVec>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     append_rotary_kernel(DevPass dp, Heads h, rbkv_rotary r, int32_t offset, const void* q,
                          void* q_out, const void* __restrict__ k_new,
                          const void* __restrict__ v_new, void* __restrict__ k_cache,
                          void* __restrict__ v_cache) {
-  using P = Pack<T, kVec>;
-  using Raw = typename P::Raw;
-  __shared__ __align__(16) float cos_s[kThreads], sin_s[kThreads];
+  using Word = typename Unit<T, kVec>::Word;
+  __shared__ __align__(16) float2 turns_s[kThreads];
   // Launched to overlap its predecessor's tail: wait for it (it may have
   // produced the inputs, or still read cache blocks that are written here).
   ptx::pdl_wait_previous();
@@ -108,95 +139,59 @@ __global__ void __launch_bounds__(kThreads)
     if (tid == 0 && rows > 0) atomicCAS(dp.status, 0, kDevInvalid);
     return;
   }
-  const uint32_t units_q = (uint32_t)h.q * h.per, units_k = (uint32_t)h.kv * h.per;
-  const uint32_t units = units_q + 2 * units_k;
-  const int half = r.rotary_dim / 2;
-  // a unit: its head's tensor (0 q, 1 k, 2 v), head, and its two vectors' places
-  struct Unit {
-    int kind, head, col, e0, e1;
-  };
-  auto locate = [&](uint32_t u) {
-    Unit x;
-    x.kind = u < units_q ? 0 : u < units_q + units_k ? 1 : 2;
-    u -= x.kind == 0 ? 0 : x.kind == 1 ? units_q : units_q + units_k;
-    x.head = h.per == 1 ? u : __umulhi(u, h.inverse);
-    x.col = (int)(u - (uint32_t)x.head * h.per);
-    const bool apart = x.kind != 2 && x.col < h.rotating && !r.interleaved;
-    x.e0 = (apart ? 1 : 2) * x.col * kVec;
-    x.e1 = x.e0 + (apart ? half : kVec);
-    return x;
-  };
+  // A thread's units: one column of every `step`-th head (of Q's, then K's, then V's)
+  const int step = kThreads / h.per, heads = h.q + 2 * h.kv, half = r.rotary_dim / 2;
+  const int head0 = tid / h.per, col = tid - head0 * h.per;
+  const bool turns = col < h.rotating, apart = turns && !r.interleaved;
+  const int e0 = (apart ? 1 : 2) * col * kVec, e1 = e0 + (apart ? half : kVec);
+  const int v0 = 2 * col * kVec, v1 = v0 + kVec;
+  const bool live = head0 < step;
   for (int row = blockIdx.x; row < rows; row += gridDim.x) {
-    for (uint32_t u0 = tid; u0 - tid < units; u0 += kUnroll * kThreads) {
-      Raw a[kUnroll], b[kUnroll];
+    float2 t[kVec];
+    for (int x0 = 0; x0 < heads; x0 += kUnroll * step) {
+      Word a[kUnroll], b[kUnroll];
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
-        const uint32_t u = u0 + i * kThreads;
-        if (u >= units) continue;
-        const Unit x = locate(u);
-        const void* src = x.kind == 0 ? q : x.kind == 1 ? k_new : v_new;
-        const T* p = (const T*)src +
-                     ((int64_t)row * (x.kind == 0 ? h.q : h.kv) + x.head) * h.dim;
-        a[i] = *reinterpret_cast<const Raw*>(p + x.e0);
-        b[i] = *reinterpret_cast<const Raw*>(p + x.e1);
+        const int x = x0 + i * step + head0;
+        if (!live || x >= heads) continue;
+        const bool is_q = x < h.q, is_v = x >= h.q + h.kv;
+        const T* p = is_q ? (const T*)q + ((int64_t)row * h.q + x) * h.dim
+                          : (const T*)(is_v ? v_new : k_new) +
+                                ((int64_t)row * h.kv + (x - h.q - (is_v ? h.kv : 0))) * h.dim;
+        a[i] = *reinterpret_cast<const Word*>(p + (is_v ? v0 : e0));
+        b[i] = *reinterpret_cast<const Word*>(p + (is_v ? v1 : e1));
       }
       const int slot = dp.slot[row];
-      if (u0 == (uint32_t)tid) {
+      if (x0 == 0) {
         const uint32_t at = (uint32_t)(dp.position[row] + offset);
         __syncthreads();      // (the previous row's are no longer needed)
         if (tid < half) {
           float s, c;
           sincospif((float)(int64_t)(r.turns[tid] * at) * 0x1p-63f, &s, &c);
-          cos_s[tid] = c * r.scale;
-          sin_s[tid] = s * r.scale;
+          turns_s[turn_at<kVec>(tid)] = make_float2(c * r.scale, s * r.scale);
         }
         __syncthreads();
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) t[e] = turns_s[turn_at<kVec>(col * kVec + e)];
+        }
       }
       const int blk = slot / h.block, in_block = slot - blk * h.block;
       const bool inside = slot >= 0 && blk < dp.num_blocks;
       if (!inside && tid == 0) atomicCAS(dp.status, 0, kDevBounds);
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
-        const uint32_t u = u0 + i * kThreads;
-        if (u >= units) continue;
-        const Unit x = locate(u);
-        if (x.kind != 2 && x.col < h.rotating) {
-          float m[2 * kVec], c[kVec], s[kVec];
-          P::open(a[i], m);
-          P::open(b[i], m + kVec);
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            c[e] = cos_s[x.col * kVec + e];
-            s[e] = sin_s[x.col * kVec + e];
-          }
-          if (r.interleaved) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              const float v = m[2 * e], w = m[2 * e + 1];
-              m[2 * e] = v * c[e] - w * s[e];
-              m[2 * e + 1] = w * c[e] + v * s[e];
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              const float v = m[e], w = m[kVec + e];
-              m[e] = v * c[e] - w * s[e];
-              m[kVec + e] = w * c[e] + v * s[e];
-            }
-          }
-          a[i] = P::close(m);
-          b[i] = P::close(m + kVec);
-        }
-        T* to;
-        if (x.kind == 0) {
-          to = (T*)q_out + ((int64_t)row * h.q + x.head) * h.dim;
-        } else {
-          if (!inside) continue;
-          to = (T*)(x.kind == 1 ? k_cache : v_cache) +
-               (((int64_t)blk * h.kv + x.head) * h.block + in_block) * h.dim;
-        }
-        *reinterpret_cast<Raw*>(to + x.e0) = a[i];
-        *reinterpret_cast<Raw*>(to + x.e1) = b[i];
+        const int x = x0 + i * step + head0;
+        if (!live || x >= heads) continue;
+        const bool is_q = x < h.q, is_v = x >= h.q + h.kv;
+        if (turns && !is_v) Unit<T, kVec>::rotate(a[i], b[i], t, r.interleaved);
+        if (!is_q && !inside) continue;
+        T* to = is_q ? (T*)q_out + ((int64_t)row * h.q + x) * h.dim
+                     : (T*)(is_v ? v_cache : k_cache) +
+                           (((int64_t)blk * h.kv + (x - h.q - (is_v ? h.kv : 0))) * h.block +
+                            in_block) * h.dim;
+        *reinterpret_cast<Word*>(to + (is_v ? v0 : e0)) = a[i];
+        *reinterpret_cast<Word*>(to + (is_v ? v1 : e1)) = b[i];
       }
     }
   }
@@ -215,9 +210,7 @@ cudaError_t launch(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r, 
   h.kv = s.H_kv;
   h.dim = s.D;
   h.block = s.B;
-  h.per = (uint32_t)(s.D / (2 * kVec));
-  // (u / per = umulhi(u, inverse) for the units of a tensor's row: u per < 2^32)
-  h.inverse = (uint32_t)((((uint64_t)1 << 32) + h.per - 1) / h.per);
+  h.per = s.D / (2 * kVec);        // (at most kThreads: 256 / 2)
   h.rotating = r.rotary_dim / (2 * kVec);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min(dp.num_tokens, std::max(1, sms) * 16));

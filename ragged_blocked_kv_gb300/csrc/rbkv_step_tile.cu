@@ -1139,9 +1139,10 @@ cudaError_t launch_step_tile(const DevStep& ds, const ShapeInfo& s, const StepWo
   // Pairs of query tiles pay where a sequence has more than one and keys enough for
   // the second one's to be read from HBM again (64 trees of 64 tokens, groups of 4:
   // 221 us without, 187 with, behind 2200 keys, 134 and 129 behind 1100); the walk of
-  // the lanes costs the others (behind 300, 84.5 and 88.5), and what the tables can
-  // hold is all the host knows.
-  const bool lanes = ds.place && (int64_t)ds.max_tokens * s.g > kRows &&
+  // the lanes costs the others (behind 300, 84.5 and 88.5; trees of one tile behind
+  // up to 8192, 190 and 197), and what the tables can hold is all the host knows: keys
+  // of a sequence, and its rows on average.
+  const bool lanes = ds.place && (int64_t)ds.max_tokens * s.g > (int64_t)kRows * ds.num_seqs &&
                      (int64_t)ds.max_blocks * s.B >= 2 * kStepPairTiles * kKeys;
   auto fn = !ds.place ? launch<false, false> : lanes ? launch<true, true> : launch<true, false>;
   return fn(ds, s, w, q, k_cache, v_cache, o, st);
