@@ -51,6 +51,16 @@
 // to 8000 per unit.  Alone, 512 rows of 32 heads behind 4096 keys (34 GFLOP) take 33.5 us,
 // 1.03 PFLOP/s and 54% of the library's best product; 64 rows of 64 heads
 // behind 15999 keys 38 us.  (Tensor pipe 39% active; issue 31%.)
+//
+// Drafted tokens (rbkv_step_attention_draft) are the same kernel with another mask:
+// a row sees a run of keys from the first and, behind it, those of its ancestors
+// (rbkv_step.h).  Only a unit's last tile or two hold such keys; their scores are
+// hidden in tensor memory in front of the softmax, which stays as it is.  Two query
+// tiles of one sequence may be walked side by side (StepLanes).  Of a unit's 8000
+// cycles beside its key tiles (1500 each), as stamped behind 1100 keys, the queries
+// take 2800 (3300 in 16-byte loads), the results 2500, the hidden scores 1300; a
+// call's first 18000 cycles are cold caches.
+//
 // Every wait is bounded; on timeout the kernel records RBKV_ERR_TIMEOUT, lets
 // its copies and MMAs drain (bounded), frees its tensor memory and returns.
 #include <algorithm>
@@ -112,6 +122,45 @@ struct __align__(16) Segment {
 static_assert(sizeof(Segment) == 48, "Segment is 12 int32");
 enum { kPrefix = 1, kHead = 2, kWhole = 4 };
 
+// Drafted tokens: the values of tile j of a segment, landed at vt, that no row or
+// not every row sees, for the products: zeros behind the unit's last key (unwritten
+// cache slots may hold anything, and 0 * NaN is NaN) and in place of those that are
+// not finite and that some rows do not see, with a mark in `found` (the epilogue
+// looks them up).  The walking warp does so under the tile's softmax: done
+// by the softmax threads it took a unit's last tile 2000 cycles longer.
+__device__ __forceinline__ void clean_values(const Segment& it, int j, uint8_t* vt,
+                                             volatile uint32_t* found, uint32_t mark) {
+  const int lane = threadIdx.x & 31, key0 = it.kb + j * kKeys;
+  const int all_see = it.tree >= 0 ? it.tree : it.pos + 1;
+  const bool ragged = all_see < it.ke && key0 + kKeys > all_see;
+  if (!ragged && (j < it.n - 1 || it.ke % kKeys == 0)) return;
+  const int valid = min(it.ke - key0, kKeys), from = ragged ? max(all_see - key0, 0) : valid;
+  // a lane: 16 bytes of every other row
+  uint8_t* mine = vt + ((lane >> 3) & 1) * kHalf + ((lane & 7) << 4);
+  const int odd = lane >> 4;
+#pragma unroll 8
+  for (int r = valid + odd; r < kKeys; r += 2)
+    *reinterpret_cast<uint4*>(mine + r * 128) = make_uint4(0, 0, 0, 0);
+  // (0 x, summed, is 0 where all of them are finite and NaN elsewhere)
+  __nv_bfloat162 sum = __float2bfloat162_rn(0.f), zero = sum;
+#pragma unroll 8
+  for (int r = from + odd; r < valid; r += 2) {
+    const uint4 w = *reinterpret_cast<const uint4*>(mine + r * 128);
+    sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero, sum);
+    sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.y), zero, sum);
+    sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.z), zero, sum);
+    sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.w), zero, sum);
+  }
+  if (__low2float(sum) != 0.f || __high2float(sum) != 0.f) {
+    for (int r = from + odd; r < valid; r += 2)
+      zero_nonfinite(reinterpret_cast<uint4*>(mine + r * 128));
+    *found = mark;
+  }
+  // the PV MMAs read these rows through the async proxy
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Drafted tokens: the road of the step (see StepLanes), and a CTA's walk over its
 // lane of its pair's part: single units' steps [x, end), then pairs' places [px, pend).
 struct Road {
@@ -162,7 +211,8 @@ struct Bars {
   // k + 1 of the last segment k that held non-finite values of keys which some
   // of its rows see, by k & 1 (every softmax warp has stored segment k before
   // any of them reports a P of k + 1, hence before segment k + 2 has scores)
-  volatile uint32_t nonfinite[2];
+  // (drafted tokens: by k % kSegments, the walking warp finds them)
+  volatile uint32_t nonfinite[kSegments];
 };
 static_assert(kStages * kTileBytes + (int)sizeof(Bars) <= kStepTileSmem,
               "shared-memory layout overflows its allocation");
@@ -423,6 +473,17 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+__device__ __forceinline__ void load8(float* v, const void* p) {
+  uint32_t r[8];
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // A row's 32 floats as 256-bit stores (whole sectors per lane).
 __device__ __forceinline__ void store8(float* p, const float* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
@@ -475,6 +536,7 @@ __device__ __noinline__ void hide_others(uint32_t s_col, const uint4* set, int b
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const int run = lim - 32 * x;
+    if (by + 32 * x + 32 <= 0) continue;      // (in front of the tree: every row sees these)
     const uint32_t sees = own[x] | (run <= 0 ? 0u : run >= 32 ? ~0u : (1u << run) - 1u);
     float v[32];
     tmem_ld32(s_col + 32 * x, v);
@@ -529,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(&bars->kv_empty[s], 1);
     }
     bars->abort_flag = bars->missing = 0;
-    bars->nonfinite[0] = bars->nonfinite[1] = 0;
+    for (int i = 0; i < kSegments; ++i) bars->nonfinite[i] = 0;
     ptx::fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -771,6 +833,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           // reported.
           ok = wait_phase(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag);
           ok = ok && wait_phase(&bars->kv_full[gv % kStages], (gv / kStages) & 1, abort_flag);
+          if constexpr (kDraft) {
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok)
+              clean_values(it, j, kv_s + (gv % kStages) * kTileBytes,
+                           &bars->nonfinite[k % kSegments], k + 1);
+          }
           if (ok && j + 2 < it.n)
             ok = wait_phase(&bars->kv_full[gk % kStages], (gk / kStages) & 1, abort_flag);
           // (not before the barrier's last phase is over: it would count for that)
@@ -801,8 +869,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (tok < u.n_tok) {
         const uint4* src = reinterpret_cast<const uint4*>(
             q + ((int64_t)(u.row + tok) * shp.H_q + u.kv_head * g + hh) * 128);
+        if (kDraft && ((uintptr_t)q & 31) == 0) {
+          // (whole sectors per lane: 16-byte loads of a row each took 3300 cycles)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q4[i] = src[i];
+          for (int i = 0; i < 8; ++i) load8(qv + 8 * i, src + 2 * i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) q4[i] = src[i];
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) q4[i] = make_uint4(0, 0, 0, 0);
@@ -950,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
         l = l * corr + ps;
         const bool ragged = all_see < it.ke && key0 + kKeys > all_see;
-        if (ragged || (j == it.n - 1 && (it.ke % kKeys) != 0)) {
+        if (!kDraft && (ragged || (j == it.n - 1 && (it.ke % kKeys) != 0))) {
           // keys past the unit's end may be anything (unwritten cache slots, and
           // 0 * NaN is NaN): their V rows are zeroed.  So are non-finite values
           // of keys that some rows do not see; the epilogue looks them up.
@@ -1024,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_arrive(&bars->o_free);
 #pragma unroll
       for (int c = 0; c < 128; ++c) ov[c] *= inv;
-      if (bars->nonfinite[k & 1] == k + 1) {
+      if (bars->nonfinite[kDraft ? k % kSegments : k & 1] == k + 1) {
         // (written before the last P was reported, so before its product)
         const int end = kDraft && it.tree >= 0 ? it.ke : min(it.ke, pos + 1);
         for (int key = max(it.kb, all_see); key < end; ++key) {
