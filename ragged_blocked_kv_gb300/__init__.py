@@ -520,17 +520,24 @@ class Rotary:
         return self._c
 
 
+def _empty_on(stream, shape, dtype, device):
+    """An uninitialised tensor, allocated on the stream that uses it."""
+    import torch
+    with torch.cuda.device(device), \
+            torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream).value or 0, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def kv_append_rotary(p: Pass, rotary: Rotary, q, k_new, v_new, k_cache, v_cache, q_out=None,
                      stream=None):
     """``kv_append`` with the rotation on the way: rotated keys and the values into the
     caches, rotated queries into ``q_out`` (which may be ``q``), by the rows' positions
     in their sequences; returns ``q_out`` ``[T][H_q][D]``."""
-    import torch
     c = p.config
     T, dt = p.num_tokens, c.torch_dtype
     row, qshape = (T, c.num_heads_kv, c.head_dim), (T, c.num_heads_q, c.head_dim)
     if q_out is None:
-        q_out = torch.empty(qshape, dtype=dt, device=q.device)
+        q_out = _empty_on(stream, qshape, dt, q.device)
     _check(lib().rbkv_kv_append_rotary(p._h, rotary._on(q.device), _dev_ptr(q, "q", dt, qshape),
                                        _dev_ptr(q_out, "q_out", dt, qshape),
                                        _dev_ptr(k_new, "k_new", dt, row),
@@ -624,13 +631,12 @@ class Frame:
                          stream=None):
         """``kv_append_rotary`` of the loaded pass; returns ``q_out`` ([max_tokens][H_q][D];
         rows past the pass's are left as they were)."""
-        import torch
         c = self.config
         dt = c.torch_dtype
         row = (self.max_tokens, c.num_heads_kv, c.head_dim)
         qshape = (self.max_tokens, c.num_heads_q, c.head_dim)
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=dt, device=q.device)
+            q_out = _empty_on(stream, qshape, dt, q.device)
         _check(lib().rbkv_frame_kv_append_rotary(
             self._h, rotary._on(q.device), _dev_ptr(q, "q", dt, qshape),
             _dev_ptr(q_out, "q_out", dt, qshape), _dev_ptr(k_new, "k_new", dt, row),
@@ -810,7 +816,7 @@ class StepTables(_Arrays):
         ``q`` (rows past the step's are left as they were); returns ``q_out``."""
         prefix_len = _int32(int(prefix_len), "prefix_len")
         if q_out is None:
-            q_out = self._outputs(None, q, 0, stream)[0]
+            q_out = _empty_on(stream, self._q_shape, self._dt, self.device)
         dt, row, cache = self._dt, self._kv_shape, self._cache_shape
         self._call(self._f_append_rotary, self._drafted(draft), rotary._on(self.device),
                    prefix_len, self._ptr(q, "q", dt, self._q_shape),
@@ -864,14 +870,11 @@ class StepTables(_Arrays):
         """O and a workspace where none was given, allocated on the stream that
         uses them."""
         import torch
-        with _device(self.device):
-            st = torch.cuda.ExternalStream(_stream(stream).value or 0, self.device)
-            with torch.cuda.stream(st):
-                if o is None:
-                    o = torch.empty(self._q_shape, dtype=self._dt, device=self.device)
-                if workspace is None:
-                    need = int(lib().rbkv_step_workspace_bytes(self._c, self._t, prefix_len))
-                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if o is None:
+            o = _empty_on(stream, self._q_shape, self._dt, self.device)
+        if workspace is None:
+            workspace = _empty_on(stream, (self.workspace_bytes(prefix_len),), torch.uint8,
+                                  self.device)
         return o, workspace
 
     def device_status(self, stream=None) -> None:

@@ -70,8 +70,17 @@ __device__ __forceinline__ void plan_lanes(const DraftArgs& a, const StepPlan& p
     single = step_singles_len(seen, e.n_new, tokens, pairs);
     pair = step_pairs_len(seen, e.n_new, tokens, pairs);
   };
-  int mine[2] = {0, 0}, at[2];
-  for (int i = i0; i < i1; ++i) {
+  // (the first few sequences of a thread are kept for the second pass)
+  constexpr int kHeld = 4;
+  int mine[2] = {0, 0}, at[2], held[2][kHeld];
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x) {
+    held[0][x] = held[1][x] = 0;
+    if (i0 + x < i1) lengths(i0 + x, held[0][x], held[1][x]);
+    mine[0] += held[0][x];
+    mine[1] += held[1][x];
+  }
+  for (int i = i0 + kHeld; i < i1; ++i) {
     int single, pair;
     lengths(i, single, pair);
     mine[0] += single;
@@ -98,14 +107,18 @@ __device__ __forceinline__ void plan_lanes(const DraftArgs& a, const StepPlan& p
       total[x] += sums[x][w];
     }
   }
-  for (int i = i0; i < i1; ++i) {
-    StepLanes e;
-    lengths(i, e.single_len, e.pair_len);
-    e.single_cum = at[0];
-    e.pair_cum = at[1];
-    out[1 + i] = e;
-    at[0] += e.single_len;
-    at[1] += e.pair_len;
+  auto put = [&](int i, int single, int pair) {
+    out[1 + i] = StepLanes{at[0], single, at[1], pair};
+    at[0] += single;
+    at[1] += pair;
+  };
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x)
+    if (i0 + x < i1) put(i0 + x, held[0][x], held[1][x]);
+  for (int i = i0 + kHeld; i < i1; ++i) {
+    int single, pair;
+    lengths(i, single, pair);
+    put(i, single, pair);
   }
   const int serial = plan.header[kPlanSerial];
   if (tid == 0) out[0] = StepLanes{serial, total[0], ~serial, total[1]};

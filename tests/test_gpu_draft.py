@@ -311,6 +311,35 @@ def test_several_query_tiles_per_sequence(rbkv, shape, prefix, batch):
     _check(want, parent, q, kc, vc, ids, prefix, rows, o, shape)
 
 
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (16, 1, 128, 16, "bf16"),
+                                   (9, 9, 128, 32, "bf16")], ids=str)
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_long_chains_in_pairs(rbkv, shape, prefix):
+    """Prompt chunks behind many keys beside trees: pairs whose first tile has fewer keys,
+    the last one not whole."""
+    batch = ([2000, 0, 5000, 70, 1500], [700, 1300, 128, 300, 333])
+    t, d, want, parent, q, kc, vc, ids, rows, o = _attend(rbkv, shape, prefix, batch, seed=12)
+    _check(want, parent, q, kc, vc, ids, prefix, rows, o, shape)
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (8, 2, 64, 16, "f32")], ids=str)
+def test_tensors_on_16_byte_addresses(rbkv, shape):
+    t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, 0, *TREES, pad=1)
+    parent = random_trees(np.random.default_rng(3), TREES[1], t.max_tokens)
+    n = 16 // q.element_size()
+
+    def off(x):
+        y = torch.zeros(x.numel() + n, dtype=x.dtype, device="cuda")[n:].view(x.shape)
+        return y.copy_(x)
+
+    qd, o, kd, vd = off(q), off(torch.zeros_like(q)), off(kc), off(vc)
+    assert qd.data_ptr() % 32 == 16
+    d = rbkv.StepDraft(t).plan(i32(parent))
+    t.attention(qd, kd, vd, o=o, draft=d)
+    t.device_status()
+    _check(want, parent, q, kc, vc, ids, 0, rows, o.cpu(), shape)
+
+
 # ---- acceptance ------------------------------------------------------------------
 @pytest.mark.parametrize("seen,n_new", BATCHES + [([60, 5, 31], [90, 300, 20])],
                          ids=lambda x: str(len(x)))
