@@ -379,6 +379,43 @@ def test_accept_and_compact_against_oracle(rbkv, seen, n_new, given, words):
     t.device_status()
 
 
+def test_thousands_of_sequences(rbkv):
+    """Plans, acceptance and move of 5000 sequences; more kept for a plan than a thread holds."""
+    S = 5000
+    rng = np.random.default_rng(21)
+    n_new = rng.integers(0, 9, S)
+    n_new[::500] = 100
+    t, want, rng = _built(rbkv, rng.integers(0, 90, S), n_new, block=32, seed=3, cfg=(8, 1, 128),
+                          dtype="bf16")
+    T = t.max_tokens
+    parent = random_trees(rng, n_new, T)
+    tokens, chosen = rng.integers(0, 2, T), rng.integers(0, 2, T)
+    d = rbkv.StepDraft(t).plan(i32(parent))
+    plan = D.plan(want, parent, T)
+    assert np.array_equal(d.place.cpu().numpy(), plan.place)
+    assert np.array_equal(d.ancestors.cpu().numpy(), plan.ancestors)
+    caches = [torch.randn(t.config.cache_shape()).to(torch.bfloat16) for _ in range(2)]
+    dev = [c.cuda() for c in caches]
+    done = D.accept(want, parent, tokens, chosen, None, 32)
+    d.accept(i32(tokens), i32(chosen))
+    d.compact(*dev)
+    t.device_status()
+    assert np.array_equal(d.path.cpu().numpy(), done.path)
+    assert t.ctx.tolist() == done.ctx.tolist()
+    assert np.array_equal(t.free.cpu().numpy(), free_words(done.free))
+    for c, x in zip(caches, dev):
+        D.compact(want, done, c, 32)
+        assert torch.equal(c, x.cpu())
+    q = torch.randn(T, 8, 128).to(torch.bfloat16)
+    kc, vc = caches
+    rows = int(want.q_start[-1])
+    o = t.attention(q.cuda(), *dev, draft=d).cpu()
+    t.device_status()
+    ref = draft_reference(want, parent, q, kc, vc, [], 0)
+    err = (o[:rows].double() - ref[0]).abs()
+    assert (err <= error_bound(ref, 128, "bf16")).all()
+
+
 def test_given_out_of_range(rbkv):
     t, want, rng = _built(rbkv, [3, 9, 0], [6, 5, 200])
     parent = random_trees(rng, [6, 5, 200], t.max_tokens)
