@@ -292,8 +292,8 @@ typedef struct {
 /* rbkv_kv_append with the rotation on the way: k_cache receives the rotated
  * keys, v_cache the values, and q_out ([T][H_q][D]) the rotated queries, all
  * by the rows' positions in their sequences (fp32 arithmetic, each output
- * rounded once).  q_out may be q; it must not overlap it in part, or any other
- * tensor of the call.  16-byte aligned tensors.
+ * rounded once).  q_out may be q; otherwise what is written (q_out and the
+ * caches) overlaps nothing else of the call.  16-byte aligned tensors.
  * Errors: as rbkv_kv_append, and RBKV_ERR_INVALID for a bad rotary. */
 rbkv_status rbkv_kv_append_rotary(rbkv_pass* p, const rbkv_rotary* rotary, const void* q,
                                   void* q_out, const void* k_new, const void* v_new,
@@ -696,7 +696,8 @@ rbkv_status rbkv_step_draft_accept(const rbkv_config* cfg, const rbkv_step_table
 /* Move the kept tokens' rows of a layer's caches to the slots that follow the
  * sequence's cached tokens: once per layer, after the acceptance and before the
  * next build (without an acceptance nothing is moved and RBKV_ERR_INVALID
- * recorded). */
+ * recorded).  A second call on the same caches would move the moved rows.  The
+ * two caches must not overlap. */
 rbkv_status rbkv_step_draft_compact(const rbkv_config* cfg, const rbkv_step_tables* t,
                                     const rbkv_step_draft* d, void* k_cache, void* v_cache,
                                     rbkv_stream stream);

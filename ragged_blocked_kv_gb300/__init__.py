@@ -486,7 +486,13 @@ class Rotary:
             if scaling != "none":
                 raise ValueError("inv_freq takes no scaling")
         else:
-            theta = self._theta(float(base), scaling, float(factor), original_length, low, high)
+            try:
+                theta = self._theta(float(base), scaling, float(factor), original_length, low,
+                                    high)
+            except OverflowError:
+                raise ValueError("angles per position are out of range") from None
+        if not (np.abs(theta) < 2.0 ** 900).all():
+            raise ValueError("angles per position are out of range")
         self.inv_freq = theta
         turns = [round(math.ldexp(float(x) / (2 * math.pi), 64)) % 2 ** 64 for x in theta]
         self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns],
@@ -528,6 +534,14 @@ def _empty_on(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _on_current(*tensors):
+    """Tensors of a call that runs on the current device."""
+    import torch
+    for t in tensors:
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"a tensor is on {t.device}, the call on the current device")
+
+
 def kv_append_rotary(p: Pass, rotary: Rotary, q, k_new, v_new, k_cache, v_cache, q_out=None,
                      stream=None):
     """``kv_append`` with the rotation on the way: rotated keys and the values into the
@@ -536,6 +550,7 @@ def kv_append_rotary(p: Pass, rotary: Rotary, q, k_new, v_new, k_cache, v_cache,
     c = p.config
     T, dt = p.num_tokens, c.torch_dtype
     row, qshape = (T, c.num_heads_kv, c.head_dim), (T, c.num_heads_q, c.head_dim)
+    _on_current(q, k_new, v_new, k_cache, v_cache, *(() if q_out is None else (q_out,)))
     if q_out is None:
         q_out = _empty_on(stream, qshape, dt, q.device)
     _check(lib().rbkv_kv_append_rotary(p._h, rotary._on(q.device), _dev_ptr(q, "q", dt, qshape),
@@ -635,6 +650,7 @@ class Frame:
         dt = c.torch_dtype
         row = (self.max_tokens, c.num_heads_kv, c.head_dim)
         qshape = (self.max_tokens, c.num_heads_q, c.head_dim)
+        _on_current(q, k_new, v_new, k_cache, v_cache, *(() if q_out is None else (q_out,)))
         if q_out is None:
             q_out = _empty_on(stream, qshape, dt, q.device)
         _check(lib().rbkv_frame_kv_append_rotary(
@@ -947,7 +963,7 @@ class StepDraft(_Arrays):
         return self
 
     def compact(self, k_cache, v_cache, stream=None) -> None:
-        """Move the kept tokens' rows of a layer's caches together."""
+        """Move the kept tokens' rows of a layer's caches together: once per layer."""
         t = self.tables
         t._call(self._f_compact, self._d, t._ptr(k_cache, "k_cache", t._dt, t._cache_shape),
                 t._ptr(v_cache, "v_cache", t._dt, t._cache_shape), stream=stream)

@@ -259,6 +259,12 @@ rbkv_status check_append_rotary(const rbkv_config* c, const rbkv_rotary* r, int6
       overlap(q_out, q_bytes, k_cache, cache) || overlap(q_out, q_bytes, v_cache, cache) ||
       overlap(q_out, q_bytes, r->turns, 4 * (int64_t)r->rotary_dim))
     return invalid("q_out overlaps another tensor");
+  if (overlap(k_cache, cache, v_cache, cache)) return invalid("the caches overlap");
+  for (const void* c2 : {k_cache, v_cache})
+    if (overlap(c2, cache, q, q_bytes) || overlap(c2, cache, k_new, kv_bytes) ||
+        overlap(c2, cache, v_new, kv_bytes) ||
+        overlap(c2, cache, r->turns, 4 * (int64_t)r->rotary_dim))
+      return invalid("a cache overlaps what the call reads");
   return RBKV_OK;
 }
 

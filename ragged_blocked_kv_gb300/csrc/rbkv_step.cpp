@@ -428,6 +428,10 @@ rbkv_status rbkv_step_draft_compact(const rbkv_config* cfg, const rbkv_step_tabl
   if (!k_cache || !v_cache) return invalid("NULL tensor");
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
     return invalid("tensors must be 16-byte aligned");
+  // (a row of one cache may be written before the other's columns have read it)
+  const int64_t cache = (int64_t)cfg->num_blocks * cfg->block_size * cfg->num_heads_kv *
+                        cfg->head_dim * (cfg->dtype == RBKV_BF16 ? 2 : 4);
+  if (overlap(k_cache, cache, v_cache, cache)) return invalid("the caches overlap");
   cudaError_t e =
       launch_draft_compact(draft_args(cfg, t, d), shape(cfg), k_cache, v_cache,
                            (cudaStream_t)stream);

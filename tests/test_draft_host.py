@@ -48,6 +48,10 @@ def test_rotary_refusals(rbkv):
     # q_out on part of q, on the new rows, on the caches, on what the call reads
     for at in (3 * FAR + 16, 4 * FAR, 5 * FAR, 6 * FAR + 1024, 7 * FAR, 2 * FAR, FAKE):
         assert _append(rbkv, q_out=at) == INVALID, hex(at)
+    assert _append(rbkv, kc=6 * FAR, vc=6 * FAR) == INVALID          # one cache for both
+    assert _append(rbkv, kc=6 * FAR, vc=6 * FAR + 65536) == INVALID  # (32 blocks of 8 KB)
+    for name in ("q", "k", "v"):
+        assert _append(rbkv, **{"q_out": 9 * FAR, name: 7 * FAR + 64}) == INVALID, name
     assert _append(rbkv, prefix=-1) == INVALID and _append(rbkv, prefix=(1 << 30) + 1) == INVALID
     assert _append(rbkv, d=_draft(rbkv, place=None)) == INVALID
     assert _append(rbkv, d=_draft(rbkv, place=9 * FAR), q_out=9 * FAR) == INVALID
@@ -102,6 +106,8 @@ def test_draft_refusals(rbkv):
     assert L.rbkv_step_draft_compact(c, tt, d, None, a, None) == INVALID
     assert L.rbkv_step_draft_compact(c, tt, d, a, None, None) == INVALID
     assert L.rbkv_step_draft_compact(c, tt, d, a + 8, a, None) == INVALID
+    assert L.rbkv_step_draft_compact(c, tt, d, a, a, None) == INVALID
+    assert L.rbkv_step_draft_compact(c, tt, d, a, a + 65536, None) == INVALID
     attend = L.rbkv_step_attention_draft
     assert attend(c, tt, d, a, a, a, None, 0, place, None, 0, None) == INVALID    # o on place
     assert attend(c, tt, d, a, a, a, None, 3, a + 4096, None, 0, None) == INVALID
@@ -139,7 +145,8 @@ def test_rotary_tables(rbkv):
     {"base": 0.0}, {"base": -3.0}, {"factor": 0.0}, {"base": math.inf}, {"scaling": "other"},
     {"scaling": "parts"}, {"scaling": "parts", "original_length": 10, "low": 2.0, "high": 2.0},
     {"inv_freq": [1.0]}, {"inv_freq": [1.0] * 15 + [math.nan]},
-    {"inv_freq": [1.0] * 16, "scaling": "linear"}])
+    {"inv_freq": [1.0] * 16, "scaling": "linear"}, {"inv_freq": [1e300] * 16},
+    {"base": 1e-300, "factor": 1e300, "scaling": "base"}])
 def test_rotary_arguments(rbkv, args):
     with pytest.raises(ValueError):
         rbkv.Rotary(**{"rotary_dim": 32, "device": "cpu", **args})
