@@ -175,7 +175,7 @@ struct Road {
 struct LaneWalk {
   int64_t x, end, px, pend;
   int unit;                  // tiled sequence, and its entries
-  bool in_pairs;
+  int pair_unit;             // where the pairs' part begins (-1: it has been entered)
   StepLanes lanes;
   StepSeq seq;
 };
@@ -225,6 +225,22 @@ static_assert(kStages * kTileBytes + (int)sizeof(Bars) <= kStepTileSmem,
 __device__ __forceinline__ uint32_t ring_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ uint32_t ring_v(int j, int n) {
   return j + 1 < n ? 2 * j + 2 : 2 * n - 1;
+}
+
+// The last of n entries whose place is at or before v: 32 places tested at a time by
+// the warp (in front of the first segment every round trip counts).
+template <class F>
+__device__ __forceinline__ int last_at(int n, int64_t v, F cum) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const bool le = lane * step < n && cum(lo + lane * step) <= v;
+    const int k = max(31 - __clz(__ballot_sync(0xffffffffu, le)), 0);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
 }
 
 // Walks a CTA's part [x, end) of the line.
@@ -308,17 +324,6 @@ __device__ __forceinline__ Road draft_road(const DevStep& ds, const ShapeInfo& s
   r.pairs = min((int64_t)gridDim.x / 2, r.total);
   return r;
 }
-// The last of the tiled sequences whose place is at or before v.
-template <class F>
-__device__ __forceinline__ int last_at(int n, int64_t v, F cum) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cum(mid) <= v) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
 
 __device__ __forceinline__ void enter_unit(LaneWalk& w, const DevStep& ds, const StepPlan& plan,
                                            int unit) {
@@ -327,25 +332,34 @@ __device__ __forceinline__ void enter_unit(LaneWalk& w, const DevStep& ds, const
   w.seq = plan.tiled[unit];
 }
 
-__device__ __forceinline__ void start_lane(Lane* lane) {
-  LaneWalk& w = lane->walk;
-  const DevStep& ds = lane->ds;
-  const ShapeInfo& s = lane->s;
-  const StepWork& work = lane->work;
-  const Road& road = lane->road;
-  const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
+// (by a warp)
+__device__ __forceinline__ void start_lane(Lane* lane, const DevStep& ds, const ShapeInfo& s,
+                                           const StepPlan& plan, const StepWork& work) {
+  const Road road = draft_road(ds, s, work);
   const int c = (int)blockIdx.x, n = plan.header[kPlanTiled];
+  LaneWalk w;
   w.x = road.begin(c);
   w.end = min(road.begin(c + 1), road.single);
   w.px = max(road.cut(c >> 1), road.half) - road.half;
   w.pend = max(road.cut((c >> 1) + 1), road.half) - road.half;
   w.unit = -1;
-  w.in_pairs = false;
+  w.pair_unit = 0;
   const StepLanes* lanes = ds.work + 1;
+  if (w.px < w.pend)
+    w.pair_unit =
+        last_at(n, step_div(w.px, s.H_kv), [&](int i) { return lanes[i].pair_cum; });
   if (w.end > max(w.x, work.tile_prefix))
     enter_unit(w, ds, plan,
                last_at(n, step_div(max(w.x - work.tile_prefix, (int64_t)0), s.H_kv),
                        [&](int i) { return lanes[i].single_cum; }));
+  if ((threadIdx.x & 31) == 0) {
+    lane->ds = ds;
+    lane->s = s;
+    lane->work = work;
+    lane->road = road;
+    lane->walk = w;
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ bool next_segment(Lane* lane, Segment* to) {
@@ -429,10 +443,9 @@ __device__ __forceinline__ bool next_segment(Lane* lane, Segment* to) {
     return true;
   }
   while (w.px < w.pend) {
-    if (!w.in_pairs) {
-      w.in_pairs = true;
-      enter_unit(w, ds, plan, last_at(plan.header[kPlanTiled], step_div(w.px, s.H_kv),
-                                      [&](int i) { return ds.work[1 + i].pair_cum; }));
+    if (w.pair_unit >= 0) {
+      enter_unit(w, ds, plan, w.pair_unit);
+      w.pair_unit = -1;
     }
     while (w.px >= (int64_t)s.H_kv * ((int64_t)w.lanes.pair_cum + w.lanes.pair_len))
       enter_unit(w, ds, plan, w.unit + 1);
@@ -778,13 +791,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp == kWalkWarp) {
       // ------------------------------------------- the walk, and landed tiles
       Walk walk;
-      if (kLanes && lane == 0) {
-        bars->lane.ds = ds;
-        bars->lane.s = shp;
-        bars->lane.work = work;
-        bars->lane.road = draft_road(ds, shp, work);
-        start_lane(&bars->lane);
-      }
+      if constexpr (kLanes) start_lane(&bars->lane, ds, shp, plan, work);
       walk.x = step_cut(blockIdx.x, work.tile_total, ctas);
       walk.end = step_cut(blockIdx.x + 1, work.tile_total, ctas);
       walk.unit = 0;
@@ -792,6 +799,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the tiled sequence that holds this CTA's first step
         const int64_t v = step_div(walk.x - work.tile_prefix, shp.H_kv);
         int hi = plan.header[kPlanTiled] - 1;
+        if constexpr (kDraft)
+          walk.unit = hi = last_at(hi + 1, v, [&](int i) { return plan.tiled[i].cum; });
         while (walk.unit < hi) {
           const int mid = (walk.unit + hi + 1) >> 1;
           if (plan.tiled[mid].cum <= v) walk.unit = mid;
