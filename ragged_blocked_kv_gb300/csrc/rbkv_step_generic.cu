@@ -13,7 +13,7 @@
 // in shared memory.  All arithmetic is fp32 FMAs.  Bound by the shared-memory
 // reads of q and the weights, and by latency at the sizes it is used for: 69
 // rows of 8 heads, dim 64, fp32, behind 333 keys and up to 100 own ones take
-// 18.9 us (eight rows of a block everywhere: 20.9).
+// 18.5 us (eight rows of a block everywhere: 20.9).
 #include <algorithm>
 #include <atomic>
 
@@ -64,10 +64,17 @@ __host__ __device__ constexpr int smem_floats(int D, int rows) {
   return rows * D + kWarps * 32 * rows + kWarps * rows * D + kWarps * rows * 2;
 }
 
+// (Two blocks of four rows on an SM, one of eight: left to itself the compiler takes
+// fewer registers and keeps fewer loads in flight - fp32, head dim 64: 18.8 us where
+// this takes 18.5 for 69 rows behind 333 keys, 24.6 and 22.2 for 64 rows of 450
+// own keys; bf16, 32 rows of 32 heads behind 1000, 66 and 50; at head dim 128
+// 29.3 and 30.4 for 32 rows behind 500.  One block of four rows: 12.9 for the first,
+// but 42 instead of 33 for 32 rows behind 2000 keys and 84 instead of 55 for one row
+// behind 8000, bf16.)
 // kPer: head-dim elements per lane, D = 32 dpl with dpl <= kPer.  kRows: packed
 // rows of a block, 4 or 8.
 template <class T, int kPer, int kRows, bool kDraft>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kRows == 4 && kPer <= 4 ? 2 : 1)
     step_generic_kernel(DevStep ds, ShapeInfo s, const T* __restrict__ q,
                         const T* __restrict__ k_cache, const T* __restrict__ v_cache,
                         T* __restrict__ o, float* __restrict__ part_o,
@@ -143,9 +150,11 @@ __global__ void __launch_bounds__(kThreads)
         const int lim = r < ra || r >= rb ? 0 : causal ? lim0 + tok[r] - tok0 : n;
         bool sees = off >= 0 && key < lim;
         if constexpr (kDraft) {
-          // (every row's word of the set is requested, wherever the row is used)
-          if (tree >= 0 && k0 + 32 > tree && r >= ra && r < rb)
-            sees = off >= 0 && (key < tree || draft_bit(ds.ancestors[tok[r]], key - tree));
+          if (tree >= 0 && k0 + 32 > tree && r >= ra && r < rb) {
+            const int i = key - tree;          // the key's token
+            const uint32_t* set = reinterpret_cast<const uint32_t*>(ds.ancestors + tok[r]);
+            sees = off >= 0 && (i < 0 || (i < kStepTreeTokens && (set[i >> 5] >> (i & 31) & 1u)));
+          }
         }
         const float sc = sees ? x[r] : -INFINITY;
         const float mn = fmaxf(m[r], warp_max(sc));
@@ -194,21 +203,46 @@ __global__ void __launch_bounds__(kThreads)
     };
 
     int c = 0;      // chunks dealt so far
-    for (int k0 = 0; k0 < ds.prefix_len; k0 += 32, ++c)
-      if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, 0, 0, false, -1);
-    for (int ra = 0; ra < rows;) {
-      // the rows of one sequence: row0 + ra .. row0 + rb - 1
-      const int t = (row0 + ra) / g;
-      const StepRow info = plan.rows[t];
-      const StepSeq e = info.unit >= 0 ? plan.streamed[info.unit] : plan.tiled[-1 - info.unit];
-      const int rb = min(rows, (e.row + e.n_new) * g - row0);
-      const int lim0 = e.ctx - e.n_new + info.token + 1;      // keys that token t sees
-      const int n = lim0 + (row0 + rb - 1) / g - t;           // and the last one
-      const int32_t* table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
-      const int tree = kDraft && e.n_new <= kStepTreeTokens ? e.ctx - e.n_new : -1;
-      for (int k0 = 0; k0 < n; k0 += 32, ++c)
-        if (c % stride == mine) chunk(table, k0, n, ra, rb, lim0, t, true, tree);
-      ra = rb;
+    if constexpr (kDraft) {
+      // the prefix, for all rows, then the rows of each sequence: one loop, so that the
+      // chunk's code is there once (16 trees of 20, bf16, head dim 64: 53.2 us with two
+      // copies, 42.3 with one; 64 in fp32 145.6 and 113.8)
+      int done = 0;   // rows whose own keys are done
+      for (bool prefix = true; prefix || done < rows; prefix = false) {
+        const int32_t* table = ds.prefix_table;
+        int ra = 0, rb = rows, n = ds.prefix_len, lim0 = 0, t = 0, tree = -1;
+        if (!prefix) {
+          // the rows of one sequence: row0 + ra .. row0 + rb - 1
+          ra = done;
+          t = (row0 + ra) / g;
+          const StepRow info = plan.rows[t];
+          const StepSeq e = info.unit >= 0 ? plan.streamed[info.unit] : plan.tiled[-1 - info.unit];
+          rb = min(rows, (e.row + e.n_new) * g - row0);
+          lim0 = e.ctx - e.n_new + info.token + 1;      // keys that token t sees
+          n = lim0 + (row0 + rb - 1) / g - t;           // and the last one
+          table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
+          if (e.n_new <= kStepTreeTokens) tree = e.ctx - e.n_new;
+          done = rb;
+        }
+        for (int k0 = 0; k0 < n; k0 += 32, ++c)
+          if (c % stride == mine) chunk(table, k0, n, ra, rb, lim0, t, !prefix, tree);
+      }
+    } else {
+      for (int k0 = 0; k0 < ds.prefix_len; k0 += 32, ++c)
+        if (c % stride == mine) chunk(ds.prefix_table, k0, ds.prefix_len, 0, rows, 0, 0, false, -1);
+      for (int ra = 0; ra < rows;) {
+        // the rows of one sequence: row0 + ra .. row0 + rb - 1
+        const int t = (row0 + ra) / g;
+        const StepRow info = plan.rows[t];
+        const StepSeq e = info.unit >= 0 ? plan.streamed[info.unit] : plan.tiled[-1 - info.unit];
+        const int rb = min(rows, (e.row + e.n_new) * g - row0);
+        const int lim0 = e.ctx - e.n_new + info.token + 1;      // keys that token t sees
+        const int n = lim0 + (row0 + rb - 1) / g - t;           // and the last one
+        const int32_t* table = ds.block_table + (int64_t)e.seq * ds.max_blocks;
+        for (int k0 = 0; k0 < n; k0 += 32, ++c)
+          if (c % stride == mine) chunk(table, k0, n, ra, rb, lim0, t, true, -1);
+        ra = rb;
+      }
     }
 
     // ---- join the warps ----

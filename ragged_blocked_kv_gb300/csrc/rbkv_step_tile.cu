@@ -903,14 +903,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto place_of = [&](const Segment& u) {
       return kDraft && u.tree >= 0 && tok < u.n_tok ? ds.place[u.row + tok] : 0;
     };
-    Segment it;
-    bool more = segment(0, it);
+    // With lanes, the softmax runs once over whatever tensor memory holds before the
+    // first segment is there: its instructions are in the caches then (one tree of 64
+    // behind 32768 keys 54.5 to 52.7 us, 64 behind 2200 183.5 to 180.3; on the line a
+    // mixed batch lost 3 us by it).
+    Segment it = {};
     int place = 0;
-    if (more) {
-      place = place_of(it);
-      write_q(it, 0);
+    bool more = true;
+    if constexpr (kLanes) {
+      it.n = 1;
+      it.tree = -1;
+    } else {
+      more = segment(0, it);
+      if (more) {
+        place = place_of(it);
+        write_q(it, 0);
+      }
     }
-    for (uint32_t k = 0; more && ok; ++k) {
+    for (int k = kLanes ? -1 : 0; more && ok; ++k) {
+      const bool dry = kLanes && k < 0;
       // the last key this row sees
       int pos = it.flags & kPrefix ? it.pos : it.pos + tok;
       int all_see = it.pos + 1;              // keys that every row sees
@@ -925,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < it.n; ++j) {
         const uint32_t t = tc0 + j;
         // tcgen05.ld/st are warp-collective: every decision below is warp-uniform
-        const bool got = wait_phase(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag);
+        const bool got = dry || wait_phase(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag);
         const uint32_t s_col = lane_base + (t & 1) * kKeys;   // S of the tile; then its P
         const int key0 = it.kb + j * kKeys;
         // (a block id outside the pool is noted before its K tile lands)
@@ -1065,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           ptx::fence_proxy_async_smem();
         }
         tc_fence_before();
-        ptx::mbar_arrive(&bars->p_full[t & 1]);
+        if (!dry) ptx::mbar_arrive(&bars->p_full[t & 1]);
       }
       if (!ok) break;
       // the next unit's queries, while this one's last products run
@@ -1074,6 +1085,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (more) {
         place = place_of(nx);
         write_q(nx, (k + 1) & 1);
+      }
+      if (dry) {
+        it = nx;
+        continue;
       }
       const uint32_t tl = tc0 + it.n - 1;
       const bool fin = ptx::mbar_wait(&bars->o_done[tl & 1], (tl >> 1) & 1, kWaitLimit);
@@ -1107,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_arrive(&bars->o_free);
 #pragma unroll
       for (int c = 0; c < 128; ++c) ov[c] *= inv;
-      if (bars->nonfinite[kDraft ? k % kSegments : k & 1] == k + 1) {
+      if (bars->nonfinite[kDraft ? k % kSegments : k & 1] == (uint32_t)k + 1) {
         // (written before the last P was reported, so before its product)
         const int end = kDraft && it.tree >= 0 ? it.ke : min(it.ke, pos + 1);
         for (int key = max(it.kb, all_see); key < end; ++key) {
