@@ -13,7 +13,7 @@
 // in shared memory.  All arithmetic is fp32 FMAs.  Bound by the shared-memory
 // reads of q and the weights, and by latency at the sizes it is used for: 69
 // rows of 8 heads, dim 64, fp32, behind 333 keys and up to 100 own ones take
-// 18.5 us (eight rows of a block everywhere: 20.9).
+// 17.9 us (eight rows of a block everywhere: 20.9).
 #include <algorithm>
 #include <atomic>
 
@@ -64,17 +64,26 @@ __host__ __device__ constexpr int smem_floats(int D, int rows) {
   return rows * D + kWarps * 32 * rows + kWarps * rows * D + kWarps * rows * 2;
 }
 
-// (Two blocks of four rows on an SM, one of eight: left to itself the compiler takes
-// fewer registers and keeps fewer loads in flight - fp32, head dim 64: 18.8 us where
-// this takes 18.5 for 69 rows behind 333 keys, 24.6 and 22.2 for 64 rows of 450
-// own keys; bf16, 32 rows of 32 heads behind 1000, 66 and 50; at head dim 128
-// 29.3 and 30.4 for 32 rows behind 500.  One block of four rows: 12.9 for the first,
-// but 42 instead of 33 for 32 rows behind 2000 keys and 84 instead of 55 for one row
-// behind 8000, bf16.)
+// Blocks on an SM that the compiler is to leave registers for: two of four rows, one
+// of eight (0: its own choice).  Left to itself it takes fewer registers and keeps
+// fewer loads in flight: fp32, head dim 64, 64 rows of 450 own keys 24.7 us where
+// this takes 20.9, 32 rows behind 2000 33.7 and 31.2; bf16, 32 rows of 32 heads
+// behind 1000, 66 and 48; 300 rows in fp32 of head dim 128 88 and 75.  Its own choice
+// is the better one for four rows of fp32 at head dim 128 (32 rows behind 500 29.3 and
+// 30.4) and for eight of bf16 at head dim 64 (256 rows of 32 heads 172 and 180).  One
+// block of four rows takes 12.9 instead of 18.5 for 69 rows behind 333 keys, but 42
+// instead of 33 for 32 behind 2000 and 84 instead of 55 for one behind 8000.
+template <class T, int kPer, int kRows, bool kDraft>
+__host__ __device__ constexpr int min_blocks() {
+  if (!kDraft && kRows == 4 && kPer == 4 && sizeof(T) == 4) return 0;
+  if (!kDraft && kRows == 8 && kPer == 2 && sizeof(T) == 2) return 0;
+  return kRows == 4 && kPer <= 4 ? 2 : 1;
+}
+
 // kPer: head-dim elements per lane, D = 32 dpl with dpl <= kPer.  kRows: packed
 // rows of a block, 4 or 8.
 template <class T, int kPer, int kRows, bool kDraft>
-__global__ void __launch_bounds__(kThreads, kRows == 4 && kPer <= 4 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, (min_blocks<T, kPer, kRows, kDraft>()))
     step_generic_kernel(DevStep ds, ShapeInfo s, const T* __restrict__ q,
                         const T* __restrict__ k_cache, const T* __restrict__ v_cache,
                         T* __restrict__ o, float* __restrict__ part_o,
@@ -168,9 +177,11 @@ __global__ void __launch_bounds__(kThreads, kRows == 4 && kPer <= 4 ? 2 : 1)
         p_s[lane * kRows + r] = sees ? p : -1.f;
       }
       __syncwarp();
-      // several value rows in flight: their latency is what a chunk waits for
+      // several value rows in flight: their latency is what a chunk waits for (32
+      // registers instead of 16: 64 rows of 450 own keys 21.9 to 20.9 us)
       const int count = min(32, n - k0);
-      constexpr int kAhead = 16 / kPer;
+      constexpr int kAhead =
+          (kRows == 4 && min_blocks<T, kPer, kRows, kDraft>() > 0 ? 32 : 16) / kPer;
       for (int j0 = 0; j0 < count; j0 += kAhead) {
         float v[kAhead][kPer];
 #pragma unroll
