@@ -322,6 +322,61 @@ def test_long_chains_in_pairs(rbkv, shape, prefix):
     _check(want, parent, q, kc, vc, ids, prefix, rows, o, shape)
 
 
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (16, 1, 128, 16, "bf16"),
+                                   (9, 9, 128, 32, "bf16")], ids=str)
+@pytest.mark.parametrize("prefix", [0, 900])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_pairs_with_values_that_are_not_finite(rbkv, shape, prefix, value):
+    """As the two tests above, where query tiles are walked in pairs: what a token does not
+    follow does not reach it, what it follows does."""
+    starts = np.concatenate([[0], np.cumsum(WIDE[1])])
+    pokes = [(0, 90), (1, 99), (2, 40), (4, 300), (5, 3), (7, 0)]
+
+    def poison(want, parent, kc, vc):
+        for s, i in pokes:
+            b, off = divmod(int(want.slot[starts[s] + i]), shape[3])
+            vc[b, :, off, 5] = value
+
+    parent = np.concatenate([D.chain(n) if n > 128 else
+                             [-1 if i == 0 else (i - 1) // 2 for i in range(n)]
+                             for n in WIDE[1]] + [[0, 0, 0]]).astype(np.int64)
+    t, d, want, parent, q, kc, vc, ids, rows, o = _attend(rbkv, shape, prefix, WIDE, seed=13,
+                                                          parent=parent, poison=poison, fill=value)
+    hit = torch.zeros(o[:rows].shape, dtype=torch.bool)
+    for s, i in pokes:
+        p, _ = D.parents_of(want, parent, s)
+        for j in range(len(p)):
+            if i in D.way_up(p, j):
+                hit[starts[s] + j, :, 5] = True
+    kc, vc = (torch.nan_to_num(x.float(), 0, 0, 0) for x in (kc, vc))
+    ref = draft_reference(want, parent, q, kc, vc, ids, prefix)
+    err = (o[:rows].double() - ref[0]).abs()
+    assert (err[~hit] <= error_bound(ref, shape[2], shape[4])[~hit]).all()
+    assert not torch.isfinite(o[:rows][hit]).any()
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (16, 1, 128, 16, "bf16")], ids=str)
+def test_pairs_with_bad_block_ids(rbkv, shape):
+    """The first block of the first sequence (a call's first tile) and the last of others."""
+    t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, 0, *WIDE, pad=1)
+    parent = random_trees(np.random.default_rng(2), WIDE[1], t.max_tokens)
+    d = rbkv.StepDraft(t).plan(i32(parent))
+    gone = [(0, 0), (2, 2063 // shape[3]), (5, 100 // shape[3])]
+    table = want.table.copy()
+    for s, c in gone:
+        table[s, c] = 10 ** 6
+    t.block_table.copy_(i32(table))
+    o = t.attention(q.cuda(), kd, vd, draft=d).cpu()[:rows].double()
+    assert _status(rbkv, t) == BOUNDS
+    own = torch.zeros(rows, dtype=torch.bool)
+    for s, c in gone:
+        own[int(want.q_start[s]):int(want.q_start[s + 1])] = True
+    ref = draft_reference(want, parent, q, kc, vc, ids, 0)
+    err = (o - ref[0]).abs()
+    assert (err[~own] <= error_bound(ref, shape[2], shape[4])[~own]).all()
+    assert torch.isfinite(o).all() and (err[own] > 0).any()
+
+
 @pytest.mark.parametrize("shape", [(32, 8, 128, 64, "bf16"), (8, 2, 64, 16, "f32")], ids=str)
 def test_tensors_on_16_byte_addresses(rbkv, shape):
     t, want, q, kd, vd, kc, vc, ids, rows = _case(rbkv, *shape, 0, *TREES, pad=1)
