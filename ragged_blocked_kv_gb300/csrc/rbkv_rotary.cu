@@ -16,7 +16,8 @@
 // is two 16-byte vectors that hold both elements of their pairs (so that q_out may
 // be q); a thread has the same units' column in every few heads, and so keeps its
 // pairs' turns in registers.  Values and the elements behind R are only copied.
-// Where R / 2 elements are not whole vectors a unit is one pair (kVec = 1).
+// Where R / 2 elements are not whole vectors the words are narrower, down to one
+// element (kVec = 1).
 //
 // Bound by memory and, in few rows, by the call: 2048 rows of 32 and 8 heads of
 // 128, bf16, 50 MB, 10.6 us (4.8 TB/s with the launch; the copy alone would take
@@ -86,6 +87,38 @@ template <> struct Unit<float, 4> {
     turn(beside ? a.z : a.y, beside ? a.w : b.y, t[1]);
     turn(beside ? b.x : a.z, beside ? b.y : b.z, t[2]);
     turn(beside ? b.z : a.w, b.w, t[3]);
+  }
+};
+template <> struct Unit<__nv_bfloat16, 2> {
+  using Word = uint32_t;
+  static __device__ __forceinline__ void rotate(uint32_t& a, uint32_t& b, const float2* t,
+                                                bool beside) {
+    float x0 = low(a), x1 = high(a), y0 = low(b), y1 = high(b);
+    turn(x0, beside ? x1 : y0, t[0]);
+    turn(beside ? y0 : x1, y1, t[1]);
+    a = ptx::pack_bf16x2(x0, x1);
+    b = ptx::pack_bf16x2(y0, y1);
+  }
+};
+template <> struct Unit<__nv_bfloat16, 4> {
+  using Word = uint2;
+  static __device__ __forceinline__ void rotate(uint2& a, uint2& b, const float2* t,
+                                                bool beside) {
+    if (beside) {
+      Unit<__nv_bfloat16, 2>::rotate(a.x, a.y, t, true);
+      Unit<__nv_bfloat16, 2>::rotate(b.x, b.y, t + 2, true);
+    } else {
+      Unit<__nv_bfloat16, 2>::rotate(a.x, b.x, t, false);
+      Unit<__nv_bfloat16, 2>::rotate(a.y, b.y, t + 2, false);
+    }
+  }
+};
+template <> struct Unit<float, 2> {
+  using Word = float2;
+  static __device__ __forceinline__ void rotate(float2& a, float2& b, const float2* t,
+                                                bool beside) {
+    turn(a.x, beside ? a.y : b.x, t[0]);
+    turn(beside ? b.x : a.y, b.y, t[1]);
   }
 };
 template <> struct Unit<__nv_bfloat16, 1> {
@@ -273,10 +306,18 @@ cudaError_t launch_append_rotary(const DevPass& dp, const ShapeInfo& s, const rb
                                  const void* v_new, void* k_cache, void* v_cache, cudaStream_t st,
                                  bool overlap_previous) {
   if (dp.num_tokens == 0) return cudaSuccess;
-  // both vectors of a unit lie among the rotated elements, or both behind them
-  const bool vectors = r.rotary_dim % (s.dtype == 0 ? 16 : 8) == 0;
-  auto fn = s.dtype == 0 ? (vectors ? launch<__nv_bfloat16, 8> : launch<__nv_bfloat16, 1>)
-                         : (vectors ? launch<float, 4> : launch<float, 1>);
+  // the widest words of which both of a unit lie among the rotated elements, or both
+  // behind them (512 rows of 32 and 8 heads of 128, bf16: 20 elements rotated in words
+  // of one 10.4 us, of two 6.9, the call's own time; 24 in words of four 7.0)
+  const int R = r.rotary_dim;
+  auto fn = launch<float, 1>;
+  if (s.dtype == 0)
+    fn = R % 16 == 0  ? launch<__nv_bfloat16, 8>
+         : R % 8 == 0 ? launch<__nv_bfloat16, 4>
+         : R % 4 == 0 ? launch<__nv_bfloat16, 2>
+                      : launch<__nv_bfloat16, 1>;
+  else
+    fn = R % 8 == 0 ? launch<float, 4> : R % 4 == 0 ? launch<float, 2> : launch<float, 1>;
   return fn(dp, s, r, offset, q, q_out, k_new, v_new, k_cache, v_cache, st, overlap_previous);
 }
 

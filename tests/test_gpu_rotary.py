@@ -16,7 +16,8 @@ SHAPES = [((8, 2, 64, 16, "f32"), 64), ((4, 4, 32, 5, "f32"), 8), ((3, 1, 256, 1
           ((8, 2, 64, 16, "bf16"), 16), ((6, 2, 96, 24, "bf16"), 24), ((6, 2, 96, 24, "bf16"), 96),
           ((32, 8, 128, 64, "bf16"), 128), ((32, 32, 128, 64, "bf16"), 64),
           ((64, 1, 128, 16, "bf16"), 20), ((5, 5, 32, 7, "f32"), 2), ((10, 2, 160, 32, "bf16"), 80),
-          ((8, 8, 64, 16, "f32"), 20)]
+          ((8, 8, 64, 16, "f32"), 20), ((8, 8, 64, 16, "f32"), 22), ((8, 2, 64, 16, "bf16"), 6),
+          ((4, 1, 128, 8, "bf16"), 40), ((4, 1, 128, 8, "bf16"), 124)]
 
 
 def _rope(rbkv, R, layout, **kw):
