@@ -8,7 +8,6 @@ import numpy as np
 import torch
 
 import oracle
-from step_harness import i32
 
 
 def random_tree(rng, n):
@@ -98,7 +97,3 @@ def rotary_bound(x, position, theta, layout, scale, exact, dtype):
     bound[..., a] = bound[..., b] = pair
     out = 2.0 ** -8 if dtype == "bf16" else u
     return bound * (1 + 2 * out) + out * np.abs(exact) * (np.arange(x.shape[-1]) < R) + 1e-37
-
-
-def put(array):
-    return i32(array)
