@@ -447,7 +447,25 @@ def kv_append(p: Pass, k_new, v_new, k_cache, v_cache, stream=None) -> None:
                                 _stream(stream)))
 
 
-class Rotary:
+class _Arrays:
+    """An object whose device arrays the library holds by address."""
+
+    _HELD = frozenset()
+    _HOW = "write into it (copy_, fill_, ...)"
+
+    def __setattr__(self, name, value):
+        # (plain attributes, for fast reads: a small step's time is the host's)
+        if name in self._HELD and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} cannot be replaced: {self._HOW}")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._HELD:
+            raise AttributeError(f"{name} cannot be deleted")
+        object.__delattr__(self, name)
+
+
+class Rotary(_Arrays):
     """A rotary position embedding: the table of its angles per position, on the GPU.
 
     Pair i of a head's first ``rotary_dim`` elements (i and i + rotary_dim / 2 for
@@ -464,10 +482,13 @@ class Rotary:
         q = t.append_rotary(rope, q, k_new, v_new, k_cache, v_cache)
 
     Angles are kept as 64-bit fractions of a turn: far positions lose nothing.  The
-    table is written by the stream that is current here, in the constructor.
+    table is written by the stream that is current here, in the constructor.  Calls hold
+    its address and the other values as they were then: for others make another Rotary.
     """
 
     LAYOUTS = {"half": 0, "interleaved": 1}
+    _HELD = frozenset(("rotary_dim", "layout", "scale", "inv_freq", "turns"))
+    _HOW = "make another Rotary"
 
     def __init__(self, rotary_dim: int, base: float = 10000.0, layout: str = "half",
                  scaling: str = "none", factor: float = 1.0, original_length: int = 0,
@@ -480,7 +501,7 @@ class Rotary:
         if layout not in self.LAYOUTS:
             raise ValueError("layout must be 'half' or 'interleaved'")
         if inv_freq is not None:
-            theta = np.asarray(inv_freq, np.float64)
+            theta = np.array(inv_freq, np.float64)
             if theta.shape != (self.rotary_dim // 2,) or not np.isfinite(theta).all():
                 raise ValueError("inv_freq must be rotary_dim / 2 finite values")
             if scaling != "none":
@@ -493,6 +514,7 @@ class Rotary:
                 raise ValueError("angles per position are out of range") from None
         if not (np.abs(theta) < 2.0 ** 900).all():
             raise ValueError("angles per position are out of range")
+        theta.setflags(write=False)
         self.inv_freq = theta
         turns = [round(math.ldexp(float(x) / (2 * math.pi), 64)) % 2 ** 64 for x in theta]
         self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns],
@@ -684,23 +706,6 @@ class Frame:
             self.close()
         except Exception:
             pass
-
-
-class _Arrays:
-    """An object whose device arrays the library holds by address."""
-
-    _HELD = frozenset()
-
-    def __setattr__(self, name, value):
-        # (plain attributes, for fast reads: a small step's time is the host's)
-        if name in self._HELD and self.__dict__.get(name, value) is not value:
-            raise AttributeError(f"{name} cannot be replaced: write into it (copy_, fill_, ...)")
-        object.__setattr__(self, name, value)
-
-    def __delattr__(self, name):
-        if name in self._HELD:
-            raise AttributeError(f"{name} cannot be deleted")
-        object.__delattr__(self, name)
 
 
 class StepTables(_Arrays):

@@ -1,0 +1,31 @@
+"""What a Rotary holds, without a GPU."""
+import numpy as np
+import pytest
+
+OTHERS = {"rotary_dim": 32, "layout": "interleaved", "scale": 2.0,
+          "inv_freq": np.ones(32), "turns": None}
+
+
+@pytest.mark.parametrize("name", OTHERS)
+def test_what_calls_hold_cannot_be_replaced(rbkv, name):
+    """Calls hold the table's address, and the values as they were: a replaced table would be
+    read after it was freed, a replaced value not at all."""
+    r = rbkv.Rotary(64, device="cpu")
+    before, held = getattr(r, name), r._c._obj.turns
+    with pytest.raises(AttributeError, match="make another Rotary"):
+        setattr(r, name, before.clone() if name == "turns" else OTHERS[name])
+    with pytest.raises(AttributeError, match="cannot be deleted"):
+        delattr(r, name)
+    assert getattr(r, name) is before and held == r.turns.data_ptr()
+    setattr(r, name, before)                             # (itself: nothing changes)
+
+
+def test_angles_are_the_objects_own(rbkv):
+    """The table is made from a copy of what is given, and the copy does not change."""
+    given = np.array([1.0, 0.5])
+    r = rbkv.Rotary(4, inv_freq=given, device="cpu")
+    given[0] = 3.0
+    assert r.inv_freq.tolist() == [1.0, 0.5]
+    for x in (r, rbkv.Rotary(4, device="cpu")):
+        with pytest.raises(ValueError):
+            x.inv_freq[0] = 2.0
