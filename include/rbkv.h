@@ -286,7 +286,7 @@ typedef struct {
   const uint64_t* turns;
   int32_t rotary_dim;    /* even, 2 .. head_dim */
   int32_t interleaved;   /* 0 or 1 */
-  float scale;
+  float scale;           /* finite */
 } rbkv_rotary;
 
 /* rbkv_kv_append with the rotation on the way: k_cache receives the rotated

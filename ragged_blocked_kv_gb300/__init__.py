@@ -500,6 +500,8 @@ class Rotary(_Arrays):
             raise ValueError("rotary_dim must be even, in [2, 256]")
         if layout not in self.LAYOUTS:
             raise ValueError("layout must be 'half' or 'interleaved'")
+        if not math.isfinite(C.c_float(self.scale).value):
+            raise ValueError("scale must be finite in fp32")
         if inv_freq is not None:
             theta = np.array(inv_freq, np.float64)
             if theta.shape != (self.rotary_dim // 2,) or not np.isfinite(theta).all():

@@ -25,6 +25,7 @@
 // every unit 12.4 us, all of a unit's elements as fp32 at once 11.8, four units in
 // flight instead of three (48 heads are three to a thread) 12.8, two 12.2.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <string>
 
@@ -274,6 +275,7 @@ rbkv_status check_append_rotary(const rbkv_config* c, const rbkv_rotary* r, int6
   if (r->rotary_dim < 2 || r->rotary_dim > c->head_dim || r->rotary_dim % 2)
     return invalid("rotary_dim must be even, in [2, head_dim]");
   if (r->interleaved != 0 && r->interleaved != 1) return invalid("interleaved must be 0 or 1");
+  if (!std::isfinite(r->scale)) return invalid("scale must be finite");
   const void* all[] = {q, q_out, k_new, v_new, k_cache, v_cache};
   for (const void* p : all) {
     if (!p) return invalid("NULL tensor");

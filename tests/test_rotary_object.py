@@ -1,6 +1,11 @@
 """What a Rotary holds, without a GPU."""
+import math
+
 import numpy as np
 import pytest
+
+from test_draft_host import _append, _rotary
+from test_step_host import INVALID
 
 OTHERS = {"rotary_dim": 32, "layout": "interleaved", "scale": 2.0,
           "inv_freq": np.ones(32), "turns": None}
@@ -29,3 +34,17 @@ def test_angles_are_the_objects_own(rbkv):
     for x in (r, rbkv.Rotary(4, device="cpu")):
         with pytest.raises(ValueError):
             x.inv_freq[0] = 2.0
+
+
+@pytest.mark.parametrize("scale", [math.nan, math.inf, -math.inf, 1e39, -1e300])
+def test_scales_that_are_not_finite_are_refused(rbkv, scale):
+    """(in fp32, the type that calls take)"""
+    with pytest.raises(ValueError, match="scale must be finite"):
+        rbkv.Rotary(64, scale=scale, device="cpu")
+    assert _append(rbkv, r=_rotary(rbkv, scale=scale)) == INVALID
+    assert b"scale" in rbkv.lib().rbkv_last_error()
+
+
+def test_scales_that_are_finite(rbkv):
+    for scale in (0.0, -1.5, 3e38, 1e-45):
+        assert rbkv.Rotary(64, scale=scale, device="cpu").scale == scale
