@@ -521,9 +521,21 @@ class Rotary(_Arrays):
         turns = [round(math.ldexp(float(x) / (2 * math.pi), 64)) % 2 ** 64 for x in theta]
         self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns],
                                   dtype=torch.int64, device=device)
-        self._c = C.byref(_Rotary(self.turns.data_ptr(), self.rotary_dim, self.LAYOUTS[layout],
-                                  self.scale))
+        self._bind()
+
+    def _bind(self):
+        self._c = C.byref(_Rotary(self.turns.data_ptr(), self.rotary_dim,
+                                  self.LAYOUTS[self.layout], self.scale))
         self._device = self.turns.device
+
+    # (copies hold the address of their own table)
+    def __getstate__(self):
+        return {name: self.__dict__[name] for name in self._HELD}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self.inv_freq.setflags(write=False)
+        self._bind()
 
     def _theta(self, base, scaling, factor, original_length, low, high):
         R = self.rotary_dim

@@ -1,9 +1,12 @@
 """What a Rotary holds, without a GPU."""
+import copy
 import math
+import pickle
 
 import numpy as np
 import pytest
 
+from ragged_blocked_kv_gb300.layer import DecoderLayer
 from test_draft_host import _append, _rotary
 from test_step_host import INVALID
 
@@ -48,3 +51,28 @@ def test_scales_that_are_not_finite_are_refused(rbkv, scale):
 def test_scales_that_are_finite(rbkv):
     for scale in (0.0, -1.5, 3e38, 1e-45):
         assert rbkv.Rotary(64, scale=scale, device="cpu").scale == scale
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))],
+                         ids=["copy", "deepcopy", "pickle"])
+def test_copies_hold_their_own_table(rbkv, how):
+    r = rbkv.Rotary(64, layout="interleaved", scale=1.5, device="cpu")
+    s = how(r)
+    want = (r.turns.tolist(), r.inv_freq.tolist(), 64, "interleaved", 1.5)
+    mine = s.turns.data_ptr()
+    assert (mine == r.turns.data_ptr()) == (how is copy.copy)
+    del r
+    assert (s.turns.tolist(), s.inv_freq.tolist(), s.rotary_dim, s.layout, s.scale) == want
+    c = s._c._obj
+    assert (c.turns, c.rotary_dim, c.interleaved, c.scale) == (mine, 64, 1, 1.5)
+    with pytest.raises(AttributeError, match="make another Rotary"):
+        s.turns = s.turns.clone()
+    with pytest.raises(ValueError):
+        s.inv_freq[0] = 2.0
+
+
+def test_a_layer_with_rotary_positions_can_be_copied(rbkv):
+    layer = DecoderLayer(None, {}, 2, 1, 64, rotary=rbkv.Rotary(64, device="cpu"))
+    other = copy.deepcopy(layer)
+    assert other.rotary.turns.tolist() == layer.rotary.turns.tolist()
+    assert other.rotary._c._obj.turns == other.rotary.turns.data_ptr()
