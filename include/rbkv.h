@@ -686,8 +686,9 @@ rbkv_status rbkv_step_attention_draft(const rbkv_config* cfg, const rbkv_step_ta
  * to the free bits.  The slots and the tables of the step stay as they are
  * until the next build.  given out of range is recorded as RBKV_ERR_INVALID and
  * taken for the nearest allowed; so is a step whose trees were not planned,
- * which is left alone.  A second call for the same step has to come before any
- * other call that takes blocks. */
+ * which is left alone.  Another acceptance of the same step takes this one's
+ * place, blocks that it keeps held again: it has to come before any other call
+ * that takes blocks, and before the kept rows are moved. */
 rbkv_status rbkv_step_draft_accept(const rbkv_config* cfg, const rbkv_step_tables* t,
                                    const rbkv_step_draft* d, const int32_t* tokens,
                                    const int32_t* chosen, const int32_t* given,

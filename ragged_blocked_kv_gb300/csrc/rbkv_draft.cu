@@ -358,16 +358,24 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) draft_accept_kernel(DraftAr
       a.next_token[s] = next;
       a.ctx[s] = seen + kept;
     }
-    // blocks behind the kept tokens (an or: the order does not matter)
+    // The step's new blocks: those behind the kept tokens are free, the others held
+    // (an earlier acceptance of this step may have freed them).  Bits that no other
+    // warp changes: the order does not matter.
     const uint32_t B = (uint32_t)a.block_size;
+    const int first = (int)(((uint32_t)seen + B - 1) / B);
     const int from = (int)(((uint32_t)(seen + kept) + B - 1) / B);
     const int to = (int)(((uint32_t)(seen + n) + B - 1) / B);
-    for (int c = from + lane; c < to; c += 32) {
+    for (int c = first + lane; c < to; c += 32) {
       const int32_t id = a.table[(int64_t)s * a.max_blocks + c];
-      if (id < 0 || id >= a.num_blocks)
+      if (id < 0 || id >= a.num_blocks) {
         atomicCAS(a.status, 0, kDevBounds);
+        continue;
+      }
+      unsigned int* word = (unsigned int*)&a.free_words[id >> 5];
+      if (c < from)
+        atomicAnd(word, ~(1u << (id & 31)));
       else
-        atomicOr((unsigned int*)&a.free_words[id >> 5], 1u << (id & 31));
+        atomicOr(word, 1u << (id & 31));
     }
   }
 }

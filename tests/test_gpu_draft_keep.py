@@ -1,0 +1,76 @@
+"""What an acceptance of drafted tokens keeps, and what it gives back."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from step_harness import free_words, i32
+from test_gpu_draft import _built
+
+pytestmark = pytest.mark.gpu
+D = oracle.draft
+
+
+def _kept(t, d, done):
+    assert np.array_equal(d.path.cpu().numpy(), done.path)
+    assert d.accepted.tolist() == done.accepted.tolist()
+    assert d.next_token.tolist() == done.next_token.tolist()
+    assert t.ctx.tolist() == done.ctx.tolist()
+    assert np.array_equal(t.free.cpu().numpy(), free_words(done.free))
+
+
+def _built_again(rng, t, done, last, seen, n_new, block):
+    """The next step (no longer than the last): tables, no block held twice or held and
+    free."""
+    n_new = np.array([rng.integers(0, min(n, a + n - int(c)) + 1)
+                      for a, n, c in zip(seen, n_new, done.ctx)])
+    want = oracle.step.build(done.ctx, n_new, last.table, done.free, block, t.max_tokens)
+    assert want.status == 0
+    t.build(t.ctx, i32(n_new))
+    t.device_status()
+    assert t.ctx.tolist() == want.ctx.tolist()
+    assert np.array_equal(t.free.cpu().numpy(), free_words(want.free))
+    assert np.array_equal(t.slot.cpu().numpy(), want.slot)
+    held = [t.block_table[s, :-(-int(c) // block)] for s, c in enumerate(want.ctx)]
+    held = torch.cat(held).tolist()
+    assert len(held) == len(set(held)) and not any(want.free[b] for b in held)
+
+
+# ---- a second acceptance -----------------------------------------------------------
+KEEP = [([0], [128]), ([60, 5, 31, 0], [90, 300, 20, 0]), ([7, 8, 9, 16], [17, 16, 1, 40]),
+        ([20] * 200, [9] * 200)]
+
+
+@pytest.mark.parametrize("seen,n_new", KEEP, ids=lambda x: str(len(x)))
+@pytest.mark.parametrize("block", [1, 8, 64])
+def test_another_acceptance_of_the_same_step(rbkv, seen, n_new, block):
+    """Short, long and short paths in turn: what is held and what is free goes by the last."""
+    t, want, rng = _built(rbkv, seen, n_new, block=block, seed=block)
+    T = t.max_tokens
+    parent = np.concatenate([D.chain(n) for n in n_new] + [[-1] * (T - sum(n_new))])
+    parent = parent.astype(np.int64)
+    d = rbkv.StepDraft(t).plan(i32(parent))
+    tokens = rng.integers(0, 5, T)
+    follow = np.concatenate([tokens[1:], [9]])           # (a chain's choices that all agree)
+    half = np.where(rng.random(T) < 0.5, follow, 9)
+    some = np.array([rng.integers(1, n + 1) if n else 0 for n in n_new])
+    for chosen, given in ((tokens + 9, None), (follow, None), (half, None), (follow, some),
+                          (tokens + 9, some), (half, None)):
+        done = D.accept(want, parent, tokens, chosen, given, block)
+        d.accept(i32(tokens), i32(chosen), None if given is None else i32(given))
+        _kept(t, d, done)
+    t.device_status()
+    _built_again(rng, t, done, want, seen, n_new, block)
+
+
+def test_two_drafts_of_one_step_accept(rbkv):
+    """Another draft of the same step, planned and accepted after the first."""
+    t, want, rng = _built(rbkv, [3, 40], [60, 50], block=8)
+    parent = np.concatenate([D.chain(60), D.chain(50)])
+    tokens = np.arange(t.max_tokens)
+    for chosen in (tokens, tokens + 1, tokens):
+        d = rbkv.StepDraft(t).plan(i32(parent))
+        d.accept(i32(tokens), i32(chosen))
+        done = D.accept(want, parent, tokens, chosen, None, 8)
+        _kept(t, d, done)
+    t.device_status()
