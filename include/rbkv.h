@@ -688,7 +688,8 @@ rbkv_status rbkv_step_attention_draft(const rbkv_config* cfg, const rbkv_step_ta
  * taken for the nearest allowed; so is a step whose trees were not planned,
  * which is left alone.  Another acceptance of the same step takes this one's
  * place, blocks that it keeps held again: it has to come before any other call
- * that takes blocks, and before the kept rows are moved. */
+ * that takes blocks, and before the kept rows are moved.  A sequence that has
+ * been released since the build keeps nothing (accepted 0, next_token -1). */
 rbkv_status rbkv_step_draft_accept(const rbkv_config* cfg, const rbkv_step_tables* t,
                                    const rbkv_step_draft* d, const int32_t* tokens,
                                    const int32_t* chosen, const int32_t* given,

@@ -74,7 +74,9 @@ class Accepted:
     free: List[bool]
 
 
-def accept(step: Step, parent, tokens, chosen, given, block_size: int) -> Accepted:
+def accept(step: Step, parent, tokens, chosen, given, block_size: int,
+           released=()) -> Accepted:
+    """``released``: sequences given back since the build, which keep nothing."""
     S = len(step.ctx)
     path = np.full(len(tokens), -1)
     accepted, last = np.zeros(S, np.int64), np.full(S, -1)
@@ -83,6 +85,11 @@ def accept(step: Step, parent, tokens, chosen, given, block_size: int) -> Accept
         p, _ = parents_of(step, parent, s)
         q0, n = int(step.q_start[s]), len(p)
         if n == 0:
+            continue
+        if s in released:
+            ctx[s] = 0
+            for c in range(-(-int(step.ctx[s]) // block_size)):
+                free[int(step.table[s, c])] = True
             continue
         g = 1 if given is None else min(max(int(given[s]), 1), n)
         kept = list(range(g))

@@ -974,7 +974,8 @@ class StepDraft(_Arrays):
         sequence s that are not drafted (a prompt chunk: all of them).  From the last
         given token the path goes on to the lowest child that is the chosen token.
         Cuts ``t.ctx`` back to the kept tokens and frees the blocks behind them.  Another
-        acceptance before the next build, and before ``compact``, takes its place."""
+        acceptance before the next build, and before ``compact``, takes its place.  A
+        sequence released since the build keeps nothing."""
         t, i32 = self.tables, self.tables._i32
         t._call(self._f_accept, self._d, t._ptr(tokens, "tokens", i32, self._rows),
                 t._ptr(chosen, "chosen", i32, self._rows),

@@ -218,8 +218,11 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) draft_accept_kernel(DraftAr
     a.path[r] = -1;
   const int warps = gridDim.x * kAcceptWarps;
   for (int s = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5); s < a.num_seqs; s += warps) {
-    const int q0 = a.q_start[s], n = a.q_start[s + 1] - q0;
-    if (n == 0) {
+    const int q0 = a.q_start[s], n = a.q_start[s + 1] - q0, length = a.ctx[s];
+    // (a sequence with new tokens has a length, unless it has been released since: its
+    // blocks are free, and it keeps nothing)
+    if (n == 0 || length == 0) {
+      for (int i = lane; i < n; i += 32) a.path[q0 + i] = -1;
       if (lane == 0) {
         a.accepted[s] = 0;
         a.next_token[s] = -1;

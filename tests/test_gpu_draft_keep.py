@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import oracle
+from draft_harness import random_trees
 from step_harness import free_words, i32
 from test_gpu_draft import _built
 
@@ -74,3 +75,31 @@ def test_two_drafts_of_one_step_accept(rbkv):
         done = D.accept(want, parent, tokens, chosen, None, 8)
         _kept(t, d, done)
     t.device_status()
+
+
+# ---- released sequences ------------------------------------------------------------
+@pytest.mark.parametrize("again", [False, True])
+@pytest.mark.parametrize("seen,n_new", KEEP, ids=lambda x: str(len(x)))
+def test_a_released_sequence_keeps_nothing(rbkv, seen, n_new, again):
+    """Released between the build and the acceptance, or between two: its blocks stay free,
+    its length 0, nothing of it is moved, and the next step may take its slot."""
+    block, S = 8, len(n_new)
+    t, want, rng = _built(rbkv, seen, n_new, block=block, seed=S, cfg=(8, 2, 64))
+    T = t.max_tokens
+    parent, tokens = random_trees(rng, n_new, T), np.zeros(T, np.int64)
+    d = rbkv.StepDraft(t).plan(i32(parent))
+    if again:
+        d.accept(i32(tokens), i32(tokens))
+    gone = np.arange(S) % 3 == 0
+    t.release(i32(gone))
+    done = D.accept(want, parent, tokens, tokens, None, block, released=np.flatnonzero(gone))
+    caches = [torch.randn(t.config.cache_shape()) for _ in range(2)]
+    dev = [c.cuda() for c in caches]
+    d.accept(i32(tokens), i32(tokens))
+    _kept(t, d, done)
+    d.compact(*dev)
+    for c, x in zip(caches, dev):
+        D.compact(want, done, c, block)
+        assert torch.equal(c, x.cpu())
+    t.device_status()
+    _built_again(rng, t, done, want, seen, n_new, block)
