@@ -658,8 +658,9 @@ rbkv_status rbkv_step_draft_plan(const rbkv_config* cfg, const rbkv_step_tables*
 /* rbkv_step_append with the rotation on the way, as rbkv_kv_append_rotary, by
  * the positions prefix_len + position[r], or prefix_len + place[r] when d is
  * not NULL (the trees must have been planned: else nothing is written and
- * RBKV_ERR_INVALID recorded).  q, q_out: [max_tokens][H_q][D]; rows past the
- * step's are neither read nor written. */
+ * RBKV_ERR_INVALID recorded).  Trees need d: a kept token comes to lie at its
+ * place, which is not its row's position.  q, q_out: [max_tokens][H_q][D]; rows
+ * past the step's are neither read nor written. */
 rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tables* t,
                                     const rbkv_step_draft* d, const rbkv_rotary* rotary,
                                     int32_t prefix_len, const void* q, void* q_out,
@@ -681,7 +682,11 @@ rbkv_status rbkv_step_attention_draft(const rbkv_config* cfg, const rbkv_step_ta
  * chosen to follow it.  The first given[s] new tokens of sequence s (in [1,
  * new tokens]; NULL: 1 each) are kept as they are; from the last of them the
  * path goes on to the lowest child whose token is the chosen one, until there
- * is none.  Writes path, accepted and next_token, sets ctx[s] to the tokens
+ * is none.  (Rows that rbkv_step_append_rotary turned by their places lie there
+ * only if the given tokens are a chain, each following the one before it: the
+ * first that does not, and those behind it, are then not given, and
+ * RBKV_ERR_INVALID is recorded.  Other rows are kept in the order they came in.)
+ * Writes path, accepted and next_token, sets ctx[s] to the tokens
  * cached before the step plus the kept ones, and returns the blocks behind them
  * to the free bits.  The slots and the tables of the step stay as they are
  * until the next build.  given out of range is recorded as RBKV_ERR_INVALID and

@@ -74,9 +74,11 @@ class Accepted:
     free: List[bool]
 
 
-def accept(step: Step, parent, tokens, chosen, given, block_size: int,
-           released=()) -> Accepted:
-    """``released``: sequences given back since the build, which keep nothing."""
+def accept(step: Step, parent, tokens, chosen, given, block_size: int, released=(),
+           turned: bool = False) -> Accepted:
+    """``released``: sequences given back since the build, which keep nothing.  ``turned``:
+    the rows were rotated by their places, so that given tokens are kept as far as each
+    follows the one before it."""
     S = len(step.ctx)
     path = np.full(len(tokens), -1)
     accepted, last = np.zeros(S, np.int64), np.full(S, -1)
@@ -92,6 +94,8 @@ def accept(step: Step, parent, tokens, chosen, given, block_size: int,
                 free[int(step.table[s, c])] = True
             continue
         g = 1 if given is None else min(max(int(given[s]), 1), n)
+        if turned:
+            g = next((i for i in range(1, g) if p[i] != i - 1), g)
         kept = list(range(g))
         while True:
             at = kept[-1]

@@ -972,7 +972,10 @@ class StepDraft(_Arrays):
         """Keep a path of every tree.  ``tokens[r]``: the token of row r; ``chosen[r]``:
         the one chosen to follow it; ``given[s]`` (1 each): leading new tokens of
         sequence s that are not drafted (a prompt chunk: all of them).  From the last
-        given token the path goes on to the lowest child that is the chosen token.
+        given token the path goes on to the lowest child that is the chosen token.  Rows
+        turned by ``append_rotary(draft=...)``: given tokens have to be a chain, each
+        following the one before it (those behind the first that does not are not given,
+        and ``t.device_status`` says so).
         Cuts ``t.ctx`` back to the kept tokens and frees the blocks behind them.  Another
         acceptance before the next build, and before ``compact``, takes its place.  A
         sequence released since the build keeps nothing."""

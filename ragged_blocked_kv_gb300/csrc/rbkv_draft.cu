@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) draft_accept_kernel(DraftAr
   if (blockIdx.x == 0 && threadIdx.x == 0)
     reinterpret_cast<StepLanes*>(a.work)->pair_cum = plan.header[kPlanSerial];
   const int T = plan.header[kPlanRows];
+  const bool turned = plan.header[kPlanTurned] == plan.header[kPlanSerial];
   for (int64_t r = T + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.max_tokens;
        r += (int64_t)gridDim.x * blockDim.x)
     a.path[r] = -1;
@@ -252,6 +253,22 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) draft_accept_kernel(DraftAr
           parent[x] = parent_of(set[x], i);
           token[x] = a.tokens[q0 + i];
           chosen[x] = a.chosen[q0 + i];
+        }
+      }
+      // Rows that were rotated by their places: a given token that does not follow the one
+      // before it would come to lie at another position.
+      if (turned && given > 1) {
+        int chain = given;
+#pragma unroll
+        for (int x = 3; x >= 0; --x) {
+          const int i = lane + 32 * x;
+          const uint32_t v = __ballot_sync(kAll, i >= 1 && i < given && parent[x] != i - 1);
+          if (v) chain = 32 * x + __ffs(v) - 1;
+        }
+        if (chain < given) {
+          if (lane == 0) atomicCAS(a.status, 0, kDevInvalid);
+          kept = given = chain;
+          cur = given - 1;
         }
       }
       // M, and the path

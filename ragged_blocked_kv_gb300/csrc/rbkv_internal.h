@@ -119,6 +119,9 @@ struct DevPass {
   // that it was built for, to be compared with what it is used with; and for
   // drafted tokens the serials of the build and of their plan.  Null otherwise.
   const int32_t* built_for[4];
+  // Where the append notes the build whose rows it rotates by the places of drafted
+  // tokens.  Null otherwise.
+  int32_t* turned;
 };
 
 enum { kCountTokens = 0, kCountDecode = 1, kCountGeneric = 2, kCountChunk = 3, kCountCombine = 4 };

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 8)
     if (tid == 0 && rows > 0) atomicCAS(dp.status, 0, kDevInvalid);
     return;
   }
+  if (dp.turned && blockIdx.x == 0 && tid == 0) *dp.turned = *dp.built_for[2];
   // A thread's units: one column of every `step`-th head (of Q's, then K's, then V's)
   const int step = kThreads / h.per, heads = h.q + 2 * h.kv, half = r.rotary_dim / 2;
   const int head0 = tid / h.per, col = tid - head0 * h.per;

@@ -370,6 +370,7 @@ rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tabl
     dp.position = d->place;
     dp.built_for[2] = t->plan + kPlanSerial;
     dp.built_for[3] = d->work;
+    dp.turned = t->plan + kPlanTurned;
   }
   cudaError_t e = launch_append_rotary(dp, s, *rotary, prefix_len, q, q_out, k_new, v_new, k_cache,
                                        v_cache, (cudaStream_t)stream, true);

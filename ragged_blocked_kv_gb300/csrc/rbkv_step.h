@@ -46,6 +46,7 @@ enum {
   kPlanMaxBlocks = 9,
   kPlanPool = 10,       // blocks of the pool
   kPlanSerial = 11,     // builds so far
+  kPlanTurned = 12,     // serial of the last build whose rows were rotated by their places
   kPlanHeader = 16
 };
 

@@ -6,7 +6,8 @@ import torch
 import oracle
 from draft_harness import random_trees
 from step_harness import free_words, i32
-from test_gpu_draft import _built
+from test_gpu_draft import _built, _status
+from test_gpu_step import INVALID
 
 pytestmark = pytest.mark.gpu
 D = oracle.draft
@@ -103,3 +104,69 @@ def test_a_released_sequence_keeps_nothing(rbkv, seen, n_new, again):
         assert torch.equal(c, x.cpu())
     t.device_status()
     _built_again(rng, t, done, want, seen, n_new, block)
+
+
+# ---- given tokens that are no chain --------------------------------------------------
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("seen,n_new", KEEP + [([4, 9, 0], [3, 128, 33])],
+                         ids=lambda x: str(len(x)))
+def test_given_tokens_that_are_no_chain(rbkv, seen, n_new, turned):
+    """Rows that were rotated by their places: a given token that does not follow the one
+    before it would lie at another position than it was turned by.  So it, and what comes
+    after it, is no longer given, and the status says so.  Rows as they came are kept as
+    they are."""
+    block = 8
+    t, want, rng = _built(rbkv, seen, n_new, block=block, seed=7, cfg=(8, 2, 64))
+    T, rows = t.max_tokens, int(want.q_start[-1])
+    parent = random_trees(rng, n_new, T)
+    tokens, chosen = rng.integers(0, 2, T), rng.integers(0, 2, T)
+    caches = [torch.randn(t.config.cache_shape(), device="cuda") for _ in range(2)]
+    q, k, v = (torch.randn(T, h, 64, device="cuda") for h in (8, 2, 2))
+    d = rbkv.StepDraft(t)
+    rope = rbkv.Rotary(64)
+    for some in (np.array([min(n, 3) for n in n_new]), np.array([max(n - 1, min(n, 1)) for n in n_new]),
+                 np.array(n_new)):
+        d.plan(i32(parent))
+        if turned:
+            t.append_rotary(rope, q, k, v, *caches, draft=d)
+        else:
+            t.append(k, v, *caches)
+        d.accept(i32(tokens), i32(chosen), i32(some))
+        done = D.accept(want, parent, tokens, chosen, some, block, turned=turned)
+        _kept(t, d, done)
+        if not turned:
+            t.device_status()
+            continue
+        place = d.place.cpu().numpy()
+        for r in np.flatnonzero(done.path >= 0):
+            assert place[done.path[r]] == want.position[r]
+        if (D.accept(want, parent, tokens, chosen, some, block).path == done.path).all():
+            t.device_status()
+        else:
+            assert _status(rbkv, t) == INVALID
+    # a chain that is given is kept whole, with a chunk behind it
+    chains = np.concatenate([D.chain(n) for n in n_new] + [[0] * (T - rows)]).astype(np.int64)
+    d.plan(i32(chains))
+    t.append_rotary(rope, q, k, v, *caches, draft=d)
+    d.accept(i32(tokens), i32(tokens + 1), i32(n_new))
+    t.device_status()
+    assert d.accepted.tolist() == list(n_new)
+
+
+def test_rows_turned_in_an_earlier_step(rbkv):
+    """The rotation of the step before says nothing of this one's rows."""
+    t, want, rng = _built(rbkv, [0], [4], block=8, pad=4, cfg=(8, 2, 64))
+    caches = [torch.randn(t.config.cache_shape(), device="cuda") for _ in range(2)]
+    q, k, v = (torch.randn(t.max_tokens, h, 64, device="cuda") for h in (8, 2, 2))
+    d = rbkv.StepDraft(t)
+    tree, tokens = i32([-1, 0, 0, 0] + [0] * (t.max_tokens - 4)), i32([0] * t.max_tokens)
+    d.plan(tree)
+    t.append_rotary(rbkv.Rotary(64), q, k, v, *caches, draft=d)
+    d.accept(tokens, tokens + 1, i32([3]))
+    assert d.accepted.tolist() == [2] and _status(rbkv, t) == INVALID
+    t.build(t.ctx, i32([4]))
+    d.plan(tree)
+    t.append(k, v, *caches)
+    d.accept(tokens, tokens + 1, i32([3]))
+    t.device_status()
+    assert d.accepted.tolist() == [3] and t.ctx.tolist() == [5]
