@@ -103,8 +103,11 @@ class DecoderLayer:
 
     def forward_into(self, x, out, buf: dict, attend, rows: int, stream=None) -> None:
         """The layer on the first `rows` rows of fixed buffers: x -> out, with
-        attend(q, k, v, o) running the KV append (with the rotation, where positions
-        are rotary: self.rotary) and attention (a plain pass or a frame); allocates nothing, so it can be captured in a graph."""
+        attend(q, k, v, o) running the KV append and attention (a plain pass or a
+        frame); allocates nothing, so it can be captured in a graph.  With rotary
+        positions it is attend(q, k, v, o, rotary=...), and the append is
+        kv_append_rotary with these: a callback that takes none is refused
+        (TypeError)."""
         rb, w = self.rbkv, self.w
         T = rows
         a, h, b, act = buf["a"][:T], buf["h"][:T], buf["b"][:T], buf["act"][:T]
@@ -113,7 +116,10 @@ class DecoderLayer:
         ws = buf["gemm_ws"]
         rb.gemm_qkv(a, w["w_qkv"], self.hq, self.hkv, self.d, out=(q, k, v), workspace=ws,
                     stream=stream)
-        attend(q, k, v, o)
+        if self.rotary is None:
+            attend(q, k, v, o)
+        else:
+            attend(q, k, v, o, rotary=self.rotary)
         rb.gemm(o.view(T, self.hq * self.d), w["w_o"], c=h, residual=x, epilogue="residual",
                 workspace=ws, stream=stream)
         rb.rmsnorm(h, w["g_mlp"], y=b, eps=self.eps, stream=stream)
