@@ -672,10 +672,21 @@ rbkv_status ensure_plan(rbkv_pass* p) {
 }
 
 
-// Position of every pass row in its sequence.
+// Position of every pass row in its sequence (rows lie in sequence order).  Every load
+// of a frame pays for it, rotated or not (a captured append must find them): 512
+// decodes 12.5 us, 12.1 without positions; with a chunk of 1536 rows 15.8 and 15.2.
+// Written through q_start[i] + j, the vectors read anew for every row, 12.8 and 16.8.
 void fill_positions(const rbkv_pass& p, int32_t* out) {
-  for (size_t i = 0; i < p.seen.size(); ++i)
-    for (int32_t j = 0; j < p.n_new[i]; ++j) out[p.q_start[i] + j] = p.seen[i] + j;
+  const int32_t *seen = p.seen.data(), *n_new = p.n_new.data();
+  for (size_t i = 0, n = p.seen.size(); i < n; ++i) {
+    const int32_t at = seen[i], rows = n_new[i];
+    if (rows == 1) {
+      *out++ = at;
+      continue;
+    }
+    for (int32_t j = 0; j < rows; ++j) out[j] = at + j;
+    out += rows;
+  }
 }
 
 // Plan (if needed), pack and upload the metadata on `st`; order `st` after
