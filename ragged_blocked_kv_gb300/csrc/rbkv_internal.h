@@ -245,6 +245,11 @@ rbkv_status attention_on_device(rbkv_pass* p, const void* q, const void* k_cache
 rbkv_status set_error(rbkv_status st, const char* msg);
 // Whether the kernels can run this shape (records the message when not).
 rbkv_status check_config(const rbkv_config* c);
+// Whether the na bytes at a meet the nb bytes at b.
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
 // Wait for the stream, then read and clear four status words on the device.
 rbkv_status read_status_words(int32_t* words, cudaStream_t st);
 // Count n kernel launches made outside rbkv_host.cpp (rbkv_kernel_launches).

@@ -260,11 +260,6 @@ cudaError_t launch(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r, 
                             k_new, v_new, k_cache, v_cache);
 }
 
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
 }  // namespace
 
 rbkv_status check_append_rotary(const rbkv_config* c, const rbkv_rotary* r, int64_t rows,

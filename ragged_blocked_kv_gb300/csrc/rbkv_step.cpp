@@ -18,11 +18,6 @@ rbkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(RBKV_ERR_CUDA, (std::string(what) + ": " + cudaGetErrorString(e)).c_str());
 }
 
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 rbkv_status check_tables(const rbkv_config* c, const rbkv_step_tables* t) {
