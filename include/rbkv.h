@@ -704,7 +704,7 @@ rbkv_status rbkv_step_draft_accept(const rbkv_config* cfg, const rbkv_step_table
  * sequence's cached tokens: once per layer, after the acceptance and before the
  * next build (without an acceptance nothing is moved and RBKV_ERR_INVALID
  * recorded).  A second call on the same caches would move the moved rows.  The
- * two caches must not overlap. */
+ * caches overlap neither one another nor an array of the step. */
 rbkv_status rbkv_step_draft_compact(const rbkv_config* cfg, const rbkv_step_tables* t,
                                     const rbkv_step_draft* d, void* k_cache, void* v_cache,
                                     rbkv_stream stream);

@@ -149,6 +149,22 @@ bool written_by_draft(const rbkv_config* c, const rbkv_step_tables* t, const rbk
          overlap(p, 4 * n, d->work, 16 * (S + 1));
 }
 
+// Whether n bytes at p, which a call writes, meet an array of the step that it reads
+// or writes.  d: null without drafted tokens.
+bool meets_step(const rbkv_step_tables* t, const rbkv_step_draft* d, const void* p, int64_t n) {
+  const int64_t S = t->num_seqs, T = t->max_tokens;
+  return overlap(p, n, t->q_start, 4 * (S + 1)) || overlap(p, n, t->slot, 4 * T) ||
+         overlap(p, n, t->position, 4 * T) || overlap(p, n, t->plan, 4 * step_plan_ints(S, T)) ||
+         overlap(p, n, t->status, 16) ||
+         (d && (overlap(p, n, d->place, 4 * T) || overlap(p, n, d->path, 4 * T) ||
+                overlap(p, n, d->accepted, 4 * S) || overlap(p, n, d->work, 16 * (S + 1))));
+}
+
+int64_t cache_bytes(const rbkv_config* c) {
+  return (int64_t)c->num_blocks * c->block_size * c->num_heads_kv * c->head_dim *
+         (c->dtype == RBKV_BF16 ? 2 : 4);
+}
+
 DevPass append_pass(const rbkv_config* c, const rbkv_step_tables* t) {
   DevPass dp = {};
   dp.status = t->status;
@@ -356,10 +372,9 @@ rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tabl
   const ShapeInfo s = shape(cfg);
   const int64_t T = t->max_tokens;
   const int64_t q_bytes = T * s.H_q * s.D * (s.dtype == RBKV_BF16 ? 2 : 4);
-  if (overlap(q_out, q_bytes, t->slot, 4 * T) || overlap(q_out, q_bytes, t->position, 4 * T) ||
-      overlap(q_out, q_bytes, t->plan, 4 * step_plan_ints(t->num_seqs, T)) ||
-      (d && (overlap(q_out, q_bytes, d->place, 4 * T) || overlap(q_out, q_bytes, d->work, 16))))
-    return invalid("q_out overlaps an array that the call reads");
+  if (meets_step(t, d, q_out, q_bytes) || meets_step(t, d, k_cache, cache_bytes(cfg)) ||
+      meets_step(t, d, v_cache, cache_bytes(cfg)))
+    return invalid("q_out or a cache overlaps an array of the step");
   DevPass dp = append_pass(cfg, t);
   if (d) {
     dp.position = d->place;
@@ -425,9 +440,10 @@ rbkv_status rbkv_step_draft_compact(const rbkv_config* cfg, const rbkv_step_tabl
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
     return invalid("tensors must be 16-byte aligned");
   // (a row of one cache may be written before the other's columns have read it)
-  const int64_t cache = (int64_t)cfg->num_blocks * cfg->block_size * cfg->num_heads_kv *
-                        cfg->head_dim * (cfg->dtype == RBKV_BF16 ? 2 : 4);
+  const int64_t cache = cache_bytes(cfg);
   if (overlap(k_cache, cache, v_cache, cache)) return invalid("the caches overlap");
+  if (meets_step(t, d, k_cache, cache) || meets_step(t, d, v_cache, cache))
+    return invalid("a cache overlaps an array of the step");
   cudaError_t e =
       launch_draft_compact(draft_args(cfg, t, d), shape(cfg), k_cache, v_cache,
                            (cudaStream_t)stream);
