@@ -6,7 +6,7 @@
 // grow by doubling: S(i) starts as {i} with a pointer to the parent; a round
 // unites S(i) with the set that the pointer names and follows that one's pointer,
 // so S(i) holds the nearest 2^k tokens of the path after k rounds: as many rounds
-// as the logarithm of the deepest path has bits.
+// as the greatest depth has bits, 7 at most.
 //
 // Acceptance: from the last given token, the lowest child whose token is the
 // one chosen, until there is none.  (i is a child of c when c is the highest bit
@@ -16,13 +16,17 @@
 // outside M - all of them at once, in votes.  Only where siblings are alike does
 // that find more than a path (a token on it is then not the parent of the next), and
 // the path is walked, a broadcast, four compares and votes to a step: of 256 trees
-// of up to 60 tokens, chains among them, 15 us, where the votes take 5.
+// of up to 60 tokens, chains among them, 15 us, where the votes take 5.  The new
+// blocks' bits are written as the path leaves them, held or free (0.1 to 0.25 us
+// more than setting the free ones alone), so that a second acceptance may keep more
+// than the first.
 //
 // Move: kept token d of a sequence lies in the slot of token p_d >= d, and
 // goes to the slot of token d.  p rises, so a row is never written before it has
 // been read when a thread moves its columns in the order of d.
 //
-// All three are latency: a few dependent loads, for a few KB.
+// All three are latency: a few dependent loads, for a few KB (acceptance and move of
+// 16 trees of 8 in a graph 3.5 and 2.8 us, of 256 of 60 5.1 and 3.2).
 #include <algorithm>
 
 #include "rbkv_step.h"

@@ -228,7 +228,9 @@ __device__ __forceinline__ uint32_t ring_v(int j, int n) {
 }
 
 // The last of n entries whose place is at or before v: 32 places tested at a time by
-// the warp (in front of the first segment every round trip counts).
+// the warp (in front of the first segment every round trip counts; against halving,
+// in a graph: 64 trees of 32 tokens 185.7 and 184.7 us, a mixed batch of 98 sequences
+// 206.2 and 204.3, one tree 49.0 either way).
 template <class F>
 __device__ __forceinline__ int last_at(int n, int64_t v, F cum) {
   const int lane = threadIdx.x & 31;
