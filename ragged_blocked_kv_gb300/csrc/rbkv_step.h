@@ -241,16 +241,19 @@ __host__ __device__ __forceinline__ bool step_prefix_streamed(int32_t max_tokens
 
 #ifdef __CUDACC__
 // Whether the step was built for what it is used with: else its lengths and
-// lists would lead out of the tables.
+// lists would lead out of the tables.  kDraft: and whether its trees were planned for
+// this build.  (Not asked of ds.place: that branch, untaken, cost a step without drafts
+// 1 us: 512 rows behind 4096 keys 124.5 to 125.3 in a graph, 64 rows of 64 heads behind
+// 15999 59.5 to 60.6.)
+template <bool kDraft>
 __device__ __forceinline__ bool step_matches(const DevStep& ds, const ShapeInfo& s,
                                              const StepPlan& plan) {
   static_assert(kPlanGroup == 5 && kPlanBlock == 6 && kPlanSeqs == 7 && kPlanTokens == 8 &&
                     kPlanMaxBlocks == 9, "the header's second and third vector");
   const int4 b = *reinterpret_cast<const int4*>(plan.header + 4);
   const int2 c = *reinterpret_cast<const int2*>(plan.header + 8);
-  // (drafted tokens: whether their trees were planned for this build)
   int32_t stale = 0;
-  if (ds.place) stale = ds.work[0].single_cum ^ plan.header[kPlanSerial];
+  if constexpr (kDraft) stale = ds.work[0].single_cum ^ plan.header[kPlanSerial];
   // (no short cuts: all of it in one round trip)
   return ((b.y ^ s.g) | (b.z ^ s.B) | (b.w ^ ds.num_seqs) | (c.x ^ ds.max_tokens) |
           (c.y ^ ds.max_blocks) | stale) == 0;
@@ -258,10 +261,11 @@ __device__ __forceinline__ bool step_matches(const DevStep& ds, const ShapeInfo&
 // The step's rows; 0, and RBKV_ERR_INVALID in the status words, where it was
 // built for something else.  (The tile and the streaming kernel leave the report
 // to the join.)
+template <bool kDraft>
 __device__ __forceinline__ int32_t step_rows(const DevStep& ds, const ShapeInfo& s,
                                              const StepPlan& plan) {
   const int32_t rows = plan.header[kPlanRows];
-  if (step_matches(ds, s, plan)) return rows;
+  if (step_matches<kDraft>(ds, s, plan)) return rows;
   if (rows > 0 && threadIdx.x == 0) atomicCAS(ds.status, 0, kDevInvalid);
   return 0;
 }

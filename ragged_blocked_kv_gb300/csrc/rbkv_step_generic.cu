@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, (min_blocks<T, kPer, kRows, kDraft>(
   float* p_s = smem + kRows * D + warp * 32 * kRows;
   float* join_o = smem + kRows * D + kWarps * 32 * kRows;
   float* join_ml = join_o + kWarps * kRows * D;
-  const int T_rows = step_rows(ds, s, plan);
+  const int T_rows = step_rows<kDraft>(ds, s, plan);
   const int n_rows = T_rows * g;               // packed rows of a KV head
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int stride = kWarps * splits, mine = split * kWarps + warp;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, (min_blocks<T, kPer, kRows, kDraft>(
 }
 
 // O of the splits of a step: one warp per (row, query head).
-template <class T>
+template <class T, bool kDraft>
 __global__ void __launch_bounds__(128)
     step_generic_join_kernel(DevStep ds, ShapeInfo s, const float* __restrict__ part_o,
                              const float* __restrict__ part_lse, T* __restrict__ o, int splits) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(128)
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const int lane = threadIdx.x & 31, D = s.D;
-  const int64_t rows = (int64_t)step_rows(ds, s, plan) * s.H_q;
+  const int64_t rows = (int64_t)step_rows<kDraft>(ds, s, plan) * s.H_q;
   const int64_t all = (int64_t)ds.max_tokens * s.H_q;
   for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); w < rows;
        w += (int64_t)gridDim.x * 4) {
@@ -399,7 +399,7 @@ cudaError_t launch_rows(const DevStep& ds, const ShapeInfo& s, const void* q, co
   cfg.gridDim = dim3((unsigned)std::min<int64_t>((warps + 3) / 4, (int64_t)sms * 16));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, step_generic_join_kernel<T>, ds, s, (const float*)part_o,
+  return cudaLaunchKernelEx(&cfg, step_generic_join_kernel<T, kDraft>, ds, s, (const float*)part_o,
                             (const float*)part_lse, (T*)o, splits);
 }
 

@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
-  if (!step_matches(ds, shp, plan)) {
+  if (!step_matches<kDraft>(ds, shp, plan)) {
     ptx::pdl_wait_previous();
     return;
   }
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, W > 1 ? 2 : kJoinBlocks)
   const int kvh = h / g, hh = h - kvh * g;
   const bool pre_streamed = pre && step_prefix_streamed(ds.max_tokens, g);
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
-  const int T = step_rows(ds, shp, plan);
+  const int T = step_rows<kDraft>(ds, shp, plan);
   for (int t = blockIdx.y; t < T; t += gridDim.y) {
     const int64_t w = (int64_t)t * shp.H_q + h;
     // the two main sources, requested before anything that depends on the

@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::pdl_launch_dependents();
   const StepPlan plan = step_plan(ds.plan, ds.num_seqs, ds.max_tokens);
   const StepWork work = step_work(ds, shp, plan);
-  const int64_t ctas = !step_matches(ds, shp, plan) ? 0
+  const int64_t ctas = !step_matches<kDraft>(ds, shp, plan) ? 0
                        : kLanes ? 2 * draft_road(ds, shp, work).pairs
                                 : min((int64_t)gridDim.x, work.tile_total);
   if (blockIdx.x >= ctas) return;
