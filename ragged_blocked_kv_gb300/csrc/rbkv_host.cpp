@@ -212,6 +212,7 @@ struct rbkv_pass {
   std::vector<cudaStream_t> streams;   // every stream device work of the pass was put on
   cudaEvent_t upload_ev = nullptr;
   DevPass dp{};
+  const int32_t* position = nullptr;   // of every row, on the device
   void use_stream(cudaStream_t st) {
     last_stream = st;
     if (std::find(streams.begin(), streams.end(), st) == streams.end()) streams.push_back(st);
@@ -750,7 +751,7 @@ rbkv_status ensure_device(rbkv_pass* p, cudaStream_t st) {
     DevPass& dp = p->dp;
     dp.status = base;
     dp.slot = base + o_slot;
-    dp.position = base + o_pos;
+    p->position = base + o_pos;
     dp.block_ids = base + o_blocks;
     dp.decode_items = (const WorkItem*)(base + o_dec);
     dp.generic_items = (const WorkItem*)(base + o_gen);
@@ -1167,8 +1168,8 @@ rbkv_status rbkv_kv_append_rotary(rbkv_pass* p, const rbkv_rotary* rotary, const
   if (rs != RBKV_OK) return rs;
   const ShapeInfo s = shape_of(p->cfg);
   cudaError_t e = launch_counted(RBKV_KERNEL_KV_APPEND, st, [&] {
-    return launch_append_rotary(p->dp, s, *rotary, 0, q, q_out, k_new, v_new, k_cache, v_cache,
-                                st, !g_prof.on);
+    return launch_append_rotary(p->dp, DevTurns{p->position}, s, *rotary, q, q_out, k_new, v_new,
+                                k_cache, v_cache, st, !g_prof.on);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv_append_rotary launch");
   return RBKV_OK;
@@ -1388,7 +1389,6 @@ rbkv_status rbkv_frame_create(const rbkv_config* cfg, const rbkv_frame_caps* cap
   dp.status = base;
   dp.counts = base + 4;
   dp.slot = base + f->o_slot;
-  dp.position = base + f->o_pos;
   dp.block_ids = base + f->o_blocks;
   dp.decode_items = (const WorkItem*)(base + f->o_dec);
   dp.generic_items = nullptr;
@@ -1518,8 +1518,8 @@ rbkv_status rbkv_frame_kv_append_rotary(rbkv_frame* f, const rbkv_rotary* rotary
   cudaStream_t st = (cudaStream_t)stream;
   const ShapeInfo s = shape_of(f->cfg);
   cudaError_t e = launch_counted(RBKV_KERNEL_KV_APPEND, st, [&] {
-    return launch_append_rotary(f->dp, s, *rotary, 0, q, q_out, k_new, v_new, k_cache, v_cache,
-                                st, !g_prof.on);
+    return launch_append_rotary(f->dp, DevTurns{f->dev + f->o_pos}, s, *rotary, q, q_out, k_new,
+                                v_new, k_cache, v_cache, st, !g_prof.on);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kv_append_rotary launch");
   return RBKV_OK;

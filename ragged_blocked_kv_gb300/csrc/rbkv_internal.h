@@ -92,7 +92,6 @@ static_assert(sizeof(ChunkItem) == 32, "ChunkItem is 8 int32");
 struct DevPass {
   int32_t* status;                 // device status words (rbkv_status code, wait site, ...)
   const int32_t* slot;             // [T]
-  const int32_t* position;         // [T]
   const int32_t* block_ids;        // all block tables
   const WorkItem* decode_items;    // fast decode path
   const WorkItem* generic_items;   // CUDA-core path
@@ -116,12 +115,21 @@ struct DevPass {
   // Null for a plain pass.
   const int32_t* counts;
   // A step built on the device (rbkv_step_*): {block size, rows of its arrays}
-  // that it was built for, to be compared with what it is used with; and for
-  // drafted tokens the serials of the build and of their plan.  Null otherwise.
-  const int32_t* built_for[4];
-  // Where the append notes the build whose rows it rotates by the places of drafted
-  // tokens.  Null otherwise.
-  int32_t* turned;
+  // that it was built for, to be compared with what it is used with.  Null
+  // otherwise.
+  const int32_t* built_for[2];
+};
+
+// What an append with a rotation needs beside a DevPass: row t turns by offset +
+// position[t].  (Not in DevPass: as parameters of the plain append, in a graph, these
+// words made 64 rows take 2.90 us instead of 2.87, 2048 rows 5.68 instead of 5.63.)
+struct DevTurns {
+  const int32_t* position;         // [T]
+  int32_t offset;
+  // Drafted tokens: the serials of the build and of their plan, to be compared, and
+  // where the build whose rows were turned by places is noted.  Null otherwise.
+  const int32_t* planned_for[2];
+  int32_t* noted;
 };
 
 enum { kCountTokens = 0, kCountDecode = 1, kCountGeneric = 2, kCountChunk = 3, kCountCombine = 4 };
@@ -185,12 +193,11 @@ cudaError_t launch_kv_append(const DevPass& dp, const ShapeInfo& s, const void* 
 // kernel that may overlap its predecessor and waits for it before storing.
 cudaError_t launch_meta_upload(const void* src, void* dst, size_t bytes, cudaStream_t st,
                                bool overlap_previous);
-// The append with a rotation on the way, by the positions offset + position[t]
-// (rbkv_rotary.cu).
-cudaError_t launch_append_rotary(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r,
-                                 int32_t offset, const void* q, void* q_out, const void* k_new,
-                                 const void* v_new, void* k_cache, void* v_cache, cudaStream_t st,
-                                 bool overlap_previous);
+// The append with a rotation on the way (rbkv_rotary.cu).
+cudaError_t launch_append_rotary(const DevPass& dp, const DevTurns& at, const ShapeInfo& s,
+                                 const rbkv_rotary& r, const void* q, void* q_out,
+                                 const void* k_new, const void* v_new, void* k_cache,
+                                 void* v_cache, cudaStream_t st, bool overlap_previous);
 // Checks of its arguments, for `rows` rows.
 rbkv_status check_append_rotary(const rbkv_config* c, const rbkv_rotary* r, int64_t rows,
                                 const void* q, const void* q_out, const void* k_new,

@@ -155,7 +155,7 @@ __device__ __forceinline__ int turn_at(int p) {
 
 template <class T, int kVec>
 __global__ void __launch_bounds__(kThreads, 8)
-    append_rotary_kernel(DevPass dp, Heads h, rbkv_rotary r, int32_t offset, const void* q,
+    append_rotary_kernel(DevPass dp, DevTurns pos, Heads h, rbkv_rotary r, const void* q,
                          void* q_out, const void* __restrict__ k_new,
                          const void* __restrict__ v_new, void* __restrict__ k_cache,
                          void* __restrict__ v_cache) {
@@ -169,11 +169,11 @@ __global__ void __launch_bounds__(kThreads, 8)
   const int tid = threadIdx.x;
   if (dp.built_for[0] &&
       (*dp.built_for[0] != h.block || *dp.built_for[1] != dp.num_tokens ||
-       (dp.built_for[2] && *dp.built_for[2] != *dp.built_for[3]))) {
+       (pos.noted && *pos.planned_for[0] != *pos.planned_for[1]))) {
     if (tid == 0 && rows > 0) atomicCAS(dp.status, 0, kDevInvalid);
     return;
   }
-  if (dp.turned && blockIdx.x == 0 && tid == 0) *dp.turned = *dp.built_for[2];
+  if (pos.noted && blockIdx.x == 0 && tid == 0) *pos.noted = *pos.planned_for[0];
   // A thread's units: one column of every `step`-th head (of Q's, then K's, then V's)
   const int step = kThreads / h.per, heads = h.q + 2 * h.kv, half = r.rotary_dim / 2;
   const int head0 = tid / h.per, col = tid - head0 * h.per;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 8)
       }
       const int slot = dp.slot[row];
       if (x0 == 0) {
-        const uint32_t at = (uint32_t)(dp.position[row] + offset);
+        const uint32_t at = (uint32_t)(pos.position[row] + pos.offset);
         __syncthreads();      // (the previous row's are no longer needed)
         if (tid < half) {
           float s, c;
@@ -233,9 +233,10 @@ __global__ void __launch_bounds__(kThreads, 8)
 }
 
 template <class T, int kVec>
-cudaError_t launch(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r, int32_t offset,
-                   const void* q, void* q_out, const void* k_new, const void* v_new,
-                   void* k_cache, void* v_cache, cudaStream_t st, bool overlap_previous) {
+cudaError_t launch(const DevPass& dp, const DevTurns& at, const ShapeInfo& s,
+                   const rbkv_rotary& r, const void* q, void* q_out, const void* k_new,
+                   const void* v_new, void* k_cache, void* v_cache, cudaStream_t st,
+                   bool overlap_previous) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -256,7 +257,7 @@ cudaError_t launch(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = overlap_previous ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, kVec>, dp, h, r, offset, q, q_out,
+  return cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, kVec>, dp, at, h, r, q, q_out,
                             k_new, v_new, k_cache, v_cache);
 }
 
@@ -299,10 +300,10 @@ rbkv_status check_append_rotary(const rbkv_config* c, const rbkv_rotary* r, int6
   return RBKV_OK;
 }
 
-cudaError_t launch_append_rotary(const DevPass& dp, const ShapeInfo& s, const rbkv_rotary& r,
-                                 int32_t offset, const void* q, void* q_out, const void* k_new,
-                                 const void* v_new, void* k_cache, void* v_cache, cudaStream_t st,
-                                 bool overlap_previous) {
+cudaError_t launch_append_rotary(const DevPass& dp, const DevTurns& at, const ShapeInfo& s,
+                                 const rbkv_rotary& r, const void* q, void* q_out,
+                                 const void* k_new, const void* v_new, void* k_cache,
+                                 void* v_cache, cudaStream_t st, bool overlap_previous) {
   if (dp.num_tokens == 0) return cudaSuccess;
   // the widest words of which both of a unit lie among the rotated elements, or both
   // behind them (512 rows of 32 and 8 heads of 128, bf16: 20 elements rotated in words
@@ -316,7 +317,7 @@ cudaError_t launch_append_rotary(const DevPass& dp, const ShapeInfo& s, const rb
                       : launch<__nv_bfloat16, 1>;
   else
     fn = R % 8 == 0 ? launch<float, 4> : R % 4 == 0 ? launch<float, 2> : launch<float, 1>;
-  return fn(dp, s, r, offset, q, q_out, k_new, v_new, k_cache, v_cache, st, overlap_previous);
+  return fn(dp, at, s, r, q, q_out, k_new, v_new, k_cache, v_cache, st, overlap_previous);
 }
 
 }  // namespace rbkv

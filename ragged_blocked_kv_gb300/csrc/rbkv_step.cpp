@@ -169,7 +169,6 @@ DevPass append_pass(const rbkv_config* c, const rbkv_step_tables* t) {
   DevPass dp = {};
   dp.status = t->status;
   dp.slot = t->slot;
-  dp.position = t->position;
   dp.num_tokens = t->max_tokens;
   dp.num_blocks = c->num_blocks;
   dp.counts = t->plan + kPlanRows;
@@ -375,15 +374,10 @@ rbkv_status rbkv_step_append_rotary(const rbkv_config* cfg, const rbkv_step_tabl
   if (meets_step(t, d, q_out, q_bytes) || meets_step(t, d, k_cache, cache_bytes(cfg)) ||
       meets_step(t, d, v_cache, cache_bytes(cfg)))
     return invalid("q_out or a cache overlaps an array of the step");
-  DevPass dp = append_pass(cfg, t);
-  if (d) {
-    dp.position = d->place;
-    dp.built_for[2] = t->plan + kPlanSerial;
-    dp.built_for[3] = d->work;
-    dp.turned = t->plan + kPlanTurned;
-  }
-  cudaError_t e = launch_append_rotary(dp, s, *rotary, prefix_len, q, q_out, k_new, v_new, k_cache,
-                                       v_cache, (cudaStream_t)stream, true);
+  DevTurns at = {t->position, prefix_len};
+  if (d) at = DevTurns{d->place, prefix_len, {t->plan + kPlanSerial, d->work}, t->plan + kPlanTurned};
+  cudaError_t e = launch_append_rotary(append_pass(cfg, t), at, s, *rotary, q, q_out, k_new, v_new,
+                                       k_cache, v_cache, (cudaStream_t)stream, true);
   if (e != cudaSuccess) return cuda_fail(e, "step append_rotary launch");
   note_launches(1);
   return RBKV_OK;
