@@ -846,9 +846,10 @@ class StepTables(_Arrays):
     def append_rotary(self, rotary: Rotary, q, k_new, v_new, k_cache, v_cache, q_out=None,
                       prefix_len: int = 0, draft: Optional["StepDraft"] = None, stream=None):
         """``append`` with the rotation on the way, by the positions prefix_len +
-        ``position`` (prefix_len + ``draft.place`` with drafted tokens): rotated keys
-        and the values into the caches, rotated queries into ``q_out``, which may be
-        ``q`` (rows past the step's are left as they were); returns ``q_out``."""
+        ``position``, or prefix_len + ``draft.place`` (trees need their ``draft``: a kept
+        token comes to lie at its place): rotated keys and the values into the caches,
+        rotated queries into ``q_out``, which may be ``q`` (rows past the step's are left
+        as they were); returns ``q_out``."""
         prefix_len = _int32(int(prefix_len), "prefix_len")
         if q_out is None:
             q_out = _empty_on(stream, self._q_shape, self._dt, self.device)
